@@ -8,6 +8,9 @@ or the tensors are not on a GPU, the call raises.
     import implicit_gemm_conv_amd as igc
     y = igc.conv_fwd(x, w, stride=1, padding=1)        # x (N,[D,]H,W,C), w (Co,[KD,]KH,KW,C)
     dx = igc.conv_bwd_data(dy, w, x.shape, stride=1, padding=1)   # gradient w.r.t. x
+
+The sequence operators (seq_conv, gated_scan, pack8 and their backward and single-row calls)
+are in sequence.py and exported here.
 """
 import ctypes
 import os
@@ -322,3 +325,7 @@ def from_torch_weight(w_oc_first: torch.Tensor) -> torch.Tensor:
     """(C_out, C_in, [KD,] KH, KW) PyTorch-style filter -> (C_out, [KD,] KH, KW, C_in)."""
     perm = (0, *range(2, w_oc_first.dim()), 1)
     return w_oc_first.permute(perm).contiguous()
+
+
+from .sequence import (Packed8, gated_scan, gated_scan_bwd, gated_scan_step, pack8, seq_conv,  # noqa: E402
+                       seq_conv_bwd, seq_conv_step, unpack8)
