@@ -71,8 +71,9 @@ __global__ __launch_bounds__(256) void seq_conv_fwd_kernel(ConvArgs a) {
     const int byte = group_byte(top);
     const float inv = group_inverse(byte);
     a.kept.e[((int64_t)b * groups + g) * a.c + ch] = (uint8_t)byte;
-    for (int t = t0; t < t1; ++t)
-      a.kept.q[((int64_t)b * a.t + t) * a.c + ch] = (int8_t)quantise(to_f32(x[(int64_t)t * a.x.st]), inv);
+    int8_t* q = a.kept.q + (((int64_t)b * groups + g) * a.c + ch) * kGroup;
+    for (int j = 0; j < kGroup; ++j)
+      q[j] = t0 + j < t1 ? (int8_t)quantise(to_f32(x[(int64_t)(t0 + j) * a.x.st]), inv) : 0;
   }
   if (a.state_out && g == groups - 1) {
     T* out = (T*)a.state_out + (int64_t)b * (K - 1) * a.c + ch;
@@ -103,8 +104,8 @@ __global__ __launch_bounds__(256) void seq_conv_bwd_kernel(ConvArgs a) {
   const uint8_t* starts = a.starts ? a.starts + (int64_t)b * a.t : nullptr;
   const auto row = [&](int s) -> float {
     if (s < 0 || !a.kept.q) return row_before(x, a.x.st, state, s, K, a.c);
-    return (float)a.kept.q[((int64_t)b * a.t + s) * a.c + ch] *
-           group_scale(a.kept.e[((int64_t)b * groups + s / kGroup) * a.c + ch]);
+    const int64_t at = ((int64_t)b * groups + s / kGroup) * a.c + ch;
+    return (float)a.kept.q[at * kGroup + s % kGroup] * group_scale(a.kept.e[at]);
   };
   float w[K], win[K], acc[K], dw[K], db = 0.f;
 #pragma unroll

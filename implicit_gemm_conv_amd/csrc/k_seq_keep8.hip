@@ -2,77 +2,117 @@
 // consecutive rows of one channel share a power of two: down a channel values
 // are of one scale where channels of one row are not, and neighbouring lanes
 // hold neighbouring channels, so the largest of a group needs no exchange
-// between lanes.
+// between lanes.  A lane takes V channels of one group: 16 row pieces of V
+// values on one side, V runs of 16 bytes on the other.
 #include "seq_device.h"
 
 namespace convseq {
 
 namespace {
 
-// One thread per channel and group.
-template <typename T>
-__global__ __launch_bounds__(256) void pack8_kernel(int t, int c, int groups, Rows x, Kept k) {
-  const int cb = (c + 255) / 256;
-  const int ch = (int)(blockIdx.x % cb) * 256 + threadIdx.x, part = blockIdx.x / cb;
-  if (ch >= c) return;
-  const int b = part / groups, g = part % groups;
-  const int t0 = g * kGroup, n = min(t - t0, kGroup);
-  const T* p = (const T*)x.p + b * x.sb + (int64_t)t0 * x.st + ch;
-  float v[kGroup];
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < kGroup; ++j) {
-    v[j] = j < n ? to_f32(p[(int64_t)j * x.st]) : 0.f;
-    top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
-  }
-  const int byte = group_byte(top);
-  const float inv = group_inverse(byte);
-  k.e[(int64_t)part * c + ch] = (uint8_t)byte;
-#pragma unroll
-  for (int j = 0; j < kGroup; ++j)
-    if (j < n) k.q[((int64_t)b * t + t0 + j) * c + ch] = (int8_t)quantise(v[j], inv);
+// Where a lane of the grid works: channels ch.., group g of batch b.
+struct Place {
+  int ch, b, g, t0, n;
+  int64_t at;  // (b, g, ch) as an index of e
+};
+template <int V>
+__device__ __forceinline__ bool place(int t, int c, int groups, Place* p) {
+  const int cb = (c + 64 * V - 1) / (64 * V);
+  const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int part = (int)(wave / cb);
+  p->ch = ((int)(wave % cb) * 64 + (threadIdx.x & 63)) * V;
+  p->b = part / groups;
+  p->g = part % groups;
+  p->t0 = p->g * kGroup;
+  p->n = min(t - p->t0, kGroup);
+  p->at = (int64_t)part * c + p->ch;
+  return p->ch < c;
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void unpack8_kernel(int t, int c, int groups, Kept k, T* out) {
-  const int cb = (c + 255) / 256;
-  const int ch = (int)(blockIdx.x % cb) * 256 + threadIdx.x, part = blockIdx.x / cb;
-  if (ch >= c) return;
-  const int b = part / groups, g = part % groups;
-  const int t0 = g * kGroup, n = min(t - t0, kGroup);
-  const float scale = group_scale(k.e[(int64_t)part * c + ch]);
+template <typename T, int V>
+__global__ __launch_bounds__(256) void pack8_kernel(int parts, int t, int c, int groups, Rows x, Kept k) {
+  Place p;
+  if (!place<V>(t, c, groups, &p) || p.at >= (int64_t)parts * c) return;
+  typedef Pack<T, V> P;
+  const T* in = (const T*)x.p + p.b * x.sb + (int64_t)p.t0 * x.st + p.ch;
+  P raw[kGroup];
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j) raw[j] = *(const P*)(in + (int64_t)min(j, p.n - 1) * x.st);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float v[kGroup];
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) v[j] = raw[j].get(i);
+    int byte;
+    const uint4 q = pack_group(v, p.n, &byte);
+    *(uint4*)(k.q + (p.at + i) * kGroup) = q;
+    k.e[p.at + i] = (uint8_t)byte;
+  }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(256) void unpack8_kernel(int parts, int t, int c, int groups, Kept k, T* out) {
+  Place p;
+  if (!place<V>(t, c, groups, &p) || p.at >= (int64_t)parts * c) return;
+  typedef Pack<T, V> P;
+  uint4 q[V];
+  float s[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    q[i] = *(const uint4*)(k.q + (p.at + i) * kGroup);
+    s[i] = group_scale(k.e[p.at + i]);
+  }
+  T* to = out + ((int64_t)p.b * t + p.t0) * c + p.ch;
 #pragma unroll
   for (int j = 0; j < kGroup; ++j)
-    if (j < n) {
-      const int64_t at = ((int64_t)b * t + t0 + j) * c + ch;
-      out[at] = from_f32<T>((float)k.q[at] * scale);
+    if (j < p.n) {
+      P v;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+        v.set(i, held(w[j >> 2], j & 3) * s[i]);
+      }
+      *(P*)(to + (int64_t)j * c) = v;
     }
+}
+
+template <int V>
+unsigned blocks(int64_t parts, int c) {
+  return (unsigned)((parts * ((c + 64 * V - 1) / (64 * V)) + 3) / 4);
+}
+
+template <typename T, int V>
+hipError_t pack_as(int b, int t, int c, const Rows& x, const Kept& k, hipStream_t s) {
+  const int groups = (t + kGroup - 1) / kGroup;
+  hipLaunchKernelGGL((pack8_kernel<T, V>), dim3(blocks<V>((int64_t)b * groups, c)), dim3(256), 0, s, b * groups, t, c,
+                     groups, x, k);
+  return hipGetLastError();
+}
+template <typename T, int V>
+hipError_t unpack_as(int b, int t, int c, const Kept& k, void* out, hipStream_t s) {
+  const int groups = (t + kGroup - 1) / kGroup;
+  hipLaunchKernelGGL((unpack8_kernel<T, V>), dim3(blocks<V>((int64_t)b * groups, c)), dim3(256), 0, s, b * groups, t, c,
+                     groups, k, (T*)out);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_pack8(int b, int t, int c, int dtype, const Rows& x, const Kept& k, hipStream_t s) {
-  const int groups = (t + kGroup - 1) / kGroup;
-  const dim3 grid((unsigned)((c + 255) / 256 * b * groups));
   if (dtype == convfwd::kF32)
-    hipLaunchKernelGGL(pack8_kernel<float>, grid, dim3(256), 0, s, t, c, groups, x, k);
-  else if (dtype == convfwd::kF16)
-    hipLaunchKernelGGL(pack8_kernel<_Float16>, grid, dim3(256), 0, s, t, c, groups, x, k);
-  else
-    hipLaunchKernelGGL(pack8_kernel<__bf16>, grid, dim3(256), 0, s, t, c, groups, x, k);
-  return hipGetLastError();
+    return c % 2 == 0 && pieces(x, 8, 4) ? pack_as<float, 2>(b, t, c, x, k, s) : pack_as<float, 1>(b, t, c, x, k, s);
+  const bool wide = c % 4 == 0 && pieces(x, 8, 2);
+  if (dtype == convfwd::kF16) return wide ? pack_as<_Float16, 4>(b, t, c, x, k, s) : pack_as<_Float16, 1>(b, t, c, x, k, s);
+  return wide ? pack_as<__bf16, 4>(b, t, c, x, k, s) : pack_as<__bf16, 1>(b, t, c, x, k, s);
 }
 
 hipError_t launch_unpack8(int b, int t, int c, int dtype, const Kept& k, void* out, hipStream_t s) {
-  const int groups = (t + kGroup - 1) / kGroup;
-  const dim3 grid((unsigned)((c + 255) / 256 * b * groups));
   if (dtype == convfwd::kF32)
-    hipLaunchKernelGGL(unpack8_kernel<float>, grid, dim3(256), 0, s, t, c, groups, k, (float*)out);
-  else if (dtype == convfwd::kF16)
-    hipLaunchKernelGGL(unpack8_kernel<_Float16>, grid, dim3(256), 0, s, t, c, groups, k, (_Float16*)out);
-  else
-    hipLaunchKernelGGL(unpack8_kernel<__bf16>, grid, dim3(256), 0, s, t, c, groups, k, (__bf16*)out);
-  return hipGetLastError();
+    return c % 2 == 0 && (uintptr_t)out % 8 == 0 ? unpack_as<float, 2>(b, t, c, k, out, s)
+                                                 : unpack_as<float, 1>(b, t, c, k, out, s);
+  const bool wide = c % 4 == 0 && (uintptr_t)out % 8 == 0;
+  if (dtype == convfwd::kF16) return wide ? unpack_as<_Float16, 4>(b, t, c, k, out, s) : unpack_as<_Float16, 1>(b, t, c, k, out, s);
+  return wide ? unpack_as<__bf16, 4>(b, t, c, k, out, s) : unpack_as<__bf16, 1>(b, t, c, k, out, s);
 }
 
 }  // namespace convseq

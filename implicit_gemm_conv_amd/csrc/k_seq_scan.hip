@@ -20,50 +20,8 @@ template <typename T>
 __device__ __forceinline__ float value(const Rows& x, const Kept& k, int b, int t, int ch, int tt, int c) {
   if (!k.q) return to_f32(((const T*)x.p)[b * x.sb + (int64_t)t * x.st + ch]);
   const int groups = (tt + kGroup - 1) / kGroup;
-  return (float)k.q[((int64_t)b * tt + t) * c + ch] *
-         group_scale(k.e[((int64_t)b * groups + t / kGroup) * c + ch]);
-}
-
-template <typename T>
-__device__ __forceinline__ void pack_group(const Rows& x, const Kept& k, int b, int t0, int t1, int ch, int tt,
-                                           int c) {
-  const int groups = (tt + kGroup - 1) / kGroup;
-  uint32_t top = 0;
-  const T* p = (const T*)x.p + b * x.sb + ch;
-  for (int t = t0; t < t1; ++t) top = max(top, __float_as_uint(to_f32(p[(int64_t)t * x.st])) & 0x7fffffffu);
-  const int byte = group_byte(top);
-  const float inv = group_inverse(byte);
-  k.e[((int64_t)b * groups + t0 / kGroup) * c + ch] = (uint8_t)byte;
-  for (int t = t0; t < t1; ++t)
-    k.q[((int64_t)b * tt + t) * c + ch] = (int8_t)quantise(to_f32(p[(int64_t)t * x.st]), inv);
-}
-
-// One thread per channel of a sequence, row after row.
-template <typename T>
-__global__ __launch_bounds__(64) void seq_scan_fwd_kernel(ScanArgs a) {
-  const int cb = (a.c + 63) / 64;
-  const int ch = (int)(blockIdx.x % cb) * 64 + threadIdx.x, b = blockIdx.x / cb;
-  if (ch >= a.c) return;
-  const float rate = channel_rate(a.lam[ch], a.decay);
-  const int64_t bc = (int64_t)b * a.c + ch;
-  const int pieces = (a.t + kEvery - 1) / kEvery;
-  float h = a.h0 ? a.h0[bc] : 0.f;
-  for (int t = 0; t < a.t; ++t) {
-    if (a.states && t % kEvery == 0) a.states[((int64_t)b * pieces + t / kEvery) * a.c + ch] = h;
-    const float x = value<T>(a.x, Kept{}, b, t, ch, a.t, a.c);
-    const Gate g = gates(value<T>(a.r, Kept{}, b, t, ch, a.t, a.c), value<T>(a.i, Kept{}, b, t, ch, a.t, a.c), rate);
-    const float in = g.t * inv_sqrt(g.t) * (g.i * x);
-    h = a.starts && a.starts[(int64_t)b * a.t + t] ? in : fmaf(g.a, h, in);
-    ((T*)a.y)[((int64_t)b * a.t + t) * a.c + ch] = from_f32<T>(h);
-  }
-  if (a.h_last) a.h_last[bc] = h;
-  if (a.kept[0].q)
-    for (int t = 0; t < a.t; t += kGroup) {
-      const int t1 = min(a.t, t + kGroup);
-      pack_group<T>(a.x, a.kept[0], b, t, t1, ch, a.t, a.c);
-      pack_group<T>(a.r, a.kept[1], b, t, t1, ch, a.t, a.c);
-      pack_group<T>(a.i, a.kept[2], b, t, t1, ch, a.t, a.c);
-    }
+  const int64_t at = ((int64_t)b * groups + t / kGroup) * c + ch;
+  return (float)k.q[at * kGroup + t % kGroup] * group_scale(k.e[at]);
 }
 
 // One thread per channel of a sequence: piece after piece from the last, h
@@ -147,15 +105,7 @@ hipError_t for_type(int dtype, const F& f) {
 
 }  // namespace
 
-int64_t scan_fwd_work_bytes(int, int, int) { return 0; }
 int64_t scan_bwd_work_bytes(int b, int, int c) { return (int64_t)b * c * 4; }
-
-hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t s) {
-  return for_type(a.dtype, [&](auto t) {
-    hipLaunchKernelGGL((seq_scan_fwd_kernel<decltype(t)>), dim3((a.c + 63) / 64 * a.b), dim3(64), 0, s, a);
-    return hipGetLastError();
-  });
-}
 
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t s) {
   return for_type(a.dtype, [&](auto t) {

@@ -1,0 +1,209 @@
+// k_seq_scan_fwd.hip -- gated linear recurrence, forward, in one pass over the
+// inputs.
+//
+//   r = sigmoid(gate_r), i = sigmoid(gate_i), u = decay * softplus(lam) * r, a = e^-u
+//   h_t = a_t h_{t-1} + sqrt(1 - a^2) i x_t
+//
+// A workgroup of 8 waves takes a tile of 128 rows by 64 V channels, a wave 16
+// rows of it, a lane V channels of those rows.  The lane runs the recurrence
+// over its rows from zero, keeping for each row the product A of the a so far
+// and the h so far; the waves' totals are composed through LDS, the tiles'
+// through memory (seq_carry.h), and h_t = H_t + A_t h_before is stored.  Each
+// input is read once and y written once: memory bound, 4 elements a value.
+#include "seq_carry.h"
+
+namespace convseq {
+
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kTile = kWaves * kGroup;  // rows
+
+template <typename T, int V, bool STARTS, bool KEEP>
+__global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a, int cols, int tiles) {
+  __shared__ Carry totals[kWaves][64 * V];
+  __shared__ float entry[64 * V];
+  __shared__ int ticket;
+  typedef Pack<T, V> P;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+
+  int id = blockIdx.x;
+  if (tiles > 1) {
+    if (threadIdx.x == 0)
+      ticket = __hip_atomic_fetch_add((int*)a.work, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    id = __builtin_amdgcn_readfirstlane(ticket);
+  }
+  const int tile = id / (cols * a.b), column = id % (cols * a.b);
+  const int b = column / cols;
+  const int ch = (column % cols * 64 + lane) * V;
+  const int chl = min(ch, a.c - V);  // lanes past the last channel read it again
+  const bool own = ch < a.c;
+  const int t0 = tile * kTile + wave * kGroup;
+  const int n = min(max(a.t - t0, 0), kGroup);  // rows of this wave
+
+  const T* px = (const T*)a.x.p + b * a.x.sb + chl;
+  const T* pr = (const T*)a.r.p + b * a.r.sb + chl;
+  const T* pi = (const T*)a.i.p + b * a.i.sb + chl;
+  P rx[kGroup], rr[kGroup], ri[kGroup];
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j) {
+    const int64_t t = min(t0 + j, a.t - 1);  // rows past the last read it again
+    rx[j] = *(const P*)(px + t * a.x.st);
+    rr[j] = *(const P*)(pr + t * a.r.st);
+    ri[j] = *(const P*)(pi + t * a.i.st);
+  }
+  uint32_t first = 0;  // bit j: row t0 + j begins a sequence
+  if (STARTS) {
+    const bool f = lane < n && a.starts[(int64_t)b * a.t + t0 + lane];
+    first = (uint32_t)__ballot(f);
+  }
+  float rate[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) rate[i] = channel_rate(a.lam[chl + i], a.decay);
+
+  if (KEEP && n > 0 && own) {
+    const int groups = (a.t + kGroup - 1) / kGroup;
+    const int64_t at = ((int64_t)b * groups + t0 / kGroup) * a.c + ch;
+    const auto keep = [&](const P(&raw)[kGroup], const Kept& k) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float v[kGroup];
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) v[j] = raw[j].get(i);
+        int byte;
+        const uint4 q = pack_group(v, n, &byte);
+        *(uint4*)(k.q + (at + i) * kGroup) = q;
+        k.e[at + i] = (uint8_t)byte;
+      }
+    };
+    keep(rx, a.kept[0]);
+    keep(rr, a.kept[1]);
+    keep(ri, a.kept[2]);
+  }
+
+  Carry run[kGroup][V];
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const Gate g = gates(rr[j].get(i), ri[j].get(i), rate[i]);
+      Carry c = {g.a, g.t * inv_sqrt(g.t) * (g.i * rx[j].get(i))};
+      if (STARTS && (first >> j & 1)) c.a = -0.f;
+      if (j >= n) c = Carry{1.f, 0.f};
+      run[j][i] = j == 0 ? c : STARTS ? compose(run[j - 1][i], c)
+                                      : Carry{run[j - 1][i].a * c.a, fmaf(c.a, run[j - 1][i].h, c.h)};
+    }
+
+  // the waves' totals; before = what the waves above do to the state, whole = the tile
+#pragma unroll
+  for (int i = 0; i < V; ++i) totals[wave][lane * V + i] = run[kGroup - 1][i];
+  __syncthreads();
+  Carry before[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) before[i] = Carry{1.f, 0.f};
+  for (int w = 0; w < wave; ++w)
+#pragma unroll
+    for (int i = 0; i < V; ++i) before[i] = compose(before[i], totals[w][lane * V + i]);
+
+  if (wave == kWaves - 1) {
+    // this wave has the tile's total, and fetches the state before it
+    float h[V];
+    Carry whole[V];
+    uint64_t* words = (uint64_t*)((char*)a.work + kTicketBytes);
+    const int64_t step = (int64_t)cols * a.b * 64 * V;
+    uint64_t* mine = words + tile * step + ((int64_t)column * 64 + lane) * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) whole[i] = compose(before[i], run[kGroup - 1][i]);
+    if (tile == 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) h[i] = a.h0 ? a.h0[(int64_t)b * a.c + chl + i] : 0.f;
+    } else {
+      if (tile < tiles - 1)
+#pragma unroll
+        for (int i = 0; i < V; ++i) publish(mine + i, whole[i]);
+      look_back<V>(words + ((int64_t)column * 64 + lane) * V, step, tile, h);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float after = apply(whole[i], h[i]);
+      if (tile < tiles - 1)
+        publish(mine + i, Carry{__uint_as_float(kWhole), after});
+      else if (a.h_last && own)
+        a.h_last[(int64_t)b * a.c + ch + i] = after;
+      entry[lane * V + i] = h[i];
+    }
+  }
+  __syncthreads();
+
+  float h[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) h[i] = apply(before[i], entry[lane * V + i]);
+  if (!own || n == 0) return;
+  if (a.states && t0 % kEvery == 0) {
+    const int pieces = (a.t + kEvery - 1) / kEvery;
+#pragma unroll
+    for (int i = 0; i < V; ++i) a.states[((int64_t)b * pieces + t0 / kEvery) * a.c + ch + i] = h[i];
+  }
+  T* y = (T*)a.y + ((int64_t)b * a.t + t0) * a.c + ch;
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j)
+    if (j < n) {
+      P v;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v.set(i, STARTS ? apply(run[j][i], h[i]) : fmaf(run[j][i].a, h[i], run[j][i].h));
+      *(P*)(y + (int64_t)j * a.c) = v;
+    }
+}
+
+// No rows: the state passes through.
+__global__ __launch_bounds__(256) void scan_pass_kernel(const float* h0, int64_t n, float* h_last) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) h_last[i] = h0 ? h0[i] : 0.f;
+}
+
+int tiles_of(int t) { return (t + kTile - 1) / kTile; }
+
+template <typename T, int V, bool STARTS, bool KEEP>
+hipError_t run(const ScanArgs& a, hipStream_t s) {
+  const int cols = (a.c + 64 * V - 1) / (64 * V), tiles = tiles_of(a.t);
+  if (tiles > 1) {
+    const hipError_t e = carry_clear(a.work, kTicketBytes + (int64_t)(tiles - 1) * cols * a.b * 64 * V * 8, s);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((seq_scan_fwd_kernel<T, V, STARTS, KEEP>), dim3((unsigned)(cols * a.b * tiles)),
+                     dim3(kWaves * 64), 0, s, a, cols, tiles);
+  return hipGetLastError();
+}
+template <typename T, int V>
+hipError_t run_as(const ScanArgs& a, hipStream_t s) {
+  if (a.starts) return a.kept[0].q ? run<T, V, true, true>(a, s) : run<T, V, true, false>(a, s);
+  return a.kept[0].q ? run<T, V, false, true>(a, s) : run<T, V, false, false>(a, s);
+}
+template <typename T>
+hipError_t run_16(const ScanArgs& a, hipStream_t s) {
+  const bool wide = a.c % 2 == 0 && pieces(a.x, 4, 2) && pieces(a.r, 4, 2) && pieces(a.i, 4, 2) && (uintptr_t)a.y % 4 == 0;
+  return wide ? run_as<T, 2>(a, s) : run_as<T, 1>(a, s);
+}
+
+}  // namespace
+
+// Words for the wider of the two column widths.
+int64_t scan_fwd_work_bytes(int b, int t, int c) {
+  const int tiles = tiles_of(t);
+  return tiles > 1 && b > 0 ? kTicketBytes + (int64_t)(tiles - 1) * b * ((c + 127) / 128) * 128 * 8 : 0;
+}
+
+hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t s) {
+  if (a.t == 0) {
+    const int64_t n = (int64_t)a.b * a.c;
+    if (a.h_last)
+      hipLaunchKernelGGL(scan_pass_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.h0, n, a.h_last);
+    return hipGetLastError();
+  }
+  if (a.dtype == convfwd::kF32) return run_as<float, 1>(a, s);
+  if (a.dtype == convfwd::kF16) return run_16<_Float16>(a, s);
+  return run_16<__bf16>(a, s);
+}
+
+}  // namespace convseq

@@ -23,7 +23,7 @@ int check_extents(int64_t b, int64_t t, int64_t c, int dtype) {
   const int64_t blocks = (t + kGroup - 1) / kGroup, cols = (c + 63) / 64;
   const int64_t lim = (int64_t)1 << 22;
   if (c >= (int64_t)1 << 26 || b >= lim || blocks >= lim) return CONVFWD_ERR_TOO_LARGE;
-  if (b * (blocks > 0 ? blocks : 1) >= (int64_t)1 << 31 || b * (blocks > 0 ? blocks : 1) * cols >= lim * 4)
+  if (b * (blocks > 0 ? blocks : 1) >= (int64_t)1 << 31 || b * (blocks > 0 ? blocks : 1) * cols >= lim * 2)
     return CONVFWD_ERR_TOO_LARGE;
   return CONVFWD_OK;
 }
@@ -68,8 +68,8 @@ class Buffers {
   void kept(const convseq_kept* k, int64_t b, int64_t t, int64_t c, bool write, Kept* to) {
     *to = Kept{nullptr, nullptr};
     if (!k) return;
-    const int64_t q = b * t * c, e = b * ((t + kGroup - 1) / kGroup) * c;
-    add(k->q, q, 1, true, write);
+    const int64_t e = b * ((t + kGroup - 1) / kGroup) * c;
+    add(k->q, e * kGroup, kGroup, true, write);
     add(k->e, e, 1, true, write);
     *to = Kept{(int8_t*)k->q, (uint8_t*)k->e};
   }

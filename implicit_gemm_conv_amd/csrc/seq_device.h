@@ -33,6 +33,45 @@ __device__ __forceinline__ int quantise(float v, float inverse) {
   return (int)__builtin_rintf(__builtin_amdgcn_fmed3f(v * inverse, -127.f, 127.f));
 }
 
+// The 16 values of a group, of which n lie inside T, as 16 bytes; *byte gets
+// the group's byte.
+__device__ __forceinline__ uint4 pack_group(const float (&v)[kGroup], int n, int* byte) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < kGroup; ++j)
+    if (j < n) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+  *byte = group_byte(top);
+  const float inv = group_inverse(*byte);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    w[k] = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (4 * k + j < n) w[k] |= (uint32_t)(quantise(v[4 * k + j], inv) & 0xff) << (8 * j);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Byte j of four packed ones, as a signed number.
+__device__ __forceinline__ float held(uint32_t w, int j) { return (float)(int8_t)(w >> (8 * j)); }
+
+// ---- V neighbouring channels of a row as one access ----
+template <typename T, int V>
+struct Pack;  // V * sizeof(T) bytes
+template <typename T>
+struct Pack<T, 1> {
+  T v;
+  __device__ __forceinline__ float get(int) const { return to_f32(v); }
+  __device__ __forceinline__ void set(int, float f) { v = from_f32<T>(f); }
+};
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Pack {
+  typedef T type __attribute__((ext_vector_type(V)));
+  type v;
+  __device__ __forceinline__ float get(int i) const { return to_f32((T)v[i]); }
+  __device__ __forceinline__ void set(int i, float f) { v[i] = from_f32<T>(f); }
+};
+
 // ---- gates ----
 // 1 / (1 + 2^(-x log2 e)) on the hardware's exp2 and reciprocal (1 ulp each):
 // 0 and 1 at the infinities, NaN for NaN.

@@ -17,11 +17,16 @@ struct Rows {
   int64_t sb, st;
 };
 
-// A (B, T, C) tensor in 8 bits, dense.
+// A (B, T, C) tensor in 8 bits: q (B, groups, C, 16), e (B, groups, C).
 struct Kept {
   int8_t* q;
   uint8_t* e;
 };
+
+// Whether every row of a view can be read in pieces of `bytes`, `elem` bytes an element.
+inline bool pieces(const Rows& r, int bytes, int elem) {
+  return ((uintptr_t)r.p | (uint64_t)(r.sb * elem) | (uint64_t)(r.st * elem)) % bytes == 0;
+}
 
 struct ConvArgs {
   int b, t, c, k, act, dtype;

@@ -84,19 +84,13 @@ def _seq():
 
 
 class Packed8(NamedTuple):
-    """A tensor in 8 bits: q (its shape, int8) and e (B, groups of 16 rows, C, uint8); the value
-    held is q * 2^(e - 127), NaN where e is 255.  dtype is the original's."""
+    """A tensor in 8 bits: q (B, groups of 16 rows, C, 16) int8 and e (B, groups, C) uint8; the
+    value held at row t is q[b, t // 16, c, t % 16] * 2^(e - 127), NaN where e is 255.  shape and
+    dtype are the original's."""
     q: torch.Tensor
     e: torch.Tensor
+    shape: torch.Size
     dtype: torch.dtype
-
-    @property
-    def shape(self):
-        return self.q.shape
-
-    @property
-    def device(self):
-        return self.q.device
 
 
 class SeqConv(NamedTuple):
@@ -169,14 +163,16 @@ def _starts(starts, b, t, device):
     return _dense(starts, (b, t), starts.dtype, device, "starts")
 
 
-def _kept_input(p, like, what):
-    """An input given in 8 bits, standing for a tensor of like's shape."""
-    shape = like.shape
-    groups = (shape[0], -(-shape[1] // GROUP_ROWS), shape[2])
-    if p.q.shape != shape or p.e.shape != groups or p.q.dtype != torch.int8 or p.e.dtype != torch.uint8 \
-            or p.q.device != like.device or p.e.device != like.device:
-        raise ValueError(f"{what} in 8 bits must stand for a tensor of shape {tuple(shape)} on {like.device}")
-    return Packed8(p.q.contiguous(), p.e.contiguous(), p.dtype)
+def _kept_input(p, shape, device, what):
+    """An input given in 8 bits, standing for a (B, T, C) tensor: its C struct."""
+    b, t, c = shape
+    groups = -(-t // GROUP_ROWS)
+    held = p.shape[0] if len(p.shape) == 2 else math.prod(p.shape[1:-1])
+    if held != t or p.q.shape != (b, groups, c, GROUP_ROWS) or p.e.shape != (b, groups, c) or p.q.dtype != torch.int8 \
+            or p.e.dtype != torch.uint8 or p.q.device != device or p.e.device != device \
+            or not p.q.is_contiguous() or not p.e.is_contiguous():
+        raise ValueError(f"{what} in 8 bits must stand for a tensor of shape {tuple(shape)} on {device}")
+    return p
 
 
 def _filter(w, bias, x, activation):
@@ -197,9 +193,11 @@ def _rows(x):
 
 
 def _new_kept(x, shape):
-    b, t, c = shape
-    return Packed8(torch.empty((b, t, c), dtype=torch.int8, device=x.device),
-                   torch.empty((b, -(-t // GROUP_ROWS), c), dtype=torch.uint8, device=x.device), x.dtype)
+    """Room for x (B, T, C) in 8 bits, as the tensor of the given shape."""
+    b, t, c = x.shape
+    groups = -(-t // GROUP_ROWS)
+    return Packed8(torch.empty((b, groups, c, GROUP_ROWS), dtype=torch.int8, device=x.device),
+                   torch.empty((b, groups, c), dtype=torch.uint8, device=x.device), shape, x.dtype)
 
 
 def _kept_ptrs(kept):
@@ -265,7 +263,7 @@ def seq_conv_bwd(dy, x, w, bias=None, activation=None, state=None, starts=None, 
     w, bias = _filter(w, bias, dy, activation)
     k = w.shape[1]
     packed = isinstance(x, Packed8)
-    x = _kept_input(x, dy, "x") if packed else _sequence(x, "x", dy)
+    x = _kept_input(x, dy.shape, dy.device, "x") if packed else _sequence(x, "x", dy)
     state = _dense(state, (b, k - 1, c), dy.dtype, dy.device, "state")
     dlast = _dense(dstate, (b, k - 1, c), dy.dtype, dy.device, "dstate")
     starts = _starts(starts, b, t, dy.device)
@@ -358,7 +356,7 @@ def gated_scan_bwd(dy, x, gate_r, gate_i, lam, states, decay=8.0, starts=None, d
     if any(isinstance(v, Packed8) != packed for v in ins):
         raise ValueError("x, gate_r and gate_i must all be tensors or all be in 8 bits")
     names = ("x", "gate_r", "gate_i")
-    ins = tuple(_kept_input(v, dy, n) if packed else _sequence(v, n, dy) for v, n in zip(ins, names))
+    ins = tuple(_kept_input(v, dy.shape, dy.device, n) if packed else _sequence(v, n, dy) for v, n in zip(ins, names))
     lam = _dense(lam, (c,), torch.float32, dy.device, "lam")
     states = _dense(states, (b, -(-t // STATE_ROWS), c), torch.float32, dy.device, "states")
     if states is None:
@@ -414,10 +412,10 @@ def pack8(x) -> Packed8:
     shape = x.shape
     rows = _sequence(x if x.dim() == 3 else x[None] if x.dim() == 2 else x.flatten(1, -2), "x")
     b, t, c = rows.shape
-    kept = _new_kept(rows, rows.shape)
+    kept = _new_kept(rows, shape)
     with _on(rows) as stream:
         _check(_seq().convseq_pack8(b, t, c, _DTYPES[rows.dtype], _rows(rows), _kept_ptrs([kept]), stream))
-    return Packed8(kept.q.view(shape), kept.e, rows.dtype)
+    return kept
 
 
 def unpack8(p: Packed8, dtype=None, out=None) -> torch.Tensor:
@@ -427,12 +425,11 @@ def unpack8(p: Packed8, dtype=None, out=None) -> torch.Tensor:
         raise TypeError(f"unsupported dtype {dtype}")
     if not p.q.is_cuda:
         raise ValueError("q and e must be device tensors: the sequence operators run on the GPU only")
-    shape, c = p.q.shape, p.q.shape[-1]
-    b = 1 if len(shape) == 2 else shape[0]
-    q = p.q.contiguous()
-    t = shape[0] if len(shape) == 2 else math.prod(shape[1:-1])
-    q = _kept_input(Packed8(q.view(b, t, c), p.e, p.dtype), q.view(b, t, c), "q")
-    y = torch.empty(shape, dtype=dtype, device=q.device) if out is None else _out(out, shape, dtype, q.device, "out")
-    with _on(q) as stream:
-        _check(_seq().convseq_unpack8(b, t, c, _DTYPES[dtype], _kept_ptrs([q]), y.data_ptr(), stream))
+    shape, c = p.shape, p.shape[-1]
+    b, t = (1, shape[0]) if len(shape) == 2 else (shape[0], math.prod(shape[1:-1]))
+    _kept_input(p, (b, t, c), p.q.device, "p")
+    y = torch.empty(shape, dtype=dtype, device=p.q.device) if out is None \
+        else _out(out, shape, dtype, p.q.device, "out")
+    with _on(p.q) as stream:
+        _check(_seq().convseq_unpack8(b, t, c, _DTYPES[dtype], _kept_ptrs([p]), y.data_ptr(), stream))
     return y

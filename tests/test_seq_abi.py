@@ -125,7 +125,7 @@ def test_the_binding_needs_device_tensors():
     for call in (lambda: igc.seq_conv(x, w), lambda: igc.seq_conv_bwd(x, x, w), lambda: igc.pack8(x),
                  lambda: igc.seq_conv_step(x[0], w, x), lambda: igc.gated_scan(x, x, x, w[:, 0]),
                  lambda: igc.gated_scan_bwd(x, x, x, x, w[:, 0], x), lambda: igc.gated_scan_step(x[0], x[0], x[0], w[:, 0], x[0]),
-                 lambda: igc.unpack8(igc.Packed8(x.to(torch.int8), x.to(torch.uint8), x.dtype))):
+                 lambda: igc.unpack8(igc.Packed8(x.to(torch.int8), x.to(torch.uint8), x.shape, x.dtype))):
         with pytest.raises(ValueError, match="GPU only"):
             call()
 
@@ -158,7 +158,7 @@ def test_the_binding_refuses_what_does_not_fit():
             (TypeError, lambda: igc.gated_scan_step(x[0], x[0], x[0], lam, torch.zeros(30, 8, device=dev),
                                                     slots=torch.zeros(20, dtype=torch.int64, device=dev))),
             (ValueError, lambda: igc.seq_conv_step(x[0], w, torch.zeros(20, 2, 8, device=dev))),
-            (ValueError, lambda: igc.pack8(lam)), (ValueError, lambda: igc.unpack8(igc.Packed8(kept.q, kept.e[:, :1], kept.dtype))),
+            (ValueError, lambda: igc.pack8(lam)), (ValueError, lambda: igc.unpack8(igc.Packed8(kept.q, kept.e[:, :1], kept.shape, kept.dtype))),
             (TypeError, lambda: igc.unpack8(kept, torch.float64))):
         with pytest.raises(error):
             call()
