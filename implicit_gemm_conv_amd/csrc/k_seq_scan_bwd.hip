@@ -1,0 +1,317 @@
+// k_seq_scan_bwd.hip -- gated linear recurrence, backward, in one pass.
+//
+// With r = sigmoid(gate_r), i = sigmoid(gate_i), u = decay * softplus(lam) * r,
+// a = e^-u, m = sqrt(1 - a^2), h_t = a h_{t-1} + m i x_t, and g_t the whole
+// gradient of h_t:
+//
+//   c_t = a_t g_t,  g_t = dy_t + c_{t+1}     (c_t = 0 where t begins a sequence)
+//   dx = g m i,   dgate_i = g m i x (1 - i)
+//   e = g u a (a i x / m - h_{t-1}),  dgate_r = e (1 - r)
+//   dlam = (sigmoid(lam) / softplus(lam)) sum e,   dh0 = c_0
+//
+// (dm/du = a^2 / m, and u / m goes to zero with u.)  Both recurrences, h forward
+// from the state kept before each 64 rows and c backward from the sequence's
+// end, go through the same tile: a workgroup of 8 waves takes 64 rows by 64 V
+// channels, a wave 8 rows, a lane V channels of those.  The lane composes its
+// rows into one step of h and one of c; the waves' steps are composed through
+// LDS, and the tiles' steps of c through memory from the last tile to the first
+// (seq_carry.h).  Then the lane runs h down its rows and c up them, with a, r, i,
+// m i and a i x / m of each value held in registers, and stores the three
+// gradients.  Each input is read once, each gradient written once: memory
+// bound, 4 elements (or 1 element and 3 bytes) in and 3 out a value.
+#include "seq_carry.h"
+
+namespace convseq {
+
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kRows = 8;  // of a wave
+constexpr int kTile = kWaves * kRows;
+static_assert(kTile == kEvery, "a tile starts from a kept state");
+
+template <typename T, int V, bool STARTS, bool KEPT>
+__global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a, int cols, int tiles) {
+  __shared__ Carry down[kWaves][64 * V], up[kWaves][64 * V];
+  __shared__ float entry[64 * V];
+  __shared__ float sums[kWaves][64 * V];
+  __shared__ int ticket;
+  typedef Pack<T, V> P;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+
+  int id = blockIdx.x;
+  if (tiles > 1) {
+    if (threadIdx.x == 0)
+      ticket = __hip_atomic_fetch_add((int*)a.work, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    id = __builtin_amdgcn_readfirstlane(ticket);
+  }
+  const int turn = id / (cols * a.b), column = id % (cols * a.b);
+  const int tile = tiles - 1 - turn;  // from the end of the sequence
+  const int b = column / cols;
+  const int ch = (column % cols * 64 + lane) * V;
+  const int chl = min(ch, a.c - V);  // lanes past the last channel read it again
+  const bool own = ch < a.c;
+  const int t0 = tile * kTile + wave * kRows;
+  const int n = min(max(a.t - t0, 0), kRows);  // rows of this wave
+
+  P ry[kRows], raw[3][kRows];
+  uint2 q[3][V];
+  float scale[3][V];
+  const T* py = (const T*)a.dy.p + b * a.dy.sb + chl;
+  const Rows* rows[3] = {&a.x, &a.r, &a.i};
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const int64_t t = min(t0 + j, a.t - 1);  // rows past the last read it again
+    ry[j] = *(const P*)(py + t * a.dy.st);
+    if (!KEPT)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) raw[k][j] = *(const P*)((const T*)rows[k]->p + b * rows[k]->sb + t * rows[k]->st + chl);
+  }
+  if (KEPT) {
+    const int groups = (a.t + kGroup - 1) / kGroup;
+    const int64_t at = ((int64_t)b * groups + min(t0 / kGroup, groups - 1)) * a.c + chl;
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        q[k][i] = *(const uint2*)(a.kept[k].q + (at + i) * kGroup + t0 % kGroup);
+        scale[k][i] = group_scale(a.kept[k].e[at + i]);
+      }
+  }
+  const auto value = [&](int k, int j, int i) -> float {
+    if (KEPT) return held(j < 4 ? q[k][i].x : q[k][i].y, j & 3) * scale[k][i];
+    return raw[k][j].get(i);
+  };
+  uint32_t first = 0;  // bit j: row t0 + j begins a sequence
+  if (STARTS) {
+    const bool f = lane < n && a.starts[(int64_t)b * a.t + t0 + lane];
+    first = (uint32_t)__ballot(f);
+  }
+  const int pieces = (a.t + kEvery - 1) / kEvery;
+  float rate[V], h[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    rate[i] = channel_rate(a.lam[chl + i], a.decay);
+    h[i] = a.states_in[((int64_t)b * pieces + tile) * a.c + chl + i];
+  }
+
+  // gates, and this wave's steps of h and c
+  float av[kRows][V], rv[kRows][V], iv[kRows][V], mi[kRows][V], kv[kRows][V];
+  Carry step[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) step[i] = Carry{1.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < kRows; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float x = value(0, j, i);
+      const Gate g = gates(value(1, j, i), value(2, j, i), rate[i]);
+      const float rs = inv_sqrt(g.t);
+      av[j][i] = g.a;
+      rv[j][i] = g.r;
+      iv[j][i] = g.i;
+      mi[j][i] = g.t * rs * g.i;
+      kv[j][i] = g.a * g.i * x * rs;
+      const float in = mi[j][i] * x;
+      if (j < n) {
+        if (STARTS && (first >> j & 1))
+          step[i] = Carry{-0.f, in};
+        else
+          step[i] = Carry{step[i].a * g.a, fmaf(g.a, step[i].h, in)};
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    down[wave][lane * V + i] = step[i];
+    step[i] = Carry{1.f, 0.f};
+  }
+#pragma unroll
+  for (int j = kRows - 1; j >= 0; --j)
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (j < n) {
+        if (STARTS && (first >> j & 1))
+          step[i] = Carry{-0.f, 0.f};
+        else
+          step[i] = Carry{step[i].a * av[j][i], av[j][i] * (step[i].h + ry[j].get(i))};
+      }
+#pragma unroll
+  for (int i = 0; i < V; ++i) up[wave][lane * V + i] = step[i];
+  __syncthreads();
+
+  if (wave == 0) {
+    // the tile's step of c, and the c after the tile
+    float c[V];
+    Carry whole[V];
+    uint64_t* words = (uint64_t*)((char*)a.work + kTicketBytes);
+    const int64_t stride = (int64_t)cols * a.b * 64 * V;
+    uint64_t* mine = words + turn * stride + ((int64_t)column * 64 + lane) * V;
+#pragma unroll
+    for (int i = 0; i < V; ++i) whole[i] = Carry{1.f, 0.f};
+#pragma unroll
+    for (int w = kWaves - 1; w >= 0; --w)
+#pragma unroll
+      for (int i = 0; i < V; ++i) whole[i] = compose(whole[i], up[w][lane * V + i]);
+    if (turn == 0) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = a.dh_last ? a.dh_last[(int64_t)b * a.c + chl + i] : 0.f;
+    } else {
+      if (tile > 0)
+#pragma unroll
+        for (int i = 0; i < V; ++i) publish(mine + i, whole[i]);
+      look_back<V>(words + ((int64_t)column * 64 + lane) * V, stride, turn, c);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float after = apply(whole[i], c[i]);
+      if (tile > 0)
+        publish(mine + i, Carry{__uint_as_float(kWhole), after});
+      else if (a.dh0 && own)
+        a.dh0[(int64_t)b * a.c + ch + i] = after;
+      entry[lane * V + i] = c[i];
+    }
+  }
+
+  // h down the rows: kv becomes a i x / m - h_{t-1}
+  for (int w = 0; w < wave; ++w)
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = apply(down[w][lane * V + i], h[i]);
+#pragma unroll
+  for (int j = 0; j < kRows; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float in = mi[j][i] * value(0, j, i);
+      if (STARTS && (first >> j & 1)) {
+        h[i] = in;
+      } else {
+        kv[j][i] -= h[i];
+        h[i] = fmaf(av[j][i], h[i], in);
+      }
+    }
+  __syncthreads();
+
+  // c up the rows
+  float c[V], sum[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    c[i] = entry[lane * V + i];
+    sum[i] = 0.f;
+  }
+  for (int w = kWaves - 1; w > wave; --w)
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = apply(up[w][lane * V + i], c[i]);
+  const int64_t out = ((int64_t)b * a.t + t0) * a.c + ch;
+#pragma unroll
+  for (int j = kRows - 1; j >= 0; --j)
+    if (j < n) {
+      P dx, dr, di;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float g = ry[j].get(i) + c[i];
+        const float gm = g * mi[j][i];
+        const float e = g * (rate[i] * rv[j][i] * av[j][i]) * kv[j][i];
+        dx.set(i, gm);
+        di.set(i, gm * value(0, j, i) * (1.f - iv[j][i]));
+        dr.set(i, e * (1.f - rv[j][i]));
+        sum[i] += e;
+        c[i] = STARTS && (first >> j & 1) ? 0.f : av[j][i] * g;
+      }
+      if (own) {
+        *(P*)((T*)a.dx + out + (int64_t)j * a.c) = dx;
+        *(P*)((T*)a.dr + out + (int64_t)j * a.c) = dr;
+        *(P*)((T*)a.di + out + (int64_t)j * a.c) = di;
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = sum[i];
+  __syncthreads();
+  if (wave == 0 && own) {
+    float* part = (float*)((char*)a.work + kTicketBytes + (int64_t)(tiles - 1) * cols * a.b * 64 * V * 8) +
+                  ((int64_t)tile * a.b + b) * a.c + ch;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) s += sums[w][lane * V + i];
+      part[i] = s;
+    }
+  }
+}
+
+// dlam from the tiles' sums: 32 channels a workgroup, 32 threads a channel that
+// each add every 32nd part, then the threads' sums in order.
+__global__ __launch_bounds__(1024) void seq_scan_sum_kernel(const float* parts, int64_t count, int c, const float* lam,
+                                                            float* dlam) {
+  __shared__ float s[32][33];
+  const int ch = blockIdx.x * 32 + (threadIdx.x & 31), k = threadIdx.x >> 5;
+  float v = 0.f;
+  if (ch < c)
+    for (int64_t p = k; p < count; p += 32) v += parts[p * c + ch];
+  s[k][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (k == 0 && ch < c) {
+    v = 0.f;
+    for (int j = 0; j < 32; ++j) v += s[j][threadIdx.x];
+    dlam[ch] = v * channel_unit(lam[ch]);
+  }
+}
+
+// No rows: the state's gradient passes through.
+__global__ __launch_bounds__(256) void scan_pass_kernel(const float* dh_last, int64_t n, float* dh0) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < n) dh0[i] = dh_last ? dh_last[i] : 0.f;
+}
+
+int tiles_of(int t) { return (t + kTile - 1) / kTile; }
+
+template <typename T, int V, bool STARTS, bool KEPT>
+hipError_t run(const ScanArgs& a, hipStream_t s) {
+  const int cols = (a.c + 64 * V - 1) / (64 * V), tiles = tiles_of(a.t);
+  const int64_t words = kTicketBytes + (int64_t)(tiles - 1) * cols * a.b * 64 * V * 8;
+  if (tiles > 1) {
+    const hipError_t e = carry_clear(a.work, words, s);
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((seq_scan_bwd_kernel<T, V, STARTS, KEPT>), dim3((unsigned)(cols * a.b * tiles)),
+                     dim3(kWaves * 64), 0, s, a, cols, tiles);
+  hipLaunchKernelGGL(seq_scan_sum_kernel, dim3((a.c + 31) / 32), dim3(1024), 0, s,
+                     (const float*)((char*)a.work + words), (int64_t)tiles * a.b, a.c, a.lam, a.dlam);
+  return hipGetLastError();
+}
+template <typename T, int V>
+hipError_t run_as(const ScanArgs& a, hipStream_t s) {
+  if (a.starts) return a.kept[0].q ? run<T, V, true, true>(a, s) : run<T, V, true, false>(a, s);
+  return a.kept[0].q ? run<T, V, false, true>(a, s) : run<T, V, false, false>(a, s);
+}
+template <typename T>
+hipError_t run_16(const ScanArgs& a, hipStream_t s) {
+  bool wide = a.c % 2 == 0 && pieces(a.dy, 4, 2) && ((uintptr_t)a.dx | (uintptr_t)a.dr | (uintptr_t)a.di) % 4 == 0;
+  if (!a.kept[0].q) wide = wide && pieces(a.x, 4, 2) && pieces(a.r, 4, 2) && pieces(a.i, 4, 2);
+  return wide ? run_as<T, 2>(a, s) : run_as<T, 1>(a, s);
+}
+
+}  // namespace
+
+// The ticket, words for the wider of the two column widths, and the tiles' sums.
+int64_t scan_bwd_work_bytes(int b, int t, int c) {
+  const int64_t tiles = tiles_of(t);
+  if (tiles == 0 || b == 0) return 0;
+  return kTicketBytes + (tiles - 1) * b * ((c + 127) / 128) * 128 * 8 + tiles * b * c * 4;
+}
+
+hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t s) {
+  if (a.t == 0 || a.b == 0) {
+    const int64_t n = (int64_t)a.b * a.c;
+    if (a.dh0 && n > 0)
+      hipLaunchKernelGGL(scan_pass_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a.dh_last, n, a.dh0);
+    hipLaunchKernelGGL(seq_scan_sum_kernel, dim3((a.c + 31) / 32), dim3(1024), 0, s, (const float*)nullptr, (int64_t)0,
+                       a.c, a.lam, a.dlam);
+    return hipGetLastError();
+  }
+  if (a.dtype == convfwd::kF32) return run_as<float, 1>(a, s);
+  if (a.dtype == convfwd::kF16) return run_16<_Float16>(a, s);
+  return run_16<__bf16>(a, s);
+}
+
+}  // namespace convseq

@@ -5,11 +5,11 @@
 //   h_t = a_t h_{t-1} + sqrt(1 - a^2) i x_t
 //
 // A workgroup of 8 waves takes a tile of 128 rows by 64 V channels, a wave 16
-// rows of it, a lane V channels of those rows.  The lane runs the recurrence
-// over its rows from zero, keeping for each row the product A of the a so far
-// and the h so far; the waves' totals are composed through LDS, the tiles'
-// through memory (seq_carry.h), and h_t = H_t + A_t h_before is stored.  Each
-// input is read once and y written once: memory bound, 4 elements a value.
+// rows of it, a lane V channels of those rows.  The lane composes its rows into
+// one step h -> A h + H, the waves' steps are composed through LDS, the tiles'
+// through memory (seq_carry.h), and with the state before its rows known the
+// lane runs the recurrence over the a and m v it still holds.  Each input is
+// read once and y written once: memory bound, 4 elements a value.
 #include "seq_carry.h"
 
 namespace convseq {
@@ -82,22 +82,26 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
     keep(ri, a.kept[2]);
   }
 
-  Carry run[kGroup][V];
+  float av[kGroup][V], in[kGroup][V];
+  Carry total[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) total[i] = Carry{1.f, 0.f};
 #pragma unroll
   for (int j = 0; j < kGroup; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const Gate g = gates(rr[j].get(i), ri[j].get(i), rate[i]);
-      Carry c = {g.a, g.t * inv_sqrt(g.t) * (g.i * rx[j].get(i))};
-      if (STARTS && (first >> j & 1)) c.a = -0.f;
-      if (j >= n) c = Carry{1.f, 0.f};
-      run[j][i] = j == 0 ? c : STARTS ? compose(run[j - 1][i], c)
-                                      : Carry{run[j - 1][i].a * c.a, fmaf(c.a, run[j - 1][i].h, c.h)};
+      av[j][i] = j < n ? g.a : 1.f;
+      in[j][i] = j < n ? g.t * inv_sqrt(g.t) * (g.i * rx[j].get(i)) : 0.f;
+      if (STARTS && (first >> j & 1))
+        total[i] = Carry{-0.f, in[j][i]};
+      else
+        total[i] = Carry{total[i].a * av[j][i], fmaf(av[j][i], total[i].h, in[j][i])};
     }
 
   // the waves' totals; before = what the waves above do to the state, whole = the tile
 #pragma unroll
-  for (int i = 0; i < V; ++i) totals[wave][lane * V + i] = run[kGroup - 1][i];
+  for (int i = 0; i < V; ++i) totals[wave][lane * V + i] = total[i];
   __syncthreads();
   Carry before[V];
 #pragma unroll
@@ -114,7 +118,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
     const int64_t step = (int64_t)cols * a.b * 64 * V;
     uint64_t* mine = words + tile * step + ((int64_t)column * 64 + lane) * V;
 #pragma unroll
-    for (int i = 0; i < V; ++i) whole[i] = compose(before[i], run[kGroup - 1][i]);
+    for (int i = 0; i < V; ++i) whole[i] = compose(before[i], total[i]);
     if (tile == 0) {
 #pragma unroll
       for (int i = 0; i < V; ++i) h[i] = a.h0 ? a.h0[(int64_t)b * a.c + chl + i] : 0.f;
@@ -151,7 +155,10 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
     if (j < n) {
       P v;
 #pragma unroll
-      for (int i = 0; i < V; ++i) v.set(i, STARTS ? apply(run[j][i], h[i]) : fmaf(run[j][i].a, h[i], run[j][i].h));
+      for (int i = 0; i < V; ++i) {
+        h[i] = STARTS && (first >> j & 1) ? in[j][i] : fmaf(av[j][i], h[i], in[j][i]);
+        v.set(i, h[i]);
+      }
       *(P*)(y + (int64_t)j * a.c) = v;
     }
 }
