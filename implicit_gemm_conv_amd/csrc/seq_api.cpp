@@ -167,7 +167,10 @@ int convseq_conv_bwd(const convseq_conv_desc* d, const convseq_rows* dy, const c
   a.w = w; a.bias = bias; a.state = state; a.starts = (const uint8_t*)starts;
   a.dstate_out = dstate_out; a.dx = dx; a.dw = (float*)dw; a.dbias = (float*)dbias; a.dstate = dstate;
   a.work = (float*)workspace;
-  return launched(launch_conv_bwd(a, (hipStream_t)stream));
+  const auto launch = d->dtype == CONVFWD_F32   ? launch_conv_bwd_f32
+                      : d->dtype == CONVFWD_F16 ? launch_conv_bwd_f16
+                                                : launch_conv_bwd_bf16;
+  return launched(launch(a, (hipStream_t)stream));
 }
 
 int convseq_conv_step(const convseq_conv_desc* d, const void* x, int64_t x_row, const void* w,

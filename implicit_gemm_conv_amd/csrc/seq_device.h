@@ -10,6 +10,13 @@ namespace convseq {
 using convfwd::from_f32;
 using convfwd::to_f32;
 
+struct Yes {
+  static constexpr bool value = true;
+};
+struct No {
+  static constexpr bool value = false;
+};
+
 // ---- 8-bit groups ----
 // Byte of a group whose largest magnitude has the float bits `top` (sign
 // cleared; an unsigned maximum of the bits orders magnitudes and puts
@@ -55,6 +62,16 @@ __device__ __forceinline__ uint4 pack_group(const float (&v)[kGroup], int n, int
 // Byte j of four packed ones, as a signed number.
 __device__ __forceinline__ float held(uint32_t w, int j) { return (float)(int8_t)(w >> (8 * j)); }
 
+// The fp32 result itself, before it is rounded to T: the empty asm keeps the
+// compiler from merging the last fp32 operation with the rounding to fp16 on
+// some paths of a kernel and not on others, which would give a row different
+// bits by where in a tile it lies.
+template <typename T>
+__device__ __forceinline__ T rounded(float f) {
+  if (sizeof(T) == 2) asm("" : "+v"(f));
+  return from_f32<T>(f);
+}
+
 // ---- V neighbouring channels of a row as one access ----
 template <typename T, int V>
 struct Pack;  // V * sizeof(T) bytes
@@ -62,14 +79,14 @@ template <typename T>
 struct Pack<T, 1> {
   T v;
   __device__ __forceinline__ float get(int) const { return to_f32(v); }
-  __device__ __forceinline__ void set(int, float f) { v = from_f32<T>(f); }
+  __device__ __forceinline__ void set(int, float f) { v = rounded<T>(f); }
 };
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Pack {
   typedef T type __attribute__((ext_vector_type(V)));
   type v;
   __device__ __forceinline__ float get(int i) const { return to_f32((T)v[i]); }
-  __device__ __forceinline__ void set(int i, float f) { v[i] = from_f32<T>(f); }
+  __device__ __forceinline__ void set(int i, float f) { v[i] = rounded<T>(f); }
 };
 
 // ---- gates ----

@@ -82,12 +82,16 @@ struct ScanStepArgs {
   void* y;
 };
 
+int conv_bwd_groups(int b, int t, int c);  // groups of 16 rows a wave of the backward pass walks
+int conv_bwd_blocks(int t, int per);       // its workgroups along a sequence
 int64_t conv_bwd_work_bytes(int b, int t, int c, int k);
 int64_t scan_fwd_work_bytes(int b, int t, int c);
 int64_t scan_bwd_work_bytes(int b, int t, int c);
 
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t s);
-hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t s);
+hipError_t launch_conv_bwd_f32(const ConvArgs& a, hipStream_t s);
+hipError_t launch_conv_bwd_f16(const ConvArgs& a, hipStream_t s);
+hipError_t launch_conv_bwd_bf16(const ConvArgs& a, hipStream_t s);
 hipError_t launch_conv_step(const ConvStepArgs& a, hipStream_t s);
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t s);
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t s);
