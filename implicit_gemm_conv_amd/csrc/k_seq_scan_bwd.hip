@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
   __shared__ float sums[kWaves][64 * V];
   __shared__ int ticket;
   typedef Pack<T, V> P;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   int id = blockIdx.x;
   if (tiles > 1) {
@@ -76,12 +76,13 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         q[k][i] = *(const uint2*)(a.kept[k].q + (at + i) * kGroup + t0 % kGroup);
-        scale[k][i] = group_scale(a.kept[k].e[at + i]);
+        scale[k][i] = (k > 0 ? -kLog2e : 1.f) * group_scale(a.kept[k].e[at + i]);
       }
   }
+  // x, and the gates' logits times -log2 e
   const auto value = [&](int k, int j, int i) -> float {
     if (KEPT) return held(j < 4 ? q[k][i].x : q[k][i].y, j & 3) * scale[k][i];
-    return raw[k][j].get(i);
+    return k > 0 ? -kLog2e * raw[k][j].get(i) : raw[k][j].get(i);
   };
   uint32_t first = 0;  // bit j: row t0 + j begins a sequence
   if (STARTS) {
@@ -89,7 +90,8 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
     first = (uint32_t)__ballot(f);
   }
   const int pieces = (a.t + kEvery - 1) / kEvery;
-  float rate[V], h[V];
+  Rate rate[V];
+  float h[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     rate[i] = channel_rate(a.lam[chl + i], a.decay);
@@ -103,22 +105,18 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
   for (int i = 0; i < V; ++i) step[i] = Carry{1.f, 0.f};
 #pragma unroll
   for (int j = 0; j < kRows; ++j)
+    if (j < n) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float x = value(0, j, i);
-      const Gate g = gates(value(1, j, i), value(2, j, i), rate[i]);
-      const float rs = inv_sqrt(g.t);
-      av[j][i] = g.a;
-      rv[j][i] = g.r;
-      iv[j][i] = g.i;
-      mi[j][i] = g.t * rs * g.i;
-      kv[j][i] = g.a * g.i * x * rs;
-      const float in = mi[j][i] * x;
-      if (j < n) {
-        if (STARTS && (first >> j & 1))
-          step[i] = Carry{-0.f, in};
-        else
-          step[i] = Carry{step[i].a * g.a, fmaf(g.a, step[i].h, in)};
+      for (int i = 0; i < V; ++i) {
+        const float x = value(0, j, i);
+        const Gate g = gates(value(1, j, i), value(2, j, i), rate[i]);
+        av[j][i] = g.a;
+        rv[j][i] = g.r;
+        iv[j][i] = g.i;
+        mi[j][i] = g.t * g.rs * g.i;
+        kv[j][i] = g.a * g.i * x * g.rs;
+        const float in = mi[j][i] * x;
+        step[i] = STARTS && (first >> j & 1) ? Carry{-0.f, in} : Carry{step[i].a * g.a, fmaf(g.a, step[i].h, in)};
       }
     }
 #pragma unroll
@@ -128,14 +126,12 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
   }
 #pragma unroll
   for (int j = kRows - 1; j >= 0; --j)
+    if (j < n) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (j < n) {
-        if (STARTS && (first >> j & 1))
-          step[i] = Carry{-0.f, 0.f};
-        else
-          step[i] = Carry{step[i].a * av[j][i], av[j][i] * (step[i].h + ry[j].get(i))};
-      }
+      for (int i = 0; i < V; ++i)
+        step[i] = STARTS && (first >> j & 1) ? Carry{-0.f, 0.f}
+                                             : Carry{step[i].a * av[j][i], av[j][i] * (step[i].h + ry[j].get(i))};
+    }
 #pragma unroll
   for (int i = 0; i < V; ++i) up[wave][lane * V + i] = step[i];
   __syncthreads();
@@ -179,14 +175,12 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
     for (int i = 0; i < V; ++i) h[i] = apply(down[w][lane * V + i], h[i]);
 #pragma unroll
   for (int j = 0; j < kRows; ++j)
+    if (j < n) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float in = mi[j][i] * value(0, j, i);
-      if (STARTS && (first >> j & 1)) {
-        h[i] = in;
-      } else {
-        kv[j][i] -= h[i];
-        h[i] = fmaf(av[j][i], h[i], in);
+      for (int i = 0; i < V; ++i) {
+        const float in = mi[j][i] * value(0, j, i);
+        if (!STARTS || !(first >> j & 1)) kv[j][i] -= h[i];
+        h[i] = STARTS && (first >> j & 1) ? in : fmaf(av[j][i], h[i], in);
       }
     }
   __syncthreads();
@@ -202,27 +196,27 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = apply(up[w][lane * V + i], c[i]);
   const int64_t out = ((int64_t)b * a.t + t0) * a.c + ch;
+  if (own) {
 #pragma unroll
-  for (int j = kRows - 1; j >= 0; --j)
-    if (j < n) {
-      P dx, dr, di;
+    for (int j = kRows - 1; j >= 0; --j)
+      if (j < n) {
+        P dx, dr, di;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float g = ry[j].get(i) + c[i];
-        const float gm = g * mi[j][i];
-        const float e = g * (rate[i] * rv[j][i] * av[j][i]) * kv[j][i];
-        dx.set(i, gm);
-        di.set(i, gm * value(0, j, i) * (1.f - iv[j][i]));
-        dr.set(i, e * (1.f - rv[j][i]));
-        sum[i] += e;
-        c[i] = STARTS && (first >> j & 1) ? 0.f : av[j][i] * g;
-      }
-      if (own) {
+        for (int i = 0; i < V; ++i) {
+          const float g = ry[j].get(i) + c[i];
+          const float gm = g * mi[j][i];
+          const float e = g * (rate[i].u * rv[j][i] * av[j][i]) * kv[j][i];
+          dx.set(i, gm);
+          di.set(i, gm * value(0, j, i) * (1.f - iv[j][i]));
+          dr.set(i, e * (1.f - rv[j][i]));
+          sum[i] += e;
+          c[i] = STARTS && (first >> j & 1) ? 0.f : av[j][i] * g;
+        }
         *(P*)((T*)a.dx + out + (int64_t)j * a.c) = dx;
         *(P*)((T*)a.dr + out + (int64_t)j * a.c) = dr;
         *(P*)((T*)a.di + out + (int64_t)j * a.c) = di;
       }
-    }
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = sum[i];
   __syncthreads();

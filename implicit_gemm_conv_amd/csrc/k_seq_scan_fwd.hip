@@ -25,7 +25,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
   __shared__ float entry[64 * V];
   __shared__ int ticket;
   typedef Pack<T, V> P;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   int id = blockIdx.x;
   if (tiles > 1) {
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
     const bool f = lane < n && a.starts[(int64_t)b * a.t + t0 + lane];
     first = (uint32_t)__ballot(f);
   }
-  float rate[V];
+  Rate rate[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) rate[i] = channel_rate(a.lam[chl + i], a.decay);
 
@@ -88,15 +88,15 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
   for (int i = 0; i < V; ++i) total[i] = Carry{1.f, 0.f};
 #pragma unroll
   for (int j = 0; j < kGroup; ++j)
+    if (j < n) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const Gate g = gates(rr[j].get(i), ri[j].get(i), rate[i]);
-      av[j][i] = j < n ? g.a : 1.f;
-      in[j][i] = j < n ? g.t * inv_sqrt(g.t) * (g.i * rx[j].get(i)) : 0.f;
-      if (STARTS && (first >> j & 1))
-        total[i] = Carry{-0.f, in[j][i]};
-      else
-        total[i] = Carry{total[i].a * av[j][i], fmaf(av[j][i], total[i].h, in[j][i])};
+      for (int i = 0; i < V; ++i) {
+        const Gate g = gates(-kLog2e * rr[j].get(i), -kLog2e * ri[j].get(i), rate[i]);
+        av[j][i] = g.a;
+        in[j][i] = g.t * g.rs * (g.i * rx[j].get(i));
+        total[i] = STARTS && (first >> j & 1) ? Carry{-0.f, in[j][i]}
+                                              : Carry{total[i].a * g.a, fmaf(g.a, total[i].h, in[j][i])};
+      }
     }
 
   // the waves' totals; before = what the waves above do to the state, whole = the tile

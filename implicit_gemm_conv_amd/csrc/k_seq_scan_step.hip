@@ -17,9 +17,9 @@ __global__ __launch_bounds__(256) void seq_scan_step_kernel(ScanStepArgs a) {
     *y = from_f32<T>(0.f);
     return;
   }
-  const Gate g = gates(to_f32(((const T*)a.r)[b * a.r_row + ch]), to_f32(((const T*)a.i)[b * a.i_row + ch]),
-                       channel_rate(a.lam[ch], a.decay));
-  const float in = g.t * inv_sqrt(g.t) * (g.i * to_f32(((const T*)a.x)[b * a.x_row + ch]));
+  const Gate g = gates(-kLog2e * to_f32(((const T*)a.r)[b * a.r_row + ch]),
+                       -kLog2e * to_f32(((const T*)a.i)[b * a.i_row + ch]), channel_rate(a.lam[ch], a.decay));
+  const float in = g.t * g.rs * (g.i * to_f32(((const T*)a.x)[b * a.x_row + ch]));
   const float h = fmaf(g.a, a.state[(int64_t)slot * a.c + ch], in);
   a.state_out[(int64_t)slot * a.c + ch] = h;
   *y = from_f32<T>(h);

@@ -90,50 +90,70 @@ struct alignas(V * sizeof(T)) Pack {
 };
 
 // ---- gates ----
-// 1 / (1 + 2^(-x log2 e)) on the hardware's exp2 and reciprocal (1 ulp each):
-// 0 and 1 at the infinities, NaN for NaN.
-__device__ __forceinline__ float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x));
-}
+// The gates work in powers of two: exp2 and the reciprocals are the hardware's
+// (1 ulp each), and log2 e is multiplied into what comes before them.
+constexpr float kLog2e = 1.44269504f;
 
-// decay * softplus(lam), and d ln(softplus) / d lam = sigmoid(lam) / softplus(lam)
-// (1 where both vanish).
-__device__ __forceinline__ float channel_rate(float lam, float decay) {
-  return decay * (fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam))));
+// 1 / (1 + 2^x), the sigmoid of -x ln 2: 1 and 0 at the infinities, NaN for NaN.
+__device__ __forceinline__ float sigmoid2(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x));
 }
+__device__ __forceinline__ float sigmoid(float x) { return sigmoid2(-kLog2e * x); }
+
+// softplus(l) = ln(1 + e^l) = max(l, 0) + 2 atanh(z), z = e / (2 + e), e = e^-|l|:
+// z <= 1/3, the series to z^15 leaves less than 1e-8 of the sum, and a small
+// softplus keeps its relative accuracy, which the decay rates near 0 need.
+__device__ __forceinline__ float softplus(float l) {
+  const float e = expf(-fabsf(l));
+  const float z = e * __builtin_amdgcn_rcpf(2.f + e), s = z * z;
+  float p = fmaf(s, 1.f / 15.f, 1.f / 13.f);
+  p = fmaf(s, p, 1.f / 11.f);
+  p = fmaf(s, p, 1.f / 9.f);
+  p = fmaf(s, p, 1.f / 7.f);
+  p = fmaf(s, p, 1.f / 5.f);
+  p = fmaf(s, p, 1.f / 3.f);
+  return fmaxf(l, 0.f) + 2.f * fmaf(s * z, p, z);
+}
+// d ln(softplus) / d lam = sigmoid(lam) / softplus(lam), 1 where both vanish.
 __device__ __forceinline__ float channel_unit(float lam) {
-  const float sp = fmaxf(lam, 0.f) + log1pf(expf(-fabsf(lam)));
-  return lam < -80.f ? 1.f : 1.f / ((1.f + expf(-lam)) * sp);
+  return lam < -80.f ? 1.f : 1.f / ((1.f + expf(-lam)) * softplus(lam));
 }
 
-// 1 - e^(-x) for x >= 0.  Below 1/4 by its series to x^6 (the next term is
-// under 5e-8 of the sum), where 1 - e would lose the leading bits; above, from e = e^(-x).
-__device__ __forceinline__ float one_minus_exp(float x, float e) {
-  float p = fmaf(x, -1.f / 720.f, 1.f / 120.f);
-  p = fmaf(x, p, -1.f / 24.f);
-  p = fmaf(x, p, 1.f / 6.f);
-  p = fmaf(x, p, -0.5f);
-  p = fmaf(x, p, 1.f);
-  return x < 0.25f ? x * p : 1.f - e;
-}
-
-// The gates of one value: u = rate * r, a = e^-u, t = 1 - a^2.
-struct Gate {
-  float r, i, u, a, t;
+// What a channel's rate = decay * softplus(lam) multiplies the open gate by.
+struct Rate {
+  float u;     // u = rate * r
+  float log2;  // log2 a = -rate log2 e * r
 };
-__device__ __forceinline__ Gate gates(float gr, float gi, float rate) {
-  Gate g;
-  g.r = sigmoid(gr);
-  g.i = sigmoid(gi);
-  g.u = rate * g.r;
-  g.a = __builtin_amdgcn_exp2f(-1.44269504f * g.u);
-  g.t = one_minus_exp(2.f * g.u, g.a * g.a);
-  return g;
+__device__ __forceinline__ Rate channel_rate(float lam, float decay) {
+  const float u = decay * softplus(lam);
+  return Rate{u, -kLog2e * u};
 }
-// 1 / sqrt(t); 0 where t vanishes, so that products with sqrt(t)'s factors
-// take their limit 0 there.  NaN stays NaN.
-__device__ __forceinline__ float inv_sqrt(float t) {
-  return t < 1e-37f ? 0.f : __builtin_amdgcn_rsqf(t);
+
+// 1 - e^(-2u) for u >= 0, given a = e^-u.  Below 2u = 1/4 by its series to (2u)^6
+// (the next term is under 5e-8 of the sum), where 1 - a^2 would lose the leading bits.
+__device__ __forceinline__ float one_minus_square(float u, float a) {
+  float p = fmaf(u, -64.f / 720.f, 32.f / 120.f);
+  p = fmaf(u, p, -16.f / 24.f);
+  p = fmaf(u, p, 8.f / 6.f);
+  p = fmaf(u, p, -2.f);
+  p = fmaf(u, p, 2.f);
+  return u < 0.125f ? u * p : fmaf(-a, a, 1.f);
+}
+
+// The gates of one value; x2 are the logits times -log2 e.
+struct Gate {
+  float r, i, a;  // a = e^-u
+  float t, rs;    // 1 - a^2 and its inverse square root, so that m = t rs.  Where t vanishes rs stays
+                  // finite, and products with m and u take their limit 0.  NaN stays NaN in t.
+};
+__device__ __forceinline__ Gate gates(float r2, float i2, const Rate& rate) {
+  Gate g;
+  g.r = sigmoid2(r2);
+  g.i = sigmoid2(i2);
+  g.a = __builtin_amdgcn_exp2f(rate.log2 * g.r);
+  g.t = one_minus_square(rate.u * g.r, g.a);
+  g.rs = __builtin_amdgcn_rsqf(fmaxf(g.t, 1e-36f));
+  return g;
 }
 
 }  // namespace convseq
