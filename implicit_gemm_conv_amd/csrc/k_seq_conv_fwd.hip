@@ -26,21 +26,22 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_fwd_kernel(ConvArgs a, i
   const bool own = chs < a.c;
   const int ch = min(chs, a.c - V);  // lanes past the last channel read it again
   const int t0 = g * kGroup, n = min(a.t - t0, kGroup);
-  const T* x = (const T*)a.x.p + b * a.x.sb + ch;
-  const T* state = a.state ? (const T*)a.state + (int64_t)b * (K - 1) * a.c + ch : nullptr;
+  const uint32_t offset = (uint32_t)ch * sizeof(T);
+  const T* x = (const T*)a.x.p + b * a.x.sb;
+  const T* state = a.state ? (const T*)a.state + (int64_t)b * (K - 1) * a.c : nullptr;
   const uint8_t* starts = a.starts ? a.starts + (int64_t)b * a.t : nullptr;
 
   P raw[K - 1 + kGroup];  // rows t0 - (K-1) on
   if (t0 > 0) {           // K - 1 < 16 rows lie before it
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) raw[j] = *(const P*)(x + (int64_t)(t0 - (K - 1) + j) * a.x.st);
+    for (int j = 0; j < K - 1; ++j) raw[j] = load_at<P>(x + (int64_t)(t0 - (K - 1) + j) * a.x.st, offset);
   } else {
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j) raw[j] = row_at<T, V>(x, a.x.st, state, j - (K - 1), K, a.c);
+    for (int j = 0; j < K - 1; ++j) raw[j] = row_at<T, V>(x, a.x.st, state, j - (K - 1), K, a.c, offset);
   }
   if (n > 0) {
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) raw[K - 1 + j] = *(const P*)(x + (int64_t)(t0 + min(j, n - 1)) * a.x.st);
+    for (int j = 0; j < kGroup; ++j) raw[K - 1 + j] = load_at<P>(x + (int64_t)(t0 + min(j, n - 1)) * a.x.st, offset);
   }
   uint32_t first = 0;  // bit j: row t0 + j begins a sequence
   int reach = K - 1;
@@ -56,21 +57,10 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_fwd_kernel(ConvArgs a, i
     bias[i] = a.bias ? to_f32(((const T*)a.bias)[ch + i]) : 0.f;
   }
 
-  if (a.kept.q && n > 0 && own) {
-    const int64_t at = ((int64_t)b * groups + g) * a.c + ch;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float v[kGroup];
-#pragma unroll
-      for (int j = 0; j < kGroup; ++j) v[j] = raw[K - 1 + j].get(i);
-      int byte;
-      const uint4 q = pack_group(v, n, &byte);
-      *(uint4*)(a.kept.q + (at + i) * kGroup) = q;
-      a.kept.e[at + i] = (uint8_t)byte;
-    }
-  }
+  if (a.kept.q && n > 0 && own)
+    keep_group<T, V>(*(const P(*)[kGroup])(raw + K - 1), n, a.kept, (int64_t)b * groups + g, a.c, ch);
 
-  T* y = (T*)a.y + ((int64_t)b * a.t + t0) * a.c + ch;
+  T* y = (T*)a.y + ((int64_t)b * a.t + t0) * a.c;
   // `plain`: 16 rows that all reach K - 1 rows back
   const auto run = [&](auto plain) {
     constexpr bool masked = !decltype(plain)::value;
@@ -89,7 +79,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_fwd_kernel(ConvArgs a, i
           }
           out.set(i, a.act ? silu(z) : z);
         }
-        if (own) *(P*)(y + (int64_t)j * a.c) = out;
+        if (own) store_at(y + (int64_t)j * a.c, offset, out);
       }
   };
   if (n == kGroup && !first && reach == K - 1)
@@ -98,15 +88,15 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_fwd_kernel(ConvArgs a, i
     run(No{});
 
   if (a.state_out && g == groups - 1 && own) {
-    T* out = (T*)a.state_out + (int64_t)b * (K - 1) * a.c + ch;
+    T* out = (T*)a.state_out + (int64_t)b * (K - 1) * a.c;
     reach = reach_before(starts, a.t, K);
     for (int j = 0; j < K - 1; ++j) {
       const int s = a.t - (K - 1) + j;
-      P v = row_at<T, V>(x, a.x.st, state, s, K, a.c);
+      P v = row_at<T, V>(x, a.x.st, state, s, K, a.c, offset);
       if (a.t > 0 && a.t - 1 - s > reach)
 #pragma unroll
         for (int i = 0; i < V; ++i) v.set(i, 0.f);
-      *(P*)(out + (int64_t)j * a.c) = v;
+      store_at(out + (int64_t)j * a.c, offset, v);
     }
   }
 }
@@ -125,7 +115,7 @@ hipError_t run(const ConvArgs& a, hipStream_t s) {
 template <typename T, int V>
 hipError_t run_wide(const ConvArgs& a, hipStream_t s) {
   constexpr int e = sizeof(T), bytes = V * e;
-  const uintptr_t at = (uintptr_t)a.y | (uintptr_t)a.state | (uintptr_t)a.state_out;
+  const uintptr_t at = (uintptr_t)a.y | (uintptr_t)a.state | (uintptr_t)a.state_out | (uintptr_t)a.kept.e * e;
   return a.c % V == 0 && pieces(a.x, bytes, e) && at % bytes == 0 ? run<T, V>(a, s) : run<T, 1>(a, s);
 }
 

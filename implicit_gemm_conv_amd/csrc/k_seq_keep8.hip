@@ -3,76 +3,59 @@
 // are of one scale where channels of one row are not, and neighbouring lanes
 // hold neighbouring channels, so the largest of a group needs no exchange
 // between lanes.  A lane takes V channels of one group: 16 row pieces of V
-// values on one side, V runs of 16 bytes on the other.
+// values on one side, two runs of 8 V bytes on the other.
 #include "seq_device.h"
 
 namespace convseq {
 
 namespace {
 
-// Where a lane of the grid works: channels ch.., group g of batch b.
+// Where a lane of the grid works: channels ch on, rows t0 .. t0 + n - 1 of batch b.
 struct Place {
-  int ch, b, g, t0, n;
-  int64_t at;  // (b, g, ch) as an index of e
+  int ch, b, t0, n, part;  // part: b and the group as one index
 };
 template <int V>
-__device__ __forceinline__ bool place(int t, int c, int groups, Place* p) {
+__device__ __forceinline__ bool place(int parts, int t, int c, int groups, Place* p) {
   const int cb = (c + 64 * V - 1) / (64 * V);
-  const int64_t wave = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int part = (int)(wave / cb);
+  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  p->part = (int)(wave / cb);
   p->ch = ((int)(wave % cb) * 64 + (threadIdx.x & 63)) * V;
-  p->b = part / groups;
-  p->g = part % groups;
-  p->t0 = p->g * kGroup;
+  p->b = p->part / groups;
+  p->t0 = p->part % groups * kGroup;
   p->n = min(t - p->t0, kGroup);
-  p->at = (int64_t)part * c + p->ch;
-  return p->ch < c;
+  return p->ch < c && p->part < parts;
 }
 
 template <typename T, int V>
 __global__ __launch_bounds__(256) void pack8_kernel(int parts, int t, int c, int groups, Rows x, Kept k) {
   Place p;
-  if (!place<V>(t, c, groups, &p) || p.at >= (int64_t)parts * c) return;
+  if (!place<V>(parts, t, c, groups, &p)) return;
   typedef Pack<T, V> P;
-  const T* in = (const T*)x.p + p.b * x.sb + (int64_t)p.t0 * x.st + p.ch;
+  const T* in = (const T*)x.p + p.b * x.sb + (int64_t)p.t0 * x.st;
   P raw[kGroup];
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j) raw[j] = *(const P*)(in + (int64_t)min(j, p.n - 1) * x.st);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float v[kGroup];
-#pragma unroll
-    for (int j = 0; j < kGroup; ++j) v[j] = raw[j].get(i);
-    int byte;
-    const uint4 q = pack_group(v, p.n, &byte);
-    *(uint4*)(k.q + (p.at + i) * kGroup) = q;
-    k.e[p.at + i] = (uint8_t)byte;
-  }
+  for (int j = 0; j < kGroup; ++j) raw[j] = load_at<P>(in + (int64_t)min(j, p.n - 1) * x.st, (uint32_t)p.ch * sizeof(T));
+  keep_group<T, V>(raw, p.n, k, p.part, c, p.ch);
 }
 
 template <typename T, int V>
 __global__ __launch_bounds__(256) void unpack8_kernel(int parts, int t, int c, int groups, Kept k, T* out) {
   Place p;
-  if (!place<V>(t, c, groups, &p) || p.at >= (int64_t)parts * c) return;
+  if (!place<V>(parts, t, c, groups, &p)) return;
   typedef Pack<T, V> P;
-  uint4 q[V];
-  float s[V];
+  Half<V> q[2];
+  float scale[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    q[i] = *(const uint4*)(k.q + (p.at + i) * kGroup);
-    s[i] = group_scale(k.e[p.at + i]);
-  }
-  T* to = out + ((int64_t)p.b * t + p.t0) * c + p.ch;
+  for (int h = 0; h < 2; ++h) q[h] = half_group<V>(k, p.part, h, c, p.ch);
+  group_scales<V>(k, p.part, c, p.ch, scale);
+  T* to = out + ((int64_t)p.b * t + p.t0) * c;
 #pragma unroll
   for (int j = 0; j < kGroup; ++j)
     if (j < p.n) {
       P v;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-        v.set(i, held(w[j >> 2], j & 3) * s[i]);
-      }
-      *(P*)(to + (int64_t)j * c) = v;
+      for (int i = 0; i < V; ++i) v.set(i, q[j / 8].get(i, j % 8) * scale[i]);
+      store_at(to + (int64_t)j * c, (uint32_t)p.ch * sizeof(T), v);
     }
 }
 
@@ -100,17 +83,17 @@ hipError_t unpack_as(int b, int t, int c, const Kept& k, void* out, hipStream_t 
 
 hipError_t launch_pack8(int b, int t, int c, int dtype, const Rows& x, const Kept& k, hipStream_t s) {
   if (dtype == convfwd::kF32)
-    return c % 2 == 0 && pieces(x, 8, 4) ? pack_as<float, 2>(b, t, c, x, k, s) : pack_as<float, 1>(b, t, c, x, k, s);
-  const bool wide = c % 4 == 0 && pieces(x, 8, 2);
+    return c % 2 == 0 && pieces(x, 8, 4) && (uintptr_t)k.e % 2 == 0 ? pack_as<float, 2>(b, t, c, x, k, s) : pack_as<float, 1>(b, t, c, x, k, s);
+  const bool wide = c % 4 == 0 && pieces(x, 8, 2) && (uintptr_t)k.e % 4 == 0;
   if (dtype == convfwd::kF16) return wide ? pack_as<_Float16, 4>(b, t, c, x, k, s) : pack_as<_Float16, 1>(b, t, c, x, k, s);
   return wide ? pack_as<__bf16, 4>(b, t, c, x, k, s) : pack_as<__bf16, 1>(b, t, c, x, k, s);
 }
 
 hipError_t launch_unpack8(int b, int t, int c, int dtype, const Kept& k, void* out, hipStream_t s) {
   if (dtype == convfwd::kF32)
-    return c % 2 == 0 && (uintptr_t)out % 8 == 0 ? unpack_as<float, 2>(b, t, c, k, out, s)
+    return c % 2 == 0 && (uintptr_t)out % 8 == 0 && (uintptr_t)k.e % 2 == 0 ? unpack_as<float, 2>(b, t, c, k, out, s)
                                                  : unpack_as<float, 1>(b, t, c, k, out, s);
-  const bool wide = c % 4 == 0 && (uintptr_t)out % 8 == 0;
+  const bool wide = c % 4 == 0 && (uintptr_t)out % 8 == 0 && (uintptr_t)k.e % 4 == 0;
   if (dtype == convfwd::kF16) return wide ? unpack_as<_Float16, 4>(b, t, c, k, out, s) : unpack_as<_Float16, 1>(b, t, c, k, out, s);
   return wide ? unpack_as<__bf16, 4>(b, t, c, k, out, s) : unpack_as<__bf16, 1>(b, t, c, k, out, s);
 }

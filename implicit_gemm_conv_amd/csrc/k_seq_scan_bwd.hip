@@ -33,7 +33,8 @@ static_assert(kTile == kEvery, "a tile starts from a kept state");
 template <typename T, int V, bool STARTS, bool KEPT>
 __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a, int cols, int tiles) {
   __shared__ Carry down[kWaves][64 * V], up[kWaves][64 * V];
-  __shared__ float entry[64 * V];
+  __shared__ float entry[64 * V], rates[64 * V];
+  __shared__ Gathered<V, kWaves> gathered;
   __shared__ float sums[kWaves][64 * V];
   __shared__ int ticket;
   typedef Pack<T, V> P;
@@ -56,137 +57,168 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
   const int n = min(max(a.t - t0, 0), kRows);  // rows of this wave
 
   P ry[kRows], raw[3][kRows];
-  uint2 q[3][V];
+  Half<V> q[3];
   float scale[3][V];
-  const T* py = (const T*)a.dy.p + b * a.dy.sb + chl;
+  const uint32_t offset = (uint32_t)chl * sizeof(T);
+  const T* py = (const T*)a.dy.p + b * a.dy.sb;
   const Rows* rows[3] = {&a.x, &a.r, &a.i};
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     const int64_t t = min(t0 + j, a.t - 1);  // rows past the last read it again
-    ry[j] = *(const P*)(py + t * a.dy.st);
+    ry[j] = load_at<P>(py + t * a.dy.st, offset);
     if (!KEPT)
 #pragma unroll
-      for (int k = 0; k < 3; ++k) raw[k][j] = *(const P*)((const T*)rows[k]->p + b * rows[k]->sb + t * rows[k]->st + chl);
+      for (int k = 0; k < 3; ++k) raw[k][j] = load_at<P>((const T*)rows[k]->p + b * rows[k]->sb + t * rows[k]->st, offset);
   }
   if (KEPT) {
     const int groups = (a.t + kGroup - 1) / kGroup;
-    const int64_t at = ((int64_t)b * groups + min(t0 / kGroup, groups - 1)) * a.c + chl;
+    const int64_t at = (int64_t)b * groups + min(t0 / kGroup, groups - 1);
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+    for (int k = 0; k < 3; ++k) {
+      q[k] = half_group<V>(a.kept[k], at, t0 / kRows % 2, a.c, chl);
+      group_scales<V>(a.kept[k], at, a.c, chl, scale[k]);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        q[k][i] = *(const uint2*)(a.kept[k].q + (at + i) * kGroup + t0 % kGroup);
-        scale[k][i] = (k > 0 ? -kLog2e : 1.f) * group_scale(a.kept[k].e[at + i]);
-      }
+      for (int i = 0; i < V; ++i) scale[k][i] *= k > 0 ? -kLog2e : 1.f;
+    }
   }
   // x, and the gates' logits times -log2 e
   const auto value = [&](int k, int j, int i) -> float {
-    if (KEPT) return held(j < 4 ? q[k][i].x : q[k][i].y, j & 3) * scale[k][i];
+    if (KEPT) return q[k].get(i, j) * scale[k][i];
     return k > 0 ? -kLog2e * raw[k][j].get(i) : raw[k][j].get(i);
   };
+  const auto renew_x = [&] {
+    if (KEPT) renew(q[0]);
+    if (!KEPT)
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) renew(raw[0][j]);
+  };
   uint32_t first = 0;  // bit j: row t0 + j begins a sequence
-  if (STARTS) {
-    const bool f = lane < n && a.starts[(int64_t)b * a.t + t0 + lane];
-    first = (uint32_t)__ballot(f);
-  }
+  if (STARTS) first = (uint32_t)__ballot(lane < n && a.starts[(int64_t)b * a.t + t0 + lane]);
   const int pieces = (a.t + kEvery - 1) / kEvery;
-  Rate rate[V];
   float h[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    rate[i] = channel_rate(a.lam[chl + i], a.decay);
-    h[i] = a.states_in[((int64_t)b * pieces + tile) * a.c + chl + i];
+  for (int i = 0; i < V; ++i) h[i] = load_at<float>(a.states_in + ((int64_t)b * pieces + tile) * a.c, (uint32_t)(chl + i) * 4);
+  if (wave < V) {
+    const int k = wave * 64 + lane;
+    rates[k] = a.decay * softplus(a.lam[min(column % cols * 64 * V + k, a.c - 1)]);
   }
+  lds_barrier();
+  Rate rate[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) rate[i] = rate_of(rates[lane * V + i]);
 
   // gates, and this wave's steps of h and c
-  float av[kRows][V], rv[kRows][V], iv[kRows][V], mi[kRows][V], kv[kRows][V];
+  float rv[kRows][V], iv[kRows][V], mi[kRows][V], kv[kRows][V];  // r, i, m i, a i x / m
   Carry step[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) step[i] = Carry{1.f, 0.f};
 #pragma unroll
   for (int j = 0; j < kRows; ++j)
     if (j < n) {
+      const bool begins = STARTS && (first >> j & 1);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float x = value(0, j, i);
         const Gate g = gates(value(1, j, i), value(2, j, i), rate[i]);
-        av[j][i] = g.a;
+        const float rs = inv_sqrt(g.t);
         rv[j][i] = g.r;
         iv[j][i] = g.i;
-        mi[j][i] = g.t * g.rs * g.i;
-        kv[j][i] = g.a * g.i * x * g.rs;
-        const float in = mi[j][i] * x;
-        step[i] = STARTS && (first >> j & 1) ? Carry{-0.f, in} : Carry{step[i].a * g.a, fmaf(g.a, step[i].h, in)};
+        mi[j][i] = g.t * rs * g.i;
+        kv[j][i] = g.a * g.i * x * rs;
+        const float in = mi[j][i] * x, h = fmaf(g.a, step[i].h, in);
+        step[i] = Carry{begins ? -0.f : step[i].a * g.a, begins ? in : h};
       }
     }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     down[wave][lane * V + i] = step[i];
-    step[i] = Carry{1.f, 0.f};
+    step[i] = Carry{STARTS ? 1.f : step[i].a, 0.f};  // without starts both steps have the product of all a
   }
+  const auto renew_rates = [&] {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      renew(rate[i].u);
+      renew(rate[i].log2);
+    }
+  };
+  const auto a_of = [&](int j, int i) { return __builtin_amdgcn_exp2f(rate[i].log2 * rv[j][i]); };
+  renew_rates();
 #pragma unroll
   for (int j = kRows - 1; j >= 0; --j)
     if (j < n) {
+      const bool begins = STARTS && (first >> j & 1);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        step[i] = STARTS && (first >> j & 1) ? Carry{-0.f, 0.f}
-                                             : Carry{step[i].a * av[j][i], av[j][i] * (step[i].h + ry[j].get(i))};
+      for (int i = 0; i < V; ++i) {
+        const float av = a_of(j, i), c = av * (step[i].h + ry[j].get(i));
+        step[i] = Carry{!STARTS ? step[i].a : begins ? -0.f : step[i].a * av, begins ? 0.f : c};
+      }
     }
 #pragma unroll
   for (int i = 0; i < V; ++i) up[wave][lane * V + i] = step[i];
   __syncthreads();
 
+  // wave 0 has the tile's step of c, and gets the c after the tile
+  float c[V];
+  Carry whole[V];
+  const CarrySpace space = carry_space(a.work, tiles - 1, cols * a.b);
+  uint64_t* words = space.words + (int64_t)column * 64 * V;
+  uint32_t* flags = space.flags + (int64_t)column * (tiles - 1);
+  const int64_t stride = (int64_t)cols * a.b * 64 * V;
+  uint64_t* mine = words + turn * stride;  // and the lane's from lane * V
   if (wave == 0) {
-    // the tile's step of c, and the c after the tile
-    float c[V];
-    Carry whole[V];
-    uint64_t* words = (uint64_t*)((char*)a.work + kTicketBytes);
-    const int64_t stride = (int64_t)cols * a.b * 64 * V;
-    uint64_t* mine = words + turn * stride + ((int64_t)column * 64 + lane) * V;
 #pragma unroll
     for (int i = 0; i < V; ++i) whole[i] = Carry{1.f, 0.f};
 #pragma unroll
     for (int w = kWaves - 1; w >= 0; --w)
 #pragma unroll
       for (int i = 0; i < V; ++i) whole[i] = compose(whole[i], up[w][lane * V + i]);
-    if (turn == 0) {
+    if (turn > 0 && tile > 0) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = a.dh_last ? a.dh_last[(int64_t)b * a.c + chl + i] : 0.f;
-    } else {
-      if (tile > 0)
-#pragma unroll
-        for (int i = 0; i < V; ++i) publish(mine + i, whole[i]);
-      look_back<V>(words + ((int64_t)column * 64 + lane) * V, stride, turn, c);
+      for (int i = 0; i < V; ++i) publish(mine + (uint32_t)(lane * V + i), whole[i]);
+      if (lane == 0) raise_flag(flags + turn, 1);
     }
+  }
+  // h down the rows while the tiles before this one finish: kv becomes a i x / m - h_{t-1}
+  for (int w = 0; w < wave; ++w)
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = apply(down[w][lane * V + i], h[i]);
+  renew_x();
+  renew_rates();
+#pragma unroll
+  for (int j = 0; j < kRows; ++j)
+    if (j < n) {
+      const bool begins = STARTS && (first >> j & 1);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float in = mi[j][i] * value(0, j, i);
+        kv[j][i] = begins ? kv[j][i] : kv[j][i] - h[i];
+        h[i] = begins ? in : fmaf(a_of(j, i), h[i], in);
+      }
+    }
+
+  if (turn == 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = a.dh_last ? a.dh_last[(int64_t)b * a.c + chl + i] : 0.f;
+  } else {
+    look_back<V, kWaves>(words, stride, flags, turn, wave, lane, wave == 0, gathered, c);
+  }
+  if (wave == 0) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const float after = apply(whole[i], c[i]);
       if (tile > 0)
-        publish(mine + i, Carry{__uint_as_float(kWhole), after});
+        publish(mine + (uint32_t)(lane * V + i), Carry{__uint_as_float(kWhole), after});
       else if (a.dh0 && own)
         a.dh0[(int64_t)b * a.c + ch + i] = after;
       entry[lane * V + i] = c[i];
     }
+    if (tile > 0 && lane == 0) raise_flag(flags + turn, 2);
   }
 
-  // h down the rows: kv becomes a i x / m - h_{t-1}
-  for (int w = 0; w < wave; ++w)
-#pragma unroll
-    for (int i = 0; i < V; ++i) h[i] = apply(down[w][lane * V + i], h[i]);
-#pragma unroll
-  for (int j = 0; j < kRows; ++j)
-    if (j < n) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float in = mi[j][i] * value(0, j, i);
-        if (!STARTS || !(first >> j & 1)) kv[j][i] -= h[i];
-        h[i] = STARTS && (first >> j & 1) ? in : fmaf(av[j][i], h[i], in);
-      }
-    }
   __syncthreads();
 
   // c up the rows
-  float c[V], sum[V];
+  float sum[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     c[i] = entry[lane * V + i];
@@ -195,7 +227,11 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
   for (int w = kWaves - 1; w > wave; --w)
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = apply(up[w][lane * V + i], c[i]);
-  const int64_t out = ((int64_t)b * a.t + t0) * a.c + ch;
+  const int64_t out = ((int64_t)b * a.t + t0) * a.c;
+  renew_x();
+  renew_rates();
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) renew(ry[j]);
   if (own) {
 #pragma unroll
     for (int j = kRows - 1; j >= 0; --j)
@@ -204,25 +240,24 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float g = ry[j].get(i) + c[i];
-          const float gm = g * mi[j][i];
-          const float e = g * (rate[i].u * rv[j][i] * av[j][i]) * kv[j][i];
+          const float gm = g * mi[j][i], ga = g * a_of(j, i);
+          const float e = ga * (rate[i].u * rv[j][i]) * kv[j][i];
           dx.set(i, gm);
           di.set(i, gm * value(0, j, i) * (1.f - iv[j][i]));
           dr.set(i, e * (1.f - rv[j][i]));
           sum[i] += e;
-          c[i] = STARTS && (first >> j & 1) ? 0.f : av[j][i] * g;
+          c[i] = STARTS && (first >> j & 1) ? 0.f : ga;
         }
-        *(P*)((T*)a.dx + out + (int64_t)j * a.c) = dx;
-        *(P*)((T*)a.dr + out + (int64_t)j * a.c) = dr;
-        *(P*)((T*)a.di + out + (int64_t)j * a.c) = di;
+        store_at((T*)a.dx + out + (int64_t)j * a.c, offset, dx);
+        store_at((T*)a.dr + out + (int64_t)j * a.c, offset, dr);
+        store_at((T*)a.di + out + (int64_t)j * a.c, offset, di);
       }
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = sum[i];
   __syncthreads();
   if (wave == 0 && own) {
-    float* part = (float*)((char*)a.work + kTicketBytes + (int64_t)(tiles - 1) * cols * a.b * 64 * V * 8) +
-                  ((int64_t)tile * a.b + b) * a.c + ch;
+    float* part = a.parts + ((int64_t)tile * a.b + b) * a.c + ch;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float s = 0.f;
@@ -260,17 +295,18 @@ __global__ __launch_bounds__(256) void scan_pass_kernel(const float* dh_last, in
 int tiles_of(int t) { return (t + kTile - 1) / kTile; }
 
 template <typename T, int V, bool STARTS, bool KEPT>
-hipError_t run(const ScanArgs& a, hipStream_t s) {
+hipError_t run(ScanArgs a, hipStream_t s) {
   const int cols = (a.c + 64 * V - 1) / (64 * V), tiles = tiles_of(a.t);
-  const int64_t words = kTicketBytes + (int64_t)(tiles - 1) * cols * a.b * 64 * V * 8;
+  const int64_t carry = tiles > 1 ? carry_bytes(tiles - 1, (int64_t)cols * a.b, 64 * V) : 0;
   if (tiles > 1) {
-    const hipError_t e = carry_clear(a.work, words, s);
+    const hipError_t e = carry_clear(a.work, carry, s);
     if (e != hipSuccess) return e;
   }
+  a.parts = (float*)((char*)a.work + carry);
   hipLaunchKernelGGL((seq_scan_bwd_kernel<T, V, STARTS, KEPT>), dim3((unsigned)(cols * a.b * tiles)),
                      dim3(kWaves * 64), 0, s, a, cols, tiles);
   hipLaunchKernelGGL(seq_scan_sum_kernel, dim3((a.c + 31) / 32), dim3(1024), 0, s,
-                     (const float*)((char*)a.work + words), (int64_t)tiles * a.b, a.c, a.lam, a.dlam);
+                     (const float*)a.parts, (int64_t)tiles * a.b, a.c, a.lam, a.dlam);
   return hipGetLastError();
 }
 template <typename T, int V>
@@ -280,18 +316,21 @@ hipError_t run_as(const ScanArgs& a, hipStream_t s) {
 }
 template <typename T>
 hipError_t run_16(const ScanArgs& a, hipStream_t s) {
-  bool wide = a.c % 2 == 0 && pieces(a.dy, 4, 2) && ((uintptr_t)a.dx | (uintptr_t)a.dr | (uintptr_t)a.di) % 4 == 0;
+  bool wide = a.c % 2 == 0 && pieces(a.dy, 4, 2) && ((uintptr_t)a.dx | (uintptr_t)a.dr | (uintptr_t)a.di) % 4 == 0 &&
+              ((uintptr_t)a.kept[0].e | (uintptr_t)a.kept[1].e | (uintptr_t)a.kept[2].e) % 2 == 0;
   if (!a.kept[0].q) wide = wide && pieces(a.x, 4, 2) && pieces(a.r, 4, 2) && pieces(a.i, 4, 2);
   return wide ? run_as<T, 2>(a, s) : run_as<T, 1>(a, s);
 }
 
 }  // namespace
 
-// The ticket, words for the wider of the two column widths, and the tiles' sums.
+// The carry for whichever of the two column widths needs more, and the tiles' sums.
 int64_t scan_bwd_work_bytes(int b, int t, int c) {
   const int64_t tiles = tiles_of(t);
   if (tiles == 0 || b == 0) return 0;
-  return kTicketBytes + (tiles - 1) * b * ((c + 127) / 128) * 128 * 8 + tiles * b * c * 4;
+  const int64_t narrow = carry_bytes(tiles - 1, (int64_t)b * ((c + 63) / 64), 64);
+  const int64_t wide = carry_bytes(tiles - 1, (int64_t)b * ((c + 127) / 128), 128);
+  return (narrow > wide ? narrow : wide) + tiles * b * c * 4;
 }
 
 hipError_t launch_scan_bwd(const ScanArgs& a, hipStream_t s) {

@@ -22,7 +22,8 @@ constexpr int kTile = kWaves * kGroup;  // rows
 template <typename T, int V, bool STARTS, bool KEEP>
 __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a, int cols, int tiles) {
   __shared__ Carry totals[kWaves][64 * V];
-  __shared__ float entry[64 * V];
+  __shared__ float entry[64 * V], rates[64 * V];
+  __shared__ Gathered<V, kWaves> gathered;
   __shared__ int ticket;
   typedef Pack<T, V> P;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -42,44 +43,40 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
   const int t0 = tile * kTile + wave * kGroup;
   const int n = min(max(a.t - t0, 0), kGroup);  // rows of this wave
 
-  const T* px = (const T*)a.x.p + b * a.x.sb + chl;
-  const T* pr = (const T*)a.r.p + b * a.r.sb + chl;
-  const T* pi = (const T*)a.i.p + b * a.i.sb + chl;
+  const uint32_t offset = (uint32_t)chl * sizeof(T);
+  const T* px = (const T*)a.x.p + b * a.x.sb;
+  const T* pr = (const T*)a.r.p + b * a.r.sb;
+  const T* pi = (const T*)a.i.p + b * a.i.sb;
   P rx[kGroup], rr[kGroup], ri[kGroup];
 #pragma unroll
   for (int j = 0; j < kGroup; ++j) {
     const int64_t t = min(t0 + j, a.t - 1);  // rows past the last read it again
-    rx[j] = *(const P*)(px + t * a.x.st);
-    rr[j] = *(const P*)(pr + t * a.r.st);
-    ri[j] = *(const P*)(pi + t * a.i.st);
+    rx[j] = load_at<P>(px + t * a.x.st, offset);
+    rr[j] = load_at<P>(pr + t * a.r.st, offset);
+    ri[j] = load_at<P>(pi + t * a.i.st, offset);
   }
   uint32_t first = 0;  // bit j: row t0 + j begins a sequence
-  if (STARTS) {
-    const bool f = lane < n && a.starts[(int64_t)b * a.t + t0 + lane];
-    first = (uint32_t)__ballot(f);
+  if (STARTS) first = (uint32_t)__ballot(lane < n && a.starts[(int64_t)b * a.t + t0 + lane]);
+  if (wave < V) {
+    const int k = wave * 64 + lane;
+    rates[k] = a.decay * softplus(a.lam[min(column % cols * 64 * V + k, a.c - 1)]);
   }
+  lds_barrier();
   Rate rate[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) rate[i] = channel_rate(a.lam[chl + i], a.decay);
+  for (int i = 0; i < V; ++i) rate[i] = rate_of(rates[lane * V + i]);
 
   if (KEEP && n > 0 && own) {
-    const int groups = (a.t + kGroup - 1) / kGroup;
-    const int64_t at = ((int64_t)b * groups + t0 / kGroup) * a.c + ch;
-    const auto keep = [&](const P(&raw)[kGroup], const Kept& k) {
+    const int64_t at = (int64_t)b * ((a.t + kGroup - 1) / kGroup) + t0 / kGroup;
+    keep_group<T, V>(rx, n, a.kept[0], at, a.c, ch);
+    keep_group<T, V>(rr, n, a.kept[1], at, a.c, ch);
+    keep_group<T, V>(ri, n, a.kept[2], at, a.c, ch);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float v[kGroup];
-#pragma unroll
-        for (int j = 0; j < kGroup; ++j) v[j] = raw[j].get(i);
-        int byte;
-        const uint4 q = pack_group(v, n, &byte);
-        *(uint4*)(k.q + (at + i) * kGroup) = q;
-        k.e[at + i] = (uint8_t)byte;
-      }
-    };
-    keep(rx, a.kept[0]);
-    keep(rr, a.kept[1]);
-    keep(ri, a.kept[2]);
+    for (int j = 0; j < kGroup; ++j) {
+      renew(rx[j]);
+      renew(rr[j]);
+      renew(ri[j]);
+    }
   }
 
   float av[kGroup][V], in[kGroup][V];
@@ -89,13 +86,14 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
 #pragma unroll
   for (int j = 0; j < kGroup; ++j)
     if (j < n) {
+      const bool begins = STARTS && (first >> j & 1);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const Gate g = gates(-kLog2e * rr[j].get(i), -kLog2e * ri[j].get(i), rate[i]);
         av[j][i] = g.a;
-        in[j][i] = g.t * g.rs * (g.i * rx[j].get(i));
-        total[i] = STARTS && (first >> j & 1) ? Carry{-0.f, in[j][i]}
-                                              : Carry{total[i].a * g.a, fmaf(g.a, total[i].h, in[j][i])};
+        in[j][i] = __builtin_amdgcn_sqrtf(g.t) * (g.i * rx[j].get(i));
+        const float h = fmaf(g.a, total[i].h, in[j][i]);
+        total[i] = Carry{begins ? -0.f : total[i].a * g.a, begins ? in[j][i] : h};
       }
     }
 
@@ -110,46 +108,52 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
 #pragma unroll
     for (int i = 0; i < V; ++i) before[i] = compose(before[i], totals[w][lane * V + i]);
 
-  if (wave == kWaves - 1) {
-    // this wave has the tile's total, and fetches the state before it
-    float h[V];
-    Carry whole[V];
-    uint64_t* words = (uint64_t*)((char*)a.work + kTicketBytes);
-    const int64_t step = (int64_t)cols * a.b * 64 * V;
-    uint64_t* mine = words + tile * step + ((int64_t)column * 64 + lane) * V;
+  // the last wave has the tile's total, and gets the state before the tile
+  const bool last = wave == kWaves - 1;
+  Carry whole[V];
+  const CarrySpace space = carry_space(a.work, tiles - 1, cols * a.b);
+  uint64_t* words = space.words + (int64_t)column * 64 * V;
+  uint32_t* flags = space.flags + (int64_t)column * (tiles - 1);
+  const int64_t step = (int64_t)cols * a.b * 64 * V;
+  uint64_t* mine = words + tile * step;  // and the lane's from lane * V
 #pragma unroll
-    for (int i = 0; i < V; ++i) whole[i] = compose(before[i], total[i]);
-    if (tile == 0) {
+  for (int i = 0; i < V; ++i) whole[i] = compose(before[i], total[i]);
+  if (last && tile > 0 && tile < tiles - 1) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) h[i] = a.h0 ? a.h0[(int64_t)b * a.c + chl + i] : 0.f;
-    } else {
-      if (tile < tiles - 1)
+    for (int i = 0; i < V; ++i) publish(mine + (uint32_t)(lane * V + i), whole[i]);
+    if (lane == 0) raise_flag(flags + tile, 1);
+  }
+  float h[V];
+  if (tile == 0) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) publish(mine + i, whole[i]);
-      look_back<V>(words + ((int64_t)column * 64 + lane) * V, step, tile, h);
-    }
+    for (int i = 0; i < V; ++i) h[i] = a.h0 ? a.h0[(int64_t)b * a.c + chl + i] : 0.f;
+  } else {
+    look_back<V, kWaves>(words, step, flags, tile, wave, lane, last, gathered, h);
+  }
+  if (last) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const float after = apply(whole[i], h[i]);
       if (tile < tiles - 1)
-        publish(mine + i, Carry{__uint_as_float(kWhole), after});
+        publish(mine + (uint32_t)(lane * V + i), Carry{__uint_as_float(kWhole), after});
       else if (a.h_last && own)
         a.h_last[(int64_t)b * a.c + ch + i] = after;
       entry[lane * V + i] = h[i];
     }
+    if (tile < tiles - 1 && lane == 0) raise_flag(flags + tile, 2);
   }
   __syncthreads();
 
-  float h[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) h[i] = apply(before[i], entry[lane * V + i]);
   if (!own || n == 0) return;
   if (a.states && t0 % kEvery == 0) {
     const int pieces = (a.t + kEvery - 1) / kEvery;
 #pragma unroll
-    for (int i = 0; i < V; ++i) a.states[((int64_t)b * pieces + t0 / kEvery) * a.c + ch + i] = h[i];
+    for (int i = 0; i < V; ++i)
+      store_at(a.states + ((int64_t)b * pieces + t0 / kEvery) * a.c, (uint32_t)(ch + i) * 4, h[i]);
   }
-  T* y = (T*)a.y + ((int64_t)b * a.t + t0) * a.c + ch;
+  T* y = (T*)a.y + ((int64_t)b * a.t + t0) * a.c;
 #pragma unroll
   for (int j = 0; j < kGroup; ++j)
     if (j < n) {
@@ -159,7 +163,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
         h[i] = STARTS && (first >> j & 1) ? in[j][i] : fmaf(av[j][i], h[i], in[j][i]);
         v.set(i, h[i]);
       }
-      *(P*)(y + (int64_t)j * a.c) = v;
+      store_at(y + (int64_t)j * a.c, offset, v);
     }
 }
 
@@ -175,7 +179,7 @@ template <typename T, int V, bool STARTS, bool KEEP>
 hipError_t run(const ScanArgs& a, hipStream_t s) {
   const int cols = (a.c + 64 * V - 1) / (64 * V), tiles = tiles_of(a.t);
   if (tiles > 1) {
-    const hipError_t e = carry_clear(a.work, kTicketBytes + (int64_t)(tiles - 1) * cols * a.b * 64 * V * 8, s);
+    const hipError_t e = carry_clear(a.work, carry_bytes(tiles - 1, (int64_t)cols * a.b, 64 * V), s);
     if (e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((seq_scan_fwd_kernel<T, V, STARTS, KEEP>), dim3((unsigned)(cols * a.b * tiles)),
@@ -189,16 +193,20 @@ hipError_t run_as(const ScanArgs& a, hipStream_t s) {
 }
 template <typename T>
 hipError_t run_16(const ScanArgs& a, hipStream_t s) {
-  const bool wide = a.c % 2 == 0 && pieces(a.x, 4, 2) && pieces(a.r, 4, 2) && pieces(a.i, 4, 2) && (uintptr_t)a.y % 4 == 0;
+  const bool wide = a.c % 2 == 0 && pieces(a.x, 4, 2) && pieces(a.r, 4, 2) && pieces(a.i, 4, 2) && (uintptr_t)a.y % 4 == 0 &&
+                    ((uintptr_t)a.kept[0].e | (uintptr_t)a.kept[1].e | (uintptr_t)a.kept[2].e) % 2 == 0;
   return wide ? run_as<T, 2>(a, s) : run_as<T, 1>(a, s);
 }
 
 }  // namespace
 
-// Words for the wider of the two column widths.
+// For whichever of the two column widths needs more.
 int64_t scan_fwd_work_bytes(int b, int t, int c) {
-  const int tiles = tiles_of(t);
-  return tiles > 1 && b > 0 ? kTicketBytes + (int64_t)(tiles - 1) * b * ((c + 127) / 128) * 128 * 8 : 0;
+  const int64_t tiles = tiles_of(t);
+  if (tiles <= 1 || b == 0) return 0;
+  const int64_t narrow = carry_bytes(tiles - 1, (int64_t)b * ((c + 63) / 64), 64);
+  const int64_t wide = carry_bytes(tiles - 1, (int64_t)b * ((c + 127) / 128), 128);
+  return narrow > wide ? narrow : wide;
 }
 
 hipError_t launch_scan_fwd(const ScanArgs& a, hipStream_t s) {

@@ -18,8 +18,8 @@ __global__ __launch_bounds__(256) void seq_scan_step_kernel(ScanStepArgs a) {
     return;
   }
   const Gate g = gates(-kLog2e * to_f32(((const T*)a.r)[b * a.r_row + ch]),
-                       -kLog2e * to_f32(((const T*)a.i)[b * a.i_row + ch]), channel_rate(a.lam[ch], a.decay));
-  const float in = g.t * g.rs * (g.i * to_f32(((const T*)a.x)[b * a.x_row + ch]));
+                       -kLog2e * to_f32(((const T*)a.i)[b * a.i_row + ch]), rate_of(a.decay * softplus(a.lam[ch])));
+  const float in = __builtin_amdgcn_sqrtf(g.t) * (g.i * to_f32(((const T*)a.x)[b * a.x_row + ch]));
   const float h = fmaf(g.a, a.state[(int64_t)slot * a.c + ch], in);
   a.state_out[(int64_t)slot * a.c + ch] = h;
   *y = from_f32<T>(h);

@@ -9,16 +9,20 @@
 // Tiles along a sequence are handed to workgroups by a ticket counter in the
 // order of the recurrence, all columns of a tile row before the next.  A tile
 // publishes its (A, H) as one 64-bit word a channel, looks back over its
-// predecessors' words, composing them until one is a whole state (marked as one
-// that forgets), and publishes its own whole state in place of its (A, H).  A
-// word that is not there yet has A's bits zero.  A waiting tile waits on tiles
-// of lower tickets only; those were taken by workgroups that already run, the
-// lowest of them waits for nobody, so every wait ends.  (A wait that could not
-// end, in a workspace that another call overwrites, gives up after kSpins and
-// puts NaN into the results.)
+// predecessors, applies their steps from the nearest whole state on, and
+// publishes its own whole state (a word that forgets) in place of its (A, H).
+// A waiting tile waits on tiles of lower tickets only; those were taken by
+// workgroups that already run, the lowest of them waits for nobody, so every
+// wait ends.  (A wait that could not end, in a workspace that another call
+// overwrites, gives up after kSpins and puts NaN into the results.)
 //
-// The words are written and read with relaxed device-wide 64-bit atomics:
-// value and presence travel in one access, so no fence is needed.
+// Words and flags are written and read with relaxed device-wide atomics.  A
+// word carries value and presence in one access (A's bits are zero until it is
+// there), so no fence is needed.  The flags, one a tile and column, only say
+// where to look: a wave reads those of 64 tiles at once, and polling them
+// instead of the words keeps the waiting off the memory the tiles stream
+// through (words of 32 tiles polled by all waves: 174 us for 1x65539x1024 bf16
+// forward, 4 at a time by one wave: 155).
 #pragma once
 
 #include "seq_device.h"
@@ -49,76 +53,127 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* word) {
   return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// The states before tile `tile` of V channels a lane, from the words of the
-// tiles before it: `words` is tile 0's, tiles are `step` words apart.  Called
-// by one whole wave.
+// What a launch's tiles share, in its workspace: the ticket, a flag a column
+// and tile, a word a tile and lane channel.
+struct CarrySpace {
+  int* ticket;
+  uint32_t* flags;   // [columns][tiles]
+  uint64_t* words;   // [tiles][columns][lane channels]
+};
+__host__ __device__ inline int64_t carry_flag_bytes(int64_t tiles, int64_t columns) {
+  return (tiles * columns * 4 + 15) / 16 * 16;
+}
+// Bytes for `tiles` tiles that publish and `columns` columns of `width` channels.
+inline int64_t carry_bytes(int64_t tiles, int64_t columns, int width) {
+  return kTicketBytes + carry_flag_bytes(tiles, columns) + tiles * columns * width * 8;
+}
+__device__ __forceinline__ CarrySpace carry_space(void* work, int64_t tiles, int64_t columns) {
+  char* p = (char*)work;
+  return CarrySpace{(int*)p, (uint32_t*)(p + kTicketBytes),
+                    (uint64_t*)(p + kTicketBytes + carry_flag_bytes(tiles, columns))};
+}
+
+// The words a workgroup gathers at once, and how many tiles it has to apply.
+constexpr int kEach = 2;  // of a wave
+template <int V, int WAVES>
+struct Gathered {
+  uint64_t words[WAVES * kEach][64 * V];
+  int span;
+};
+
+__device__ __forceinline__ void raise_flag(uint32_t* flag, uint32_t v) {
+  __hip_atomic_store(flag, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The states before tile `tile` of V channels a lane, in the waves for which
+// `fold` is set (one wave); called by all waves of a workgroup.  `words` is tile
+// 0's first word of the column, tiles are `step` words apart; `flags` is tile 0's flag:
+// 1 for a published step, 2 for a whole state.
 //
-// It walks back until every lane has seen a whole state, then applies the tiles
-// from there in the order of the recurrence.  A whole state was itself made by
-// applying its tile to the state before it, so where the walk ended, which
-// depends on timing, does not show in a single bit of the result.
-template <int V>
-__device__ __forceinline__ void look_back(const uint64_t* words, int64_t step, int tile, float (&state)[V]) {
-  constexpr int kAhead = 4;  // words read at once
-  uint64_t w[kAhead][V];
-  bool done[V];
+// The tiles from the nearest whole state on are applied in the order of the
+// recurrence.  A whole state was itself made by applying its tile to the state
+// before it, so which one was the nearest, a matter of timing, does not show in
+// a single bit of the result.
+template <int V, int WAVES>
+__device__ __forceinline__ void look_back(const uint64_t* words, int64_t step, const uint32_t* flags, int tile, int wave,
+                                          int lane, bool fold, Gathered<V, WAVES>& sh, float (&state)[V]) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    state[i] = 0.f;
-    done[i] = false;
-  }
-  int k = tile - 1;  // nearest tile not yet taken
-  int spins = 0;
-  for (;;) {
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) w[j][i] = peek(words + (int64_t)max(k - j, 0) * step + i);
-    int taken = 0;
-    bool all = false;
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      bool there = true, end = true;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        there &= done[i] || (uint32_t)w[j][i] != 0u;
-        end &= done[i] || (int)(uint32_t)w[j][i] < 0;
+  for (int i = 0; i < V; ++i) state[i] = 0.f;
+  if (fold) {
+    int span = 0;  // tiles seen, none of them whole, nearest first
+    for (int spins = 0;;) {
+      const int k = tile - 1 - span - lane;
+      const uint32_t f = k >= 0 ? __hip_atomic_load(flags + k, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0u;
+      const uint64_t there = __ballot(f != 0u), whole = __ballot(f == 2u);
+      const int n = there == ~0ull ? 64 : __builtin_ctzll(~there);  // so many in a row
+      const int d = whole ? __builtin_ctzll(whole) : 64;
+      if (d < n) {
+        span += d + 1;
+        break;
       }
-      if (taken == j && !all && k - j >= 0 && __all(there)) {
-        taken = j + 1;
-        all = __all(end);
-#pragma unroll
-        for (int i = 0; i < V; ++i) done[i] |= (int)(uint32_t)w[j][i] < 0;
+      span += n;
+      if (n == 0) {
+        if (++spins > kSpins) {
+          span = -1;
+          break;
+        }
+        __builtin_amdgcn_s_sleep(1);
       }
     }
-    k -= taken;
-    if (all) break;
-    if (taken == 0) {
-      if (++spins > kSpins) {
+    if (lane == 0) sh.span = span;
+  }
+  __syncthreads();
+  const int span = __builtin_amdgcn_readfirstlane(sh.span);
+  const bool lost = span < 0;
+  for (int from = tile - max(span, 0); from < tile; from += WAVES * kEach) {
+    const int count = min(tile - from, WAVES * kEach);
+    uint64_t w[kEach][V];
+    for (int spins = 0;;) {
+      bool there = true;
 #pragma unroll
-        for (int i = 0; i < V; ++i) state[i] = __uint_as_float(0x7fc00000u);
-        return;
+      for (int j = 0; j < kEach; ++j)
+        if (j * WAVES + wave < count) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) w[j][i] = peek(words + (int64_t)(from + j * WAVES + wave) * step + (uint32_t)(lane * V + i));
+        }
+#pragma unroll
+      for (int j = 0; j < kEach; ++j)
+        if (j * WAVES + wave < count) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) there &= (uint32_t)w[j][i] != 0u;
+        }
+      if (__all(there)) break;
+      if (++spins > kSpins) {  // gives up: a whole state of NaN
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) w[j][i] = 0x7fc0000080000000ull;
+        break;
       }
       __builtin_amdgcn_s_sleep(1);
     }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (j * WAVES + wave < count) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) sh.words[j * WAVES + wave][lane * V + i] = w[j][i];
+      }
+    __syncthreads();
+    if (fold)
+      for (int slot = 0; slot < count; ++slot)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const uint64_t v = sh.words[slot][lane * V + i];
+          state[i] = apply(Carry{__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))}, state[i]);
+        }
+    __syncthreads();
   }
-  // all words of tiles k+1 .. tile-1 are there, and the first is whole in some
-  // lane, so that every lane meets a whole state on the way up
-  for (++k; k < tile; k += kAhead) {
+  if (lost)
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i) w[j][i] = peek(words + (int64_t)min(k + j, tile - 1) * step + i);
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (k + j < tile)
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          state[i] = apply(Carry{__uint_as_float((uint32_t)w[j][i]), __uint_as_float((uint32_t)(w[j][i] >> 32))}, state[i]);
-  }
+    for (int i = 0; i < V; ++i) state[i] = __uint_as_float(0x7fc00000u);
 }
 
-// Zero for the ticket and the words; a kernel rather than a memset, which a
+// Zero for ticket, flags and words; a kernel rather than a memset, which a
 // captured graph has to be able to replay.
 static __global__ __launch_bounds__(256) void carry_clear_kernel(uint4* p, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)

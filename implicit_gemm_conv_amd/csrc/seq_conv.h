@@ -27,12 +27,13 @@ __device__ __forceinline__ int reach_before(const uint8_t* starts, int t, int k)
   return k - 1;
 }
 
-// V channels of X at row s: x, or below row 0 the carried rows (zero if there are none).
+// V channels of X at row s, `offset` bytes into the row: x, or below row 0 the carried rows (zero if there are none).
 template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> row_at(const T* x, int64_t st, const T* state, int s, int k, int c) {
+__device__ __forceinline__ Pack<T, V> row_at(const T* x, int64_t st, const T* state, int s, int k, int c,
+                                             uint32_t offset) {
   Pack<T, V> v;
-  if (s >= 0) return *(const Pack<T, V>*)(x + (int64_t)s * st);
-  if (state) return *(const Pack<T, V>*)(state + (int64_t)(s + k - 1) * c);
+  if (s >= 0) return load_at<Pack<T, V>>(x + (int64_t)s * st, offset);
+  if (state) return load_at<Pack<T, V>>(state + (int64_t)(s + k - 1) * c, offset);
 #pragma unroll
   for (int i = 0; i < V; ++i) v.set(i, 0.f);
   return v;

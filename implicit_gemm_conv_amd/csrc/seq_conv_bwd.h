@@ -35,9 +35,10 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
   const int64_t t0 = (int64_t)piece * per * kGroup;
   const bool here = t0 < a.t || piece == 0;
   const int t1 = (int)min((int64_t)a.t, t0 + per * kGroup);  // rows t0 .. t1 - 1 are this lane's
-  const T* x = (const T*)a.x.p + b * a.x.sb + ch;
-  const T* dy = (const T*)a.dy.p + b * a.dy.sb + ch;
-  const T* state = a.state ? (const T*)a.state + (int64_t)b * (K - 1) * a.c + ch : nullptr;
+  const uint32_t offset = (uint32_t)ch * sizeof(T);
+  const T* x = (const T*)a.x.p + b * a.x.sb;
+  const T* dy = (const T*)a.dy.p + b * a.dy.sb;
+  const T* state = a.state ? (const T*)a.state + (int64_t)b * (K - 1) * a.c : nullptr;
   const uint8_t* starts = a.starts ? a.starts + (int64_t)b * a.t : nullptr;
 
   float w[K][V], bias[V], win[K][V], acc[K][V], dw[K + 1][V];  // dw[K]: dbias
@@ -58,20 +59,20 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
     for (int k = 1; k < K; ++k) {
       const int s = (int)t0 - K + k;
       if (!KEPT || s < 0) {
-        const P v = row_at<T, V>(x, a.x.st, state, s, K, a.c);
+        const P v = row_at<T, V>(x, a.x.st, state, s, K, a.c, offset);
 #pragma unroll
         for (int i = 0; i < V; ++i) win[k][i] = v.get(i);
       }
     }
     if (KEPT && t0 > 0) {
-      const int64_t at = ((int64_t)b * groups + t0 / kGroup - 1) * a.c + ch;
+      const int64_t at = (int64_t)b * groups + t0 / kGroup - 1;
+      const Half<V> q = half_group<V>(a.kept, at, 1, a.c, ch);  // rows 8 .. 15, K - 1 <= 7
+      float scale[V];
+      group_scales<V>(a.kept, at, a.c, ch, scale);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const uint2 q = *(const uint2*)(a.kept.q + (at + i) * kGroup + 8);  // rows 8 .. 15, K - 1 <= 7
-        const float scale = group_scale(a.kept.e[at + i]);
+      for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int k = 1; k < K; ++k) win[k][i] = held(8 - K + k < 4 ? q.x : q.y, (8 - K + k) & 3) * scale;
-      }
+        for (int k = 1; k < K; ++k) win[k][i] = q.get(i, 8 - K + k) * scale[i];
     }
     int reach = reach_before(starts, (int)t0, K);
     // row s of dx is complete; below row 0 it is a carried row's gradient
@@ -80,8 +81,9 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
 #pragma unroll
       for (int i = 0; i < V; ++i) out.set(i, v[i]);
       if (!own) return;
-      if (s >= t0 && s < t1) *(P*)((T*)a.dx + ((int64_t)b * a.t + s) * a.c + ch) = out;
-      if (s < 0 && piece == 0 && a.dstate) *(P*)((T*)a.dstate + ((int64_t)b * (K - 1) + s + K - 1) * a.c + ch) = out;
+      if (s >= t0 && s < t1) store_at((T*)a.dx + ((int64_t)b * a.t + s) * a.c, offset, out);
+      if (s < 0 && piece == 0 && a.dstate)
+        store_at((T*)a.dstate + ((int64_t)b * (K - 1) + s + K - 1) * a.c, offset, out);
     };
 
     const int end = min(a.t, t1 + K - 1);
@@ -89,21 +91,19 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
       const bool mine = g0 < t1;             // else the rows after the piece, K - 1 of them at most
       const int n = min(end - g0, mine ? kGroup : K - 1);
       P ry[kGroup], rx[kGroup];
-      uint4 q[V];
+      Half<V> q[2];
       float scale[V];
 #pragma unroll
       for (int j = 0; j < kGroup; ++j) {
         const int64_t t = g0 + min(j, n - 1);
-        ry[j] = *(const P*)(dy + t * a.dy.st);
-        if (!KEPT) rx[j] = *(const P*)(x + t * a.x.st);
+        ry[j] = load_at<P>(dy + t * a.dy.st, offset);
+        if (!KEPT) rx[j] = load_at<P>(x + t * a.x.st, offset);
       }
       if (KEPT) {
-        const int64_t at = ((int64_t)b * groups + g0 / kGroup) * a.c + ch;
+        const int64_t at = (int64_t)b * groups + g0 / kGroup;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          q[i] = *(const uint4*)(a.kept.q + (at + i) * kGroup);
-          scale[i] = group_scale(a.kept.e[at + i]);
-        }
+        for (int h = 0; h < 2; ++h) q[h] = half_group<V>(a.kept, at, h, a.c, ch);
+        group_scales<V>(a.kept, at, a.c, ch, scale);
       }
       const uint32_t first = starts ? (uint32_t)__ballot(lane < n && starts[g0 + lane]) : 0u;
       // `plain`: 16 rows of the piece that all reach K - 1 rows back
@@ -122,12 +122,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
                 acc[k][i] = acc[k + 1][i];
               }
               acc[K - 1][i] = 0.f;
-              if (KEPT) {
-                const uint32_t word[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-                win[K - 1][i] = held(word[j >> 2], j & 3) * scale[i];
-              } else {
-                win[K - 1][i] = rx[j].get(i);
-              }
+              win[K - 1][i] = KEPT ? q[j / 8].get(i, j % 8) * scale[i] : rx[j].get(i);
               float dz = ry[j].get(i);
               if (a.act) {
                 float z = bias[i];
@@ -157,7 +152,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
     for (int k = 1; k < K; ++k) {
       const int s = end - K + k;
       if (a.dstate_out && end == a.t && (a.t == 0 || a.t - 1 - s <= at_end)) {
-        const P v = *(const P*)((const T*)a.dstate_out + ((int64_t)b * (K - 1) + k - 1) * a.c + ch);
+        const P v = load_at<P>((const T*)a.dstate_out + ((int64_t)b * (K - 1) + k - 1) * a.c, offset);
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[k][i] += v.get(i);
       }
@@ -232,7 +227,8 @@ hipError_t run(const ConvArgs& a, hipStream_t s) {
 template <typename T, int V>
 hipError_t run_wide(const ConvArgs& a, hipStream_t s) {
   constexpr int e = sizeof(T), bytes = V * e;
-  const uintptr_t at = (uintptr_t)a.dx | (uintptr_t)a.state | (uintptr_t)a.dstate | (uintptr_t)a.dstate_out;
+  const uintptr_t at = (uintptr_t)a.dx | (uintptr_t)a.state | (uintptr_t)a.dstate | (uintptr_t)a.dstate_out |
+                       (uintptr_t)a.kept.e * e;
   const bool wide = a.c % V == 0 && pieces(a.dy, bytes, e) && (a.kept.q || pieces(a.x, bytes, e)) && at % bytes == 0;
   return wide ? run<T, V>(a, s) : run<T, 1>(a, s);
 }

@@ -17,51 +17,6 @@ struct No {
   static constexpr bool value = false;
 };
 
-// ---- 8-bit groups ----
-// Byte of a group whose largest magnitude has the float bits `top` (sign
-// cleared; an unsigned maximum of the bits orders magnitudes and puts
-// infinities and NaN on top).
-__device__ __forceinline__ int group_byte(uint32_t top) {
-  const int biased = (int)(top >> 23);
-  return biased == 255 ? 255 : max(biased - 6, 1);
-}
-// 2^(127 - byte): what the group's values are multiplied by before rounding
-// (byte 255 gives 0; such a group is read back as NaN whatever it holds).
-__device__ __forceinline__ float group_inverse(int byte) {
-  return byte == 255 ? 0.f : __uint_as_float((uint32_t)(254 - byte) << 23);
-}
-// 2^(byte - 127), NaN for 255.
-__device__ __forceinline__ float group_scale(int byte) {
-  return byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)byte << 23);
-}
-// Round to nearest even within +-127.  The scaling is exact (a power of two;
-// values it takes below the normal range round to zero either way).
-__device__ __forceinline__ int quantise(float v, float inverse) {
-  return (int)__builtin_rintf(__builtin_amdgcn_fmed3f(v * inverse, -127.f, 127.f));
-}
-
-// The 16 values of a group, of which n lie inside T, as 16 bytes; *byte gets
-// the group's byte.
-__device__ __forceinline__ uint4 pack_group(const float (&v)[kGroup], int n, int* byte) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < kGroup; ++j)
-    if (j < n) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
-  *byte = group_byte(top);
-  const float inv = group_inverse(*byte);
-  uint32_t w[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    w[k] = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (4 * k + j < n) w[k] |= (uint32_t)(quantise(v[4 * k + j], inv) & 0xff) << (8 * j);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// Byte j of four packed ones, as a signed number.
-__device__ __forceinline__ float held(uint32_t w, int j) { return (float)(int8_t)(w >> (8 * j)); }
-
 // The fp32 result itself, before it is rounded to T: the empty asm keeps the
 // compiler from merging the last fp32 operation with the rounding to fp16 on
 // some paths of a kernel and not on others, which would give a row different
@@ -78,6 +33,8 @@ struct Pack;  // V * sizeof(T) bytes
 template <typename T>
 struct Pack<T, 1> {
   T v;
+  __device__ __forceinline__ T word(int) const { return v; }
+  __device__ __forceinline__ void put(int, T w) { v = w; }
   __device__ __forceinline__ float get(int) const { return to_f32(v); }
   __device__ __forceinline__ void set(int, float f) { v = rounded<T>(f); }
 };
@@ -85,9 +42,152 @@ template <typename T, int V>
 struct alignas(V * sizeof(T)) Pack {
   typedef T type __attribute__((ext_vector_type(V)));
   type v;
+  __device__ __forceinline__ T word(int i) const { return v[i]; }
+  __device__ __forceinline__ void put(int i, T w) { v[i] = w; }
   __device__ __forceinline__ float get(int i) const { return to_f32((T)v[i]); }
   __device__ __forceinline__ void set(int i, float f) { v[i] = rounded<T>(f); }
 };
+
+// Makes the compiler take a held value as a new one: what was unpacked from it
+// before is unpacked again where it is needed next, in one or two instructions,
+// and not kept in registers in between.
+template <typename P>
+__device__ __forceinline__ void renew(P& p) {
+  uint32_t w[(sizeof(P) + 3) / 4] = {};
+  __builtin_memcpy(w, &p, sizeof(P));
+#pragma unroll
+  for (unsigned k = 0; k < sizeof(w) / 4; ++k) asm("" : "+v"(w[k]));
+  __builtin_memcpy(&p, w, sizeof(P));
+}
+
+// An access at a wave-uniform base and a lane's byte offset of 32 bits, which the
+// hardware adds itself: no 64-bit address a lane and row has to be computed and
+// held.
+template <typename P>
+__device__ __forceinline__ P load_at(const void* base, uint32_t offset) {
+  return *(const P*)((const char*)base + offset);
+}
+template <typename P>
+__device__ __forceinline__ void store_at(void* base, uint32_t offset, const P& v) {
+  *(P*)((char*)base + offset) = v;
+}
+
+// ---- 8-bit groups ----
+// Byte of a group whose largest magnitude has the float bits `top` (sign
+// cleared; an unsigned maximum of the bits orders magnitudes and puts
+// infinities and NaN on top).
+__device__ __forceinline__ int group_byte(uint32_t top) {
+  const int biased = (int)(top >> 23);
+  return biased == 255 ? 255 : max(biased - 6, 1);
+}
+// 2^(127 - byte): what the group's values are multiplied by before rounding
+// (for byte 255 it does not matter; such a group is read back as NaN).
+__device__ __forceinline__ float group_inverse(int byte) { return __uint_as_float((uint32_t)(254 - byte) << 23); }
+// 2^(byte - 127), NaN for 255.
+__device__ __forceinline__ float group_scale(int byte) {
+  return byte == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float((uint32_t)byte << 23);
+}
+// The largest magnitudes' float bits of V channels over 16 rows.  16-bit types
+// compare two channels at once in their own bits.
+template <typename T, int V>
+__device__ __forceinline__ void group_top(const Pack<T, V> (&raw)[kGroup], uint32_t (&top)[V]) {
+  if constexpr (sizeof(T) == 2 && V % 2 == 0) {
+    typedef uint16_t pair __attribute__((ext_vector_type(2)));
+    pair m[V / 2];
+#pragma unroll
+    for (int k = 0; k < V / 2; ++k) m[k] = (pair)(uint16_t)0;
+#pragma unroll
+    for (int j = 0; j < kGroup; ++j) {
+      uint32_t w[V / 2];
+      __builtin_memcpy(w, &raw[j], sizeof(w));
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        const uint32_t u = w[k] & 0x7fff7fffu;
+        pair v;
+        __builtin_memcpy(&v, &u, 4);
+        m[k] = __builtin_elementwise_max(m[k], v);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      T t;
+      const uint16_t bits = m[i / 2][i % 2];
+      __builtin_memcpy(&t, &bits, 2);
+      top[i] = __float_as_uint(to_f32(t));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      top[i] = 0;
+#pragma unroll
+      for (int j = 0; j < kGroup; ++j) top[i] = max(top[i], __float_as_uint(raw[j].get(i)) & 0x7fffffffu);
+    }
+  }
+}
+// Four values to four bytes, each rounded to nearest even within +-127: the
+// scaling is exact (a power of two), and adding 1.5 * 2^23 leaves the rounded
+// whole number in the low byte of the sum.
+__device__ __forceinline__ uint32_t quantise4(float a, float b, float c, float d, float inverse) {
+  constexpr float one = 12582912.f;
+  const auto q = [&](float v) {
+    return __float_as_uint(__builtin_amdgcn_fmed3f(fmaf(v, inverse, one), one - 127.f, one + 127.f));
+  };
+  // bytes 0 of two words side by side, twice
+  const uint32_t lo = __builtin_amdgcn_perm(q(b), q(a), 0x0c0c0400u);
+  const uint32_t hi = __builtin_amdgcn_perm(q(d), q(c), 0x0c0c0400u);
+  return hi << 16 | lo;
+}
+// V channels from ch of group `at` (batch and group as one index) into 8 bits.
+// raw: the group's rows, those past the first n (n >= 1) repeating one of them.
+template <typename T, int V>
+__device__ __forceinline__ void keep_group(const Pack<T, V> (&raw)[kGroup], int n, const Kept& k, int64_t at, int c,
+                                           int ch) {
+  uint32_t top[V];
+  group_top<T, V>(raw, top);
+  Pack<uint8_t, V> e;
+  uint32_t w[4][V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int byte = group_byte(top[i]);
+    const float inv = group_inverse(byte);
+    e.put(i, (uint8_t)byte);
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      w[h][i] = quantise4(raw[4 * h].get(i), raw[4 * h + 1].get(i), raw[4 * h + 2].get(i), raw[4 * h + 3].get(i), inv);
+    if (n < kGroup)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) w[h][i] &= n >= 4 * h + 4 ? ~0u : n <= 4 * h ? 0u : (1u << 8 * (n - 4 * h)) - 1u;
+  }
+  store_at(k.e + at * c, (uint32_t)ch, e);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    Pack<uint32_t, 2 * V> q;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      q.put(2 * i, w[2 * h][i]);
+      q.put(2 * i + 1, w[2 * h + 1][i]);
+    }
+    store_at(k.q + (at * 2 + h) * c * 8, (uint32_t)ch * 8, q);
+  }
+}
+// Rows 8 h .. 8 h + 7 of V channels: byte j % 4 of word j / 4 is row j.
+template <int V>
+struct Half {
+  Pack<uint32_t, 2 * V> w;
+  __device__ __forceinline__ float get(int i, int j) const {
+    return (float)(int8_t)(w.word(2 * i + j / 4) >> 8 * (j % 4));
+  }
+};
+template <int V>
+__device__ __forceinline__ Half<V> half_group(const Kept& k, int64_t at, int h, int c, int ch) {
+  return Half<V>{load_at<Pack<uint32_t, 2 * V>>(k.q + (at * 2 + h) * c * 8, (uint32_t)ch * 8)};
+}
+template <int V>
+__device__ __forceinline__ void group_scales(const Kept& k, int64_t at, int c, int ch, float (&scale)[V]) {
+  const Pack<uint8_t, V> e = load_at<Pack<uint8_t, V>>(k.e + at * c, (uint32_t)ch);
+#pragma unroll
+  for (int i = 0; i < V; ++i) scale[i] = group_scale(e.word(i));
+}
 
 // ---- gates ----
 // The gates work in powers of two: exp2 and the reciprocals are the hardware's
@@ -119,32 +219,27 @@ __device__ __forceinline__ float channel_unit(float lam) {
   return lam < -80.f ? 1.f : 1.f / ((1.f + expf(-lam)) * softplus(lam));
 }
 
-// What a channel's rate = decay * softplus(lam) multiplies the open gate by.
+// What multiplies the open gate r: u = rate r with rate = decay * softplus(lam), and
+// log2 a = -rate log2 e r.
 struct Rate {
-  float u;     // u = rate * r
-  float log2;  // log2 a = -rate log2 e * r
+  float u, log2;
 };
-__device__ __forceinline__ Rate channel_rate(float lam, float decay) {
-  const float u = decay * softplus(lam);
-  return Rate{u, -kLog2e * u};
-}
+__device__ __forceinline__ Rate rate_of(float u) { return Rate{u, -kLog2e * u}; }
 
-// 1 - e^(-2u) for u >= 0, given a = e^-u.  Below 2u = 1/4 by its series to (2u)^6
-// (the next term is under 5e-8 of the sum), where 1 - a^2 would lose the leading bits.
+// 1 - e^(-2u) for u >= 0, given a = e^-u.  Below u = 1/8, where 1 - a^2 would lose
+// the leading bits, u times the polynomial of degree 4 nearest to (1 - e^(-2u)) / u
+// there in relative error (at most 7e-9 off, fitted at Chebyshev points).
 __device__ __forceinline__ float one_minus_square(float u, float a) {
-  float p = fmaf(u, -64.f / 720.f, 32.f / 120.f);
-  p = fmaf(u, p, -16.f / 24.f);
-  p = fmaf(u, p, 8.f / 6.f);
-  p = fmaf(u, p, -2.f);
+  float p = fmaf(u, 0.2403048575f, -0.6638176441f);
+  p = fmaf(u, p, 1.333206058f);
+  p = fmaf(u, p, -1.999997973f);
   p = fmaf(u, p, 2.f);
   return u < 0.125f ? u * p : fmaf(-a, a, 1.f);
 }
 
 // The gates of one value; x2 are the logits times -log2 e.
 struct Gate {
-  float r, i, a;  // a = e^-u
-  float t, rs;    // 1 - a^2 and its inverse square root, so that m = t rs.  Where t vanishes rs stays
-                  // finite, and products with m and u take their limit 0.  NaN stays NaN in t.
+  float r, i, a, t;  // a = e^-u, t = 1 - a^2
 };
 __device__ __forceinline__ Gate gates(float r2, float i2, const Rate& rate) {
   Gate g;
@@ -152,8 +247,18 @@ __device__ __forceinline__ Gate gates(float r2, float i2, const Rate& rate) {
   g.i = sigmoid2(i2);
   g.a = __builtin_amdgcn_exp2f(rate.log2 * g.r);
   g.t = one_minus_square(rate.u * g.r, g.a);
-  g.rs = __builtin_amdgcn_rsqf(fmaxf(g.t, 1e-36f));
   return g;
+}
+// t^(-1/2).  Where t vanishes it stays finite, so that products with t and u take
+// their limit 0; a NaN in t is not passed on, but stays in t.
+__device__ __forceinline__ float inv_sqrt(float t) { return __builtin_amdgcn_rsqf(fmaxf(t, 1e-36f)); }
+
+// A barrier for what went through LDS alone: unlike __syncthreads it does not
+// wait for global loads in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 }  // namespace convseq

@@ -17,7 +17,7 @@ struct Rows {
   int64_t sb, st;
 };
 
-// A (B, T, C) tensor in 8 bits: q (B, groups, C, 16), e (B, groups, C).
+// A (B, T, C) tensor in 8 bits: q (B, groups, 2, C, 8), e (B, groups, C).
 struct Kept {
   int8_t* q;
   uint8_t* e;
@@ -68,6 +68,7 @@ struct ScanArgs {
   const float *states_in, *dh_last;
   void *dx, *dr, *di;
   float *dlam, *dh0;
+  float* parts;  // the tiles' sums, in the workspace
   void* work;
 };
 

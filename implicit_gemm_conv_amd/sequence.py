@@ -84,9 +84,9 @@ def _seq():
 
 
 class Packed8(NamedTuple):
-    """A tensor in 8 bits: q (B, groups of 16 rows, C, 16) int8 and e (B, groups, C) uint8; the
-    value held at row t is q[b, t // 16, c, t % 16] * 2^(e - 127), NaN where e is 255.  shape and
-    dtype are the original's."""
+    """A tensor in 8 bits: q (B, groups of 16 rows, 2, C, 8) int8 and e (B, groups, C) uint8; the
+    value held at row t is q[b, t // 16, t % 16 // 8, c, t % 8] * 2^(e - 127), NaN where e is 255.
+    shape and dtype are the original's."""
     q: torch.Tensor
     e: torch.Tensor
     shape: torch.Size
@@ -168,7 +168,7 @@ def _kept_input(p, shape, device, what):
     b, t, c = shape
     groups = -(-t // GROUP_ROWS)
     held = p.shape[0] if len(p.shape) == 2 else math.prod(p.shape[1:-1])
-    if held != t or p.q.shape != (b, groups, c, GROUP_ROWS) or p.e.shape != (b, groups, c) or p.q.dtype != torch.int8 \
+    if held != t or p.q.shape != (b, groups, 2, c, GROUP_ROWS // 2) or p.e.shape != (b, groups, c) or p.q.dtype != torch.int8 \
             or p.e.dtype != torch.uint8 or p.q.device != device or p.e.device != device \
             or not p.q.is_contiguous() or not p.e.is_contiguous():
         raise ValueError(f"{what} in 8 bits must stand for a tensor of shape {tuple(shape)} on {device}")
@@ -196,7 +196,7 @@ def _new_kept(x, shape):
     """Room for x (B, T, C) in 8 bits, as the tensor of the given shape."""
     b, t, c = x.shape
     groups = -(-t // GROUP_ROWS)
-    return Packed8(torch.empty((b, groups, c, GROUP_ROWS), dtype=torch.int8, device=x.device),
+    return Packed8(torch.empty((b, groups, 2, c, GROUP_ROWS // 2), dtype=torch.int8, device=x.device),
                    torch.empty((b, groups, c), dtype=torch.uint8, device=x.device), shape, x.dtype)
 
 

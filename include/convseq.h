@@ -63,12 +63,12 @@ typedef struct {
 
 /* A (B, T, C) tensor in 8 bits: 16 consecutive rows t of a channel (the last
  * group may be short) share the byte e[b, t/16, c], and the value held at
- * (b, t, c) is q[b, t/16, c, t%16] * 2^(e - 127).  With M the largest magnitude
+ * (b, t, c) is q[b, t/16, t%16/8, c, t%8] * 2^(e - 127).  With M the largest magnitude
  * of the group, e - 127 = max(floor(log2 M) - 6, -126) and q is x / 2^(e - 127)
  * rounded to nearest even within +-127.  A group that contains an infinity or
- * a NaN has e = 255 and is read back as NaN throughout.  q (B, ceil(T/16), C,
- * 16) and e (B, ceil(T/16), C) are dense and q is 16-byte aligned; rows past T
- * are written as zero. */
+ * a NaN has e = 255 and is read back as NaN throughout.  q (B, ceil(T/16), 2,
+ * C, 8) and e (B, ceil(T/16), C) are dense and q is 16-byte aligned; rows past
+ * T are written as zero. */
 typedef struct {
   void* q; /* int8, 16-byte aligned */
   void* e; /* uint8 */

@@ -40,8 +40,8 @@ def _starts_np(s):
 
 def _rows_of(p):
     """q as (B, T, C); the rows past T of the last group have to be zero."""
-    b, g, c, n = p.q.shape
-    rows = p.q.permute(0, 1, 3, 2).reshape(b, g * n, c).cpu().numpy()
+    b, g, two, c, n = p.q.shape
+    rows = p.q.permute(0, 1, 2, 4, 3).reshape(b, g * two * n, c).cpu().numpy()
     t = int(np.prod(p.shape[1:-1])) if len(p.shape) > 2 else p.shape[0]
     assert not rows[:, t:].any()
     return rows[:, :t]
