@@ -15,9 +15,10 @@
 // channels, a wave 8 rows, a lane V channels of those.  The lane composes its
 // rows into one step of h and one of c; the waves' steps are composed through
 // LDS, and the tiles' steps of c through memory from the last tile to the first
-// (seq_carry.h).  Then the lane runs h down its rows and c up them, with a, r, i,
-// m i and a i x / m of each value held in registers, and stores the three
-// gradients.  Each input is read once, each gradient written once: memory
+// (seq_carry.h).  Then the lane runs c up its rows, with r, i, m i and
+// a i x / m - h_{t-1} of each value held in registers, and stores the three
+// gradients; a is computed again from r, which is cheaper than the registers it
+// would take (at 128, two workgroups fit a compute unit).  Each input is read once, each gradient written once: memory
 // bound, 4 elements (or 1 element and 3 bytes) in and 3 out a value.
 #include "seq_carry.h"
 
@@ -86,12 +87,6 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
     if (KEPT) return q[k].get(i, j) * scale[k][i];
     return k > 0 ? -kLog2e * raw[k][j].get(i) : raw[k][j].get(i);
   };
-  const auto renew_x = [&] {
-    if (KEPT) renew(q[0]);
-    if (!KEPT)
-#pragma unroll
-      for (int j = 0; j < kRows; ++j) renew(raw[0][j]);
-  };
   uint32_t first = 0;  // bit j: row t0 + j begins a sequence
   if (STARTS) first = (uint32_t)__ballot(lane < n && a.starts[(int64_t)b * a.t + t0 + lane]);
   const int pieces = (a.t + kEvery - 1) / kEvery;
@@ -108,10 +103,13 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
   for (int i = 0; i < V; ++i) rate[i] = rate_of(rates[lane * V + i]);
 
   // gates, and this wave's steps of h and c
-  float rv[kRows][V], iv[kRows][V], mi[kRows][V], kv[kRows][V];  // r, i, m i, a i x / m
+  float rv[kRows][V], iv[kRows][V], mi[kRows][V], kv[kRows][V];  // r, i, m i, a i x / m less what is known of h_{t-1}
   Carry step[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) step[i] = Carry{1.f, 0.f};
+  float sent[V];  // what the rows' dy make of c before the first row
+#pragma unroll
+  for (int i = 0; i < V; ++i) sent[i] = 0.f;
 #pragma unroll
   for (int j = 0; j < kRows; ++j)
     if (j < n) {
@@ -120,41 +118,24 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
       for (int i = 0; i < V; ++i) {
         const float x = value(0, j, i);
         const Gate g = gates(value(1, j, i), value(2, j, i), rate[i]);
-        const float rs = inv_sqrt(g.t);
+        const float rs = inv_sqrt(g.t), m = g.t * rs, v = g.i * x, in = m * v;
         rv[j][i] = g.r;
         iv[j][i] = g.i;
-        mi[j][i] = g.t * rs * g.i;
-        kv[j][i] = g.a * g.i * x * rs;
-        const float in = mi[j][i] * x, h = fmaf(g.a, step[i].h, in);
+        mi[j][i] = m * g.i;
+        kv[j][i] = g.a * rs * v;
+        if (!begins) kv[j][i] -= step[i].h;
+        const float h = fmaf(g.a, step[i].h, in);
         step[i] = Carry{begins ? -0.f : step[i].a * g.a, begins ? in : h};
+        // rows from a start on send nothing up (asked of the starts, not of the
+        // product, which a NaN behind the start may have taken)
+        if (!STARTS || (first & ((2u << j) - 1u)) == 0) sent[i] = fmaf(step[i].a, ry[j].get(i), sent[i]);
       }
     }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     down[wave][lane * V + i] = step[i];
-    step[i] = Carry{STARTS ? 1.f : step[i].a, 0.f};  // without starts both steps have the product of all a
+    up[wave][lane * V + i] = Carry{STARTS && first ? -0.f : step[i].a, sent[i]};
   }
-  const auto renew_rates = [&] {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      renew(rate[i].u);
-      renew(rate[i].log2);
-    }
-  };
-  const auto a_of = [&](int j, int i) { return __builtin_amdgcn_exp2f(rate[i].log2 * rv[j][i]); };
-  renew_rates();
-#pragma unroll
-  for (int j = kRows - 1; j >= 0; --j)
-    if (j < n) {
-      const bool begins = STARTS && (first >> j & 1);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float av = a_of(j, i), c = av * (step[i].h + ry[j].get(i));
-        step[i] = Carry{!STARTS ? step[i].a : begins ? -0.f : step[i].a * av, begins ? 0.f : c};
-      }
-    }
-#pragma unroll
-  for (int i = 0; i < V; ++i) up[wave][lane * V + i] = step[i];
   __syncthreads();
 
   // wave 0 has the tile's step of c, and gets the c after the tile
@@ -178,21 +159,23 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
       if (lane == 0) raise_flag(flags + turn, 1);
     }
   }
-  // h down the rows while the tiles before this one finish: kv becomes a i x / m - h_{t-1}
+  // The state before these rows reaches row j as the product of the a before it,
+  // e^-(sum of u), up to the first start: kv becomes a i x / m - h_{j-1}, while the
+  // tiles before this one finish.
   for (int w = 0; w < wave; ++w)
 #pragma unroll
     for (int i = 0; i < V; ++i) h[i] = apply(down[w][lane * V + i], h[i]);
-  renew_x();
-  renew_rates();
+  const int reached = STARTS && first ? min(n, __builtin_ctz(first)) : n;
+  float open[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) open[i] = 0.f;
 #pragma unroll
   for (int j = 0; j < kRows; ++j)
-    if (j < n) {
-      const bool begins = STARTS && (first >> j & 1);
+    if (j < reached) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float in = mi[j][i] * value(0, j, i);
-        kv[j][i] = begins ? kv[j][i] : kv[j][i] - h[i];
-        h[i] = begins ? in : fmaf(a_of(j, i), h[i], in);
+        kv[j][i] = fmaf(-__builtin_amdgcn_exp2f(rate[i].log2 * open[i]), h[i], kv[j][i]);
+        open[i] += rv[j][i];
       }
     }
 
@@ -228,10 +211,17 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = apply(up[w][lane * V + i], c[i]);
   const int64_t out = ((int64_t)b * a.t + t0) * a.c;
-  renew_x();
-  renew_rates();
+  if (KEPT) renew(q[0]);
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) renew(ry[j]);
+  for (int j = 0; j < kRows; ++j) {
+    renew(ry[j]);
+    if (!KEPT) renew(raw[0][j]);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    renew(rate[i].u);
+    renew(rate[i].log2);
+  }
   if (own) {
 #pragma unroll
     for (int j = kRows - 1; j >= 0; --j)
@@ -240,10 +230,13 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float g = ry[j].get(i) + c[i];
-          const float gm = g * mi[j][i], ga = g * a_of(j, i);
+          const float gm = g * mi[j][i], ga = g * __builtin_amdgcn_exp2f(rate[i].log2 * rv[j][i]);
+          // x (1 - i), x's power of two in the subtraction's place
+          const float xi = KEPT ? q[0].get(i, j) * fmaf(-scale[0][i], iv[j][i], scale[0][i])
+                                : raw[0][j].get(i) * (1.f - iv[j][i]);
           const float e = ga * (rate[i].u * rv[j][i]) * kv[j][i];
           dx.set(i, gm);
-          di.set(i, gm * value(0, j, i) * (1.f - iv[j][i]));
+          di.set(i, gm * xi);
           dr.set(i, e * (1.f - rv[j][i]));
           sum[i] += e;
           c[i] = STARTS && (first >> j & 1) ? 0.f : ga;
