@@ -130,9 +130,10 @@ def _sequence(x, what, like=None, dims=3):
         raise ValueError(f"{what} must be a device tensor: the sequence operators run on the GPU only")
     if x.dim() != dims:
         raise ValueError(f"{what} must have {dims} dimensions, got shape {tuple(x.shape)}")
-    if x.dtype not in _DTYPES:
-        raise TypeError(f"unsupported dtype {x.dtype}")
-    if like is not None and (x.shape != like.shape or x.dtype != like.dtype or x.device != like.device):
+    if like is None:
+        if x.dtype not in _DTYPES:
+            raise TypeError(f"unsupported dtype {x.dtype}")
+    elif x.shape != like.shape or x.dtype != like.dtype or x.device != like.device:
         raise ValueError(f"{what} must be {like.dtype} of shape {tuple(like.shape)} on {like.device}, "
                          f"got {x.dtype} {tuple(x.shape)} on {x.device}")
     return x if x.stride(-1) == 1 or x.shape[-1] == 1 and x.is_contiguous() else x.contiguous()
@@ -207,23 +208,25 @@ def _kept_ptrs(kept):
     return (KeptPtr * len(kept))(*(KeptPtr(p.q.data_ptr(), p.e.data_ptr()) for p in kept))
 
 
-class _on:
-    """The device of x made current, and its current stream."""
-
-    def __init__(self, x):
-        self._device = torch.cuda.device(x.device)
-        self._x = x
-
-    def __enter__(self):
-        self._device.__enter__()
-        return torch.cuda.current_stream(self._x.device).cuda_stream
-
-    def __exit__(self, *exc):
-        return self._device.__exit__(*exc)
+def _call(x, fn, *args):
+    """fn(*args, stream) on the current stream of x's device, which is made current if it is not."""
+    index = x.get_device()
+    if index == torch.cuda.current_device():
+        return _check(fn(*args, _raw_stream(index)))
+    with torch.cuda.device(index):
+        return _check(fn(*args, _raw_stream(index)))
 
 
-def _workspace(n_bytes, device):
-    return torch.empty(_check(n_bytes), dtype=torch.uint8, device=device) if n_bytes else None
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the handle alone, without a Stream object around it (2 us), where this torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
+def _workspace(n_bytes, x):
+    return torch.empty(_check(n_bytes), dtype=torch.uint8, device=x.device) if n_bytes else None
 
 
 # ---- causal depthwise convolution ---------------------------------------------------------------
@@ -242,15 +245,13 @@ def seq_conv(x, w, bias=None, activation=None, state=None, starts=None, keep8=Fa
     k = w.shape[1]
     state = _dense(state, (b, k - 1, c), x.dtype, x.device, "state")
     starts = _starts(starts, b, t, x.device)
-    y = torch.empty((b, t, c), dtype=x.dtype, device=x.device) if out is None \
+    y = x.new_empty((b, t, c)) if out is None \
         else _out(out, (b, t, c), x.dtype, x.device, "out")
-    last = torch.empty((b, k - 1, c), dtype=x.dtype, device=x.device)
+    last = x.new_empty((b, k - 1, c))
     kept = _new_kept(x, x.shape) if keep8 else None
     d = ConvDesc(b, t, c, k, ACTIVATIONS[activation], _DTYPES[x.dtype])
-    with _on(x) as stream:
-        _check(_seq().convseq_conv_fwd(d, _rows(x), w.data_ptr(), _ptr(bias), _ptr(state), _ptr(starts),
-                                       y.data_ptr(), last.data_ptr(), _kept_ptrs([kept] if keep8 else None),
-                                       stream))
+    _call(x, _seq().convseq_conv_fwd, d, _rows(x), w.data_ptr(), _ptr(bias), _ptr(state), _ptr(starts), y.data_ptr(),
+          last.data_ptr(), _kept_ptrs((kept,) if keep8 else None))
     return SeqConv(y, last, kept)
 
 
@@ -267,22 +268,20 @@ def seq_conv_bwd(dy, x, w, bias=None, activation=None, state=None, starts=None, 
     state = _dense(state, (b, k - 1, c), dy.dtype, dy.device, "state")
     dlast = _dense(dstate, (b, k - 1, c), dy.dtype, dy.device, "dstate")
     starts = _starts(starts, b, t, dy.device)
-    dx = torch.empty((b, t, c), dtype=dy.dtype, device=dy.device)
+    dx = dy.new_empty((b, t, c))
     dw = torch.empty((c, k), dtype=torch.float32, device=dy.device)
     db = None if bias is None else torch.empty((c,), dtype=torch.float32, device=dy.device)
     dfirst = None if state is None else torch.empty_like(state)
     d = ConvDesc(b, t, c, k, ACTIVATIONS[activation], _DTYPES[dy.dtype])
-    with _on(dy) as stream:
-        work = _workspace(_seq().convseq_conv_bwd_workspace(d), dy.device)
-        _check(_seq().convseq_conv_bwd(d, _rows(dy), None if packed else _rows(x),
-                                       _kept_ptrs([x] if packed else None), w.data_ptr(), _ptr(bias), _ptr(state),
-                                       _ptr(starts), _ptr(dlast), dx.data_ptr(), dw.data_ptr(), _ptr(db),
-                                       _ptr(dfirst), _ptr(work), stream))
+    work = _workspace(_seq().convseq_conv_bwd_workspace(d), dy)
+    _call(dy, _seq().convseq_conv_bwd, d, _rows(dy), None if packed else _rows(x), _kept_ptrs((x,) if packed else None),
+          w.data_ptr(), _ptr(bias), _ptr(state), _ptr(starts), _ptr(dlast), dx.data_ptr(), dw.data_ptr(), _ptr(db),
+          _ptr(dfirst), _ptr(work))
     return SeqConvGrad(dx, dw, db, dfirst)
 
 
 def _slots(slots, b, pool, device):
-    """The streams' slots in a pool of states: (pointer, pool size)."""
+    """The streams' slots in a pool of states, checked; None where stream b has slot b."""
     if slots is None:
         if pool != b:
             raise ValueError(f"state holds {pool} streams, x has {b}: give slots")
@@ -307,12 +306,11 @@ def seq_conv_step(x, w, state, bias=None, activation=None, slots=None, state_out
     _out(state, pool, x.dtype, x.device, "state")
     slots = _slots(slots, b, pool[0], x.device)
     state_out = state if state_out is None else _out(state_out, pool, x.dtype, x.device, "state_out")
-    y = torch.empty((b, c), dtype=x.dtype, device=x.device) if out is None \
+    y = x.new_empty((b, c)) if out is None \
         else _out(out, (b, c), x.dtype, x.device, "out")
     d = ConvDesc(b, 1, c, k, ACTIVATIONS[activation], _DTYPES[x.dtype])
-    with _on(x) as stream:
-        _check(_seq().convseq_conv_step(d, x.data_ptr(), x.stride(0), w.data_ptr(), _ptr(bias), state.data_ptr(),
-                                        state_out.data_ptr(), _ptr(slots), pool[0], y.data_ptr(), stream))
+    _call(x, _seq().convseq_conv_step, d, x.data_ptr(), x.stride(0), w.data_ptr(), _ptr(bias), state.data_ptr(),
+          state_out.data_ptr(), _ptr(slots), pool[0], y.data_ptr())
     return y, state_out
 
 
@@ -331,17 +329,15 @@ def gated_scan(x, gate_r, gate_i, lam, decay=8.0, h0=None, starts=None, train=Fa
     lam = _dense(lam, (c,), torch.float32, x.device, "lam")
     h0 = _dense(h0, (b, c), torch.float32, x.device, "h0")
     starts = _starts(starts, b, t, x.device)
-    y = torch.empty((b, t, c), dtype=x.dtype, device=x.device) if out is None \
+    y = x.new_empty((b, t, c)) if out is None \
         else _out(out, (b, t, c), x.dtype, x.device, "out")
     h = torch.empty((b, c), dtype=torch.float32, device=x.device)
     states = torch.empty((b, -(-t // STATE_ROWS), c), dtype=torch.float32, device=x.device) if train else None
     kept = tuple(_new_kept(x, x.shape) for _ in range(3)) if keep8 else None
     d = ScanDesc(b, t, c, _DTYPES[x.dtype], decay)
-    with _on(x) as stream:
-        work = _workspace(_seq().convseq_scan_fwd_workspace(d), x.device)
-        _check(_seq().convseq_scan_fwd(d, _rows(x), _rows(gate_r), _rows(gate_i), lam.data_ptr(), _ptr(h0),
-                                       _ptr(starts), y.data_ptr(), h.data_ptr(), _ptr(states), _kept_ptrs(kept),
-                                       _ptr(work), stream))
+    work = _workspace(_seq().convseq_scan_fwd_workspace(d), x)
+    _call(x, _seq().convseq_scan_fwd, d, _rows(x), _rows(gate_r), _rows(gate_i), lam.data_ptr(), _ptr(h0), _ptr(starts),
+          y.data_ptr(), h.data_ptr(), _ptr(states), _kept_ptrs(kept), _ptr(work))
     return GatedScan(y, h, states, kept)
 
 
@@ -363,16 +359,15 @@ def gated_scan_bwd(dy, x, gate_r, gate_i, lam, states, decay=8.0, starts=None, d
         raise ValueError("states is needed: call gated_scan with train=True")
     dh = _dense(dh, (b, c), torch.float32, dy.device, "dh")
     starts = _starts(starts, b, t, dy.device)
-    dx, dr, di = (torch.empty((b, t, c), dtype=dy.dtype, device=dy.device) for _ in range(3))
+    dx, dr, di = (dy.new_empty((b, t, c)) for _ in range(3))
     dlam = torch.empty((c,), dtype=torch.float32, device=dy.device)
     dh0 = torch.empty((b, c), dtype=torch.float32, device=dy.device)
     d = ScanDesc(b, t, c, _DTYPES[dy.dtype], decay)
     rows = (None,) * 3 if packed else tuple(_rows(v) for v in ins)
-    with _on(dy) as stream:
-        work = _workspace(_seq().convseq_scan_bwd_workspace(d), dy.device)
-        _check(_seq().convseq_scan_bwd(d, _rows(dy), *rows, _kept_ptrs(ins if packed else None), lam.data_ptr(),
-                                       states.data_ptr(), _ptr(starts), _ptr(dh), dx.data_ptr(), dr.data_ptr(),
-                                       di.data_ptr(), dlam.data_ptr(), dh0.data_ptr(), _ptr(work), stream))
+    work = _workspace(_seq().convseq_scan_bwd_workspace(d), dy)
+    _call(dy, _seq().convseq_scan_bwd, d, _rows(dy), *rows, _kept_ptrs(ins if packed else None), lam.data_ptr(),
+          states.data_ptr(), _ptr(starts), _ptr(dh), dx.data_ptr(), dr.data_ptr(), di.data_ptr(), dlam.data_ptr(),
+          dh0.data_ptr(), _ptr(work))
     return GatedScanGrad(dx, dr, di, dlam, dh0)
 
 
@@ -390,13 +385,12 @@ def gated_scan_step(x, gate_r, gate_i, lam, h, decay=8.0, slots=None, h_out=None
     _out(h, pool, torch.float32, x.device, "h")
     slots = _slots(slots, b, pool[0], x.device)
     h_out = h if h_out is None else _out(h_out, pool, torch.float32, x.device, "h_out")
-    y = torch.empty((b, c), dtype=x.dtype, device=x.device) if out is None \
+    y = x.new_empty((b, c)) if out is None \
         else _out(out, (b, c), x.dtype, x.device, "out")
     d = ScanDesc(b, 1, c, _DTYPES[x.dtype], decay)
-    with _on(x) as stream:
-        _check(_seq().convseq_scan_step(d, x.data_ptr(), x.stride(0), gate_r.data_ptr(), gate_r.stride(0),
-                                        gate_i.data_ptr(), gate_i.stride(0), lam.data_ptr(), h.data_ptr(),
-                                        h_out.data_ptr(), _ptr(slots), pool[0], y.data_ptr(), stream))
+    _call(x, _seq().convseq_scan_step, d, x.data_ptr(), x.stride(0), gate_r.data_ptr(), gate_r.stride(0),
+          gate_i.data_ptr(), gate_i.stride(0), lam.data_ptr(), h.data_ptr(), h_out.data_ptr(), _ptr(slots), pool[0],
+          y.data_ptr())
     return y, h_out
 
 
@@ -413,8 +407,7 @@ def pack8(x) -> Packed8:
     rows = _sequence(x if x.dim() == 3 else x[None] if x.dim() == 2 else x.flatten(1, -2), "x")
     b, t, c = rows.shape
     kept = _new_kept(rows, shape)
-    with _on(rows) as stream:
-        _check(_seq().convseq_pack8(b, t, c, _DTYPES[rows.dtype], _rows(rows), _kept_ptrs([kept]), stream))
+    _call(rows, _seq().convseq_pack8, b, t, c, _DTYPES[rows.dtype], _rows(rows), _kept_ptrs((kept,)))
     return kept
 
 
@@ -430,6 +423,5 @@ def unpack8(p: Packed8, dtype=None, out=None) -> torch.Tensor:
     _kept_input(p, (b, t, c), p.q.device, "p")
     y = torch.empty(shape, dtype=dtype, device=p.q.device) if out is None \
         else _out(out, shape, dtype, p.q.device, "out")
-    with _on(p.q) as stream:
-        _check(_seq().convseq_unpack8(b, t, c, _DTYPES[dtype], _kept_ptrs([p]), y.data_ptr(), stream))
+    _call(p.q, _seq().convseq_unpack8, b, t, c, _DTYPES[dtype], _kept_ptrs((p,)), y.data_ptr())
     return y

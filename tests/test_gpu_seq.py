@@ -300,7 +300,8 @@ def test_in_a_graph():
 
 
 class _Guarded:
-    """torch with empty() giving tensors between two bands of a known byte."""
+    """torch with empty() giving tensors between two bands of a known byte, and inputs whose
+    new_empty() does."""
 
     BAND = 4096
 
@@ -320,6 +321,9 @@ class _Guarded:
     def empty_like(self, t):
         return self.empty(t.shape, t.dtype, t.device)
 
+    def new_empty(self, t, shape):
+        return self.empty(shape, t.dtype, t.device)
+
     def check(self):
         for raw, n in self.whole:
             assert (raw[:self.BAND] == 0xA5).all() and (raw[self.BAND + n:] == 0xA5).all()
@@ -331,6 +335,7 @@ class _Guarded:
 def test_nothing_is_written_outside_the_outputs(monkeypatch, dtype, b, t, c, starts, state):
     guard = _Guarded()
     monkeypatch.setattr(sequence, "torch", guard)
+    monkeypatch.setattr(torch.Tensor, "new_empty", lambda self, shape: guard.new_empty(self, shape))
     x, w, bias, st = _conv_inputs(dtype, b, t, c, 4, state)
     s = starts_of(starts, b, t, DEV)
     xs, gr, gi, lam, h0 = scan_inputs(t, b, t, c, DT[dtype], DEV, state)
