@@ -10,20 +10,25 @@ namespace convseq {
 
 namespace {
 
-// Where a lane of the grid works: channels ch on, rows t0 .. t0 + n - 1 of batch b.
+// Where a lane of the grid works: channels ch on, rows t0 .. t0 + n - 1 of batch
+// b.  Lanes are dealt over all (group, V channels) pairs in a row, so that none
+// idles behind a channel count that 64 V does not divide (65 channels in waves of
+// their own would leave half the lanes without work).
 struct Place {
   int ch, b, t0, n, part;  // part: b and the group as one index
 };
 template <int V>
 __device__ __forceinline__ bool place(int parts, int t, int c, int groups, Place* p) {
-  const int cb = (c + 64 * V - 1) / (64 * V);
-  const int64_t wave = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  p->part = (int)(wave / cb);
-  p->ch = ((int)(wave % cb) * 64 + (threadIdx.x & 63)) * V;
+  const uint32_t pieces = (uint32_t)c / V;  // of a group
+  const int64_t first = ((int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * 64;
+  // the wave's first piece by wave-uniform division, the lane's from there
+  const uint32_t at = (uint32_t)(first % pieces) + (threadIdx.x & 63), step = at / pieces;
+  p->part = (int)(first / pieces) + (int)step;
+  p->ch = (int)(at - step * pieces) * V;
   p->b = p->part / groups;
-  p->t0 = p->part % groups * kGroup;
+  p->t0 = (p->part - p->b * groups) * kGroup;
   p->n = min(t - p->t0, kGroup);
-  return p->ch < c && p->part < parts;
+  return p->part < parts;
 }
 
 template <typename T, int V>
@@ -31,10 +36,10 @@ __global__ __launch_bounds__(256) void pack8_kernel(int parts, int t, int c, int
   Place p;
   if (!place<V>(parts, t, c, groups, &p)) return;
   typedef Pack<T, V> P;
-  const T* in = (const T*)x.p + p.b * x.sb + (int64_t)p.t0 * x.st;
+  const T* in = (const T*)x.p + p.b * x.sb + (int64_t)p.t0 * x.st + p.ch;
   P raw[kGroup];
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j) raw[j] = load_at<P>(in + (int64_t)min(j, p.n - 1) * x.st, (uint32_t)p.ch * sizeof(T));
+  for (int j = 0; j < kGroup; ++j) raw[j] = *(const P*)(in + (int64_t)min(j, p.n - 1) * x.st);
   keep_group<T, V>(raw, p.n, k, p.part, c, p.ch);
 }
 
@@ -48,20 +53,20 @@ __global__ __launch_bounds__(256) void unpack8_kernel(int parts, int t, int c, i
 #pragma unroll
   for (int h = 0; h < 2; ++h) q[h] = half_group<V>(k, p.part, h, c, p.ch);
   group_scales<V>(k, p.part, c, p.ch, scale);
-  T* to = out + ((int64_t)p.b * t + p.t0) * c;
+  T* to = out + ((int64_t)p.b * t + p.t0) * c + p.ch;
 #pragma unroll
   for (int j = 0; j < kGroup; ++j)
     if (j < p.n) {
       P v;
 #pragma unroll
       for (int i = 0; i < V; ++i) v.set(i, q[j / 8].get(i, j % 8) * scale[i]);
-      store_at(to + (int64_t)j * c, (uint32_t)p.ch * sizeof(T), v);
+      *(P*)(to + (int64_t)j * c) = v;
     }
 }
 
 template <int V>
 unsigned blocks(int64_t parts, int c) {
-  return (unsigned)((parts * ((c + 64 * V - 1) / (64 * V)) + 3) / 4);
+  return (unsigned)((parts * (c / V) + 255) / 256);
 }
 
 template <typename T, int V>

@@ -41,14 +41,8 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
   typedef Pack<T, V> P;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  int id = blockIdx.x;
-  if (tiles > 1) {
-    if (threadIdx.x == 0)
-      ticket = __hip_atomic_fetch_add((int*)a.work, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    id = __builtin_amdgcn_readfirstlane(ticket);
-  }
-  const int turn = id / (cols * a.b), column = id % (cols * a.b);
+  const int columns = cols * a.b, column = (blockIdx.x + blockIdx.x / columns) % columns;
+  const int turn = tiles > 1 ? take_ticket(a.work, column, &ticket) : 0;
   const int tile = tiles - 1 - turn;  // from the end of the sequence
   const int b = column / cols;
   const int ch = (column % cols * 64 + lane) * V;
@@ -136,7 +130,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
     down[wave][lane * V + i] = step[i];
     up[wave][lane * V + i] = Carry{STARTS && first ? -0.f : step[i].a, sent[i]};
   }
-  __syncthreads();
+  lds_barrier();
 
   // wave 0 has the tile's step of c, and gets the c after the tile
   float c[V];
@@ -198,7 +192,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
     if (tile > 0 && lane == 0) raise_flag(flags + turn, 2);
   }
 
-  __syncthreads();
+  lds_barrier();
 
   // c up the rows
   float sum[V];
@@ -248,7 +242,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = sum[i];
-  __syncthreads();
+  lds_barrier();
   if (wave == 0 && own) {
     float* part = a.parts + ((int64_t)tile * a.b + b) * a.c + ch;
 #pragma unroll

@@ -28,14 +28,8 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
   typedef Pack<T, V> P;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  int id = blockIdx.x;
-  if (tiles > 1) {
-    if (threadIdx.x == 0)
-      ticket = __hip_atomic_fetch_add((int*)a.work, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    id = __builtin_amdgcn_readfirstlane(ticket);
-  }
-  const int tile = id / (cols * a.b), column = id % (cols * a.b);
+  const int columns = cols * a.b, column = (blockIdx.x + blockIdx.x / columns) % columns;
+  const int tile = tiles > 1 ? take_ticket(a.work, column, &ticket) : 0;
   const int b = column / cols;
   const int ch = (column % cols * 64 + lane) * V;
   const int chl = min(ch, a.c - V);  // lanes past the last channel read it again
@@ -100,7 +94,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
   // the waves' totals; before = what the waves above do to the state, whole = the tile
 #pragma unroll
   for (int i = 0; i < V; ++i) totals[wave][lane * V + i] = total[i];
-  __syncthreads();
+  lds_barrier();
   Carry before[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) before[i] = Carry{1.f, 0.f};
@@ -142,7 +136,7 @@ __global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a
     }
     if (tile < tiles - 1 && lane == 0) raise_flag(flags + tile, 2);
   }
-  __syncthreads();
+  lds_barrier();
 
 #pragma unroll
   for (int i = 0; i < V; ++i) h[i] = apply(before[i], entry[lane * V + i]);

@@ -6,15 +6,16 @@
 // bit set (forgets()), H is its own, and selections, not products with zero,
 // keep a NaN from crossing.
 //
-// Tiles along a sequence are handed to workgroups by a ticket counter in the
-// order of the recurrence, all columns of a tile row before the next.  A tile
+// The tiles of a column (64 V channels of one sequence) are handed to workgroups
+// by the column's ticket counter, in the order of the recurrence.  A tile
 // publishes its (A, H) as one 64-bit word a channel, looks back over its
 // predecessors, applies their steps from the nearest whole state on, and
 // publishes its own whole state (a word that forgets) in place of its (A, H).
-// A waiting tile waits on tiles of lower tickets only; those were taken by
+// A waiting tile waits on lower tickets of its column only; those were taken by
 // workgroups that already run, the lowest of them waits for nobody, so every
 // wait ends.  (A wait that could not end, in a workspace that another call
-// overwrites, gives up after kSpins and puts NaN into the results.)
+// overwrites, gives up after kSpins and puts NaN into the results.)  One counter
+// for all columns would cost 3 us where a few hundred workgroups start at once.
 //
 // Words and flags are written and read with relaxed device-wide atomics.  A
 // word carries value and presence in one access (A's bits are zero until it is
@@ -31,7 +32,7 @@ namespace convseq {
 
 constexpr uint32_t kWhole = 0x80000000u;  // A of a published state
 constexpr int kSpins = 1 << 20;
-constexpr int kTicketBytes = 256;
+constexpr int kTicketBytes = 64;  // a column's counter, a cache line of its own
 
 struct Carry {
   float a, h;
@@ -53,31 +54,40 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* word) {
   return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// What a launch's tiles share, in its workspace: the ticket, a flag a column
-// and tile, a word a tile and lane channel.
+// What a launch's tiles share, in its workspace: a ticket a column, a flag a
+// column and tile, a word a tile and lane channel.
 struct CarrySpace {
-  int* ticket;
-  uint32_t* flags;   // [columns][tiles]
-  uint64_t* words;   // [tiles][columns][lane channels]
+  char* tickets;
+  uint32_t* flags;  // [columns][tiles]
+  uint64_t* words;  // [tiles][columns][lane channels]
 };
-__host__ __device__ inline int64_t carry_flag_bytes(int64_t tiles, int64_t columns) {
-  return (tiles * columns * 4 + 15) / 16 * 16;
+__host__ __device__ inline int64_t carry_head_bytes(int64_t tiles, int64_t columns) {
+  return columns * kTicketBytes + (tiles * columns * 4 + 15) / 16 * 16;
 }
 // Bytes for `tiles` tiles that publish and `columns` columns of `width` channels.
 inline int64_t carry_bytes(int64_t tiles, int64_t columns, int width) {
-  return kTicketBytes + carry_flag_bytes(tiles, columns) + tiles * columns * width * 8;
+  return carry_head_bytes(tiles, columns) + tiles * columns * width * 8;
 }
 __device__ __forceinline__ CarrySpace carry_space(void* work, int64_t tiles, int64_t columns) {
   char* p = (char*)work;
-  return CarrySpace{(int*)p, (uint32_t*)(p + kTicketBytes),
-                    (uint64_t*)(p + kTicketBytes + carry_flag_bytes(tiles, columns))};
+  return CarrySpace{p, (uint32_t*)(p + columns * kTicketBytes), (uint64_t*)(p + carry_head_bytes(tiles, columns))};
+}
+// The workgroup's place in the order of its column.
+__device__ __forceinline__ int take_ticket(void* work, int column, int* shared) {
+  if (threadIdx.x == 0)
+    *shared = __hip_atomic_fetch_add((int*)((char*)work + (int64_t)column * kTicketBytes), 1, __ATOMIC_RELAXED,
+                                     __HIP_MEMORY_SCOPE_AGENT);
+  lds_barrier();
+  return __builtin_amdgcn_readfirstlane(*shared);
 }
 
 // The words a workgroup gathers at once, and how many tiles it has to apply.
 constexpr int kEach = 2;  // of a wave
+constexpr int kFold = 4;
 template <int V, int WAVES>
 struct Gathered {
   uint64_t words[WAVES * kEach][64 * V];
+  static_assert(WAVES * kEach % kFold == 0, "whole groups");
   int span;
 };
 
@@ -122,7 +132,7 @@ __device__ __forceinline__ void look_back(const uint64_t* words, int64_t step, c
     }
     if (lane == 0) sh.span = span;
   }
-  __syncthreads();
+  lds_barrier();
   const int span = __builtin_amdgcn_readfirstlane(sh.span);
   const bool lost = span < 0;
   for (int from = tile - max(span, 0); from < tile; from += WAVES * kEach) {
@@ -154,26 +164,31 @@ __device__ __forceinline__ void look_back(const uint64_t* words, int64_t step, c
     }
 #pragma unroll
     for (int j = 0; j < kEach; ++j)
-      if (j * WAVES + wave < count) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) sh.words[j * WAVES + wave][lane * V + i] = w[j][i];
-      }
-    __syncthreads();
+      for (int i = 0; i < V; ++i)  // past the last tile: a step that changes nothing
+        sh.words[j * WAVES + wave][lane * V + i] = j * WAVES + wave < count ? w[j][i] : 0x3f800000ull;
+    lds_barrier();
     if (fold)
-      for (int slot = 0; slot < count; ++slot)
+      for (int slot = 0; slot < count; slot += kFold) {
+        uint64_t v[kFold][V];  // read together, applied one after the other
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const uint64_t v = sh.words[slot][lane * V + i];
-          state[i] = apply(Carry{__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))}, state[i]);
-        }
-    __syncthreads();
+        for (int j = 0; j < kFold; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[j][i] = sh.words[slot + j][lane * V + i];
+#pragma unroll
+        for (int j = 0; j < kFold; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            state[i] = apply(Carry{__uint_as_float((uint32_t)v[j][i]), __uint_as_float((uint32_t)(v[j][i] >> 32))}, state[i]);
+      }
+    lds_barrier();
   }
   if (lost)
 #pragma unroll
     for (int i = 0; i < V; ++i) state[i] = __uint_as_float(0x7fc00000u);
 }
 
-// Zero for ticket, flags and words; a kernel rather than a memset, which a
+// Zero for tickets, flags and words; a kernel rather than a memset, which a
 // captured graph has to be able to replay.
 static __global__ __launch_bounds__(256) void carry_clear_kernel(uint4* p, int64_t n) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)

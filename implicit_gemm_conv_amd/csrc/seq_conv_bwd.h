@@ -4,8 +4,9 @@
 //   dx_s = sum_j w_{K-1-j} dz_{s+j},   dw_k = sum_t dz_t X(t - (K-1) + k),   dbias = sum_t dz_t
 //
 // A lane walks down G groups of 16 rows of V channels with the last K values of
-// X and the K unfinished rows of dx in registers: row t gives dz_t to the K rows
-// it looked at, and row t - (K-1) is then complete and stored.  It ends with the
+// X and the K unfinished rows of dx in registers, loading 8 rows while it works on
+// the 8 before: row t gives dz_t to the K rows it looked at, and row t - (K-1) is
+// then complete and stored.  It ends with the
 // K-1 rows after its own, for what they send back.  dw and dbias gather in
 // registers, are added over the 4 waves of the workgroup (4 consecutive pieces
 // of the same channels) in LDS and over the workgroups by a second kernel, both
@@ -20,6 +21,16 @@ namespace convseq {
 namespace {
 
 constexpr int kWaves = 4;
+constexpr int kChunk = 8;  // rows loaded at once
+
+// Rows in flight: dy, x or its 8 bits, and which of them begin a sequence.
+template <typename T, int V, bool KEPT>
+struct Chunk {
+  Pack<T, V> dy[kChunk], x[KEPT ? 1 : kChunk];
+  Half<V> q;
+  float scale[V];
+  uint32_t first;
+};
 
 template <typename T, int K, int V, bool KEPT>
 __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, int cols, int blocks, int per) {
@@ -87,30 +98,34 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
     };
 
     const int end = min(a.t, t1 + K - 1);
-    for (int g0 = (int)t0; g0 < end; g0 += kGroup) {
-      const bool mine = g0 < t1;             // else the rows after the piece, K - 1 of them at most
-      const int n = min(end - g0, mine ? kGroup : K - 1);
-      P ry[kGroup], rx[kGroup];
-      Half<V> q[2];
-      float scale[V];
+    Chunk<T, V, KEPT> now, next;
+    const auto load = [&](int g0, Chunk<T, V, KEPT>& to) {
+      const int n = min(end - g0, kChunk);
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
+      for (int j = 0; j < kChunk; ++j) {
         const int64_t t = g0 + min(j, n - 1);
-        ry[j] = load_at<P>(dy + t * a.dy.st, offset);
-        if (!KEPT) rx[j] = load_at<P>(x + t * a.x.st, offset);
+        to.dy[j] = load_at<P>(dy + t * a.dy.st, offset);
+        if (!KEPT) to.x[j] = load_at<P>(x + t * a.x.st, offset);
       }
       if (KEPT) {
         const int64_t at = (int64_t)b * groups + g0 / kGroup;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) q[h] = half_group<V>(a.kept, at, h, a.c, ch);
-        group_scales<V>(a.kept, at, a.c, ch, scale);
+        to.q = half_group<V>(a.kept, at, g0 / kChunk % 2, a.c, ch);
+        group_scales<V>(a.kept, at, a.c, ch, to.scale);
       }
-      const uint32_t first = starts ? (uint32_t)__ballot(lane < n && starts[g0 + lane]) : 0u;
-      // `plain`: 16 rows of the piece that all reach K - 1 rows back
+      to.first = starts ? (uint32_t)__ballot(lane < n && starts[g0 + lane]) : 0u;
+    };
+    if (t0 < end) load((int)t0, next);
+    for (int g0 = (int)t0; g0 < end; g0 += kChunk) {
+      now = next;
+      if (g0 + kChunk < end) load(g0 + kChunk, next);
+      const bool mine = g0 < t1;  // else the rows after the piece, K - 1 of them at most
+      const int n = min(end - g0, kChunk);
+      const uint32_t first = now.first;
+      // `plain`: 8 rows of the piece that all reach K - 1 rows back
       const auto run = [&](auto plain) {
         constexpr bool masked = !decltype(plain)::value;
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
+        for (int j = 0; j < kChunk; ++j)
           if (!masked || j < n) {
             if (masked) reach = first >> j & 1 ? 0 : min(reach + 1, K - 1);
             const auto live = [&](int k) { return !masked || K - 1 - k <= reach; };
@@ -122,8 +137,8 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
                 acc[k][i] = acc[k + 1][i];
               }
               acc[K - 1][i] = 0.f;
-              win[K - 1][i] = KEPT ? q[j / 8].get(i, j % 8) * scale[i] : rx[j].get(i);
-              float dz = ry[j].get(i);
+              win[K - 1][i] = KEPT ? now.q.get(i, j) * now.scale[i] : now.x[j].get(i);
+              float dz = now.dy[j].get(i);
               if (a.act) {
                 float z = bias[i];
 #pragma unroll
@@ -141,7 +156,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
             store(g0 + j - (K - 1), acc[0]);
           }
       };
-      if (mine && n == kGroup && !first && reach == K - 1)
+      if (mine && n == kChunk && !first && reach == K - 1)
         run(Yes{});
       else
         run(No{});
@@ -165,7 +180,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
   for (int k = 0; k <= K; ++k) {
 #pragma unroll
     for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = dw[k][i];
-    __syncthreads();
+    lds_barrier();
     if (wave == 0 && own)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -174,7 +189,7 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_bwd_kernel(ConvArgs a, i
         for (int u = 0; u < kWaves; ++u) s += sums[u][lane * V + i];
         part[(int64_t)k * a.c + i] = s;
       }
-    __syncthreads();
+    lds_barrier();
   }
 }
 

@@ -143,15 +143,15 @@ def _dense(t, shape, dtype, device, what):
     """A dense operand of one exact shape and type (None stays None)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != device:
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} on {device}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _out(t, shape, dtype, device, what):
     """An output the caller gave: as _dense, but it has to be contiguous as it is."""
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
@@ -177,12 +177,16 @@ def _kept_input(p, shape, device, what):
 
 
 def _filter(w, bias, x, activation):
-    if activation not in ACTIVATIONS:
+    """w (C, K) and bias (C), checked, and the activation's number."""
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError(f"activation must be one of 'none', 'silu', got {activation!r}")
-    if w.dim() != 2 or w.shape[0] != x.shape[-1] or w.shape[1] < 1:
-        raise ValueError(f"w must be (C, K) with C = {x.shape[-1]}, got {tuple(w.shape)}")
-    w = _dense(w, w.shape, x.dtype, x.device, "w")
-    return w, _dense(bias, (x.shape[-1],), x.dtype, x.device, "bias")
+    shape, c = w.shape, x.shape[-1]
+    if len(shape) != 2 or shape[0] != c or shape[1] < 1:
+        raise ValueError(f"w must be (C, K) with C = {c}, got {tuple(shape)}")
+    device, dtype = x.device, x.dtype
+    return (_dense(w, shape, dtype, device, "w"), None if bias is None else _dense(bias, (c,), dtype, device, "bias"),
+            shape[1], act)
 
 
 def _ptr(t):
@@ -190,7 +194,8 @@ def _ptr(t):
 
 
 def _rows(x):
-    return Rows(x.data_ptr(), x.stride(0), x.stride(1))
+    batch, row, _ = x.stride()
+    return Rows(x.data_ptr(), batch, row)
 
 
 def _new_kept(x, shape):
@@ -241,15 +246,14 @@ def seq_conv(x, w, bias=None, activation=None, state=None, starts=None, keep8=Fa
     """
     x = _sequence(x, "x")
     b, t, c = x.shape
-    w, bias = _filter(w, bias, x, activation)
-    k = w.shape[1]
+    w, bias, k, act = _filter(w, bias, x, activation)
     state = _dense(state, (b, k - 1, c), x.dtype, x.device, "state")
     starts = _starts(starts, b, t, x.device)
     y = x.new_empty((b, t, c)) if out is None \
         else _out(out, (b, t, c), x.dtype, x.device, "out")
     last = x.new_empty((b, k - 1, c))
     kept = _new_kept(x, x.shape) if keep8 else None
-    d = ConvDesc(b, t, c, k, ACTIVATIONS[activation], _DTYPES[x.dtype])
+    d = ConvDesc(b, t, c, k, act, _DTYPES[x.dtype])
     _call(x, _seq().convseq_conv_fwd, d, _rows(x), w.data_ptr(), _ptr(bias), _ptr(state), _ptr(starts), y.data_ptr(),
           last.data_ptr(), _kept_ptrs((kept,) if keep8 else None))
     return SeqConv(y, last, kept)
@@ -261,8 +265,7 @@ def seq_conv_bwd(dy, x, w, bias=None, activation=None, state=None, starts=None, 
     arguments are the forward pass's."""
     dy = _sequence(dy, "dy")
     b, t, c = dy.shape
-    w, bias = _filter(w, bias, dy, activation)
-    k = w.shape[1]
+    w, bias, k, act = _filter(w, bias, dy, activation)
     packed = isinstance(x, Packed8)
     x = _kept_input(x, dy.shape, dy.device, "x") if packed else _sequence(x, "x", dy)
     state = _dense(state, (b, k - 1, c), dy.dtype, dy.device, "state")
@@ -272,7 +275,7 @@ def seq_conv_bwd(dy, x, w, bias=None, activation=None, state=None, starts=None, 
     dw = torch.empty((c, k), dtype=torch.float32, device=dy.device)
     db = None if bias is None else torch.empty((c,), dtype=torch.float32, device=dy.device)
     dfirst = None if state is None else torch.empty_like(state)
-    d = ConvDesc(b, t, c, k, ACTIVATIONS[activation], _DTYPES[dy.dtype])
+    d = ConvDesc(b, t, c, k, act, _DTYPES[dy.dtype])
     work = _workspace(_seq().convseq_conv_bwd_workspace(d), dy)
     _call(dy, _seq().convseq_conv_bwd, d, _rows(dy), None if packed else _rows(x), _kept_ptrs((x,) if packed else None),
           w.data_ptr(), _ptr(bias), _ptr(state), _ptr(starts), _ptr(dlast), dx.data_ptr(), dw.data_ptr(), _ptr(db),
@@ -298,19 +301,20 @@ def seq_conv_step(x, w, state, bias=None, activation=None, slots=None, state_out
     state is touched.  Two streams must not share a slot.  Returns (y, state)."""
     x = _sequence(x, "x", dims=2)
     b, c = x.shape
-    w, bias = _filter(w, bias, x, activation)
-    k = w.shape[1]
-    if state.dim() != 3:
-        raise ValueError(f"state must be (S, K-1, C), got {tuple(state.shape)}")
-    pool = (state.shape[0], k - 1, c)
-    _out(state, pool, x.dtype, x.device, "state")
-    slots = _slots(slots, b, pool[0], x.device)
-    state_out = state if state_out is None else _out(state_out, pool, x.dtype, x.device, "state_out")
-    y = x.new_empty((b, c)) if out is None \
-        else _out(out, (b, c), x.dtype, x.device, "out")
-    d = ConvDesc(b, 1, c, k, ACTIVATIONS[activation], _DTYPES[x.dtype])
-    _call(x, _seq().convseq_conv_step, d, x.data_ptr(), x.stride(0), w.data_ptr(), _ptr(bias), state.data_ptr(),
-          state_out.data_ptr(), _ptr(slots), pool[0], y.data_ptr())
+    w, bias, k, act = _filter(w, bias, x, activation)
+    device, dtype = x.device, x.dtype
+    streams = state.shape[0] if state.dim() else -1
+    pool = (streams, k - 1, c)
+    _out(state, pool, dtype, device, "state")
+    if state_out is None:
+        state_out = state
+    else:
+        _out(state_out, pool, dtype, device, "state_out")
+    slots = _slots(slots, b, streams, device)
+    y = x.new_empty((b, c)) if out is None else _out(out, (b, c), dtype, device, "out")
+    _call(x, _seq().convseq_conv_step, ConvDesc(b, 1, c, k, act, _DTYPES[dtype]), x.data_ptr(), x.stride(0), w.data_ptr(),
+          None if bias is None else bias.data_ptr(), state.data_ptr(), state_out.data_ptr(), _ptr(slots), streams,
+          y.data_ptr())
     return y, state_out
 
 
@@ -378,19 +382,19 @@ def gated_scan_step(x, gate_r, gate_i, lam, h, decay=8.0, slots=None, h_out=None
     x = _sequence(x, "x", dims=2)
     gate_r, gate_i = _sequence(gate_r, "gate_r", x, 2), _sequence(gate_i, "gate_i", x, 2)
     b, c = x.shape
-    lam = _dense(lam, (c,), torch.float32, x.device, "lam")
-    if h.dim() != 2:
-        raise ValueError(f"h must be (S, C), got {tuple(h.shape)}")
-    pool = (h.shape[0], c)
-    _out(h, pool, torch.float32, x.device, "h")
-    slots = _slots(slots, b, pool[0], x.device)
-    h_out = h if h_out is None else _out(h_out, pool, torch.float32, x.device, "h_out")
-    y = x.new_empty((b, c)) if out is None \
-        else _out(out, (b, c), x.dtype, x.device, "out")
-    d = ScanDesc(b, 1, c, _DTYPES[x.dtype], decay)
-    _call(x, _seq().convseq_scan_step, d, x.data_ptr(), x.stride(0), gate_r.data_ptr(), gate_r.stride(0),
-          gate_i.data_ptr(), gate_i.stride(0), lam.data_ptr(), h.data_ptr(), h_out.data_ptr(), _ptr(slots), pool[0],
-          y.data_ptr())
+    device, dtype = x.device, x.dtype
+    lam = _dense(lam, (c,), torch.float32, device, "lam")
+    streams = h.shape[0] if h.dim() else -1
+    _out(h, (streams, c), torch.float32, device, "h")
+    if h_out is None:
+        h_out = h
+    else:
+        _out(h_out, (streams, c), torch.float32, device, "h_out")
+    slots = _slots(slots, b, streams, device)
+    y = x.new_empty((b, c)) if out is None else _out(out, (b, c), dtype, device, "out")
+    _call(x, _seq().convseq_scan_step, ScanDesc(b, 1, c, _DTYPES[dtype], decay), x.data_ptr(), x.stride(0),
+          gate_r.data_ptr(), gate_r.stride(0), gate_i.data_ptr(), gate_i.stride(0), lam.data_ptr(), h.data_ptr(),
+          h_out.data_ptr(), _ptr(slots), streams, y.data_ptr())
     return y, h_out
 
 
