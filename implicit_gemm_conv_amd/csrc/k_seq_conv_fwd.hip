@@ -61,9 +61,10 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_fwd_kernel(ConvArgs a, i
     keep_group<T, V>(*(const P(*)[kGroup])(raw + K - 1), n, a.kept, (int64_t)b * groups + g, a.c, ch);
 
   T* y = (T*)a.y + ((int64_t)b * a.t + t0) * a.c;
-  // `plain`: 16 rows that all reach K - 1 rows back
-  const auto run = [&](auto plain) {
+  // `plain`: 16 rows that all reach K - 1 rows back, with or without the activation
+  const auto run = [&](auto plain, auto activated) {
     constexpr bool masked = !decltype(plain)::value;
+    const bool act = masked ? a.act != 0 : decltype(activated)::value;
 #pragma unroll
     for (int j = 0; j < kGroup; ++j)
       if (!masked || j < n) {
@@ -77,15 +78,17 @@ __global__ __launch_bounds__(kWaves * 64) void seq_conv_fwd_kernel(ConvArgs a, i
             const float sum = fmaf(w[k][i], raw[j + k].get(i), z);
             z = !masked || K - 1 - k <= reach ? sum : z;
           }
-          out.set(i, a.act ? silu(z) : z);
+          out.set(i, act ? silu(z) : z);
         }
         if (own) store_at(y + (int64_t)j * a.c, offset, out);
       }
   };
-  if (n == kGroup && !first && reach == K - 1)
-    run(Yes{});
+  if (n < kGroup || first || reach < K - 1)
+    run(No{}, No{});
+  else if (a.act)
+    run(Yes{}, Yes{});
   else
-    run(No{});
+    run(Yes{}, No{});
 
   if (a.state_out && g == groups - 1 && own) {
     T* out = (T*)a.state_out + (int64_t)b * (K - 1) * a.c;

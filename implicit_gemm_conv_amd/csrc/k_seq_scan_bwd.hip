@@ -32,7 +32,7 @@ constexpr int kTile = kWaves * kRows;
 static_assert(kTile == kEvery, "a tile starts from a kept state");
 
 template <typename T, int V, bool STARTS, bool KEPT>
-__global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_bwd_kernel(ScanArgs a, int cols, int tiles) {
+__global__ __launch_bounds__(kWaves * 64, V == 1 ? 6 : 4) void seq_scan_bwd_kernel(ScanArgs a, int cols, int tiles) {
   __shared__ Carry down[kWaves][64 * V], up[kWaves][64 * V];
   __shared__ float entry[64 * V], rates[64 * V];
   __shared__ Gathered<V, kWaves> gathered;

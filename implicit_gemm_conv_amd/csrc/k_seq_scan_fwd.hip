@@ -20,7 +20,7 @@ constexpr int kWaves = 8;
 constexpr int kTile = kWaves * kGroup;  // rows
 
 template <typename T, int V, bool STARTS, bool KEEP>
-__global__ __launch_bounds__(kWaves * 64, 4) void seq_scan_fwd_kernel(ScanArgs a, int cols, int tiles) {
+__global__ __launch_bounds__(kWaves * 64, V == 1 ? 6 : 4) void seq_scan_fwd_kernel(ScanArgs a, int cols, int tiles) {
   __shared__ Carry totals[kWaves][64 * V];
   __shared__ float entry[64 * V], rates[64 * V];
   __shared__ Gathered<V, kWaves> gathered;

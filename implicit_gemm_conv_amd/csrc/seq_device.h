@@ -5,6 +5,12 @@
 #include "conv_device.h"
 #include "seq_params.h"
 
+// Every fused multiply-add is written as one; none is made from a product and a
+// sum.  What the compiler fuses can differ between the variants of a kernel and
+// between its code for whole and for ragged tiles, and a value would get
+// different bits by where in a tile, or in how wide a lane, it is computed.
+#pragma clang fp contract(off)
+
 namespace convseq {
 
 using convfwd::from_f32;
