@@ -38,6 +38,9 @@ class KeptPtr(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("e", ctypes.c_void_p)]
 
 
+_Kept3 = KeptPtr * 3
+
+
 class ConvDesc(ctypes.Structure):
     """Mirror of convseq_conv_desc."""
     _fields_ = [(n, ctypes.c_int32) for n in ("b", "t", "c", "k", "act", "dtype")]
@@ -133,7 +136,7 @@ def _sequence(x, what, like=None, dims=3):
     if like is None:
         if x.dtype not in _DTYPES:
             raise TypeError(f"unsupported dtype {x.dtype}")
-    elif x.shape != like.shape or x.dtype != like.dtype or x.device != like.device:
+    elif x.shape != like.shape or x.dtype is not like.dtype or x.device != like.device:
         raise ValueError(f"{what} must be {like.dtype} of shape {tuple(like.shape)} on {like.device}, "
                          f"got {x.dtype} {tuple(x.shape)} on {x.device}")
     return x if x.stride(-1) == 1 or x.shape[-1] == 1 and x.is_contiguous() else x.contiguous()
@@ -168,10 +171,11 @@ def _kept_input(p, shape, device, what):
     """An input given in 8 bits, standing for a (B, T, C) tensor: its C struct."""
     b, t, c = shape
     groups = -(-t // GROUP_ROWS)
-    held = p.shape[0] if len(p.shape) == 2 else math.prod(p.shape[1:-1])
-    if held != t or p.q.shape != (b, groups, 2, c, GROUP_ROWS // 2) or p.e.shape != (b, groups, c) or p.q.dtype != torch.int8 \
-            or p.e.dtype != torch.uint8 or p.q.device != device or p.e.device != device \
-            or not p.q.is_contiguous() or not p.e.is_contiguous():
+    q, e, held = p.q, p.e, p.shape
+    held = held[1] if len(held) == 3 else held[0] if len(held) == 2 else math.prod(held[1:-1])
+    if held != t or q.shape != (b, groups, 2, c, GROUP_ROWS // 2) or e.shape != (b, groups, c) \
+            or q.dtype is not torch.int8 or e.dtype is not torch.uint8 or q.device != device or e.device != device \
+            or not q.is_contiguous() or not e.is_contiguous():
         raise ValueError(f"{what} in 8 bits must stand for a tensor of shape {tuple(shape)} on {device}")
     return p
 
@@ -202,15 +206,18 @@ def _new_kept(x, shape):
     """Room for x (B, T, C) in 8 bits, as the tensor of the given shape."""
     b, t, c = x.shape
     groups = -(-t // GROUP_ROWS)
-    return Packed8(torch.empty((b, groups, 2, c, GROUP_ROWS // 2), dtype=torch.int8, device=x.device),
-                   torch.empty((b, groups, c), dtype=torch.uint8, device=x.device), shape, x.dtype)
+    return Packed8(x.new_empty((b, groups, 2, c, GROUP_ROWS // 2), dtype=torch.int8),
+                   x.new_empty((b, groups, c), dtype=torch.uint8), shape, x.dtype)
+
+
+def _kept_ptr(p):
+    """One convseq_kept, NULL for none."""
+    return None if p is None else KeptPtr(p.q.data_ptr(), p.e.data_ptr())
 
 
 def _kept_ptrs(kept):
-    """A C array of convseq_kept, NULL for none."""
-    if kept is None:
-        return None
-    return (KeptPtr * len(kept))(*(KeptPtr(p.q.data_ptr(), p.e.data_ptr()) for p in kept))
+    """A C array of three convseq_kept, NULL for none."""
+    return None if kept is None else _Kept3(*[(p.q.data_ptr(), p.e.data_ptr()) for p in kept])
 
 
 def _call(x, fn, *args):
@@ -231,7 +238,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _workspace(n_bytes, x):
-    return torch.empty(_check(n_bytes), dtype=torch.uint8, device=x.device) if n_bytes else None
+    return x.new_empty(_check(n_bytes), dtype=torch.uint8) if n_bytes else None
 
 
 # ---- causal depthwise convolution ---------------------------------------------------------------
@@ -255,7 +262,7 @@ def seq_conv(x, w, bias=None, activation=None, state=None, starts=None, keep8=Fa
     kept = _new_kept(x, x.shape) if keep8 else None
     d = ConvDesc(b, t, c, k, act, _DTYPES[x.dtype])
     _call(x, _seq().convseq_conv_fwd, d, _rows(x), w.data_ptr(), _ptr(bias), _ptr(state), _ptr(starts), y.data_ptr(),
-          last.data_ptr(), _kept_ptrs((kept,) if keep8 else None))
+          last.data_ptr(), _kept_ptr(kept))
     return SeqConv(y, last, kept)
 
 
@@ -272,12 +279,12 @@ def seq_conv_bwd(dy, x, w, bias=None, activation=None, state=None, starts=None, 
     dlast = _dense(dstate, (b, k - 1, c), dy.dtype, dy.device, "dstate")
     starts = _starts(starts, b, t, dy.device)
     dx = dy.new_empty((b, t, c))
-    dw = torch.empty((c, k), dtype=torch.float32, device=dy.device)
-    db = None if bias is None else torch.empty((c,), dtype=torch.float32, device=dy.device)
+    dw = dy.new_empty((c, k), dtype=torch.float32)
+    db = None if bias is None else dy.new_empty((c,), dtype=torch.float32)
     dfirst = None if state is None else torch.empty_like(state)
     d = ConvDesc(b, t, c, k, act, _DTYPES[dy.dtype])
     work = _workspace(_seq().convseq_conv_bwd_workspace(d), dy)
-    _call(dy, _seq().convseq_conv_bwd, d, _rows(dy), None if packed else _rows(x), _kept_ptrs((x,) if packed else None),
+    _call(dy, _seq().convseq_conv_bwd, d, _rows(dy), None if packed else _rows(x), _kept_ptr(x if packed else None),
           w.data_ptr(), _ptr(bias), _ptr(state), _ptr(starts), _ptr(dlast), dx.data_ptr(), dw.data_ptr(), _ptr(db),
           _ptr(dfirst), _ptr(work))
     return SeqConvGrad(dx, dw, db, dfirst)
@@ -335,8 +342,8 @@ def gated_scan(x, gate_r, gate_i, lam, decay=8.0, h0=None, starts=None, train=Fa
     starts = _starts(starts, b, t, x.device)
     y = x.new_empty((b, t, c)) if out is None \
         else _out(out, (b, t, c), x.dtype, x.device, "out")
-    h = torch.empty((b, c), dtype=torch.float32, device=x.device)
-    states = torch.empty((b, -(-t // STATE_ROWS), c), dtype=torch.float32, device=x.device) if train else None
+    h = x.new_empty((b, c), dtype=torch.float32)
+    states = x.new_empty((b, -(-t // STATE_ROWS), c), dtype=torch.float32) if train else None
     kept = tuple(_new_kept(x, x.shape) for _ in range(3)) if keep8 else None
     d = ScanDesc(b, t, c, _DTYPES[x.dtype], decay)
     work = _workspace(_seq().convseq_scan_fwd_workspace(d), x)
@@ -364,8 +371,8 @@ def gated_scan_bwd(dy, x, gate_r, gate_i, lam, states, decay=8.0, starts=None, d
     dh = _dense(dh, (b, c), torch.float32, dy.device, "dh")
     starts = _starts(starts, b, t, dy.device)
     dx, dr, di = (dy.new_empty((b, t, c)) for _ in range(3))
-    dlam = torch.empty((c,), dtype=torch.float32, device=dy.device)
-    dh0 = torch.empty((b, c), dtype=torch.float32, device=dy.device)
+    dlam = dy.new_empty((c,), dtype=torch.float32)
+    dh0 = dy.new_empty((b, c), dtype=torch.float32)
     d = ScanDesc(b, t, c, _DTYPES[dy.dtype], decay)
     rows = (None,) * 3 if packed else tuple(_rows(v) for v in ins)
     work = _workspace(_seq().convseq_scan_bwd_workspace(d), dy)
@@ -411,7 +418,7 @@ def pack8(x) -> Packed8:
     rows = _sequence(x if x.dim() == 3 else x[None] if x.dim() == 2 else x.flatten(1, -2), "x")
     b, t, c = rows.shape
     kept = _new_kept(rows, shape)
-    _call(rows, _seq().convseq_pack8, b, t, c, _DTYPES[rows.dtype], _rows(rows), _kept_ptrs((kept,)))
+    _call(rows, _seq().convseq_pack8, b, t, c, _DTYPES[rows.dtype], _rows(rows), _kept_ptr(kept))
     return kept
 
 
@@ -425,7 +432,6 @@ def unpack8(p: Packed8, dtype=None, out=None) -> torch.Tensor:
     shape, c = p.shape, p.shape[-1]
     b, t = (1, shape[0]) if len(shape) == 2 else (shape[0], math.prod(shape[1:-1]))
     _kept_input(p, (b, t, c), p.q.device, "p")
-    y = torch.empty(shape, dtype=dtype, device=p.q.device) if out is None \
-        else _out(out, shape, dtype, p.q.device, "out")
-    _call(p.q, _seq().convseq_unpack8, b, t, c, _DTYPES[dtype], _kept_ptrs((p,)), y.data_ptr())
+    y = p.q.new_empty(shape, dtype=dtype) if out is None else _out(out, shape, dtype, p.q.device, "out")
+    _call(p.q, _seq().convseq_unpack8, b, t, c, _DTYPES[dtype], _kept_ptr(p), y.data_ptr())
     return y

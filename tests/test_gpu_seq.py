@@ -321,8 +321,8 @@ class _Guarded:
     def empty_like(self, t):
         return self.empty(t.shape, t.dtype, t.device)
 
-    def new_empty(self, t, shape):
-        return self.empty(shape, t.dtype, t.device)
+    def new_empty(self, t, shape, dtype=None):
+        return self.empty(shape, t.dtype if dtype is None else dtype, t.device)
 
     def check(self):
         for raw, n in self.whole:
@@ -335,7 +335,7 @@ class _Guarded:
 def test_nothing_is_written_outside_the_outputs(monkeypatch, dtype, b, t, c, starts, state):
     guard = _Guarded()
     monkeypatch.setattr(sequence, "torch", guard)
-    monkeypatch.setattr(torch.Tensor, "new_empty", lambda self, shape: guard.new_empty(self, shape))
+    monkeypatch.setattr(torch.Tensor, "new_empty", lambda self, shape, dtype=None: guard.new_empty(self, shape, dtype))
     x, w, bias, st = _conv_inputs(dtype, b, t, c, 4, state)
     s = starts_of(starts, b, t, DEV)
     xs, gr, gi, lam, h0 = scan_inputs(t, b, t, c, DT[dtype], DEV, state)
