@@ -54,16 +54,27 @@ __global__ __launch_bounds__(kWaves * 64, V == 1 ? 6 : 4) void seq_scan_bwd_kern
   P ry[kRows], raw[3][kRows];
   Half<V> q[3];
   float scale[3][V];
-  const uint32_t offset = (uint32_t)chl * sizeof(T);
-  const T* py = (const T*)a.dy.p + b * a.dy.sb;
-  const Rows* rows[3] = {&a.x, &a.r, &a.i};
+  // rows past the last read it again
+  const int64_t row = min(t0, a.t - 1);
+  const auto walk = [&](const Rows& r) {
+    return RowWalk((const T*)r.p + b * r.sb + row * r.st, r.st * (int64_t)sizeof(T));
+  };
+  {
+    uint32_t offset = (uint32_t)chl * sizeof(T);
+    renew(offset);
+    RowWalk wy = walk(a.dy), wx = walk(a.x), wr = walk(a.r), wi = walk(a.i);
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    const int64_t t = min(t0 + j, a.t - 1);  // rows past the last read it again
-    ry[j] = load_at<P>(py + t * a.dy.st, offset);
-    if (!KEPT)
-#pragma unroll
-      for (int k = 0; k < 3; ++k) raw[k][j] = load_at<P>((const T*)rows[k]->p + b * rows[k]->sb + t * rows[k]->st, offset);
+    for (int j = 0; j < kRows; ++j) {
+      ry[j] = wy.load<P>(offset);
+      wy.step(j + 1 < n);
+      if (KEPT) continue;
+      raw[0][j] = wx.load<P>(offset);
+      raw[1][j] = wr.load<P>(offset);
+      raw[2][j] = wi.load<P>(offset);
+      wx.step(j + 1 < n);
+      wr.step(j + 1 < n);
+      wi.step(j + 1 < n);
+    }
   }
   if (KEPT) {
     const int groups = (a.t + kGroup - 1) / kGroup;
@@ -216,10 +227,14 @@ __global__ __launch_bounds__(kWaves * 64, V == 1 ? 6 : 4) void seq_scan_bwd_kern
     renew(rate[i].u);
     renew(rate[i].log2);
   }
-  if (own) {
+  const auto run_up = [&](auto whole) {
+    uint32_t offset = (uint32_t)ch * sizeof(T);
+    renew(offset);
+    const int64_t end = out + (int64_t)(kRows - 1) * a.c, up = -(int64_t)a.c * (int64_t)sizeof(T);
+    RowWalk px((T*)a.dx + end, up), pr((T*)a.dr + end, up), pi((T*)a.di + end, up);
 #pragma unroll
-    for (int j = kRows - 1; j >= 0; --j)
-      if (j < n) {
+    for (int j = kRows - 1; j >= 0; --j) {
+      if (decltype(whole)::value || j < n) {
         P dx, dr, di;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -235,10 +250,21 @@ __global__ __launch_bounds__(kWaves * 64, V == 1 ? 6 : 4) void seq_scan_bwd_kern
           sum[i] += e;
           c[i] = STARTS && (first >> j & 1) ? 0.f : ga;
         }
-        store_at((T*)a.dx + out + (int64_t)j * a.c, offset, dx);
-        store_at((T*)a.dr + out + (int64_t)j * a.c, offset, dr);
-        store_at((T*)a.di + out + (int64_t)j * a.c, offset, di);
+        px.store(offset, dx);
+        pr.store(offset, dr);
+        pi.store(offset, di);
       }
+      px.step();
+      pr.step();
+      pi.step();
+      if (decltype(whole)::value) __builtin_amdgcn_sched_barrier(0);  // rows worked on together cost registers
+    }
+  };
+  if (own) {
+    if (n == kRows)
+      run_up(Yes{});
+    else
+      run_up(No{});
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) sums[wave][lane * V + i] = sum[i];

@@ -26,7 +26,7 @@ constexpr int kWaves = 8;
 constexpr int kTile = kWaves * kGroup;  // rows
 
 template <typename T, bool STARTS, bool KEEP>
-__global__ __launch_bounds__(kWaves * 64, 6) void seq_scan_fwd_kernel(ScanArgs a, int cols, int tiles) {
+__global__ __launch_bounds__(kWaves * 64, KEEP ? 6 : 8) void seq_scan_fwd_kernel(ScanArgs a, int cols, int tiles) {
   __shared__ Carry totals[kWaves][64];
   __shared__ float entry[64], rates[64];
   __shared__ Gathered<1, kWaves> gathered;
@@ -45,17 +45,25 @@ __global__ __launch_bounds__(kWaves * 64, 6) void seq_scan_fwd_kernel(ScanArgs a
   const int t0 = tile * kTile + wave * kGroup;
   const int n = min(max(a.t - t0, 0), kGroup);  // rows of this wave
 
-  const uint32_t offset = (uint32_t)chl * sizeof(T);
-  const T* px = (const T*)a.x.p + b * a.x.sb;
-  const T* pr = (const T*)a.r.p + b * a.r.sb;
-  const T* pi = (const T*)a.i.p + b * a.i.sb;
+  // rows past the last read it again
+  const int64_t row = min(t0, a.t - 1);
+  const auto walk = [&](const Rows& r) {
+    return RowWalk((const T*)r.p + b * r.sb + row * r.st, r.st * (int64_t)sizeof(T));
+  };
   P rx[kGroup], rr[kGroup], ri[kGroup];
+  {
+    uint32_t offset = (uint32_t)chl * sizeof(T);
+    renew(offset);
+    RowWalk wx = walk(a.x), wr = walk(a.r), wi = walk(a.i);
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j) {
-    const int64_t t = min(t0 + j, a.t - 1);  // rows past the last read it again
-    rx[j] = load_at<P>(px + t * a.x.st, offset);
-    rr[j] = load_at<P>(pr + t * a.r.st, offset);
-    ri[j] = load_at<P>(pi + t * a.i.st, offset);
+    for (int j = 0; j < kGroup; ++j) {
+      rx[j] = wx.load<P>(offset);
+      rr[j] = wr.load<P>(offset);
+      ri[j] = wi.load<P>(offset);
+      wx.step(j + 1 < n);
+      wr.step(j + 1 < n);
+      wi.step(j + 1 < n);
+    }
   }
   uint32_t first = 0;  // bit j: row t0 + j begins a sequence
   if (STARTS) first = (uint32_t)__ballot(lane < n && a.starts[(int64_t)b * a.t + t0 + lane]);
@@ -130,15 +138,24 @@ __global__ __launch_bounds__(kWaves * 64, 6) void seq_scan_fwd_kernel(ScanArgs a
     const int pieces = (a.t + kEvery - 1) / kEvery;
     store_at(a.states + ((int64_t)b * pieces + t0 / kEvery) * a.c, (uint32_t)ch * 4, h);
   }
-  T* y = (T*)a.y + ((int64_t)b * a.t + t0) * a.c;
+  const auto store_rows = [&](auto whole) {
+    uint32_t offset = (uint32_t)ch * sizeof(T);
+    renew(offset);
+    RowWalk y((T*)a.y + ((int64_t)b * a.t + t0) * a.c, (int64_t)a.c * sizeof(T));
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j)
-    if (j < n) {
-      h = STARTS && (first >> j & 1) ? in[j] : fmaf(av[j], h, in[j]);
-      P v;
-      v.set(0, h);
-      store_at(y + (int64_t)j * a.c, offset, v);
-    }
+    for (int j = 0; j < kGroup; ++j)
+      if (decltype(whole)::value || j < n) {
+        h = STARTS && (first >> j & 1) ? in[j] : fmaf(av[j], h, in[j]);
+        P v;
+        v.set(0, h);
+        y.store(offset, v);
+        y.step();
+      }
+  };
+  if (n == kGroup)
+    store_rows(Yes{});
+  else
+    store_rows(No{});
 }
 
 // No rows: the state passes through.

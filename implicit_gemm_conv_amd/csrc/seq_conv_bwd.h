@@ -40,7 +40,7 @@ __global__ __launch_bounds__(kWaves * 64, K * V <= 8 ? 4 : 2) void seq_conv_bwd_
   __shared__ float sums[kWaves][64 * V];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int groups = (a.t + kGroup - 1) / kGroup;
-  const int id = blockIdx.x / cols, b = id / blocks;
+  const int id = blockIdx.x / cols, b = __builtin_amdgcn_readfirstlane(id / blocks);
   const int piece = __builtin_amdgcn_readfirstlane(id % blocks * kWaves + wave);
   const int chs = ((int)(blockIdx.x % cols) * 64 + lane) * V;
   const bool own = chs < a.c;
@@ -105,11 +105,16 @@ __global__ __launch_bounds__(kWaves * 64, K * V <= 8 ? 4 : 2) void seq_conv_bwd_
     Chunk<T, V, KEPT> now, next;
     const auto load = [&](int g0, Chunk<T, V, KEPT>& to) {
       const int n = min(end - g0, kChunk);
+      uint32_t from = offset;
+      renew(from);
+      RowWalk wy(dy + (int64_t)g0 * a.dy.st, a.dy.st * (int64_t)sizeof(T));
+      RowWalk wx(x + (int64_t)g0 * a.x.st, a.x.st * (int64_t)sizeof(T));
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const int64_t t = g0 + min(j, n - 1);
-        to.dy[j] = load_at<P>(dy + t * a.dy.st, offset);
-        if (!KEPT) to.x[j] = load_at<P>(x + t * a.x.st, offset);
+      for (int j = 0; j < kChunk; ++j) {  // rows past the last repeat it
+        to.dy[j] = wy.load<P>(from);
+        if (!KEPT) to.x[j] = wx.load<P>(from);
+        wy.step(j + 1 < n);
+        wx.step(j + 1 < n);
       }
       if (KEPT) {
         const int64_t at = (int64_t)b * groups + g0 / kGroup;
@@ -165,7 +170,9 @@ __global__ __launch_bounds__(kWaves * 64, K * V <= 8 ? 4 : 2) void seq_conv_bwd_
               P out;
 #pragma unroll
               for (int i = 0; i < V; ++i) out.set(i, acc[0][i]);
-              store_at((T*)a.dx + ((int64_t)b * a.t + g0 + j - (K - 1)) * a.c, offset, out);
+              uint32_t to = offset;
+              renew(to);
+              RowWalk((T*)a.dx + ((int64_t)b * a.t + g0 + j - (K - 1)) * a.c, 0).store(to, out);
             }
             // row by row: rows worked on together cost registers
             if (!masked) __builtin_amdgcn_sched_barrier(0);

@@ -33,6 +33,20 @@ __device__ __forceinline__ T rounded(float f) {
   return from_f32<T>(f);
 }
 
+// An access of 2 to 16 bytes as a plain type.
+template <int N>
+struct Words {
+  typedef uint32_t type __attribute__((ext_vector_type(N / 4)));
+};
+template <>
+struct Words<2> {
+  typedef uint16_t type;
+};
+template <>
+struct Words<4> {
+  typedef uint32_t type;
+};
+
 // ---- V neighbouring channels of a row as one access ----
 template <typename T, int V>
 struct Pack;  // V * sizeof(T) bytes
@@ -68,7 +82,8 @@ __device__ __forceinline__ void renew(P& p) {
 
 // An access at a wave-uniform base and a lane's byte offset of 32 bits, which the
 // hardware adds itself: no 64-bit address a lane and row has to be computed and
-// held.
+// held.  The compiler sees that it may do so where the offset's widening stands in
+// the same block of code: renew() the offset at the start of a block of accesses.
 template <typename P>
 __device__ __forceinline__ P load_at(const void* base, uint32_t offset) {
   return *(const P*)((const char*)base + offset);
@@ -77,6 +92,37 @@ template <typename P>
 __device__ __forceinline__ void store_at(void* base, uint32_t offset, const P& v) {
   *(P*)((char*)base + offset) = v;
 }
+
+// Walks over rows `stride` bytes apart, one scalar addition a row.  The row's
+// pointer is pinned to scalar registers: otherwise the compiler adds the lane's
+// offset first and steps the sums, a 64-bit vector addition and a register pair a
+// row.  (It is typed as global memory because the pinning hides where it came from.)
+struct RowWalk {
+  typedef __attribute__((address_space(1))) char* Global;
+  Global at;
+  int64_t stride;
+  __device__ __forceinline__ RowWalk(const void* first, int64_t stride_) : at((Global)(uintptr_t)first), stride(stride_) {}
+  // a step that is not taken repeats the row; one path for both, so that the loads
+  // stay together where they are issued
+  __device__ __forceinline__ void step(bool taken = true) { at += taken ? stride : 0; }
+  template <typename P>
+  __device__ __forceinline__ P load(uint32_t offset) {
+    typedef typename Words<sizeof(P)>::type W;
+    asm("" : "+s"(at));
+    const W w = *(const __attribute__((address_space(1))) W*)(at + offset);
+    P v;
+    __builtin_memcpy(&v, &w, sizeof(P));
+    return v;
+  }
+  template <typename P>
+  __device__ __forceinline__ void store(uint32_t offset, const P& v) {
+    typedef typename Words<sizeof(P)>::type W;
+    asm("" : "+s"(at));
+    W w;
+    __builtin_memcpy(&w, &v, sizeof(P));
+    *(__attribute__((address_space(1))) W*)(at + offset) = w;
+  }
+};
 
 // ---- 8-bit groups ----
 // Byte of a group whose largest magnitude has the float bits `top` (sign
