@@ -11,7 +11,8 @@
 // registers, are added over the 4 waves of the workgroup (4 consecutive pieces
 // of the same channels) in LDS and over the workgroups by a second kernel, both
 // in a fixed order.  Memory bound: dy and x (or its 8 bits) read once, dx
-// written once.
+// written once; 4x4096x2048 bf16 from 8 bits takes 44.6 us, the vector ALU busy
+// 60% of it.
 #pragma once
 
 #include "seq_conv.h"
@@ -33,7 +34,7 @@ struct Chunk {
 };
 
 // Four waves a SIMD (128 registers) where the windows leave room for it: at three
-// 4x4096x2048 bf16 takes 60 us instead of 50.
+// 4x4096x2048 bf16 from 8 bits takes 57 us instead of 44.6.
 template <typename T, int K, int V, bool KEPT>
 __global__ __launch_bounds__(kWaves * 64, K * V <= 8 ? 4 : 2) void seq_conv_bwd_kernel(ConvArgs a, int cols, int blocks, int per) {
   typedef Pack<T, V> P;
