@@ -17,10 +17,13 @@
 // overwrites, gives up after kSpins and puts NaN into the results.)  One counter
 // for all columns would cost 3 us where a few hundred workgroups start at once.
 //
-// Words and flags are written and read with relaxed device-wide atomics.  A
-// word carries value and presence in one access (A's bits are zero until it is
-// there), so no fence is needed.  The flags, one a tile and column, only say
-// where to look: a wave reads those of 64 tiles at once, and polling them
+// Words and flags are written and read with relaxed device-wide atomics, in no
+// order between them.  A word says by itself, in one access, whether it is there
+// (A's bits are zero until then) and whether it is a whole state (A's sign), so no
+// fence is needed: a reader that wants a whole state waits until the word is one,
+// whatever the flag said, since the flag may be seen before the word that it
+// announces and the tile's step, published earlier, still be in its place.  The
+// flags, one a tile and column, only say where to look: a wave reads those of 64 tiles at once, and polling them
 // instead of the words keeps the waiting off the memory the tiles stream
 // through (words of 32 tiles polled by all waves: 174 us for an early 1x65539x1024
 // bf16 forward, 4 at a time by one wave: 155).
@@ -135,7 +138,8 @@ __device__ __forceinline__ void look_back(const uint64_t* words, int64_t step, c
   lds_barrier();
   const int span = __builtin_amdgcn_readfirstlane(sh.span);
   const bool lost = span < 0;
-  for (int from = tile - max(span, 0); from < tile; from += WAVES * kEach) {
+  const int oldest = tile - max(span, 0);  // the one that has to be a whole state
+  for (int from = oldest; from < tile; from += WAVES * kEach) {
     const int count = min(tile - from, WAVES * kEach);
     uint64_t w[kEach][V];
     for (int spins = 0;;) {
@@ -150,7 +154,8 @@ __device__ __forceinline__ void look_back(const uint64_t* words, int64_t step, c
       for (int j = 0; j < kEach; ++j)
         if (j * WAVES + wave < count) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) there &= (uint32_t)w[j][i] != 0u;
+          for (int i = 0; i < V; ++i)
+            there &= from + j * WAVES + wave == oldest ? (int)(uint32_t)w[j][i] < 0 : (uint32_t)w[j][i] != 0u;
         }
       if (__all(there)) break;
       if (++spins > kSpins) {  // gives up: a whole state of NaN
