@@ -11,14 +11,12 @@
 // the recurrence over the a and m i x it still holds.  Each input is read once
 // and y written once: memory bound, 4 elements a value.
 //
-// 1x65539x1024 bf16 takes 122 us (4.4 TB/s, where a copy reaches 5.1), 4x4096x2048
-// with 8 bits kept 99 us, the vector ALU busy 60% of it.  One channel a lane: its
+// 1x65539x1024 bf16 takes 125 us (4.3 TB/s, where a copy reaches 5.1), 4x4096x2048
+// with 8 bits kept 95 to 99 us, the vector ALU busy 58% of it.  One channel a lane: its
 // registers let four workgroups (three with 8 bits) share a compute unit and cover
-// each other's waits.  Side by side, before the fourth fitted, two channels a lane
-// (two workgroups) took 142 us instead of 140 and 101 instead of 97; three instead of
-// four take 127 instead of 122.  Tiles of 64 rows take 190 us instead of 122 on the
-// one long sequence, which has twice the tiles to look back over, and 95 instead of
-// 99 on the other.
+// each other's waits; three for four costs 1% (126 us for 125).  Tiles of 64 rows
+// take 190 us on the one long sequence, which has twice the tiles to look back over,
+// and 93 on the other.
 #include "seq_carry.h"
 
 namespace convseq {
@@ -38,7 +36,7 @@ __global__ __launch_bounds__(kWaves * 64, KEEP ? 6 : 8) void seq_scan_fwd_kernel
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   // turned by one a tile row: each column's tiles go to all 8 dies, not to one of
-  // them (1x65539x1024 bf16: 122 us instead of 176)
+  // them (1x65539x1024 bf16: 125 us instead of 199)
   const int columns = cols * a.b, column = (blockIdx.x + blockIdx.x / columns) % columns;
   const int tile = tiles > 1 ? take_ticket(a.work, column, &ticket) : 0;
   const int b = column / cols;

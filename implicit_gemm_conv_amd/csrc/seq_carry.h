@@ -25,8 +25,8 @@
 // announces and the tile's step, published earlier, still be in its place.  The
 // flags, one a tile and column, only say where to look: a wave reads those of 64 tiles at once, and polling them
 // instead of the words keeps the waiting off the memory the tiles stream
-// through (words of 32 tiles polled by all waves: 174 us for an early 1x65539x1024
-// bf16 forward, 4 at a time by one wave: 155).
+// through (words of 32 tiles polled by all waves took an early 1x65539x1024 bf16
+// forward 174 us, 4 at a time by one wave 155).
 #pragma once
 
 #include "seq_device.h"
