@@ -136,7 +136,7 @@ __global__ __launch_bounds__(kWaves * 64, V == 1 ? 6 : 4) void seq_scan_bwd_kern
         kv[j][i] = g.a * rs * v;
         if (!begins) kv[j][i] -= step[i].h;
         const float h = fmaf(g.a, step[i].h, in);
-        step[i] = Carry{begins ? -0.f : step[i].a * g.a, begins ? in : h};
+        step[i] = Carry{begins ? -0.f : positive(step[i].a * g.a), begins ? in : h};
         // rows from a start on send nothing up (asked of the starts, not of the
         // product, which a NaN behind the start may have taken)
         if (!STARTS || (first & ((2u << j) - 1u)) == 0) sent[i] = fmaf(step[i].a, ry[j].get(i), sent[i]);
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(kWaves * 64, V == 1 ? 6 : 4) void seq_scan_bwd_kern
 #pragma unroll
         for (int i = 0; i < V; ++i) {
           const float g = ry[j].get(i) + c[i];
-          const float gm = g * mi[j][i], ga = g * __builtin_amdgcn_exp2f(rate[i].log2 * rv[j][i]);
+          const float gm = g * mi[j][i], ga = g * positive(__builtin_amdgcn_exp2f(rate[i].log2 * rv[j][i]));
           // x (1 - i), x's power of two in the subtraction's place
           const float xi = KEPT ? q[0].get(i, j) * fmaf(-scale[0][i], iv[j][i], scale[0][i])
                                 : raw[0][j].get(i) * (1.f - iv[j][i]);

@@ -98,6 +98,8 @@ __global__ __launch_bounds__(kWaves * 64, KEEP ? 6 : 8) void seq_scan_fwd_kernel
       total = Carry{begins ? -0.f : total.a * g.a, begins ? in[j] : h};
     }
 
+  total.a = positive(total.a);
+
   // the waves' totals; before = what the waves above do to the state
   totals[wave][lane] = total;
   lds_barrier();

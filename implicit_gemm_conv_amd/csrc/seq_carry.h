@@ -1,7 +1,8 @@
 // seq_carry.h -- the state of a recurrence h -> A h + H carried between tiles
 // of one launch.
 //
-// A piece of rows acts on the state before it as h -> A h + H with A in [0, 1].
+// A piece of rows acts on the state before it as h -> A h + H with A in (0, 1]:
+// a product that fp32 would round to zero is its smallest number (positive()).
 // A piece that holds a start forgets that state: its A is stored with the sign
 // bit set (forgets()), H is its own, and selections, not products with zero,
 // keep a NaN from crossing.
@@ -45,13 +46,14 @@ __device__ __forceinline__ bool forgets(float a) { return (int)__float_as_uint(a
 
 // first, then second
 __device__ __forceinline__ Carry compose(Carry first, Carry second) {
-  return forgets(second.a) ? second : Carry{first.a * second.a, fmaf(second.a, first.h, second.h)};
+  return forgets(second.a) ? second : Carry{positive(first.a * second.a), fmaf(second.a, first.h, second.h)};
 }
 __device__ __forceinline__ float apply(Carry c, float h) { return forgets(c.a) ? c.h : fmaf(c.a, h, c.h); }
 
 __device__ __forceinline__ void publish(uint64_t* word, Carry c) {
-  const uint32_t a = max(__float_as_uint(c.a), 1u);  // A = 0 as the smallest number: bits zero mean absent
-  __hip_atomic_store(word, (uint64_t)__float_as_uint(c.h) << 32 | a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // A is positive or has its sign set: bits zero mean absent
+  __hip_atomic_store(word, (uint64_t)__float_as_uint(c.h) << 32 | __float_as_uint(c.a), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ uint64_t peek(const uint64_t* word) {
   return __hip_atomic_load(word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

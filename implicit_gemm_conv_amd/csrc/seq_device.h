@@ -289,6 +289,12 @@ __device__ __forceinline__ float one_minus_square(float u, float a) {
   return u < 0.125f ? u * p : fmaf(-a, a, 1.f);
 }
 
+// a and its products are positive numbers, and are kept so where fp32 would round
+// them to zero (to 2^-149, its smallest number): an infinite state stays infinite
+// instead of becoming NaN, and every reader of a product computes with the same
+// one.  A sign bit, and a NaN, stay as they are.
+__device__ __forceinline__ float positive(float a) { return __uint_as_float(max(__float_as_uint(a), 1u)); }
+
 // The gates of one value; x2 are the logits times -log2 e.
 struct Gate {
   float r, i, a, t;  // a = e^-u, t = 1 - a^2
@@ -297,7 +303,7 @@ __device__ __forceinline__ Gate gates(float r2, float i2, const Rate& rate) {
   Gate g;
   g.r = sigmoid2(r2);
   g.i = sigmoid2(i2);
-  g.a = __builtin_amdgcn_exp2f(rate.log2 * g.r);
+  g.a = positive(__builtin_amdgcn_exp2f(rate.log2 * g.r));
   g.t = one_minus_square(rate.u * g.r, g.a);
   return g;
 }

@@ -124,6 +124,8 @@ typedef struct {
  * h_t = a * h_{t-1} + sqrt(1 - a^2) * i * x_t,  y = h
  *
  * with h_{-1} = h0[b,c] (fp32; zeros if NULL) and h_{t-1} absent at a start.
+ * a and its products are positive and count as 2^-149 where fp32 would round
+ * them to zero: an infinite state, or state's gradient, stays infinite.
  * y (B, T, C), h_last (B, C) fp32 (may be NULL), states (B, ceil(T/64), C)
  * fp32 (may be NULL): the h before rows 0, 64, 128, ..., from which the
  * backward pass starts each piece.  kept (may be NULL): x, gate_r and gate_i in
