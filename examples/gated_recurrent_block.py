@@ -64,7 +64,9 @@ class GatedRecurrentBlock:
                 torch.zeros((streams, c), device=device))
 
     def forward(self, u, state=None, starts=None, train=False):
-        """y, the state after the last row, and with train what backward needs."""
+        """y, the state after the last row, and with train what backward needs (the carried rows of
+        `state` among it, not a copy of them).  Training takes `state` as given: backward returns
+        no gradient of it, so none goes back into the piece before."""
         w = self._weights()
         rows, h0 = state if state is not None else (None, None)
         p = project(u, w["w_in"])
@@ -72,13 +74,13 @@ class GatedRecurrentBlock:
         gate_r, gate_i = project(f.y, w["w_gates"]).chunk(2, dim=-1)
         s = igc.gated_scan(f.y, gate_r, gate_i, w["lam"], decay=self.decay, h0=h0, starts=starts, train=train,
                            keep8=train)
-        kept = (igc.pack8(u), f.kept, s.kept, s.states, igc.pack8(s.y), starts) if train else None
+        kept = (igc.pack8(u), f.kept, s.kept, s.states, igc.pack8(s.y), rows, starts) if train else None
         return project(s.y, w["w_out"]), (f.state, s.h), kept
 
     def backward(self, dy, kept):
         """Gradients of the parameters and of u, from activations that were kept in 8 bits."""
         w = self._weights()
-        u8, p8, scan8, states, h8, starts = kept
+        u8, p8, scan8, states, h8, rows, starts = kept
         g = {}
         dh, g["w_out"] = project_bwd(dy, igc.unpack8(h8), w["w_out"])
         s = igc.gated_scan_bwd(dh, *scan8, w["lam"], states, decay=self.decay, starts=starts)
@@ -86,7 +88,8 @@ class GatedRecurrentBlock:
         x = igc.unpack8(scan8[0])
         dgates = torch.cat([s.dgate_r, s.dgate_i], dim=-1)
         dx, g["w_gates"] = project_bwd(dgates, x, w["w_gates"])
-        c = igc.seq_conv_bwd(s.dx + dx, p8, w["w_conv"], bias=w["b_conv"], activation="silu", starts=starts)
+        c = igc.seq_conv_bwd(s.dx + dx, p8, w["w_conv"], bias=w["b_conv"], activation="silu", state=rows,
+                             starts=starts)
         g["w_conv"], g["b_conv"] = c.dw, c.dbias
         du, g["w_in"] = project_bwd(c.dx, igc.unpack8(u8), w["w_in"])
         return du, g
