@@ -14,9 +14,10 @@ namespace {
 
 int elem_bytes(int dtype) { return dtype == CONVFWD_F32 ? 4 : 2; }
 
-// Extents and type shared by every call.  A launch has at most one workgroup
-// per 16 rows and 64 channels, of at most 1024 threads, and a grid holds less
-// than 2^32 threads.
+// Extents and type shared by every call.  A launch over rows has at most one
+// workgroup per 16 rows and 64 channels, of at most 512 threads; one over
+// channels alone (the sums of the backward passes) 1024 threads per 32 channels
+// along x.  Each dimension of a grid holds less than 2^32 threads.
 int check_extents(int64_t b, int64_t t, int64_t c, int dtype) {
   if (b < 0 || t < 0 || c < 1) return CONVFWD_ERR_BAD_DESC;
   if (dtype != CONVFWD_F32 && dtype != CONVFWD_F16 && dtype != CONVFWD_BF16) return CONVFWD_ERR_UNSUPPORTED;
@@ -98,7 +99,7 @@ class Buffers {
     uintptr_t lo, hi;
     bool out;
   };
-  Range b_[24];  // the longest call adds 20
+  Range b_[24];  // the longest call adds 17
   int n_ = 0, rc_ = CONVFWD_OK;
 };
 

@@ -218,14 +218,14 @@ __global__ __launch_bounds__(kWaves * 64, K * V <= 8 ? 4 : 2) void seq_conv_bwd_
   }
 }
 
-// dw and dbias from the workgroups' parts: 32 channels of one tap a workgroup,
-// 32 threads a channel that each add every 32nd part, then the threads' sums in order.
+// dw and dbias from the workgroups' parts: 32 channels of one tap a workgroup (the
+// taps along the grid's y: along x, with 2^21 groups of channels, they would pass
+// its 2^32 threads), 32 threads a channel that each add every 32nd part, then the threads' sums in order.
 template <int K>
-__global__ __launch_bounds__(1024) void seq_conv_sum_kernel(const float* work, int64_t parts, int c, int cols, float* dw,
-                                                            float* db) {
+__global__ __launch_bounds__(1024) void seq_conv_sum_kernel(const float* work, int64_t parts, int c, float* dw, float* db) {
   __shared__ float s[32][33];
-  const int k = blockIdx.x / cols;
-  const int ch = (int)(blockIdx.x % cols) * 32 + (threadIdx.x & 31), turn = threadIdx.x >> 5;
+  const int k = blockIdx.y;
+  const int ch = (int)blockIdx.x * 32 + (threadIdx.x & 31), turn = threadIdx.x >> 5;
   float v = 0.f;
   if (ch < c)
     for (int64_t p = turn; p < parts; p += 32) v += work[(p * (K + 1) + k) * c + ch];
@@ -256,9 +256,8 @@ hipError_t run(const ConvArgs& a, hipStream_t s) {
       else
         hipLaunchKernelGGL((seq_conv_bwd_kernel<T, K, V, false>), grid, block, 0, s, a, cols, blocks, per);
     }
-    const int sums = (a.c + 31) / 32;
-    hipLaunchKernelGGL((seq_conv_sum_kernel<K>), dim3((unsigned)(sums * (a.dbias ? K + 1 : K))), dim3(1024), 0, s, a.work,
-                       parts, a.c, sums, a.dw, a.dbias);
+    hipLaunchKernelGGL((seq_conv_sum_kernel<K>), dim3((unsigned)((a.c + 31) / 32), a.dbias ? K + 1 : K), dim3(1024), 0, s,
+                       a.work, parts, a.c, a.dw, a.dbias);
     return hipGetLastError();
   });
 }

@@ -85,3 +85,22 @@ def test_states_that_vanish_give_the_same_bits():
     for _ in range(200):
         wrong += torch.stack([(g != w).any() for g, w in zip(run(), want)])
     assert wrong.tolist() == [0] * len(wrong)
+
+
+@pytest.mark.parametrize("c", [(1 << 24) + 1, 1 << 24])
+def test_sums_over_very_many_channels(c):
+    """8 taps and a bias of 2^24 channels: 2^19 groups of 32 channels, each with nine sums of 1024 threads, are
+    more threads than one dimension of a grid holds.  Small whole numbers: every sum has to be exact."""
+    t, k = 2, 8
+    gen = torch.Generator(DEV).manual_seed(c)
+
+    def whole(*shape):
+        return torch.randint(-3, 4, shape, generator=gen, device=DEV, dtype=torch.int8).half()
+
+    x, dy, w, bias, state = whole(1, t, c), whole(1, t, c), whole(c, k), whole(c), whole(1, k - 1, c)
+    g = igc.seq_conv_bwd(dy, x, w, bias, state=state)
+    rows = torch.cat([state, x], 1)[0]
+    for j in range(k):
+        assert torch.equal(g.dw[:, j], sum((dy[0, n] * rows[n + j]).float() for n in range(t))), j
+    assert torch.equal(g.dbias, dy[0].float().sum(0))
+    assert torch.equal(g.dx[0, 1], dy[0, 1] * w[:, 7]) and torch.equal(g.dx[0, 0], dy[0, 0] * w[:, 7] + dy[0, 1] * w[:, 6])
