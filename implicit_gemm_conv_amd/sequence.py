@@ -249,7 +249,8 @@ def seq_conv(x, w, bias=None, activation=None, state=None, starts=None, keep8=Fa
 
     x (B, T, C); w (C, K), K <= 8, and bias (C) of x's dtype; activation None or "silu"; state
     (B, K-1, C), the rows before x (zeros if None); starts (B, T), bool or uint8, marks rows that
-    begin a new sequence.  keep8 also writes x in 8 bits for the backward pass.
+    begin a new sequence.  keep8 also writes x in 8 bits for the backward pass, in groups of 16 rows
+    that starts do not divide: one NaN or infinity is NaN in all rows of its group there.
     """
     x = _sequence(x, "x")
     b, t, c = x.shape
@@ -333,7 +334,7 @@ def gated_scan(x, gate_r, gate_i, lam, decay=8.0, h0=None, starts=None, train=Fa
     """The gated linear recurrence h_t = a h_{t-1} + sqrt(1 - a^2) sigmoid(gate_i) x_t with
     a = exp(-decay softplus(lam) sigmoid(gate_r)), over x, gate_r, gate_i (B, T, C) of one dtype;
     lam (C) and h0 (B, C) fp32.  starts as for seq_conv.  train returns the states that
-    gated_scan_bwd needs, keep8 also x, gate_r and gate_i in 8 bits."""
+    gated_scan_bwd needs, keep8 also x, gate_r and gate_i in 8 bits (groups as for seq_conv)."""
     x = _sequence(x, "x")
     gate_r, gate_i = _sequence(gate_r, "gate_r", x), _sequence(gate_i, "gate_i", x)
     b, t, c = x.shape
@@ -411,7 +412,8 @@ def gated_scan_step(x, gate_r, gate_i, lam, h, decay=8.0, slots=None, h_out=None
 def pack8(x) -> Packed8:
     """x (B, ..., C) in 8 bits.  The dimensions between the first and the last are taken as one
     row axis (a channels-last image's positions); groups of 16 consecutive rows of a channel
-    share a power of two.  A 2-D x is one sequence of rows."""
+    share a power of two, and are read back as NaN if one of them is NaN or infinite.  A 2-D x is
+    one sequence of rows."""
     if x.dim() < 2:
         raise ValueError(f"x must have at least 2 dimensions, got shape {tuple(x.shape)}")
     shape = x.shape

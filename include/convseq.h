@@ -25,7 +25,10 @@
  *
  * starts (B, T), bytes, may be NULL: a nonzero byte marks a row that begins a
  * new sequence.  Nothing, NaN and infinities included, crosses a start, and a
- * start at row 0 shuts out the carried rows or state.
+ * start at row 0 shuts out the carried rows or state.  What a backward pass reads
+ * in 8 bits was made in groups of 16 rows that no start divides: there the
+ * sequences that share a group also share its power of two, and a NaN or an
+ * infinity in it makes all of its rows NaN, on both sides of a start.
  *
  * Ownership, streams and errors are those of convfwd.h: the caller owns every
  * buffer (workspaces included; their sizes come from the *_workspace calls,
@@ -66,7 +69,8 @@ typedef struct {
  * (b, t, c) is q[b, t/16, t%16/8, c, t%8] * 2^(e - 127).  With M the largest magnitude
  * of the group, e - 127 = max(floor(log2 M) - 6, -126) and q is x / 2^(e - 127)
  * rounded to nearest even within +-127.  A group that contains an infinity or
- * a NaN has e = 255 and is read back as NaN throughout.  q (B, ceil(T/16), 2,
+ * a NaN has e = 255 and is read back as NaN throughout, whatever starts lie in
+ * it.  q (B, ceil(T/16), 2,
  * C, 8) and e (B, ceil(T/16), C) are dense and q is 16-byte aligned; rows past
  * T are written as zero. */
 typedef struct {

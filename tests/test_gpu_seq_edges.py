@@ -104,3 +104,32 @@ def test_sums_over_very_many_channels(c):
         assert torch.equal(g.dw[:, j], sum((dy[0, n] * rows[n + j]).float() for n in range(t))), j
     assert torch.equal(g.dbias, dy[0].float().sum(0))
     assert torch.equal(g.dx[0, 1], dy[0, 1] * w[:, 7]) and torch.equal(g.dx[0, 0], dy[0, 0] * w[:, 7] + dy[0, 1] * w[:, 6])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+@pytest.mark.parametrize("t,at,end,c", [(100, 37, 46, 40), (700, 304, 320, 66), (300, 255, 262, 7)])
+def test_from_8_bits_sequences_part_at_groups(bad, t, at, end, c):
+    """Rows at .. end - 1 of one sequence hold NaN or infinities.  From 8 bits the groups of 16 rows that hold one
+    are NaN whole; sequences that have no row in those groups do not notice."""
+    b, lo, hi = 2, at // 16 * 16, -(-end // 16) * 16
+    x, gr, gi, dy = (normal(t + k, (b, t, c), torch.bfloat16, 1.0, DEV) for k in range(4))
+    w, bias = normal(1, (c, 4), torch.bfloat16, 0.5, DEV), normal(2, (c,), torch.bfloat16, 0.3, DEV)
+    lam = normal(3, (c,), torch.float32, 1.0, DEV) - 5
+    s = torch.zeros((b, t), dtype=torch.bool, device=DEV)
+    s[:, [lo, at, end]] = True
+    if hi < t:
+        s[:, hi] = True
+    out = []
+    for value in (1.0, bad):
+        v = [z.clone() for z in (x, gr, gi, dy)]
+        for z in v:
+            z[:, at:end] = value
+        f = igc.seq_conv(v[0], w, bias, "silu", starts=s, keep8=True)
+        assert torch.equal(torch.isnan(igc.unpack8(f.kept)).any(2)[0],
+                           (torch.arange(t, device=DEV) // 16 * 16 >= lo) & (torch.arange(t, device=DEV) < hi) & (value != 1.0))
+        g = igc.seq_conv_bwd(v[3], f.kept, w, bias, "silu", starts=s)
+        r = igc.gated_scan(*v[:3], lam, starts=s, train=True, keep8=True)
+        d = igc.gated_scan_bwd(v[3], *r.kept, lam, r.states, starts=s)
+        out.append([torch.cat([z[:, :lo], z[:, hi:]], 1) for z in (g.dx, d.dx, d.dgate_r, d.dgate_i)] + [d.dh0])
+    for m, n in zip(*out):
+        assert torch.equal(m, n) and torch.isfinite(n.float()).all()
