@@ -306,7 +306,9 @@ def seq_conv_step(x, w, state, bias=None, activation=None, slots=None, state_out
     """One row of each of B streams: y (B, C) from x (B, C) and the carried rows state
     (S, K-1, C), which move on by one, in place or into state_out.  Stream b's rows are slot b,
     or slots[b] (int32); a stream whose slot lies outside the pool is idle: its y is zero and no
-    state is touched.  Two streams must not share a slot.  Returns (y, state)."""
+    state is touched.  Slots that no stream names are not copied to state_out: where streams may be
+    idle, update in place rather than swap two buffers.  Two streams must not share a slot.
+    Returns (y, state)."""
     x = _sequence(x, "x", dims=2)
     b, c = x.shape
     w, bias, k, act = _filter(w, bias, x, activation)
@@ -333,7 +335,8 @@ def gated_scan(x, gate_r, gate_i, lam, decay=8.0, h0=None, starts=None, train=Fa
                out=None) -> GatedScan:
     """The gated linear recurrence h_t = a h_{t-1} + sqrt(1 - a^2) sigmoid(gate_i) x_t with
     a = exp(-decay softplus(lam) sigmoid(gate_r)), over x, gate_r, gate_i (B, T, C) of one dtype;
-    lam (C) and h0 (B, C) fp32.  starts as for seq_conv.  train returns the states that
+    lam (C) and h0 (B, C) fp32.  starts as for seq_conv; a row at a start is scaled by
+    sqrt(1 - a^2) like any other.  train returns the states that
     gated_scan_bwd needs, keep8 also x, gate_r and gate_i in 8 bits (groups as for seq_conv)."""
     x = _sequence(x, "x")
     gate_r, gate_i = _sequence(gate_r, "gate_r", x), _sequence(gate_i, "gate_i", x)

@@ -113,7 +113,9 @@ int convseq_conv_bwd(const convseq_conv_desc* desc, const convseq_rows* dy, cons
  * carried rows are state[slot, :, :], slot = b, or slots[b] (int32) if slots
  * is not NULL; a slot outside [0, n_slots) marks an idle stream: its y is
  * zero and no state is touched.  The moved-on rows go to state_out at the same
- * slot, which may be state itself.  Two streams must not share a slot. */
+ * slot, which may be state itself.  Where it is another buffer, the slots that no
+ * stream names are not copied to it: a caller that swaps the two after each call
+ * has to step every stream, or update in place.  Two streams must not share a slot. */
 int convseq_conv_step(const convseq_conv_desc* desc, const void* x, int64_t x_row, const void* w,
                       const void* bias, const void* state, void* state_out, const void* slots, int32_t n_slots,
                       void* y, void* stream);
@@ -127,6 +129,8 @@ typedef struct {
 /* r = sigmoid(gate_r), i = sigmoid(gate_i), a = exp(-decay * softplus(lam[c]) * r),
  * h_t = a * h_{t-1} + sqrt(1 - a^2) * i * x_t,  y = h
  *
+ * A row at a start is scaled by sqrt(1 - a^2) like any other: h_t = sqrt(1 - a^2) * i * x_t.
+ * (There is no form in which the first row of a sequence enters unscaled.)
  * with h_{-1} = h0[b,c] (fp32; zeros if NULL) and h_{t-1} absent at a start.
  * a and its products are positive and count as 2^-149 where fp32 would round
  * them to zero: an infinite state, or state's gradient, stays infinite.

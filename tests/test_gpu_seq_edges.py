@@ -133,3 +133,21 @@ def test_from_8_bits_sequences_part_at_groups(bad, t, at, end, c):
         out.append([torch.cat([z[:, :lo], z[:, hi:]], 1) for z in (g.dx, d.dx, d.dgate_r, d.dgate_i)] + [d.dh0])
     for m, n in zip(*out):
         assert torch.equal(m, n) and torch.isfinite(n.float()).all()
+
+
+def test_slots_that_no_stream_names_are_left_alone():
+    """With a second buffer, slots of idle streams keep what they hold in both."""
+    b, pool, c, k = 4, 7, 24, 4
+    x, w = normal(1, (b, c), torch.float16, 1.0, DEV), normal(2, (c, k), torch.float16, 0.5, DEV)
+    slots = torch.tensor([5, -1, 0, 7], dtype=torch.int32, device=DEV)
+    named, rest = [5, 0], [1, 2, 3, 4, 6]
+    state, other = (normal(n, (pool, k - 1, c), torch.float16, 1.0, DEV) for n in (3, 4))
+    was = state.clone(), other.clone()
+    y, now = igc.seq_conv_step(x, w, state, slots=slots, state_out=other)
+    assert now is other and torch.equal(state, was[0]) and torch.equal(other[rest], was[1][rest])
+    assert torch.equal(other[named], torch.cat([was[0][named, 1:], x[[0, 2], None]], 1)) and not y[[1, 3]].any()
+    h, h2 = (normal(n, (pool, c), torch.float32, 1.0, DEV) for n in (5, 6))
+    was = h.clone(), h2.clone()
+    y, now = igc.gated_scan_step(x, x, x, w[:, 0].float(), h, slots=slots, h_out=h2)
+    assert now is h2 and torch.equal(h, was[0]) and torch.equal(h2[rest], was[1][rest])
+    assert torch.equal(y[[0, 2]], h2[named].half()) and not y[[1, 3]].any()
