@@ -5,10 +5,11 @@
 // makes K multiply-adds a value from registers.  The 4 waves of a workgroup
 // take 4 consecutive row groups of the same channels, so that 3 of 4 waves find
 // their K-1 earlier rows in the cache of their own compute unit.  Memory bound:
-// x read once, y written once; 1x32771x1024 fp16 takes 27.8 us (4.8 TB/s), and
-// 4x4096x2048 bf16 with 8 bits kept 37.3 us (4.6 TB/s).  V is 2 where C and the
-// buffers' alignment allow pairs, else 1: with 4 channels a lane the registers
-// leave 5 waves a SIMD instead of 8 (30.3 and 39.5 us).
+// x read once, y written once; 1x32771x1024 fp16 takes 27.1 us (5.0 TB/s), and
+// 4x4096x2048 bf16 with 8 bits kept 38 to 40 us (4.2 to 4.5 TB/s).  V is 2 where C and
+// the buffers' alignment allow pairs, else 1.  With 1, 2 and 4 channels a lane, calls back
+// to back on inputs in turn: 30.0, 28.7 and 32.2 us, and 36.3, 35.7 and 37.5 (at 4 the
+// registers leave 5 waves a SIMD instead of 8).
 #include "seq_conv.h"
 
 namespace convseq {

@@ -4,9 +4,12 @@
 // hold neighbouring channels, so the largest of a group needs no exchange
 // between lanes.  A lane takes V channels of one group: 16 row pieces of V
 // values on one side, two runs of 8 V bytes on the other.  Memory bound: 8x8192x2048
-// bf16 takes 85 us to pack (4.8 TB/s; 91 with 4 channels a lane instead of 2) and 65
-// to unpack (6.3 TB/s, part of the 143 MB still in the last-level cache), a copy of
-// as many bytes 160 for both.
+// bf16, calls back to back on inputs in turn, takes 73 us to pack and 79 to unpack (5.6
+// and 5.2 TB/s, where a copy reaches 5.1 to 5.3); into new memory a pack takes 90 at the
+// median, and what was just packed comes back in 65, part of it from the last-level
+// cache.  With 1, 2 and 4 channels a lane a pack takes 71, 73 and 75 us, apart by no more
+// than the spread, and of 4x4096x2048, which stays in the cache, 19.9, 17.8 and 19.6; an
+// unpack takes 79, 75 and 79.
 #include "seq_device.h"
 
 namespace convseq {

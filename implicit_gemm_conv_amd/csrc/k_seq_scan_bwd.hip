@@ -21,11 +21,11 @@
 // would take (at 128, two workgroups fit a compute unit).  Each input is read once, each gradient written once: memory
 // bound, 4 elements (or 1 element and 3 bytes) in and 3 out a value.
 //
-// 4x4096x2048 bf16 from 8 bits takes 121 us, the vector ALU busy 59% of it; a
-// workgroup lives 13.7 us, half of that waiting (ticket 0.8, loads 2.9, its waves
-// 1.5, look-back 1.9).  3x1999x321 fp32, one channel a lane, takes 19 us.  V is 2
+// 4x4096x2048 bf16 from 8 bits takes 123 to 127 us, the vector ALU busy 62% of it; a
+// workgroup lives 13.9 us, 8.5 of them waiting (ticket 0.7, loads 3.0, its waves 1.4 and
+// 1.7, look-back 1.7).  3x1999x321 fp32, one channel a lane, takes 19 us.  V is 2
 // where C, strides and alignment allow pairs of 16-bit values: with 1 the former
-// takes 140 us, and 64x100x512 fp16 18.0 instead of 17.4.
+// takes 139 us, and 64x100x512 fp16 18.7 instead of 18.0.
 #include "seq_carry.h"
 
 namespace convseq {

@@ -11,12 +11,13 @@
 // the recurrence over the a and m i x it still holds.  Each input is read once
 // and y written once: memory bound, 4 elements a value.
 //
-// 1x65539x1024 bf16 takes 125 us (4.3 TB/s, where a copy reaches 5.1), 4x4096x2048
-// with 8 bits kept 95 to 99 us, the vector ALU busy 58% of it.  One channel a lane: its
+// 1x65539x1024 bf16 takes 124 us (4.3 TB/s, where a copy reaches 5.1), 4x4096x2048
+// with 8 bits kept 95 to 104 us, the vector ALU busy 60% of it.  One channel a lane: its
 // registers let four workgroups (three with 8 bits) share a compute unit and cover
-// each other's waits; three for four costs 1% (126 us for 125).  Tiles of 64 rows
-// take 190 us on the one long sequence, which has twice the tiles to look back over,
-// and 93 on the other.
+// each other's waits; three for four costs 9% at 4x4096x2048 without 8 bits (69 us
+// for 64 back to back) and 1 to 2% on the long sequence.  Tiles of 64 rows take 190 us
+// on the one long sequence, which has twice the tiles to look back over, and 96 on the
+// other, where 128 take 99 to 102.
 #include "seq_carry.h"
 
 namespace convseq {
@@ -36,7 +37,7 @@ __global__ __launch_bounds__(kWaves * 64, KEEP ? 6 : 8) void seq_scan_fwd_kernel
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   // turned by one a tile row: each column's tiles go to all 8 dies, not to one of
-  // them (1x65539x1024 bf16: 125 us instead of 199)
+  // them (1x65539x1024 bf16: 125 us instead of 193)
   const int columns = cols * a.b, column = (blockIdx.x + blockIdx.x / columns) % columns;
   const int tile = tiles > 1 ? take_ticket(a.work, column, &ticket) : 0;
   const int b = column / cols;

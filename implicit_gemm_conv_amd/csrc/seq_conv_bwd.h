@@ -11,7 +11,7 @@
 // registers, are added over the 4 waves of the workgroup (4 consecutive pieces
 // of the same channels) in LDS and over the workgroups by a second kernel, both
 // in a fixed order.  Memory bound: dy and x (or its 8 bits) read once, dx
-// written once; 4x4096x2048 bf16 from 8 bits takes 44.6 us, the vector ALU busy
+// written once; 4x4096x2048 bf16 from 8 bits takes 44.8 us, the vector ALU busy
 // 60% of it.
 #pragma once
 
@@ -33,8 +33,13 @@ struct Chunk {
   uint32_t first;
 };
 
-// Four waves a SIMD (128 registers) where the windows leave room for it: at three
-// 4x4096x2048 bf16 from 8 bits takes 57 us instead of 44.6.
+// Four waves a SIMD (128 registers) where the windows leave room for it.  With the bound
+// at 4 and at 2 waves (which leaves the choice to the registers), 4x4096x2048 bf16, silu,
+// calls back to back with their sums, from x / from 8 bits:
+//   K        1-2        3            4            5            6            8
+//   4 waves  44 / 39    45 / 42      47 / 45      50 / 58      64 / 80      170 / 177 us
+//   2 waves  44 / 39    45 / 54      47 / 57      58 / 59      57 / 61      67 / 73 us
+// The rule takes the better side at V = 2 but for K = 5 from x.
 template <typename T, int K, int V, bool KEPT>
 __global__ __launch_bounds__(kWaves * 64, K * V <= 8 ? 4 : 2) void seq_conv_bwd_kernel(ConvArgs a, int cols, int blocks, int per) {
   typedef Pack<T, V> P;
