@@ -90,7 +90,8 @@ typedef struct {
  * X(b, s, c) is x[b,s,c], for s < 0 the carried row state[b, s + K-1, c]
  * (zeros if state is NULL), and zero where a start lies in (s, t].  w (C, K)
  * (the depthwise filter (C_out, 1, K, 1) of convfwd.h with its unit extents
- * dropped).  state_out (may be NULL) receives the last K-1 of the rows
+ * dropped; convfwd.h's grouped path with a low pad of K-1 computes the same z
+ * without bias, carried rows and starts, 1.3 to 2.6 times slower).  state_out (may be NULL) receives the last K-1 of the rows
  * (state, x), those before the last start zeroed: the carried rows of the
  * next piece.  kept (NULL, or both pointers set) receives x in 8 bits. */
 int convseq_conv_fwd(const convseq_conv_desc* desc, const convseq_rows* x, const void* w, const void* bias,
