@@ -1,0 +1,410 @@
+// k_norm_split.hip -- group norm over images and volumes: the sums of tiles of
+// positions, their join for each (n, group), and a second pass over x that writes
+// the result.
+#include "norm_device.h"
+
+namespace convnorm {
+
+namespace {
+
+constexpr int kLook = 4;  // rows a thread has in flight
+
+// A workgroup's part of the problem: thread (col, row) owns the channels at `ch`
+// and rows row, row + rw, ... of the tile.
+struct Part {
+  int n, tile, g0, slice, c0, width, rw, col, row, p0, p1;
+  bool live;
+};
+template <int V>
+__device__ __forceinline__ Part part_of(const NormArgs& a) {
+  const Plan& pl = a.plan;
+  Part t;
+  const int cg = a.c / a.groups;
+  unsigned b = blockIdx.x;
+  const int cb = b % pl.cblocks;
+  b /= pl.cblocks;
+  t.tile = b % pl.tiles;
+  t.n = b / pl.tiles;
+  if (pl.slices == 1) {
+    t.g0 = cb * pl.k;
+    t.slice = 0;
+    t.c0 = t.g0 * cg;
+    t.width = min(pl.cw, a.c - t.c0);
+  } else {
+    t.g0 = cb / pl.slices;
+    t.slice = cb % pl.slices;
+    t.c0 = t.g0 * cg + t.slice * pl.cw;
+    t.width = min(pl.cw, (t.g0 + 1) * cg - t.c0);
+  }
+  const int cv = pl.cw / V;
+  t.rw = kThreads / cv;
+  t.col = threadIdx.x % cv;
+  t.row = threadIdx.x / cv;
+  t.live = t.row < t.rw && t.col * V < t.width;
+  t.p0 = t.tile * pl.per;
+  t.p1 = min(t.p0 + pl.per, a.p);
+  return t;
+}
+
+// Calls f(row pointer offset in rows, pack) for the thread's rows, kLook loads ahead.
+template <typename T, int V, typename F>
+__device__ __forceinline__ void walk(const Part& t, const Rows& r, int n, const F& f) {
+  typedef Pack<T, V> P;
+  const T* at = (const T*)r.p + n * r.sb + t.c0 + t.col * V;
+  for (int p = t.p0 + t.row; p < t.p1; p += t.rw * kLook) {
+    P q[kLook];
+#pragma unroll
+    for (int u = 0; u < kLook; ++u)
+      if (p + u * t.rw < t.p1) q[u] = *(const P*)(at + (int64_t)(p + u * t.rw) * r.st);
+#pragma unroll
+    for (int u = 0; u < kLook; ++u)
+      if (p + u * t.rw < t.p1) f(p + u * t.rw, q[u]);
+  }
+}
+
+// Sums over the tile's channels of each of its groups, from a pair for each channel in LDS:
+// put(group, lane of `of` lanes, first and last channel of the group in LDS).  Groups of few
+// channels get a thread each, others a wave.
+template <typename F>
+__device__ __forceinline__ void each_group(const NormArgs& a, const Part& t, const F& f) {
+  const int cg = a.plan.slices == 1 ? a.c / a.groups : t.width, groups = t.width / cg;
+  if (cg <= 16) {
+    for (int g = threadIdx.x; g < groups; g += kThreads) f(g, 0, 1, cg);
+  } else {
+    for (int g = threadIdx.x / 64; g < groups; g += kThreads / 64) f(g, threadIdx.x % 64, 64, cg);
+  }
+}
+
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads) void norm_stats_kernel(NormArgs a) {
+  __shared__ float3 lds[kThreads * V];
+  const Part t = part_of<V>(a);
+  float cnt = 0.f, m[V], s[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) m[e] = s[e] = 0.f;
+  if (t.live) {
+    // about the thread's own first row: the squares are of differences within the data's spread
+    float first[V];
+    walk<T, V>(t, a.x, t.n, [&](int, const Pack<T, V>& q) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        if (cnt == 0.f) first[e] = q.get(e);
+        const float d = q.get(e) - first[e];
+        m[e] += d;
+        s[e] = fmaf(d, d, s[e]);
+      }
+      cnt += 1.f;
+    });
+    if (cnt > 0.f)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = m[e] / cnt;
+        s[e] = fmaf(-d, m[e], s[e]);
+        m[e] = first[e] + d;
+      }
+  }
+  // the rows of the workgroup, halves at a time
+  int top = 1;
+  while (top < t.rw) top <<= 1;
+  for (int half = top; half >= 1; half >>= 1) {
+    __syncthreads();
+    if (t.live && t.row >= half && t.row < 2 * half)
+#pragma unroll
+      for (int e = 0; e < V; ++e) lds[((t.row - half) * (a.plan.cw / V) + t.col) * V + e] = make_float3(cnt, m[e], s[e]);
+    __syncthreads();
+    if (t.live && t.row < half && t.row + half < t.rw) {
+      float n = cnt;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float3 o = lds[(t.row * (a.plan.cw / V) + t.col) * V + e];
+        n = cnt;
+        join(n, m[e], s[e], o.x, o.y, o.z);
+      }
+      cnt = n;
+    }
+  }
+  __syncthreads();
+  if (t.live && t.row == 0)
+#pragma unroll
+    for (int e = 0; e < V; ++e) lds[t.col * V + e] = make_float3(cnt, m[e], s[e]);
+  __syncthreads();
+  const float rows = (float)max(t.p1 - t.p0, 0);
+  each_group(a, t, [&](int g, int lane, int of, int cg) {
+    float mean = 0.f, sq = 0.f;
+    for (int c = lane; c < cg; c += of) mean += lds[g * cg + c].y;
+    mean = team_sum(mean, of) / (float)cg;
+    for (int c = lane; c < cg; c += of) {
+      const float3 o = lds[g * cg + c];
+      const float d = o.y - mean;
+      sq += fmaf(d * d, rows, o.z);
+    }
+    sq = team_sum(sq, of);
+    if (lane == 0)
+      ((float2*)a.part)[(((int64_t)t.n * a.groups + t.g0 + g) * a.plan.slices + t.slice) * a.plan.tiles + t.tile] =
+          make_float2(mean, sq);
+  });
+}
+
+// Values of part (slice, tile) of a group.
+__device__ __forceinline__ double count_of(const NormArgs& a, int i) {
+  const Plan& pl = a.plan;
+  const int cg = a.c / a.groups, tile = i % pl.tiles, slice = i / pl.tiles;
+  const int rows = min(pl.per, a.p - tile * pl.per), width = pl.slices == 1 ? cg : min(pl.cw, cg - slice * pl.cw);
+  return (double)rows * width;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* lds) {
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o);
+  __syncthreads();
+  if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = v;
+  __syncthreads();
+  v = 0;
+  for (int w = 0; w < kThreads / 64; ++w) v += lds[w];
+  return v;
+}
+
+// One workgroup for each (n, group): the parts' means, then the squares about the whole mean.
+__global__ __launch_bounds__(kThreads) void norm_join_kernel(NormArgs a) {
+  __shared__ double lds[kThreads / 64];
+  const int parts = a.plan.slices * a.plan.tiles;
+  const float2* part = (const float2*)a.part + (int64_t)blockIdx.x * parts;
+  double sum = 0;
+  for (int i = threadIdx.x; i < parts; i += kThreads) sum += count_of(a, i) * part[i].x;
+  const double all = (double)a.p * (a.c / a.groups);
+  const double mean = block_sum(sum, lds) / all;
+  sum = 0;
+  for (int i = threadIdx.x; i < parts; i += kThreads) {
+    const double d = part[i].x - mean;
+    sum += part[i].y + count_of(a, i) * d * d;
+  }
+  sum = block_sum(sum, lds) / all;
+  if (threadIdx.x == 0) {
+    a.mean[blockIdx.x] = (float)mean;
+    a.rstd[blockIdx.x] = (float)(1.0 / sqrt(sum + a.eps));
+  }
+}
+
+template <int V>
+struct Channels {
+  float mean[V], rstd[V], w[V], b[V];
+  __device__ __forceinline__ Channels(const NormArgs& a, const Part& t, const float* mu, const float* rs) {
+    const int cg = a.c / a.groups;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const int c = t.c0 + t.col * V + e, g = c / cg;
+      mean[e] = mu[(int64_t)t.n * a.groups + g];
+      rstd[e] = rs[(int64_t)t.n * a.groups + g];
+      w[e] = param(a.weight, a.param_f32, a.dtype, c, 1.f);
+      b[e] = param(a.bias, a.param_f32, a.dtype, c, 0.f);
+    }
+  }
+};
+
+template <typename T, int V, bool SILU>
+__global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a) {
+  const Part t = part_of<V>(a);
+  if (!t.live) return;
+  const Channels<V> k(a, t, a.mean, a.rstd);
+  T* y = (T*)a.y + (int64_t)t.n * a.p * a.c + t.c0 + t.col * V;
+  walk<T, V>(t, a.x, t.n, [&](int p, const Pack<T, V>& q) {
+    Pack<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) o.set(e, activate<SILU>(fmaf((q.get(e) - k.mean[e]) * k.rstd[e], k.w[e], k.b[e])));
+    *(Pack<T, V>*)(y + (int64_t)p * a.c) = o;
+  });
+}
+
+// f(position, pieces of x and dy) for the thread's rows.
+template <typename T, int V, typename F>
+__device__ __forceinline__ void walk2(const NormArgs& a, const Part& t, const F& f) {
+  typedef Pack<T, V> P;
+  const T* x = (const T*)a.x.p + t.n * a.x.sb + t.c0 + t.col * V;
+  const T* d = (const T*)a.dy.p + t.n * a.dy.sb + t.c0 + t.col * V;
+  constexpr int look = kLook / 2;
+  for (int p = t.p0 + t.row; p < t.p1; p += t.rw * look) {
+    P q[look], r[look];
+#pragma unroll
+    for (int u = 0; u < look; ++u)
+      if (p + u * t.rw < t.p1) {
+        q[u] = *(const P*)(x + (int64_t)(p + u * t.rw) * a.x.st);
+        r[u] = *(const P*)(d + (int64_t)(p + u * t.rw) * a.dy.st);
+      }
+#pragma unroll
+    for (int u = 0; u < look; ++u)
+      if (p + u * t.rw < t.p1) f(p + u * t.rw, q[u], r[u]);
+  }
+}
+
+// For each channel of the tile the sums of dz xhat and dz, and from them, with the
+// weights, the two sums of each group.
+template <typename T, int V, bool SILU>
+__global__ __launch_bounds__(kThreads) void norm_sums_kernel(NormArgs a) {
+  __shared__ float2 lds[kThreads * V];
+  const Part t = part_of<V>(a);
+  float dw[V], db[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
+  if (t.live) {
+    const Channels<V> k(a, t, a.mean_in, a.rstd_in);
+    walk2<T, V>(a, t, [&](int, const Pack<T, V>& q, const Pack<T, V>& r) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float hat = (q.get(e) - k.mean[e]) * k.rstd[e];
+        const float dz = r.get(e) * slope<SILU>(fmaf(hat, k.w[e], k.b[e]));
+        db[e] += dz;
+        dw[e] = fmaf(dz, hat, dw[e]);
+      }
+    });
+  }
+  int top = 1;
+  while (top < t.rw) top <<= 1;
+  for (int half = top; half >= 1; half >>= 1) {
+    __syncthreads();
+    if (t.live && t.row >= half && t.row < 2 * half)
+#pragma unroll
+      for (int e = 0; e < V; ++e) lds[((t.row - half) * (a.plan.cw / V) + t.col) * V + e] = make_float2(dw[e], db[e]);
+    __syncthreads();
+    if (t.live && t.row < half && t.row + half < t.rw)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float2 o = lds[(t.row * (a.plan.cw / V) + t.col) * V + e];
+        dw[e] += o.x;
+        db[e] += o.y;
+      }
+  }
+  __syncthreads();
+  if (t.live && t.row == 0) {
+    float2* to = (float2*)a.chan + ((int64_t)t.n * a.plan.tiles + t.tile) * a.c + t.c0 + t.col * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float w = param(a.weight, a.param_f32, a.dtype, t.c0 + t.col * V + e, 1.f);
+      to[e] = make_float2(dw[e], db[e]);
+      lds[t.col * V + e] = make_float2(dw[e] * w, db[e] * w);
+    }
+  }
+  __syncthreads();
+  each_group(a, t, [&](int g, int lane, int of, int cg) {
+    float s1 = 0.f, s2 = 0.f;
+    for (int c = lane; c < cg; c += of) {
+      s2 += lds[g * cg + c].x;
+      s1 += lds[g * cg + c].y;
+    }
+    s1 = team_sum(s1, of);
+    s2 = team_sum(s2, of);
+    if (lane == 0)
+      ((float2*)a.part)[(((int64_t)t.n * a.groups + t.g0 + g) * a.plan.slices + t.slice) * a.plan.tiles + t.tile] =
+          make_float2(s1, s2);
+  });
+}
+
+// The first N * groups workgroups: the two means of an (n, group); the others: dweight and dbias of
+// kCols channels each, from the sums of all tiles.
+constexpr int kCols = 8;
+__device__ void columns(const NormArgs& a, int block, double* lds) {
+  const int c = block * kCols + threadIdx.x % kCols, lane = threadIdx.x / kCols;
+  double dw = 0, db = 0;
+  if (c < a.c)
+    for (int64_t r = lane; r < a.plan.rows; r += kThreads / kCols) {
+      const float2 o = ((const float2*)a.chan)[r * a.c + c];
+      dw += o.x;
+      db += o.y;
+    }
+  double* mine = lds + threadIdx.x * 2;
+  mine[0] = dw;
+  mine[1] = db;
+  for (int half = kThreads / kCols / 2; half >= 1; half >>= 1) {
+    __syncthreads();
+    if (lane < half) {
+      mine[0] += mine[half * kCols * 2];
+      mine[1] += mine[half * kCols * 2 + 1];
+    }
+  }
+  if (lane == 0 && c < a.c) {
+    if (a.dweight) a.dweight[c] = (float)mine[0];
+    if (a.dbias) a.dbias[c] = (float)mine[1];
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void norm_join_bwd_kernel(NormArgs a) {
+  __shared__ double lds[2 * kThreads];
+  const int64_t slabs = (int64_t)a.n * a.groups;
+  if (blockIdx.x >= slabs) return columns(a, (int)(blockIdx.x - slabs), lds);
+  const int parts = a.plan.slices * a.plan.tiles;
+  const float2* part = (const float2*)a.part + (int64_t)blockIdx.x * parts;
+  double s1 = 0, s2 = 0;
+  for (int i = threadIdx.x; i < parts; i += kThreads) {
+    s1 += part[i].x;
+    s2 += part[i].y;
+  }
+  s1 = block_sum(s1, lds);
+  s2 = block_sum(s2, lds);
+  const double all = (double)a.p * (a.c / a.groups);
+  if (threadIdx.x == 0) ((float2*)a.two)[blockIdx.x] = make_float2((float)(s1 / all), (float)(s2 / all));
+}
+
+__global__ __launch_bounds__(kThreads) void norm_columns_kernel(NormArgs a) {
+  __shared__ double lds[2 * kThreads];
+  columns(a, blockIdx.x, lds);
+}
+
+template <typename T, int V, bool SILU>
+__global__ __launch_bounds__(kThreads) void norm_apply_bwd_kernel(NormArgs a) {
+  const Part t = part_of<V>(a);
+  if (!t.live) return;
+  const Channels<V> k(a, t, a.mean_in, a.rstd_in);
+  float s1[V], s2[V];
+  const int cg = a.c / a.groups;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float2 o = ((const float2*)a.two)[(int64_t)t.n * a.groups + (t.c0 + t.col * V + e) / cg];
+    s1[e] = o.x;
+    s2[e] = o.y;
+  }
+  T* dx = (T*)a.y + (int64_t)t.n * a.p * a.c + t.c0 + t.col * V;
+  walk2<T, V>(a, t, [&](int p, const Pack<T, V>& q, const Pack<T, V>& r) {
+    Pack<T, V> o;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float hat = (q.get(e) - k.mean[e]) * k.rstd[e];
+      const float d = r.get(e) * slope<SILU>(fmaf(hat, k.w[e], k.b[e])) * k.w[e];
+      o.set(e, k.rstd[e] * (d - s1[e] - hat * s2[e]));
+    }
+    *(Pack<T, V>*)(dx + (int64_t)p * a.c) = o;
+  });
+}
+
+}  // namespace
+
+hipError_t launch_norm_columns(const NormArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL(norm_columns_kernel, dim3((a.c + kCols - 1) / kCols), dim3(kThreads), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
+  return for_kind(a.dtype, a.plan.v, a.act, [&](auto t, auto v, auto silu) {
+    typedef decltype(t) T;
+    constexpr int V = decltype(v)::value;
+    constexpr bool SILU = decltype(silu)::value;
+    const dim3 grid((unsigned)a.plan.blocks), block(kThreads);
+    hipLaunchKernelGGL((norm_stats_kernel<T, V>), grid, block, 0, s, a);
+    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((int64_t)a.n * a.groups)), block, 0, s, a);
+    hipLaunchKernelGGL((norm_apply_kernel<T, V, SILU>), grid, block, 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
+  return for_kind(a.dtype, a.plan.v, a.act, [&](auto t, auto v, auto silu) {
+    typedef decltype(t) T;
+    constexpr int V = decltype(v)::value;
+    constexpr bool SILU = decltype(silu)::value;
+    const dim3 grid((unsigned)a.plan.blocks), block(kThreads);
+    const int cols = a.dweight || a.dbias ? (a.c + kCols - 1) / kCols : 0;
+    hipLaunchKernelGGL((norm_sums_kernel<T, V, SILU>), grid, block, 0, s, a);
+    hipLaunchKernelGGL(norm_join_bwd_kernel, dim3((unsigned)((int64_t)a.n * a.groups + cols)), block, 0, s, a);
+    hipLaunchKernelGGL((norm_apply_bwd_kernel<T, V, SILU>), grid, block, 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace convnorm
