@@ -1,0 +1,247 @@
+// delta_device.h -- device helpers shared by the gated delta rule's kernels.
+//
+// Mathematics of a chunk of 64 rows, with S the state before it.  G_i are the sums
+// of log decays up to row i, D_ij = exp(G_i - G_j) for j <= i in the same sequence,
+// L = D * (k k^T) below the diagonal and H = -(I + L beta)^-1 L, which is strictly
+// lower triangular too.  Then
+//
+//   r = v - enter * (k S),  x = r + H (beta r),  u = beta x
+//   y = scale * (enter * (q S) + R u),  R = D * (q k^T)
+//   S <- enter_last * S + k^T (leave * u)
+//
+// where enter_i = exp(G_i) (zero from a start on) and leave_j = exp(G_last - G_j)
+// (zero before the last start).  H holds no beta, so a beta of zero is nothing special.
+//
+// Products run on the bf16 matrix units at fp32's precision: an fp32 value is the
+// sum of three bf16 parts (8 significant bits each), and of the parts' products
+// those that matter to 24 bits are added in fp32.  A bf16 input is one part, an
+// fp16 input two.  bf16 has fp32's range, so nothing overflows on the way.
+//
+// A wave owns 16 columns of the state and keeps them in fp32 accumulators.  Rows of
+// accumulator tiles are dealt so that two tiles together are one operand of the next
+// product, in its natural order, without leaving their lane: row m of tile t of a
+// matrix is row_of(t, m) of it.
+#pragma once
+
+#include "conv_device.h"
+#include "delta_params.h"
+
+#pragma clang fp contract(off)
+
+namespace convdelta {
+
+using convfwd::bf168_t;
+using convfwd::f32x4_t;
+using convfwd::from_f32;
+using convfwd::to_f32;
+
+typedef __bf16 bf164_t __attribute__((ext_vector_type(4)));
+
+// The wave's number in its workgroup, known to be one for all lanes.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
+
+__device__ __forceinline__ int row_of(int t, int m) { return 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3); }
+
+// The six (tile, step of 32) pairs that hold something of a strictly or non-strictly
+// lower triangle, and of its transpose.
+__device__ constexpr int low_t(int f) { return f < 2 ? f : f < 4 ? 2 : 3; }
+__device__ constexpr int low_s(int f) { return f < 2 ? 0 : f & 1; }
+__device__ constexpr int up_t(int f) { return f < 4 ? f >> 1 : f - 2; }
+__device__ constexpr int up_s(int f) { return f < 4 ? f & 1 : 1; }
+
+// Parts of an input of type T.
+template <typename T> struct InParts;
+template <> struct InParts<__bf16> { static constexpr int n = 1; };
+template <> struct InParts<_Float16> { static constexpr int n = 2; };
+template <> struct InParts<float> { static constexpr int n = 3; };
+
+template <int N>
+struct Parts {
+  bf168_t p[N];
+};
+
+template <int N>
+__device__ __forceinline__ void split_one(float x, __bf16 (&o)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    o[k] = (__bf16)x;
+    x -= (float)o[k];
+  }
+}
+
+template <int N>
+__device__ __forceinline__ Parts<N> split(const float (&x)[8]) {
+  Parts<N> r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    __bf16 o[N];
+    split_one<N>(x[e], o);
+#pragma unroll
+    for (int k = 0; k < N; ++k) r.p[k][e] = o[k];
+  }
+  return r;
+}
+
+// acc += A B from parts, the products that matter to fp32.
+template <int NA, int NB>
+__device__ __forceinline__ f32x4_t mma(const Parts<NA>& a, const Parts<NB>& b, f32x4_t acc) {
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+      if (i + j < kParts) acc = convfwd::mfma16x16x32(a.p[i], b.p[j], acc);
+  return acc;
+}
+
+// Two accumulator tiles, scaled row by row, as one operand.
+template <int N>
+__device__ __forceinline__ Parts<N> operand(const f32x4_t& a, const f32x4_t& b) {
+  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return split<N>(x);
+}
+
+// What is not wanted is selected away, not multiplied by zero.
+__device__ __forceinline__ float times(float factor, float x) { return factor == 0.f ? 0.f : factor * x; }
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
+// ---- rows of q, k in LDS: [part][64][DK + 8] bf16 ----
+// The 8 spare elements spread the rows over the banks.
+template <int DK>
+struct RowsAt {
+  static constexpr int stride = DK + 8, part = kChunk * stride;
+};
+
+// 8 elements of a row as they come from memory, zero outside.
+template <typename T>
+struct Piece {
+  T v[8];
+};
+template <typename T>
+__device__ __forceinline__ Piece<T> load_piece(const T* row, int d0, int d, bool in, int vec) {
+  Piece<T> p;
+  if (in && vec && d0 < d) {
+    struct alignas(16) Raw { T v[8]; };
+    const Raw r = *(const Raw*)(row + d0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p.v[e] = r.v[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) p.v[e] = in && d0 + e < d ? row[d0 + e] : (T)0.f;
+  }
+  return p;
+}
+template <typename T>
+__device__ __forceinline__ Parts<InParts<T>::n> parts_of(const Piece<T>& p) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = to_f32(p.v[e]);
+  return split<InParts<T>::n>(x);
+}
+
+// Pieces of a chunk's rows that a thread of `threads` holds on their way to LDS.
+template <typename T, int DK, int THREADS>
+struct Rows64 {
+  static constexpr int pieces = kChunk * (DK / 8), each = (pieces + THREADS - 1) / THREADS;
+  Piece<T> p[each];
+  __device__ __forceinline__ void load(const Heads& h, int b, int head, int t0, int t, int d, int vec) {
+    const T* base = (const T*)h.p + b * h.sb + head * h.sh;
+#pragma unroll
+    for (int k = 0; k < each; ++k) {
+      const int i = threadIdx.x + k * THREADS, row = i / (DK / 8), d0 = i % (DK / 8) * 8;
+      p[k] = load_piece<T>(base + (int64_t)(t0 + row) * h.st, d0, d, i < pieces && t0 + row < t, vec);
+    }
+  }
+  __device__ __forceinline__ void put(__bf16* lds) const {
+#pragma unroll
+    for (int k = 0; k < each; ++k) {
+      const int i = threadIdx.x + k * THREADS, row = i / (DK / 8), d0 = i % (DK / 8) * 8;
+      if (i >= pieces) continue;
+      const auto q = parts_of<T>(p[k]);
+#pragma unroll
+      for (int n = 0; n < InParts<T>::n; ++n)
+        *(bf168_t*)(lds + n * RowsAt<DK>::part + row * RowsAt<DK>::stride + d0) = q.p[n];
+    }
+  }
+};
+
+// 8 neighbouring elements of a row of 16-bit values in LDS: an operand in its natural order.
+template <int N>
+__device__ __forceinline__ Parts<N> natural(const __bf16* at, int part) {
+  Parts<N> r;
+#pragma unroll
+  for (int n = 0; n < N; ++n) r.p[n] = *(const bf168_t*)(at + n * part);
+  return r;
+}
+
+// The transposed read: of 8 neighbouring rows of 16-bit values, row0 .. row0 + 7 for the lane's
+// quarter, this lane's column.  The hardware reads 4 rows x 16 columns a quarter of the wave, each
+// lane 4 neighbouring columns; lane p of a quarter points at row p / 4, and at the columns that the
+// lanes 4 (p % 4) .. + 3 get.  `at` is that address for the first four rows.
+template <int N>
+__device__ __forceinline__ Parts<N> transposed(const __bf16* at, int stride, int part) {
+  typedef __attribute__((address_space(3))) bf164_t* Lds;
+  Parts<N> r;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const bf164_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Lds)(at + n * part));
+    const bf164_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((Lds)(at + n * part + 4 * stride));
+    r.p[n] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+  return r;
+}
+
+// Keeps the elements whose index k0 + e lies in [lo, hi).
+template <int N>
+__device__ __forceinline__ void keep(Parts<N>& a, int k0, int lo, int hi) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k0 + e < lo || k0 + e >= hi) a.p[n][e] = (__bf16)0.f;
+}
+
+__device__ __forceinline__ int64_t chunk_index(const DeltaArgs& a, int bh, int c) { return (int64_t)bh * a.chunks + c; }
+
+// 16-byte pieces of a contiguous stretch, on their way to LDS.  Threads past the end repeat the last piece.
+template <int BYTES, int THREADS>
+struct Stretch {
+  static constexpr int pieces = BYTES / 16, each = (pieces + THREADS - 1) / THREADS;
+  convfwd::u32x4_t p[each];
+  __device__ __forceinline__ static int at(int k) { return min((int)threadIdx.x + k * THREADS, pieces - 1); }
+  __device__ __forceinline__ void load(const void* from) {
+#pragma unroll
+    for (int k = 0; k < each; ++k) p[k] = ((const convfwd::u32x4_t*)from)[at(k)];
+  }
+  __device__ __forceinline__ void put(void* to) const {
+#pragma unroll
+    for (int k = 0; k < each; ++k) ((convfwd::u32x4_t*)to)[at(k)] = p[k];
+  }
+};
+
+// Workgroups of one head lie on one die (ids are dealt round-robin to 8), so that they share its L2.
+__device__ __forceinline__ bool head_of(int heads, int blocks, int& bh, int& cb) {
+  const int slot = blockIdx.x / 8;
+  bh = slot / blocks * 8 + blockIdx.x % 8;
+  cb = slot % blocks;
+  return bh < heads;
+}
+
+template <typename F>
+inline hipError_t for_type(int dtype, const F& f) {
+  if (dtype == convfwd::kF32) return f(float{});
+  if (dtype == convfwd::kF16) return f(_Float16{});
+  return f(__bf16{});
+}
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+// Head sizes are padded to 32, 64 or 128 inside the kernels.
+template <typename F>
+inline hipError_t for_dk(int dk, const F& f) {
+  if (dk <= 32) return f(Int<32>{});
+  if (dk <= 64) return f(Int<64>{});
+  return f(Int<128>{});
+}
+
+}  // namespace convdelta

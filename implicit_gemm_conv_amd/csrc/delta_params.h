@@ -1,0 +1,78 @@
+// delta_params.h -- plain parameter structs, workspace layout and launchers
+// shared by the host side of include/convdelta.h (delta_api.cpp) and its kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace convdelta {
+
+constexpr int kChunk = 64;  // rows taken at a time; rows between the kept states
+constexpr int kMaxDk = 128;
+constexpr int kFrag = 1024;               // bytes of one 16x32 operand of 16-bit parts
+constexpr int kTri = 6;                   // 16x32 operands that cover a 64x64 triangle
+constexpr int kParts = 3;                 // 16-bit parts that hold an fp32 value
+constexpr int kMatrix = kTri * kParts * kFrag;
+
+// A (B, T, H, D) tensor with element stride 1; strides in elements.
+struct Heads {
+  const void* p;
+  int64_t sb, st, sh;
+};
+
+// What the preparing kernel leaves for each chunk of each head (index
+// ((b * Hv + h) * chunks + c) throughout).
+struct Work {
+  char* solve;     // H as operands of x = r + H (beta r): kMatrix bytes
+  char* read;      // forward: the decayed q k^T, the same way
+  char* solve_t;   // backward: the transposes of both
+  char* read_t;
+  float* rows;     // 4 x 64: enter, leave, beta, step (see delta_device.h)
+  double* sums;    // backward: 64 sums of log decays
+  int* seq;        // backward: 64 sequence numbers inside the chunk
+  float* x;        // backward: x and its counterpart, (B * Hv, chunks * 64, dvp)
+  float* z;
+  float* dstate;   // backward: the gradient of the state after each chunk, (.., Dk, dvp)
+};
+
+struct DeltaArgs {
+  int b, t, hk, hv, dk, dv, dtype;
+  int chunks, dvp;  // ceil(T / 64); Dv rounded up to 32
+  int vec;          // q and k can be read in pieces of 8 elements, 16-byte aligned
+  float scale;
+  Heads q, k, v, dy;
+  const float *log_decay, *beta, *h0, *states_in, *dh_last;
+  const uint8_t* starts;
+  void *y, *dq, *dk_, *dv_;
+  float *h_last, *states, *dlog_decay, *dbeta, *dh0;
+  Work w;
+};
+
+struct DeltaStepArgs {
+  int b, hk, hv, dk, dv, dtype, n_slots;
+  float scale;
+  Heads q, k, v;
+  const float *log_decay, *beta, *state;
+  float* state_out;
+  const int32_t* slots;
+  void* y;
+};
+
+hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t s);
+// One launcher for each type:
+//   fwd     y, the states
+//   replay  x of every chunk, from the kept states
+//   bwd     dv, z, the states' gradients
+//   grad    dq, dk, dlog_decay, dbeta
+#define CONVDELTA_LAUNCHERS(type)                                        \
+  hipError_t launch_delta_fwd_##type(const DeltaArgs& a, hipStream_t s);    \
+  hipError_t launch_delta_replay_##type(const DeltaArgs& a, hipStream_t s); \
+  hipError_t launch_delta_bwd_##type(const DeltaArgs& a, hipStream_t s);    \
+  hipError_t launch_delta_grad_##type(const DeltaArgs& a, hipStream_t s);
+CONVDELTA_LAUNCHERS(f32)
+CONVDELTA_LAUNCHERS(f16)
+CONVDELTA_LAUNCHERS(bf16)
+#undef CONVDELTA_LAUNCHERS
+hipError_t launch_delta_step(const DeltaStepArgs& a, hipStream_t s);
+
+}  // namespace convdelta
