@@ -22,16 +22,20 @@ int check(const convdelta_desc* d) {
   if (d->hv % d->hk || !isfinite(d->scale)) return CONVFWD_ERR_BAD_DESC;
   if (d->dtype != CONVFWD_F32 && d->dtype != CONVFWD_F16 && d->dtype != CONVFWD_BF16) return CONVFWD_ERR_UNSUPPORTED;
   if (d->dk > CONVDELTA_MAX_DK) return CONVFWD_ERR_UNSUPPORTED;
-  // workgroups of 256 threads: at most one for each chunk, value head and 64 columns, and the heads
-  // are rounded up to 8; a grid holds less than 2^32 threads
-  const int64_t lim = (int64_t)1 << 24, chunks = ((int64_t)d->t + kChunk - 1) / kChunk, blocks = ((int64_t)d->dv + 63) / 64;
+  // workgroups of 256 threads: at most one for each chunk, value head and 16 columns (rounded up to 32), and the
+  // heads are rounded up to 8; a grid holds less than 2^32 threads
+  const int64_t lim = (int64_t)1 << 24, chunks = ((int64_t)d->t + kChunk - 1) / kChunk, blocks = ((int64_t)d->dv + 31) / 32 * 2;
   const int64_t heads = ((int64_t)d->b * d->hv + 7) / 8 * 8;
   if (d->t >= 1 << 30 || d->hv >= lim || blocks >= lim || heads >= lim || heads * blocks >= lim) return CONVFWD_ERR_TOO_LARGE;
   if (chunks * heads >= lim || chunks * heads * blocks >= lim) return CONVFWD_ERR_TOO_LARGE;
+  // ... and one for each 2048 elements of q and k
+  if (d->hk * (int64_t)d->b >= lim || d->hk * (int64_t)d->b * chunks * 4 >= lim) return CONVFWD_ERR_TOO_LARGE;
   return CONVFWD_OK;
 }
 
 int64_t chunks_of(const convdelta_desc* d) { return ((int64_t)d->t + kChunk - 1) / kChunk; }
+
+int dkp_of(const convdelta_desc* d) { return (d->dk + 7) / 8 * 8; }
 
 // Lays the workspace out from `base` and returns its bytes.
 int64_t lay_out(const convdelta_desc* d, bool backward, char* base, Work* w) {
@@ -57,6 +61,10 @@ int64_t lay_out(const convdelta_desc* d, bool backward, char* base, Work* w) {
     w->dstate = (float*)take(4 * d->dk * dvp);
   }
   w->rows = (float*)take(4 * 4 * kChunk);
+  for (void** copy : {&w->q, &w->k}) {
+    *copy = base ? base + at : nullptr;
+    at += (int64_t)d->b * d->t * d->hk * dkp_of(d) * elem_bytes(d->dtype);  // whole 16 bytes a row
+  }
   return at;
 }
 
@@ -93,8 +101,21 @@ void fill(DeltaArgs* a, const convdelta_desc* d) {
   a->b = d->b; a->t = d->t; a->hk = d->hk; a->hv = d->hv; a->dk = d->dk; a->dv = d->dv; a->dtype = d->dtype;
   a->chunks = (int)chunks_of(d);
   a->dvp = (d->dv + 31) / 32 * 32;
+  a->dkp = dkp_of(d);
   a->scale = d->scale;
-  a->vec = pieces(a->q, d->dk, elem_bytes(d->dtype)) && pieces(a->k, d->dk, elem_bytes(d->dtype));
+}
+
+// What is launched before the recurrence; q and k become aligned rows.
+int prepare(DeltaArgs* a, bool backward, hipStream_t s) {
+  const int eb = elem_bytes(a->dtype);
+  if (!pieces(a->q, a->dk, eb) || !pieces(a->k, a->dk, eb)) {
+    const int rc = launched(launch_delta_pack(*a, a->q, a->k, s));
+    if (rc < 0) return rc;
+    const int64_t row = (int64_t)a->hk * a->dkp;
+    a->q = Heads{a->w.q, a->t * row, row, a->dkp};
+    a->k = Heads{a->w.k, a->t * row, row, a->dkp};
+  }
+  return launched(launch_delta_prep(*a, backward, s));
 }
 
 typedef hipError_t (*Launch)(const DeltaArgs&, hipStream_t);
@@ -134,7 +155,7 @@ int convdelta_fwd(const convdelta_desc* d, const convdelta_heads* q, const convd
   lay_out(d, false, (char*)workspace, &a.w);
   const hipStream_t s = (hipStream_t)stream;
   if (a.chunks > 0) {
-    const int rc = launched(launch_delta_prep(a, false, s));
+    const int rc = prepare(&a, false, s);
     if (rc < 0) return rc;
   }
   static const Launch fwd[3] = {launch_delta_fwd_f32, launch_delta_fwd_f16, launch_delta_fwd_bf16};
@@ -179,7 +200,7 @@ int convdelta_bwd(const convdelta_desc* d, const convdelta_heads* dy, const conv
   static const Launch bwd[3] = {launch_delta_bwd_f32, launch_delta_bwd_f16, launch_delta_bwd_bf16};
   static const Launch grad[3] = {launch_delta_grad_f32, launch_delta_grad_f16, launch_delta_grad_bf16};
   int rc = CONVFWD_OK;
-  if (a.chunks > 0) rc = launched(launch_delta_prep(a, true, s));
+  if (a.chunks > 0) rc = prepare(&a, true, s);
   if (a.chunks > 0 && rc == CONVFWD_OK) rc = launched(replay[d->dtype](a, s));
   if (rc == CONVFWD_OK) rc = launched(bwd[d->dtype](a, s));
   if (a.chunks > 0 && rc == CONVFWD_OK) rc = launched(grad[d->dtype](a, s));

@@ -17,10 +17,10 @@
 // those that matter to 24 bits are added in fp32.  A bf16 input is one part, an
 // fp16 input two.  bf16 has fp32's range, so nothing overflows on the way.
 //
-// A wave owns 16 columns of the state and keeps them in fp32 accumulators.  Rows of
-// accumulator tiles are dealt so that two tiles together are one operand of the next
-// product, in its natural order, without leaving their lane: row m of tile t of a
-// matrix is row_of(t, m) of it.
+// A workgroup of four waves carries 16 columns of one head's state (or of its
+// gradient).  Wave w computes rows 16 w .. + 15 of r, x and y, and a quarter of the
+// state's rows; the parts of what one step makes and the next one contracts over go
+// through LDS, column by column, so that an operand is one 16-byte read.
 #pragma once
 
 #include "conv_device.h"
@@ -40,9 +40,7 @@ typedef __bf16 bf164_t __attribute__((ext_vector_type(4)));
 // The wave's number in its workgroup, known to be one for all lanes.
 __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
 
-__device__ __forceinline__ int row_of(int t, int m) { return 32 * (t >> 1) + 8 * (m >> 2) + 4 * (t & 1) + (m & 3); }
-
-// The six (tile, step of 32) pairs that hold something of a strictly or non-strictly
+// The six (16-row tile, step of 32) pairs that hold something of a strictly or non-strictly
 // lower triangle, and of its transpose.
 __device__ constexpr int low_t(int f) { return f < 2 ? f : f < 4 ? 2 : 3; }
 __device__ constexpr int low_s(int f) { return f < 2 ? 0 : f & 1; }
@@ -93,13 +91,6 @@ __device__ __forceinline__ f32x4_t mma(const Parts<NA>& a, const Parts<NB>& b, f
   return acc;
 }
 
-// Two accumulator tiles, scaled row by row, as one operand.
-template <int N>
-__device__ __forceinline__ Parts<N> operand(const f32x4_t& a, const f32x4_t& b) {
-  const float x[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  return split<N>(x);
-}
-
 // What is not wanted is selected away, not multiplied by zero.
 __device__ __forceinline__ float times(float factor, float x) { return factor == 0.f ? 0.f : factor * x; }
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
@@ -111,60 +102,65 @@ struct RowsAt {
   static constexpr int stride = DK + 8, part = kChunk * stride;
 };
 
-// 8 elements of a row as they come from memory, zero outside.
+// 8 elements of a row as they come from memory; they stay raw until they are used, so
+// that a load in flight is not waited for.  The row is 16-byte aligned and has d elements, a
+// multiple of 8; past its end they are any of its elements, and `parts` selects zero.
 template <typename T>
-struct Piece {
-  T v[8];
-};
-template <typename T>
-__device__ __forceinline__ Piece<T> load_piece(const T* row, int d0, int d, bool in, int vec) {
-  Piece<T> p;
-  if (in && vec && d0 < d) {
-    struct alignas(16) Raw { T v[8]; };
-    const Raw r = *(const Raw*)(row + d0);
+struct Raw8 {
+  convfwd::u32x4_t w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* row, int d0, int d) {
+    const convfwd::u32x4_t* p = (const convfwd::u32x4_t*)(row + min(d0, d - 8));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) p.v[e] = r.v[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p.v[e] = in && d0 + e < d ? row[d0 + e] : (T)0.f;
+    for (unsigned k = 0; k < sizeof(T) / 2; ++k) w[k] = p[k];
   }
-  return p;
-}
-template <typename T>
-__device__ __forceinline__ Parts<InParts<T>::n> parts_of(const Piece<T>& p) {
-  float x[8];
+  __device__ __forceinline__ void get(float (&x)[8], bool in) const {
+    T v[8];
+    __builtin_memcpy(v, w, sizeof(v));
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = to_f32(p.v[e]);
-  return split<InParts<T>::n>(x);
+    for (int e = 0; e < 8; ++e) x[e] = in ? to_f32(v[e]) : 0.f;
+  }
+  __device__ __forceinline__ Parts<InParts<T>::n> parts(bool in) const {
+    float x[8];
+    get(x, in);
+    return split<InParts<T>::n>(x);
+  }
+};
+template <>
+__device__ __forceinline__ Parts<1> Raw8<__bf16>::parts(bool in) const {
+  Parts<1> r;
+  convfwd::u32x4_t v = w[0];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = in ? v[k] : 0u;
+  __builtin_memcpy(&r.p[0], &v, 16);
+  return r;
 }
 
-// Pieces of a chunk's rows that a thread of `threads` holds on their way to LDS.
+// Pieces of a chunk's rows that a thread of `threads` holds on their way to LDS.  Rows past T
+// repeat the last one: what is made of them meets a beta or a gradient of zero.
 template <typename T, int DK, int THREADS>
 struct Rows64 {
-  static constexpr int pieces = kChunk * (DK / 8), each = (pieces + THREADS - 1) / THREADS;
-  Piece<T> p[each];
-  __device__ __forceinline__ void load(const Heads& h, int b, int head, int t0, int t, int d, int vec) {
+  static constexpr int pieces = kChunk * (DK / 8), each = pieces / THREADS;
+  static_assert(pieces % THREADS == 0, "whole rounds");
+  Raw8<T> p[each];
+  __device__ __forceinline__ static int row(int k) { return (threadIdx.x + k * THREADS) / (DK / 8); }
+  __device__ __forceinline__ static int d0(int k) { return (threadIdx.x + k * THREADS) % (DK / 8) * 8; }
+  __device__ __forceinline__ void load(const Heads& h, int b, int head, int t0, int t, int d) {
     const T* base = (const T*)h.p + b * h.sb + head * h.sh;
 #pragma unroll
-    for (int k = 0; k < each; ++k) {
-      const int i = threadIdx.x + k * THREADS, row = i / (DK / 8), d0 = i % (DK / 8) * 8;
-      p[k] = load_piece<T>(base + (int64_t)(t0 + row) * h.st, d0, d, i < pieces && t0 + row < t, vec);
-    }
+    for (int k = 0; k < each; ++k) p[k].load(base + (int64_t)min(t0 + row(k), t - 1) * h.st, d0(k), d);
   }
-  __device__ __forceinline__ void put(__bf16* lds) const {
+  __device__ __forceinline__ void put(__bf16* lds, int d) const {
 #pragma unroll
     for (int k = 0; k < each; ++k) {
-      const int i = threadIdx.x + k * THREADS, row = i / (DK / 8), d0 = i % (DK / 8) * 8;
-      if (i >= pieces) continue;
-      const auto q = parts_of<T>(p[k]);
+      const auto q = p[k].parts(d0(k) < d);
 #pragma unroll
       for (int n = 0; n < InParts<T>::n; ++n)
-        *(bf168_t*)(lds + n * RowsAt<DK>::part + row * RowsAt<DK>::stride + d0) = q.p[n];
+        *(bf168_t*)(lds + n * RowsAt<DK>::part + row(k) * RowsAt<DK>::stride + d0(k)) = q.p[n];
     }
   }
 };
 
-// 8 neighbouring elements of a row of 16-bit values in LDS: an operand in its natural order.
+// 8 neighbouring elements of a row (or column) of parts in LDS: an operand.
 template <int N>
 __device__ __forceinline__ Parts<N> natural(const __bf16* at, int part) {
   Parts<N> r;
@@ -201,22 +197,6 @@ __device__ __forceinline__ void keep(Parts<N>& a, int k0, int lo, int hi) {
 }
 
 __device__ __forceinline__ int64_t chunk_index(const DeltaArgs& a, int bh, int c) { return (int64_t)bh * a.chunks + c; }
-
-// 16-byte pieces of a contiguous stretch, on their way to LDS.  Threads past the end repeat the last piece.
-template <int BYTES, int THREADS>
-struct Stretch {
-  static constexpr int pieces = BYTES / 16, each = (pieces + THREADS - 1) / THREADS;
-  convfwd::u32x4_t p[each];
-  __device__ __forceinline__ static int at(int k) { return min((int)threadIdx.x + k * THREADS, pieces - 1); }
-  __device__ __forceinline__ void load(const void* from) {
-#pragma unroll
-    for (int k = 0; k < each; ++k) p[k] = ((const convfwd::u32x4_t*)from)[at(k)];
-  }
-  __device__ __forceinline__ void put(void* to) const {
-#pragma unroll
-    for (int k = 0; k < each; ++k) ((convfwd::u32x4_t*)to)[at(k)] = p[k];
-  }
-};
 
 // Workgroups of one head lie on one die (ids are dealt round-robin to 8), so that they share its L2.
 __device__ __forceinline__ bool head_of(int heads, int blocks, int& bh, int& cb) {

@@ -169,7 +169,7 @@ struct Grad {
     const float* states = a.states_in + (((int64_t)b * a.chunks + c) * a.hv + h) * a.dk * a.dv;
     const float* dstate = a.w.dstate + at * a.dk * a.dvp;
     const float *xr = a.w.x + (at * kChunk + row) * a.dvp, *zr = a.w.z + (at * kChunk + row) * a.dvp;
-    const T* dy = (const T*)a.dy.p + b * a.dy.sb + (int64_t)(c * kChunk + row) * a.dy.st + h * a.dy.sh;
+    const T* dy = (const T*)a.dy.p + b * a.dy.sb + (int64_t)min(c * kChunk + row, a.t - 1) * a.dy.st + h * a.dy.sh;
     const bool in = c * kChunk + row < a.t, whole = a.dv % 4 == 0;
     float dot = 0.f, db = 0.f;
     __syncthreads();
@@ -187,7 +187,10 @@ struct Grad {
         dx[e] = beta * z;
         db = fmaf(x, z, db);
       }
-      const Parts<NP> yp = parts_of<T>(load_piece<T>(dy, v, a.dv, in, 0));
+      float yv[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) yv[e] = in && v + e < a.dv ? to_f32(dy[v + e]) : 0.f;
+      const Parts<NP> yp = split<NP>(yv);
       const Parts<kParts> up = split<kParts>(u), xp = split<kParts>(dx);
       __syncthreads();  // what is read of the slice before
       put_state(st);
@@ -292,14 +295,18 @@ __global__ __launch_bounds__(kT) void delta_grad_kernel(DeltaArgs a) {
   bool wild = false;
   {
     Rows64<T, DK, kT> k, q;
-    k.load(a.k, b, hk, c * kChunk, a.t, a.dk, a.vec);
-    q.load(a.q, b, hk, c * kChunk, a.t, a.dk, a.vec);
+    k.load(a.k, b, hk, c * kChunk, a.t, a.dkp);
+    q.load(a.q, b, hk, c * kChunk, a.t, a.dkp);
 #pragma unroll
-    for (int i = 0; i < Rows64<T, DK, kT>::each; ++i)
+    for (int i = 0; i < Rows64<T, DK, kT>::each; ++i) {
+      float x[8], y[8];
+      k.p[i].get(x, true);
+      q.p[i].get(y, true);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) wild = wild || !finite(to_f32(k.p[i].v[e])) || !finite(to_f32(q.p[i].v[e]));
-    k.put(s.k);
-    q.put(s.q);
+      for (int e = 0; e < 8; ++e) wild = wild || !finite(x[e]) || !finite(y[e]);
+    }
+    k.put(s.k, a.dkp);
+    q.put(s.q, a.dkp);
   }
   wild = __syncthreads_or(wild);
   const int share = a.hv / a.hk;

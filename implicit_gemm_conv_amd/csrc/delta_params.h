@@ -33,12 +33,13 @@ struct Work {
   float* x;        // backward: x and its counterpart, (B * Hv, chunks * 64, dvp)
   float* z;
   float* dstate;   // backward: the gradient of the state after each chunk, (.., Dk, dvp)
+  void *q, *k;     // (B, T, Hk, dkp) copies, where q or k are not 16-byte aligned rows of whole 16 bytes
 };
 
 struct DeltaArgs {
   int b, t, hk, hv, dk, dv, dtype;
   int chunks, dvp;  // ceil(T / 64); Dv rounded up to 32
-  int vec;          // q and k can be read in pieces of 8 elements, 16-byte aligned
+  int dkp;          // elements of a row of q and k as the kernels read them: Dk rounded up to 8
   float scale;
   Heads q, k, v, dy;
   const float *log_decay, *beta, *h0, *states_in, *dh_last;
@@ -58,6 +59,7 @@ struct DeltaStepArgs {
   void* y;
 };
 
+hipError_t launch_delta_pack(const DeltaArgs& a, const Heads& q, const Heads& k, hipStream_t s);
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t s);
 // One launcher for each type:
 //   fwd     y, the states

@@ -1,0 +1,147 @@
+// delta_team.h -- what the forward and the backward recurrence of the gated delta
+// rule share: where a lane of the four waves stands, the columns of parts in LDS, and
+// the operands that a wave fetches for a chunk.
+#pragma once
+
+#include "delta_device.h"
+
+namespace convdelta {
+
+constexpr int kTeam = 256;  // four waves
+
+// Columns of parts: [part][16 columns][ld].  The 8 spare elements spread the columns over the banks.
+template <int LEN>
+struct ColsAt {
+  static constexpr int ld = LEN + 8, part = 16 * ld;
+};
+
+template <typename T, int DK>
+struct Team {
+  static constexpr int NP = InParts<T>::n, KS = DK / 32, DT = DK / 16;
+  static constexpr int YP = NP == 3 ? 3 : 2;                // parts that an output of type T can tell apart
+  static constexpr int own = (DT + 3) / 4;                  // 16-row tiles of the state a wave holds
+  typedef ColsAt<DK> State;
+  typedef ColsAt<kChunk> Rows;
+
+  const DeltaArgs& a;
+  int wave, m, q4, lane, b, h, hk, bh, col, vcol;
+  bool live;
+
+  __device__ __forceinline__ Team(const DeltaArgs& a_, int bh_, int cb) : a(a_), bh(bh_) {
+    lane = threadIdx.x % 64;
+    wave = wave_id();
+    m = lane % 16;
+    q4 = lane / 16;
+    b = bh / a.hv;
+    h = bh % a.hv;
+    hk = h / (a.hv / a.hk);
+    col = cb * 16 + m;
+    live = col < a.dv;
+    vcol = min(col, a.dv - 1);
+  }
+  __device__ __forceinline__ int tile(int j) const { return wave * own + j; }       // of the state
+  __device__ __forceinline__ int row() const { return 16 * wave + 4 * q4; }         // the first of the lane's four
+
+  // the lane's 4 x own values of a (Dk, Dv) state, zero outside
+  __device__ __forceinline__ void load_state(const float* from, f32x4_t (&s)[own]) const {
+#pragma unroll
+    for (int j = 0; j < own; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = 16 * tile(j) + 4 * q4 + r;
+        s[j][r] = from && live && d < a.dk ? from[(int64_t)d * a.dv + col] : 0.f;
+      }
+  }
+  __device__ __forceinline__ void store_state(float* to, int64_t ld, bool in, const f32x4_t (&s)[own]) const {
+    if (!in) return;
+#pragma unroll
+    for (int j = 0; j < own; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = 16 * tile(j) + 4 * q4 + r;
+        if (d < a.dk) to[d * ld + col] = s[j][r];
+      }
+  }
+  // four neighbouring rows of the lane's column, as parts
+  template <int N, typename AT>
+  __device__ __forceinline__ void put(__bf16* cols, int at, const f32x4_t& x) const {
+    bf164_t o[N];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      __bf16 w[N];
+      split_one<N>(x[r], w);
+#pragma unroll
+      for (int n = 0; n < N; ++n) o[n][r] = w[n];
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) *(bf164_t*)(cols + n * AT::part + m * AT::ld + at) = o[n];
+  }
+  __device__ __forceinline__ void put_state(__bf16* cols, const f32x4_t (&s)[own]) const {
+#pragma unroll
+    for (int j = 0; j < own; ++j)
+      if (tile(j) < DT) put<kParts, State>(cols, 16 * tile(j) + 4 * q4, s[j]);
+  }
+  // the operand of step k of a contraction over the state's rows, or over the chunk's
+  template <int N, typename AT>
+  __device__ __forceinline__ Parts<N> get(const __bf16* cols, int k) const {
+    return natural<N>(cols + m * AT::ld + 32 * k + 8 * q4, AT::part);
+  }
+  // columns of state tile t of a chunk's rows in LDS, as rows; step k over the chunk's rows
+  __device__ __forceinline__ Parts<NP> cols_of(const __bf16* x, int t, int k) const {
+    return transposed<NP>(x + (32 * k + 8 * q4 + m / 4) * RowsAt<DK>::stride + 16 * t + 4 * (m % 4), RowsAt<DK>::stride,
+                          RowsAt<DK>::part);
+  }
+  // this wave's rows of q or k
+  __device__ __forceinline__ void load_rows(const Heads& x, int c, Raw8<T> (&to)[KS]) const {
+    const T* p = (const T*)x.p + b * x.sb + hk * x.sh + (int64_t)min(c * kChunk + 16 * wave + m, a.t - 1) * x.st;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) to[k].load(p, 32 * k + 8 * q4, a.dkp);
+  }
+  __device__ __forceinline__ Parts<NP> rows_of(const Raw8<T> (&x)[KS], int k) const { return x[k].parts(32 * k + 8 * q4 < a.dkp); }
+  // ... into LDS, row by row
+  __device__ __forceinline__ void put_rows(__bf16* to, const Raw8<T> (&x)[KS]) const {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      const Parts<NP> p = rows_of(x, k);
+#pragma unroll
+      for (int n = 0; n < NP; ++n) *(bf168_t*)(to + n * RowsAt<DK>::part + (16 * wave + m) * RowsAt<DK>::stride + 32 * k + 8 * q4) = p.p[n];
+    }
+  }
+  // the lane's four rows of its column of v, y's gradient, ...
+  __device__ __forceinline__ void load_col(const Heads& x, int c, T (&to)[4]) const {
+    const T* p = (const T*)x.p + b * x.sb + h * x.sh + vcol;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) to[r] = p[(int64_t)min(c * kChunk + row() + r, a.t - 1) * x.st];
+  }
+  __device__ __forceinline__ f32x4_t load_gate(int which, int c) const {
+    return *(const f32x4_t*)(a.w.rows + (chunk_index(a, bh, c) * 4 + which) * kChunk + row());
+  }
+  // this wave's operands of a triangular matrix: of a lower one steps 0 and, from wave 2 on, 1; of an
+  // upper one (UP) step 1 and, up to wave 1, 0
+  template <bool UP>
+  __device__ __forceinline__ bool has(int k) const { return UP ? k >= wave / 2 : k <= wave / 2; }
+  template <bool UP, int N>
+  __device__ __forceinline__ void load_matrix(const char* x, int c, Parts<N> (&to)[2]) const {
+    const char* p = x + chunk_index(a, bh, c) * kMatrix + lane * 16;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      // the operand's number in the order of low_t, low_s (up_t, up_s); one that is not there repeats the other
+      const int f = UP ? (wave < 2 ? 2 * wave + k : wave + 2) : (wave < 2 ? wave : 2 * wave - 2 + k);
+#pragma unroll
+      for (int n = 0; n < N; ++n) to[k].p[n] = *(const bf168_t*)(p + (f * kParts + n) * kFrag);
+    }
+  }
+};
+
+// acc += A B where the first N of B's parts are used.
+template <int N, int NA, int NB>
+__device__ __forceinline__ f32x4_t mma_first(const Parts<NA>& a, const Parts<NB>& b, f32x4_t acc) {
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = N - 1; j >= 0; --j)
+      if (i + j < (N > NA ? N : NA)) acc = convfwd::mfma16x16x32(a.p[i], b.p[j], acc);
+  return acc;
+}
+
+}  // namespace convdelta

@@ -14,7 +14,7 @@ template <bool UP>
 __device__ __forceinline__ void put_matrix(const float* m, char* to) {
   const int wave = wave_id(), lane = threadIdx.x % 64, q = lane / 16;
   for (int f = wave; f < kTri; f += kT / 64) {
-    const int row = row_of(UP ? up_t(f) : low_t(f), lane % 16), k0 = 32 * (UP ? up_s(f) : low_s(f)) + 8 * q;
+    const int row = 16 * (UP ? up_t(f) : low_t(f)) + lane % 16, k0 = 32 * (UP ? up_s(f) : low_s(f)) + 8 * q;
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = UP ? m[(k0 + e) * kLd + row] : m[row * kLd + k0 + e];
@@ -37,8 +37,8 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
   const int64_t at = chunk_index(a, bh, c);
   {
     Rows64<T, DK, kT> k, q;
-    k.load(a.k, b, h / (a.hv / a.hk), t0, a.t, a.dk, a.vec);
-    q.load(a.q, b, h / (a.hv / a.hk), t0, a.t, a.dk, a.vec);
+    k.load(a.k, b, h / (a.hv / a.hk), t0, a.t, a.dkp);
+    q.load(a.q, b, h / (a.hv / a.hk), t0, a.t, a.dkp);
     if (wave == 0) {
       // running sums over the rows, a lane a row; rows past T decay nothing and write nothing
       const int t = t0 + lane;
@@ -76,8 +76,8 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
         a.w.seq[at * kChunk + lane] = n;
       }
     }
-    k.put(ks);
-    q.put(qs);
+    k.put(ks, a.dkp);
+    q.put(qs, a.dkp);
   }
   __syncthreads();
   // wave w: rows 16 w .. + 15 of k k^T and q k^T
@@ -129,7 +129,33 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
   }
 }
 
+// q and k of other alignments or sizes, copied to rows of dkp elements, the spare ones zero.
+template <typename T>
+__global__ __launch_bounds__(kT) void delta_pack_kernel(DeltaArgs a, Heads q, Heads k, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * kT + threadIdx.x;
+  if (i >= n) return;
+  const int pieces = a.dkp / 8, d0 = (int)(i % pieces) * 8;
+  const int64_t r = i / pieces, h = r % a.hk, t = r / a.hk % a.t, b = r / a.hk / a.t;
+  const T *fq = (const T*)q.p + b * q.sb + t * q.st + h * q.sh, *fk = (const T*)k.p + b * k.sb + t * k.st + h * k.sh;
+  T vq[8], vk[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    vq[e] = d0 + e < a.dk ? fq[d0 + e] : (T)0.f;
+    vk[e] = d0 + e < a.dk ? fk[d0 + e] : (T)0.f;
+  }
+  __builtin_memcpy(__builtin_assume_aligned((T*)a.w.q + i * 8, 16), vq, sizeof(vq));
+  __builtin_memcpy(__builtin_assume_aligned((T*)a.w.k + i * 8, 16), vk, sizeof(vk));
+}
+
 }  // namespace
+
+hipError_t launch_delta_pack(const DeltaArgs& a, const Heads& q, const Heads& k, hipStream_t s) {
+  const int64_t n = (int64_t)a.b * a.t * a.hk * (a.dkp / 8);
+  return for_type(a.dtype, [&](auto t) {
+    hipLaunchKernelGGL((delta_pack_kernel<decltype(t)>), dim3((unsigned)((n + kT - 1) / kT)), dim3(kT), 0, s, a, q, k, n);
+    return hipGetLastError();
+  });
+}
 
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t s) {
   return for_type(a.dtype, [&](auto t) {
