@@ -1,131 +1,203 @@
 // k_delta_prep.hip -- gated delta rule, what a chunk of 64 rows holds that no
 // state enters: the decays, H and the decayed q k^T (see delta_device.h), one
 // workgroup a chunk and value head, all chunks at once.
-#include "delta_device.h"
+#include "delta_team.h"
 
 namespace convdelta {
 
 namespace {
 
-constexpr int kT = 256, kLd = kChunk + 1;
+constexpr int kT = 256, kLd = kChunk + 1, kLdX = 17;
 
-// Writes a 64x64 matrix of LDS as operands of a product with its rows (or, UP, its columns) as rows.
-template <bool UP>
+// Where row i, columns j0 .. + 7 (or, UP, column i, rows j0 .. + 7) of a lower triangle start: in place, or (H) in the
+// block across the diagonal.
+template <bool UP, bool H>
+__device__ __forceinline__ const float* place(const float* m, int i, int j0) {
+  const int bi = i / 16, bj = j0 / 16;
+  if (H && bi != bj) return UP ? m + (16 * bi + j0 % 16) * kLd + 16 * bj + i % 16 : m + (16 * bj + i % 16) * kLd + 16 * bi + j0 % 16;
+  return UP ? m + j0 * kLd + i : m + i * kLd + j0;
+}
+
+// Writes a 64x64 lower triangle of LDS as operands of a product with its rows (or, UP, its columns) as rows.
+template <bool UP, bool H>
 __device__ __forceinline__ void put_matrix(const float* m, char* to) {
   const int wave = wave_id(), lane = threadIdx.x % 64, q = lane / 16;
   for (int f = wave; f < kTri; f += kT / 64) {
     const int row = 16 * (UP ? up_t(f) : low_t(f)) + lane % 16, k0 = 32 * (UP ? up_s(f) : low_s(f)) + 8 * q;
+    const float* from = place<UP, H>(m, row, k0);
+    const bool none = UP ? k0 / 16 < row / 16 : k0 / 16 > row / 16;
     float x[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = UP ? m[(k0 + e) * kLd + row] : m[row * kLd + k0 + e];
+    for (int e = 0; e < 8; ++e) x[e] = none ? 0.f : from[UP ? e * kLd : e];
     const Parts<kParts> p = split<kParts>(x);
 #pragma unroll
     for (int n = 0; n < kParts; ++n) *(bf168_t*)(to + (f * kParts + n) * kFrag + lane * 16) = p.p[n];
   }
 }
 
-template <typename T, int DK>
-__global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backward) {
-  constexpr int NP = InParts<T>::n;
-  __shared__ __attribute__((aligned(16))) __bf16 ks[NP * RowsAt<DK>::part], qs[NP * RowsAt<DK>::part];
-  __shared__ float low[kChunk * kLd], read[kChunk * kLd];
-  __shared__ double sums[kChunk];
-  __shared__ float beta[kChunk];
-  __shared__ int seq[kChunk];
-  const int c = blockIdx.x % a.chunks, bh = blockIdx.x / a.chunks, b = bh / a.hv, h = bh % a.hv, t0 = c * kChunk;
-  const int wave = wave_id(), lane = threadIdx.x % 64;
-  const int64_t at = chunk_index(a, bh, c);
-  {
-    Rows64<T, DK, kT> k, q;
-    k.load(a.k, b, h / (a.hv / a.hk), t0, a.t, a.dkp);
-    q.load(a.q, b, h / (a.hv / a.hk), t0, a.t, a.dkp);
-    if (wave == 0) {
-      // running sums over the rows, a lane a row; rows past T decay nothing and write nothing
-      const int t = t0 + lane;
-      const bool in = t < a.t;
-      const int64_t row = ((int64_t)b * a.t + t) * a.hv + h;
-      const float bt = in ? a.beta[row] : 0.f;
-      // a decay of nothing at all is exp(-10^4), which is zero too and leaves differences of sums finite
-      float g = in ? a.log_decay[row] : 0.f;
-      g = g < -1e4f ? -1e4f : g;
-      const int start = in && a.starts ? a.starts[(int64_t)b * a.t + t] != 0 : 0;
-      double sum = g;
-      int n = start;
-      for (int o = 1; o < 64; o <<= 1) {
-        const int m = __shfl_up(n, o);
-        if (lane >= o) n += m;
-      }
-      // within a sequence only: what is not finite must not reach the next one's differences
-      for (int o = 1; o < 64; o <<= 1) {
-        const double s = __shfl_up(sum, o);
-        const int m = __shfl_up(n, o);
-        if (lane >= o && m == n) sum += s;
-      }
-      const double all = __shfl(sum, 63);
-      const int last = __shfl(n, 63);
-      sums[lane] = sum;
-      seq[lane] = n;
-      beta[lane] = bt;
-      float* rows = a.w.rows + at * 4 * kChunk;
-      rows[lane] = n == 0 ? expf((float)sum) : 0.f;
-      rows[kChunk + lane] = n == last ? expf((float)(all - sum)) : 0.f;
-      rows[2 * kChunk + lane] = bt;
-      rows[3 * kChunk + lane] = start ? 0.f : expf(g);
-      if (backward) {
-        a.w.sums[at * kChunk + lane] = sum;
-        a.w.seq[at * kChunk + lane] = n;
-      }
-    }
-    k.put(ks, a.dkp);
-    q.put(qs, a.dkp);
-  }
-  __syncthreads();
-  // wave w: rows 16 w .. + 15 of k k^T and q k^T
-  {
-    const int q4 = lane / 16, m = lane % 16;
-    for (int tj = 0; tj < 4; ++tj) {
-      f32x4_t kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
-      if (tj <= wave)
+// D += A B for 16x16 blocks in LDS, A's rows kLd apart and its columns scaled (a zero of A stays zero, whatever the
+// scale): fp32 matrix instructions, in each of which lane l supplies A[l % 16][k] and B[k][l % 16] for k = 4 step + l / 16.
+__device__ __forceinline__ f32x4_t block_product(const float* a, const float* scale, const float* b, int ldb, f32x4_t acc) {
+  const int m = threadIdx.x % 16, q4 = threadIdx.x % 64 / 16;
 #pragma unroll
-        for (int s = 0; s < DK / 32; ++s) {
-          const int col = 32 * s + 8 * q4;
-          const auto kb = natural<NP>(ks + (16 * tj + m) * RowsAt<DK>::stride + col, RowsAt<DK>::part);
-          kk = mma(natural<NP>(ks + (16 * wave + m) * RowsAt<DK>::stride + col, RowsAt<DK>::part), kb, kk);
-          qk = mma(natural<NP>(qs + (16 * wave + m) * RowsAt<DK>::stride + col, RowsAt<DK>::part), kb, qk);
-        }
-      const int j = 16 * tj + m;
+  for (int k = 0; k < 4; ++k)
+    acc = __builtin_amdgcn_mfma_f32_16x16x4f32(times(a[m * kLd + 4 * k + q4], scale[4 * k + q4]), b[(4 * k + q4) * ldb + m],
+                                               acc, 0, 0, 0);
+  return acc;
+}
+
+// L (64x64, strictly lower, the rest zero) becomes H = -(I + L beta)^-1 L, whose rows are
+// H_i = -L_i - sum over k < i of L_ik beta_k H_k.  Blocks of 16: the diagonal ones row by row, each by a wave,
+// then the ones at distance 1, 2 and 3 below them:
+//   X_ij = -L_ij - sum over j <= k < i of L_ik beta_k H_kj,  H_ij = X_ij + H_ii beta_i X_ij.
+// The diagonal blocks take L's place; the others, whose L is needed to the end, go across the diagonal.  `x` is room
+// for the X of one distance.
+__device__ __forceinline__ void invert(float* l, const float* beta, float* x) {
+  const int wave = wave_id(), lane = threadIdx.x % 64, m = lane % 16, q4 = lane / 16;
+  {
+    // column m of the diagonal block; what lies on and above the diagonal stays zero, whatever a row holds
+    float* d = l + 16 * wave * (kLd + 1);
+    const float* bt = beta + 16 * wave;
+    float bh[16], hc[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s[2] = {-d[i * kLd + m], 0.f};
+#pragma unroll
+      for (int k = 0; k < i; ++k) s[k & 1] = fmaf(-d[i * kLd + k], bh[k], s[k & 1]);
+      hc[i] = m < i ? s[0] + s[1] : 0.f;
+      bh[i] = m < i ? bt[i] * hc[i] : 0.f;
+    }
+    if (q4 == 0)  // the four quarters of the wave compute the same
+#pragma unroll
+      for (int i = 0; i < 16; ++i) d[i * kLd + m] = hc[i];
+  }
+#pragma unroll
+  for (int far = 1; far < 4; ++far) {
+    __syncthreads();
+    const int bi = wave + far, bj = wave;  // this wave's block, where there is one
+    const float* from = l + 16 * bi * kLd + 16 * bj;
+    float* to = l + 16 * bj * kLd + 16 * bi;
+    f32x4_t xs;
+    if (bi < 4) {
+      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < far; ++k)
+        acc = block_product(from + 16 * k, beta + 16 * (bj + k), k ? to - 16 * (far - k) : l + 16 * bj * (kLd + 1), kLd, acc);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 16 * wave + 4 * q4 + r;
-        const bool same = j <= i && seq[i] == seq[j];
-        const float d = same ? expf((float)(sums[i] - sums[j])) : 0.f;
-        low[i * kLd + j] = same && j < i ? d * kk[r] : 0.f;
-        read[i * kLd + j] = same ? d * qk[r] : 0.f;
+        xs[r] = -from[(4 * q4 + r) * kLd + m] - acc[r];
+        x[(16 * wave + 4 * q4 + r) * kLdX + m] = xs[r];
       }
     }
-  }
-  __syncthreads();
-  // column `lane` of H, row by row: h_i = -L_i - sum over k < i of L_ik beta_k h_k
-  if (wave == 0) {
-    float hc[kChunk], bh_[kChunk];
+    __syncthreads();
+    if (bi < 4) {
+      xs = block_product(l + 16 * bi * (kLd + 1), beta + 16 * bi, x + 16 * wave * kLdX, kLdX, xs);
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      float acc = -low[i * kLd + lane];
-#pragma unroll
-      for (int k = 0; k < i; ++k) acc = fmaf(-low[i * kLd + k], bh_[k], acc);
-      hc[i] = lane < i ? acc : 0.f;
-      bh_[i] = lane < i ? beta[i] * acc : 0.f;
+      for (int r = 0; r < 4; ++r) to[(4 * q4 + r) * kLd + m] = xs[r];
     }
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) low[i * kLd + lane] = hc[i];
   }
   __syncthreads();
-  put_matrix<false>(low, a.w.solve + at * kMatrix);
+}
+
+template <typename T, int DK>
+struct PrepLds {
+  union {
+    __bf16 k[InParts<T>::n * RowsAt<DK>::part];
+    struct {
+      float low[kChunk * kLd], read[kChunk * kLd];
+    };
+  };
+  float x[3 * 16 * kLdX];
+  double sums[kChunk];
+  float beta[kChunk];
+  int seq[kChunk];
+};
+
+template <typename T, int DK>
+__global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backward) {
+  constexpr int NP = InParts<T>::n, KS = DK / 32;
+  typedef Team<T, DK> F;
+  __shared__ __attribute__((aligned(16))) PrepLds<T, DK> s;
+  const int c = blockIdx.x % a.chunks, t0 = c * kChunk;
+  const F f(a, blockIdx.x / a.chunks, 0);
+  const int wave = f.wave, lane = f.lane, m = f.m, q4 = f.q4;
+  const int64_t at = chunk_index(a, f.bh, c);
+  Raw8<T> k[KS], q[KS];
+  f.load_rows(a.k, c, k);
+  f.load_rows(a.q, c, q);
+  if (wave == 0) {
+    // running sums over the rows, a lane a row; rows past T decay nothing and write nothing
+    const int t = t0 + lane;
+    const bool in = t < a.t;
+    const int64_t row = ((int64_t)f.b * a.t + t) * a.hv + f.h;
+    const float bt = in ? a.beta[row] : 0.f;
+    // a decay of nothing at all is exp(-10^4), which is zero too and leaves differences of sums finite
+    float g = in ? a.log_decay[row] : 0.f;
+    g = g < -1e4f ? -1e4f : g;
+    const int start = in && a.starts ? a.starts[(int64_t)f.b * a.t + t] != 0 : 0;
+    double sum = g;
+    int n = start;
+    for (int o = 1; o < 64; o <<= 1) {
+      const int p = __shfl_up(n, o);
+      if (lane >= o) n += p;
+    }
+    // within a sequence only: what is not finite must not reach the next one's differences
+    for (int o = 1; o < 64; o <<= 1) {
+      const double p = __shfl_up(sum, o);
+      const int pn = __shfl_up(n, o);
+      if (lane >= o && pn == n) sum += p;
+    }
+    const double all = __shfl(sum, 63);
+    const int last = __shfl(n, 63);
+    s.sums[lane] = sum;
+    s.seq[lane] = n;
+    s.beta[lane] = bt;
+    float* rows = a.w.rows + at * 4 * kChunk;
+    rows[lane] = n == 0 ? expf((float)sum) : 0.f;
+    rows[kChunk + lane] = n == last ? expf((float)(all - sum)) : 0.f;
+    rows[2 * kChunk + lane] = bt;
+    rows[3 * kChunk + lane] = start ? 0.f : expf(g);
+    if (backward) {
+      a.w.sums[at * kChunk + lane] = sum;
+      a.w.seq[at * kChunk + lane] = n;
+    }
+  }
+  f.put_rows(s.k, k);
+  __syncthreads();
+  // this wave's rows of k k^T and q k^T
+  f32x4_t kk[4], qk[4];
+#pragma unroll
+  for (int tj = 0; tj < 4; ++tj) {
+    kk[tj] = qk[tj] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (tj <= wave)
+#pragma unroll
+      for (int e = 0; e < KS; ++e) {
+        const auto kb = natural<NP>(s.k + (16 * tj + m) * RowsAt<DK>::stride + 32 * e + 8 * q4, RowsAt<DK>::part);
+        kk[tj] = mma(f.rows_of(k, e), kb, kk[tj]);
+        qk[tj] = mma(f.rows_of(q, e), kb, qk[tj]);
+      }
+  }
+  __syncthreads();  // k is read: its room is the matrices' now
+#pragma unroll
+  for (int tj = 0; tj < 4; ++tj) {
+    const int j = 16 * tj + m;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = f.row() + r;
+      const bool same = j <= i && s.seq[i] == s.seq[j];
+      const float d = same ? expf((float)(s.sums[i] - s.sums[j])) : 0.f;
+      s.low[i * kLd + j] = same && j < i ? d * kk[tj][r] : 0.f;
+      s.read[i * kLd + j] = same ? d * qk[tj][r] : 0.f;
+    }
+  }
+  __syncthreads();
+  invert(s.low, s.beta, s.x);
+  put_matrix<false, true>(s.low, a.w.solve + at * kMatrix);
   if (!backward) {
-    put_matrix<false>(read, a.w.read + at * kMatrix);
+    put_matrix<false, false>(s.read, a.w.read + at * kMatrix);
   } else {
-    put_matrix<true>(low, a.w.solve_t + at * kMatrix);
-    put_matrix<true>(read, a.w.read_t + at * kMatrix);
+    put_matrix<true, true>(s.low, a.w.solve_t + at * kMatrix);
+    put_matrix<true, false>(s.read, a.w.read_t + at * kMatrix);
   }
 }
 
