@@ -28,6 +28,8 @@ int check(const convdelta_desc* d) {
   const int64_t heads = ((int64_t)d->b * d->hv + 7) / 8 * 8;
   if (d->t >= 1 << 30 || d->hv >= lim || blocks >= lim || heads >= lim || heads * blocks >= lim) return CONVFWD_ERR_TOO_LARGE;
   if (chunks * heads >= lim || chunks * heads * blocks >= lim) return CONVFWD_ERR_TOO_LARGE;
+  // offsets of 32 bits: 64 rows of v or y, 128 rows of a state
+  if ((int64_t)d->hv * d->dv >= (int64_t)1 << 23 || d->dv >= 1 << 22) return CONVFWD_ERR_TOO_LARGE;
   // ... and one for each 2048 elements of q and k
   if (d->hk * (int64_t)d->b >= lim || d->hk * (int64_t)d->b * chunks * 4 >= lim) return CONVFWD_ERR_TOO_LARGE;
   return CONVFWD_OK;
@@ -56,7 +58,6 @@ int64_t lay_out(const convdelta_desc* d, bool backward, char* base, Work* w) {
     w->read_t = take(kMatrix);
     w->sums = (double*)take(8 * kChunk);
     w->seq = (int*)take(4 * kChunk);
-    w->x = (float*)take(4 * kChunk * dvp);
     w->z = (float*)take(4 * kChunk * dvp);
     w->dstate = (float*)take(4 * d->dk * dvp);
   }
@@ -93,8 +94,12 @@ void heads(Buffers* buf, const convdelta_heads* x, int64_t b, int64_t t, int64_t
   *to = Heads{x->data, x->batch_stride, x->row_stride, x->head_stride};
 }
 
-bool pieces(const Heads& h, int dk, int elem) {
-  return dk % 8 == 0 && ((uintptr_t)h.p | (uint64_t)(h.sb * elem) | (uint64_t)(h.st * elem) | (uint64_t)(h.sh * elem)) % 16 == 0;
+// 64 rows of at most 2^22 elements have offsets of 32 bits.
+bool near_rows(const Heads& h) { return h.st < (int64_t)1 << 23; }
+
+// Rows of d elements are whole pieces of 8, 16-byte aligned.
+bool pieces(const Heads& h, int d, int elem) {
+  return d % 8 == 0 && near_rows(h) && ((uintptr_t)h.p | (uint64_t)(h.sb * elem) | (uint64_t)(h.st * elem) | (uint64_t)(h.sh * elem)) % 16 == 0;
 }
 
 void fill(DeltaArgs* a, const convdelta_desc* d) {
@@ -148,6 +153,7 @@ int convdelta_fwd(const convdelta_desc* d, const convdelta_heads* q, const convd
   buf.out(states, size * chunks_of(d), 4, false);
   buf.out(workspace, work, 16);
   if (buf.result() < 0) return buf.result();
+  if (!near_rows(a.v)) return CONVFWD_ERR_TOO_LARGE;
   if (d->b == 0) return CONVFWD_OK;
   fill(&a, d);
   a.log_decay = (const float*)log_decay; a.beta = (const float*)beta; a.h0 = (const float*)h0;
@@ -189,19 +195,19 @@ int convdelta_bwd(const convdelta_desc* d, const convdelta_heads* dy, const conv
   buf.out(dh0, size, 4);
   buf.out(workspace, work, 16);
   if (buf.result() < 0) return buf.result();
+  if (!near_rows(a.v) || !near_rows(a.dy)) return CONVFWD_ERR_TOO_LARGE;
   if (d->b == 0) return CONVFWD_OK;
   fill(&a, d);
   a.log_decay = (const float*)log_decay; a.beta = (const float*)beta; a.states_in = (const float*)states;
   a.starts = (const uint8_t*)starts; a.dh_last = (const float*)dh_last;
   a.dq = dq; a.dk_ = dk; a.dv_ = dv; a.dlog_decay = (float*)dlog_decay; a.dbeta = (float*)dbeta; a.dh0 = (float*)dh0;
+  a.vec_dy = pieces(a.dy, d->dv, eb);
   lay_out(d, true, (char*)workspace, &a.w);
   const hipStream_t s = (hipStream_t)stream;
-  static const Launch replay[3] = {launch_delta_replay_f32, launch_delta_replay_f16, launch_delta_replay_bf16};
   static const Launch bwd[3] = {launch_delta_bwd_f32, launch_delta_bwd_f16, launch_delta_bwd_bf16};
   static const Launch grad[3] = {launch_delta_grad_f32, launch_delta_grad_f16, launch_delta_grad_bf16};
   int rc = CONVFWD_OK;
   if (a.chunks > 0) rc = prepare(&a, true, s);
-  if (a.chunks > 0 && rc == CONVFWD_OK) rc = launched(replay[d->dtype](a, s));
   if (rc == CONVFWD_OK) rc = launched(bwd[d->dtype](a, s));
   if (a.chunks > 0 && rc == CONVFWD_OK) rc = launched(grad[d->dtype](a, s));
   return rc;

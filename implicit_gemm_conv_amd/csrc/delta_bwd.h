@@ -123,12 +123,15 @@ struct Backward : Team<T, DK> {
     F::template put<kParts, typename F::Rows>(s.out, row(), out);
   }
   __device__ __forceinline__ void store(int c, const Chunk& x, const f32x4_t& z) const {
-    T* dv = (T*)a.dv_ + (((int64_t)F::b * a.t + c * kChunk) * a.hv + F::h) * a.dv + col;
-    float* zs = a.w.z + ((int64_t)F::bh * a.chunks + c) * kChunk * a.dvp + col;
+    const int64_t ld = (int64_t)a.hv * a.dv;
+    T* dv = (T*)a.dv_ + ((int64_t)F::b * a.t + c * kChunk) * ld + (int64_t)F::h * a.dv;
+    float* zs = a.w.z + chunk_index(a, F::bh, c) * kChunk * a.dvp;
+    const uint32_t to = (uint32_t)(row() * (uint32_t)ld + col) * (uint32_t)sizeof(T), toz = (uint32_t)(row() * a.dvp + col) * 4u;
+    const int n = a.t - c * kChunk;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (F::live && c * kChunk + row() + i < a.t) dv[(int64_t)(row() + i) * a.hv * a.dv] = from_f32<T>(x.beta[i] * z[i]);
-      if (col < a.dvp) zs[(int64_t)(row() + i) * a.dvp] = F::live ? z[i] : 0.f;
+      if (F::live && row() + i < n) store_at(dv + i * ld, to, from_f32<T>(x.beta[i] * z[i]));
+      if (col < a.dvp) store_at(zs + i * (int64_t)a.dvp, toz, F::live ? z[i] : 0.f);
     }
   }
   // (3), from the rows [0, first) where masked

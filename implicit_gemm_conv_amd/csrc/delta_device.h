@@ -102,16 +102,26 @@ struct RowsAt {
   static constexpr int stride = DK + 8, part = kChunk * stride;
 };
 
+// An access at a wave-uniform base and a lane's byte offset of 32 bits, which the hardware adds itself.
+template <typename P>
+__device__ __forceinline__ P load_at(const void* base, uint32_t offset) {
+  return *(const P*)((const char*)base + offset);
+}
+template <typename P>
+__device__ __forceinline__ void store_at(void* base, uint32_t offset, const P& v) {
+  *(P*)((char*)base + offset) = v;
+}
+
 // 8 elements of a row as they come from memory; they stay raw until they are used, so
 // that a load in flight is not waited for.  The row is 16-byte aligned and has d elements, a
 // multiple of 8; past its end they are any of its elements, and `parts` selects zero.
 template <typename T>
 struct Raw8 {
   convfwd::u32x4_t w[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const T* row, int d0, int d) {
-    const convfwd::u32x4_t* p = (const convfwd::u32x4_t*)(row + min(d0, d - 8));
+  __device__ __forceinline__ void load(const void* base, uint32_t row, int d0, int d) {
+    const uint32_t at = row + (uint32_t)min(d0, d - 8) * (uint32_t)sizeof(T);
 #pragma unroll
-    for (unsigned k = 0; k < sizeof(T) / 2; ++k) w[k] = p[k];
+    for (unsigned k = 0; k < sizeof(T) / 2; ++k) w[k] = load_at<convfwd::u32x4_t>(base, at + 16 * k);
   }
   __device__ __forceinline__ void get(float (&x)[8], bool in) const {
     T v[8];
@@ -139,15 +149,27 @@ __device__ __forceinline__ Parts<1> Raw8<__bf16>::parts(bool in) const {
 // repeat the last one: what is made of them meets a beta or a gradient of zero.
 template <typename T, int DK, int THREADS>
 struct Rows64 {
-  static constexpr int pieces = kChunk * (DK / 8), each = pieces / THREADS;
-  static_assert(pieces % THREADS == 0, "whole rounds");
+  static constexpr int pieces = kChunk * (DK / 8), each = (pieces + THREADS - 1) / THREADS;
   Raw8<T> p[each];
-  __device__ __forceinline__ static int row(int k) { return (threadIdx.x + k * THREADS) / (DK / 8); }
-  __device__ __forceinline__ static int d0(int k) { return (threadIdx.x + k * THREADS) % (DK / 8) * 8; }
+  __device__ __forceinline__ static int at(int k) { return min((int)threadIdx.x + k * THREADS, pieces - 1); }
+  __device__ __forceinline__ static int row(int k) { return at(k) / (DK / 8); }
+  __device__ __forceinline__ static int d0(int k) { return at(k) % (DK / 8) * 8; }
   __device__ __forceinline__ void load(const Heads& h, int b, int head, int t0, int t, int d) {
-    const T* base = (const T*)h.p + b * h.sb + head * h.sh;
+    const T* base = (const T*)h.p + b * h.sb + head * h.sh + t0 * h.st;
+    const uint32_t ld = (uint32_t)h.st * (uint32_t)sizeof(T);
 #pragma unroll
-    for (int k = 0; k < each; ++k) p[k].load(base + (int64_t)min(t0 + row(k), t - 1) * h.st, d0(k), d);
+    for (int k = 0; k < each; ++k) p[k].load(base, (uint32_t)min(row(k), t - 1 - t0) * ld, d0(k), d);
+  }
+  __device__ __forceinline__ bool finite() const {
+    bool all = true;
+#pragma unroll
+    for (int k = 0; k < each; ++k) {
+      float x[8];
+      p[k].get(x, true);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) all = all && convdelta::finite(x[e]);
+    }
+    return all;
   }
   __device__ __forceinline__ void put(__bf16* lds, int d) const {
 #pragma unroll

@@ -1,6 +1,5 @@
 // delta_fwd.h -- gated delta rule forward: a workgroup carries 16 columns of one
-// head's state through the chunks; kReplay computes only x of one chunk from its kept
-// state.  Included by one source for each type.
+// head's state through the chunks.  Included by one source for each type.
 //
 // A chunk takes three steps between barriers: (1) k S and q S, r; (2) x = r + H (beta r),
 // u; (3) the state, y.  Each wave has its own rows (1, 2, y) or rows of the state (3), and
@@ -12,8 +11,6 @@ namespace convdelta {
 
 namespace {
 
-enum Mode { kForward, kReplay };
-
 template <typename T, int DK>
 struct FwdLds {
   typedef Team<T, DK> F;
@@ -23,7 +20,7 @@ struct FwdLds {
   int bad[2];
 };
 
-template <typename T, int DK, Mode MODE>
+template <typename T, int DK>
 struct Forward : Team<T, DK> {
   typedef Team<T, DK> F;
   typedef FwdLds<T, DK> Lds;
@@ -59,9 +56,9 @@ struct Forward : Team<T, DK> {
   }
   __device__ __forceinline__ void fetch(int c, Chunk& x) const {
     F::load_rows(a.k, c, x.k);
-    if (MODE == kForward) F::load_rows(a.q, c, x.q);
+    F::load_rows(a.q, c, x.q);
     F::template load_matrix<false>(a.w.solve, c, x.solve);
-    if (MODE == kForward) F::template load_matrix<false>(a.w.read, c, x.read);
+    F::template load_matrix<false>(a.w.read, c, x.read);
     fetch_gates(c, x);
     F::load_col(a.v, c, x.v);
   }
@@ -84,7 +81,7 @@ struct Forward : Team<T, DK> {
     for (int k = 0; k < KS; ++k) {
       const auto sp = F::template get<kParts, typename F::State>(s.state, k);
       ks = mma(F::rows_of(x.k, k), sp, ks);
-      if (MODE == kForward) qs = mma_first<YP>(F::rows_of(x.q, k), sp, qs);
+      qs = mma_first<YP>(F::rows_of(x.q, k), sp, qs);
     }
     f32x4_t xs, u;
 #pragma unroll
@@ -93,7 +90,7 @@ struct Forward : Team<T, DK> {
       u[i] = alone && row() + i != only ? 0.f : x.beta[i] * xs[i];
     }
     F::load_rows(a.k, next, x.k);
-    if (MODE == kForward) F::load_rows(a.q, next, x.q);
+    F::load_rows(a.q, next, x.q);
     F::load_col(a.v, next, x.v);
     F::template put<kParts, typename F::Rows>(s.br, row(), u);
     __syncthreads();
@@ -117,15 +114,7 @@ struct Forward : Team<T, DK> {
       lu[i] = times(x.leave[i], u[i]);
       test = fmaf(u[i], 0.f, test);
     }
-    if (MODE == kReplay) {
-      float* to = a.w.x + ((int64_t)F::bh * a.chunks + c) * kChunk * a.dvp + col;
-      if (col < a.dvp)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!alone || row() + i == only) to[(int64_t)(row() + i) * a.dvp] = F::live ? xs[i] : 0.f;
-    } else {
-      F::template put<YP, typename F::Rows>(s.out, row(), u);
-    }
+    F::template put<YP, typename F::Rows>(s.out, row(), u);
     F::template put<kParts, typename F::Rows>(s.u, row(), lu);
     if (__any(test != 0.f)) s.bad[turn & 1] = 1;  // NaN
     __syncthreads();
@@ -134,7 +123,6 @@ struct Forward : Team<T, DK> {
     if (threadIdx.x == 0) s.bad[~turn & 1] = 0;
     ++turn;
     if (!alone && bad) return false;
-    if (MODE == kReplay && !alone) return true;
     // the state moves on
     Parts<kParts> up[2];
 #pragma unroll
@@ -154,25 +142,25 @@ struct Forward : Team<T, DK> {
         state[j] = n + more;
       }
     F::put_state(s.state, state);
-    if (MODE == kForward) {
-      f32x4_t o, more = zero;
+    f32x4_t o, more = zero;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = times(x.enter[i], qs[i]);
+    for (int i = 0; i < 4; ++i) o[i] = times(x.enter[i], qs[i]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (F::template has<false>(k)) {
-          if (alone) keep(x.read[k], 32 * k + 8 * q4, only, only + 1);
-          const auto op = F::template get<YP, typename F::Rows>(s.out, k);
-          (k ? more : o) = mma_first<YP>(x.read[k], op, k ? more : o);
-        }
-      T* y = (T*)a.y + (((int64_t)F::b * a.t + c * kChunk) * a.hv + F::h) * a.dv + col;
-      if (F::live)
+    for (int k = 0; k < 2; ++k)
+      if (F::template has<false>(k)) {
+        if (alone) keep(x.read[k], 32 * k + 8 * q4, only, only + 1);
+        const auto op = F::template get<YP, typename F::Rows>(s.out, k);
+        (k ? more : o) = mma_first<YP>(x.read[k], op, k ? more : o);
+      }
+    const int64_t ld = (int64_t)a.hv * a.dv;
+    T* y = (T*)a.y + ((int64_t)F::b * a.t + c * kChunk) * ld + (int64_t)F::h * a.dv;
+    const uint32_t to = (uint32_t)(row() * (uint32_t)ld + col) * (uint32_t)sizeof(T);
+    const int n = a.t - c * kChunk;
+    if (F::live)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (c * kChunk + row() + i < a.t && (!alone || row() + i == only))
-            y[(int64_t)(row() + i) * a.hv * a.dv] = from_f32<T>(a.scale * (o[i] + more[i]));
-      F::template load_matrix<false>(a.w.read, next, x.read);
-    }
+      for (int i = 0; i < 4; ++i)
+        if (row() + i < n && (!alone || row() + i == only)) store_at(y + i * ld, to, from_f32<T>(a.scale * (o[i] + more[i])));
+    F::template load_matrix<false>(a.w.read, next, x.read);
     fetch_gates(next, x);
     return true;
   }
@@ -195,10 +183,6 @@ struct Forward : Team<T, DK> {
         continue;
       }
       if (last) {
-        if (MODE == kReplay && alone && col < a.dvp)  // rows past T hold nothing
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (row() + i >= n) a.w.x[(((int64_t)F::bh * a.chunks + c) * kChunk + row() + i) * a.dvp + col] = 0.f;
         ++c;
         alone = false;
       } else {
@@ -210,7 +194,7 @@ struct Forward : Team<T, DK> {
 
 template <typename T, int DK>
 __global__ __launch_bounds__(kTeam, 2) void delta_fwd_kernel(DeltaArgs a, int blocks) {
-  typedef Forward<T, DK, kForward> F;
+  typedef Forward<T, DK> F;
   __shared__ __attribute__((aligned(16))) typename F::Lds s;
   int bh, cb;
   if (!head_of(a.b * a.hv, blocks, bh, cb)) return;
@@ -227,20 +211,6 @@ __global__ __launch_bounds__(kTeam, 2) void delta_fwd_kernel(DeltaArgs a, int bl
   f.store_state(a.h_last + bh * size, a.dv, f.live, f.state);
 }
 
-template <typename T, int DK>
-__global__ __launch_bounds__(kTeam, 2) void delta_replay_kernel(DeltaArgs a, int blocks) {
-  typedef Forward<T, DK, kReplay> F;
-  __shared__ __attribute__((aligned(16))) typename F::Lds s;
-  const int cb = blockIdx.x % blocks, c = blockIdx.x / blocks % a.chunks, bh = blockIdx.x / blocks / a.chunks;
-  F f(a, s, bh, cb);
-  typename F::Chunk x;
-  f.fetch(c, x);
-  f.load_state(a.states_in + (((int64_t)f.b * a.chunks + c) * a.hv + f.h) * a.dk * a.dv, f.state);
-  if (threadIdx.x == 0) s.bad[0] = s.bad[1] = 0;
-  f.put_state(s.state, f.state);
-  f.run(c, c + 1, x, [](int) {});
-}
-
 }  // namespace
 
 template <typename T>
@@ -248,16 +218,6 @@ hipError_t delta_fwd_of(const DeltaArgs& a, hipStream_t s) {
   return for_dk(a.dk, [&](auto dk) {
     const int blocks = (a.dv + 15) / 16;
     hipLaunchKernelGGL((delta_fwd_kernel<T, decltype(dk)::value>), dim3((a.b * a.hv + 7) / 8 * 8 * blocks), dim3(kTeam), 0, s, a,
-                       blocks);
-    return hipGetLastError();
-  });
-}
-
-template <typename T>
-hipError_t delta_replay_of(const DeltaArgs& a, hipStream_t s) {
-  return for_dk(a.dk, [&](auto dk) {
-    const int blocks = a.dvp / 16;
-    hipLaunchKernelGGL((delta_replay_kernel<T, decltype(dk)::value>), dim3(a.b * a.hv * a.chunks * blocks), dim3(kTeam), 0, s, a,
                        blocks);
     return hipGetLastError();
   });

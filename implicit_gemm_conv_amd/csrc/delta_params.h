@@ -30,8 +30,7 @@ struct Work {
   float* rows;     // 4 x 64: enter, leave, beta, step (see delta_device.h)
   double* sums;    // backward: 64 sums of log decays
   int* seq;        // backward: 64 sequence numbers inside the chunk
-  float* x;        // backward: x and its counterpart, (B * Hv, chunks * 64, dvp)
-  float* z;
+  float* z;        // backward: z, (B * Hv, chunks * 64, dvp)
   float* dstate;   // backward: the gradient of the state after each chunk, (.., Dk, dvp)
   void *q, *k;     // (B, T, Hk, dkp) copies, where q or k are not 16-byte aligned rows of whole 16 bytes
 };
@@ -40,6 +39,7 @@ struct DeltaArgs {
   int b, t, hk, hv, dk, dv, dtype;
   int chunks, dvp;  // ceil(T / 64); Dv rounded up to 32
   int dkp;          // elements of a row of q and k as the kernels read them: Dk rounded up to 8
+  int vec_dy;       // dy's rows are 16-byte aligned and whole pieces of 8 elements
   float scale;
   Heads q, k, v, dy;
   const float *log_decay, *beta, *h0, *states_in, *dh_last;
@@ -63,12 +63,10 @@ hipError_t launch_delta_pack(const DeltaArgs& a, const Heads& q, const Heads& k,
 hipError_t launch_delta_prep(const DeltaArgs& a, bool backward, hipStream_t s);
 // One launcher for each type:
 //   fwd     y, the states
-//   replay  x of every chunk, from the kept states
 //   bwd     dv, z, the states' gradients
 //   grad    dq, dk, dlog_decay, dbeta
 #define CONVDELTA_LAUNCHERS(type)                                        \
   hipError_t launch_delta_fwd_##type(const DeltaArgs& a, hipStream_t s);    \
-  hipError_t launch_delta_replay_##type(const DeltaArgs& a, hipStream_t s); \
   hipError_t launch_delta_bwd_##type(const DeltaArgs& a, hipStream_t s);    \
   hipError_t launch_delta_grad_##type(const DeltaArgs& a, hipStream_t s);
 CONVDELTA_LAUNCHERS(f32)

@@ -52,15 +52,15 @@ struct Team {
         s[j][r] = from && live && d < a.dk ? from[(int64_t)d * a.dv + col] : 0.f;
       }
   }
-  __device__ __forceinline__ void store_state(float* to, int64_t ld, bool in, const f32x4_t (&s)[own]) const {
+  // (a state's rows are below 2^25 bytes apart, so that 128 of them have offsets of 32 bits)
+  __device__ __forceinline__ void store_state(float* to, int ld, bool in, const f32x4_t (&s)[own]) const {
     if (!in) return;
 #pragma unroll
     for (int j = 0; j < own; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int d = 16 * tile(j) + 4 * q4 + r;
-        if (d < a.dk) to[d * ld + col] = s[j][r];
-      }
+      for (int r = 0; r < 4; ++r)
+        if (16 * tile(j) + 4 * q4 + r < a.dk)
+          store_at(to + (int64_t)(16 * tile(j) + r) * ld, (uint32_t)(4 * q4 * ld + col) * 4u, s[j][r]);
   }
   // four neighbouring rows of the lane's column, as parts
   template <int N, typename AT>
@@ -93,9 +93,10 @@ struct Team {
   }
   // this wave's rows of q or k
   __device__ __forceinline__ void load_rows(const Heads& x, int c, Raw8<T> (&to)[KS]) const {
-    const T* p = (const T*)x.p + b * x.sb + hk * x.sh + (int64_t)min(c * kChunk + 16 * wave + m, a.t - 1) * x.st;
+    const T* p = (const T*)x.p + b * x.sb + hk * x.sh + (int64_t)c * kChunk * x.st;
+    const uint32_t at = (uint32_t)min(16 * wave + m, a.t - 1 - c * kChunk) * ((uint32_t)x.st * (uint32_t)sizeof(T));
 #pragma unroll
-    for (int k = 0; k < KS; ++k) to[k].load(p, 32 * k + 8 * q4, a.dkp);
+    for (int k = 0; k < KS; ++k) to[k].load(p, at, 32 * k + 8 * q4, a.dkp);
   }
   __device__ __forceinline__ Parts<NP> rows_of(const Raw8<T> (&x)[KS], int k) const { return x[k].parts(32 * k + 8 * q4 < a.dkp); }
   // ... into LDS, row by row
@@ -107,14 +108,21 @@ struct Team {
       for (int n = 0; n < NP; ++n) *(bf168_t*)(to + n * RowsAt<DK>::part + (16 * wave + m) * RowsAt<DK>::stride + 32 * k + 8 * q4) = p.p[n];
     }
   }
-  // the lane's four rows of its column of v, y's gradient, ...
+  // the lane's four rows of its column of v or of y's gradient
   __device__ __forceinline__ void load_col(const Heads& x, int c, T (&to)[4]) const {
-    const T* p = (const T*)x.p + b * x.sb + h * x.sh + vcol;
+    const T* p = (const T*)x.p + b * x.sb + h * x.sh + (int64_t)c * kChunk * x.st;
+    const uint32_t ld = (uint32_t)x.st * (uint32_t)sizeof(T), at = (uint32_t)vcol * (uint32_t)sizeof(T);
+    const int last = a.t - 1 - c * kChunk;
+    if (last >= kChunk - 1) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) to[r] = p[(int64_t)min(c * kChunk + row() + r, a.t - 1) * x.st];
+      for (int r = 0; r < 4; ++r) to[r] = load_at<T>(p + (int64_t)r * x.st, row() * ld + at);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) to[r] = load_at<T>(p, min(row() + r, last) * ld + at);
+    }
   }
   __device__ __forceinline__ f32x4_t load_gate(int which, int c) const {
-    return *(const f32x4_t*)(a.w.rows + (chunk_index(a, bh, c) * 4 + which) * kChunk + row());
+    return load_at<f32x4_t>(a.w.rows + (chunk_index(a, bh, c) * 4 + which) * kChunk, 4u * row());
   }
   // this wave's operands of a triangular matrix: of a lower one steps 0 and, from wave 2 on, 1; of an
   // upper one (UP) step 1 and, up to wave 1, 0
@@ -122,13 +130,13 @@ struct Team {
   __device__ __forceinline__ bool has(int k) const { return UP ? k >= wave / 2 : k <= wave / 2; }
   template <bool UP, int N>
   __device__ __forceinline__ void load_matrix(const char* x, int c, Parts<N> (&to)[2]) const {
-    const char* p = x + chunk_index(a, bh, c) * kMatrix + lane * 16;
+    const char* p = x + chunk_index(a, bh, c) * kMatrix;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       // the operand's number in the order of low_t, low_s (up_t, up_s); one that is not there repeats the other
       const int f = UP ? (wave < 2 ? 2 * wave + k : wave + 2) : (wave < 2 ? wave : 2 * wave - 2 + k);
 #pragma unroll
-      for (int n = 0; n < N; ++n) to[k].p[n] = *(const bf168_t*)(p + (f * kParts + n) * kFrag);
+      for (int n = 0; n < N; ++n) to[k].p[n] = load_at<bf168_t>(p + f * kParts * kFrag, n * kFrag + lane * 16u);
     }
   }
 };

@@ -4,6 +4,5 @@
 namespace convdelta {
 
 hipError_t launch_delta_fwd_f16(const DeltaArgs& a, hipStream_t s) { return delta_fwd_of<_Float16>(a, s); }
-hipError_t launch_delta_replay_f16(const DeltaArgs& a, hipStream_t s) { return delta_replay_of<_Float16>(a, s); }
 
 }  // namespace convdelta

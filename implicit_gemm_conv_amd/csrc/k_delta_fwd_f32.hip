@@ -4,6 +4,5 @@
 namespace convdelta {
 
 hipError_t launch_delta_fwd_f32(const DeltaArgs& a, hipStream_t s) { return delta_fwd_of<float>(a, s); }
-hipError_t launch_delta_replay_f32(const DeltaArgs& a, hipStream_t s) { return delta_replay_of<float>(a, s); }
 
 }  // namespace convdelta
