@@ -40,8 +40,7 @@ struct Backward : Team<T, DK> {
   struct Chunk {
     Raw8<T> k[KS], q[KS];
     Parts<kParts> solve[2], read[2];
-    f32x4_t enter, leave, beta;
-    float stay;
+    Gates g;
     T dy[4];
   };
 
@@ -56,42 +55,42 @@ struct Backward : Team<T, DK> {
     F::load_rows(a.q, c, x.q);
     F::load_col(a.dy, c, x.dy);
   }
-  __device__ __forceinline__ void fetch_gates(int c, Chunk& x) const {
-    x.enter = F::load_gate(0, c);
-    x.leave = F::load_gate(1, c);
-    x.beta = F::load_gate(2, c);
-    x.stay = a.w.rows[chunk_index(a, F::bh, c) * 4 * kChunk + kChunk - 1];
-  }
   __device__ __forceinline__ void fetch(int c, Chunk& x) const {
     fetch_rows(c, x);
     F::template load_matrix<true>(a.w.solve_t, c, x.solve);
     F::template load_matrix<true>(a.w.read_t, c, x.read);
-    fetch_gates(c, x);
+    x.g = F::load_gates(c);
   }
   __device__ __forceinline__ f32x4_t dy_of(int c, const Chunk& x) const {
     f32x4_t d;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = F::live && c * kChunk + row() + i < a.t ? to_f32(x.dy[i]) : 0.f;
+    for (int i = 0; i < 4; ++i) d[i] = c * kChunk + row() + i < a.t ? to_f32(x.dy[i]) : 0.f;
     return d;
   }
 
   // (1) and (2) for all rows, or (masked) the rows [lo, hi) of one sequence, into z; kd is k dS.
-  __device__ __forceinline__ void solve(const Chunk& x, const f32x4_t& kd, bool masked, int lo, int hi, f32x4_t& z) {
+  __device__ __forceinline__ void solve(int c, Chunk& x, const f32x4_t& kd, bool masked, int lo, int hi, f32x4_t& z) {
+    if (masked) {
+      F::template load_matrix<true>(a.w.solve_t, c, x.solve);
+      F::template load_matrix<true>(a.w.read_t, c, x.read);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) keep(x.solve[k], 32 * k + 8 * q4, lo, hi), keep(x.read[k], 32 * k + 8 * q4, lo, hi);
+      wait_for_memory();
+    }
     f32x4_t ry = {0.f, 0.f, 0.f, 0.f}, more = ry;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       if (F::template has<true>(k)) {
-        Parts<kParts> p = x.read[k];
         Parts<NP> d = F::template get<NP, typename F::Rows>(s.dy, k);
-        if (masked) keep(p, 32 * k + 8 * q4, lo, hi), keep(d, 32 * k + 8 * q4, lo, hi);
-        (k ? more : ry) = mma(p, d, k ? more : ry);
+        if (masked) keep(d, 32 * k + 8 * q4, lo, hi);
+        (k ? more : ry) = mma(x.read[k], d, k ? more : ry);
       }
     f32x4_t du, bd;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool out = row() + i < lo || row() + i >= hi;
-      du[i] = out ? 0.f : times(x.leave[i], kd[i]) + a.scale * (ry[i] + more[i]);
-      bd[i] = out ? 0.f : x.beta[i] * du[i];
+      du[i] = out ? 0.f : times(x.g.leave[i], kd[i]) + a.scale * (ry[i] + more[i]);
+      bd[i] = out ? 0.f : x.g.beta[i] * du[i];
     }
     if (masked) __syncthreads();  // what is read of the sequence before
     F::template put<kParts, typename F::Rows>(s.bd, row(), bd);
@@ -100,10 +99,8 @@ struct Backward : Team<T, DK> {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       if (F::template has<true>(k)) {
-        Parts<kParts> p = x.solve[k];
-        if (masked) keep(p, 32 * k + 8 * q4, lo, hi);
         const auto bp = F::template get<kParts, typename F::Rows>(s.bd, k);
-        (k ? more : du) = mma(p, bp, k ? more : du);
+        (k ? more : du) = mma(x.solve[k], bp, k ? more : du);
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -116,23 +113,22 @@ struct Backward : Team<T, DK> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (c * kChunk + row() + i >= a.t) z[i] = 0.f;  // rows past T hold nothing, whatever the state's gradient is
-      in[i] = times(x.enter[i], a.scale * dy[i]);
-      out[i] = -times(x.enter[i], x.beta[i] * z[i]);
+      in[i] = times(x.g.enter[i], a.scale * dy[i]);
+      out[i] = -times(x.g.enter[i], x.g.beta[i] * z[i]);
     }
     F::template put<kParts, typename F::Rows>(s.in, row(), in);
     F::template put<kParts, typename F::Rows>(s.out, row(), out);
   }
-  __device__ __forceinline__ void store(int c, const Chunk& x, const f32x4_t& z) const {
-    const int64_t ld = (int64_t)a.hv * a.dv;
-    T* dv = (T*)a.dv_ + ((int64_t)F::b * a.t + c * kChunk) * ld + (int64_t)F::h * a.dv;
-    float* zs = a.w.z + chunk_index(a, F::bh, c) * kChunk * a.dvp;
-    const uint32_t to = (uint32_t)(row() * (uint32_t)ld + col) * (uint32_t)sizeof(T), toz = (uint32_t)(row() * a.dvp + col) * 4u;
-    const int n = a.t - c * kChunk;
+  __device__ __forceinline__ void store(int c, const f32x4_t& beta, const f32x4_t& z) const {
+    const Range zs(a.w.z + chunk_index(a, F::bh, c) * kChunk * a.dvp, (int64_t)kChunk * a.dvp * 4);
+    const uint32_t at = col < a.dvp ? (uint32_t)(row() * a.dvp + col) * 4u : kNowhere;
+    f32x4_t dx;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (F::live && row() + i < n) store_at(dv + i * ld, to, from_f32<T>(x.beta[i] * z[i]));
-      if (col < a.dvp) store_at(zs + i * (int64_t)a.dvp, toz, F::live ? z[i] : 0.f);
+      dx[i] = beta[i] * z[i];
+      zs.store(at + (uint32_t)(i * a.dvp) * 4u, F::live ? z[i] : 0.f);
     }
+    F::store_col(a.dv_, c, dx);
   }
   // (3), from the rows [0, first) where masked
   __device__ __forceinline__ void move(float stay, bool masked, int first) {
@@ -164,6 +160,7 @@ struct Backward : Team<T, DK> {
     f32x4_t dy = dy_of(c, x);
     F::template put<NP, typename F::Rows>(s.dy, row(), dy);
     __syncthreads();  // the state's parts and dy are there
+    const Gates gates = F::load_gates(next);
     F::put_rows(s.k, x.k);
     F::put_rows(s.q, x.q);
     f32x4_t kd = {0.f, 0.f, 0.f, 0.f}, more = kd;
@@ -190,7 +187,7 @@ struct Backward : Team<T, DK> {
           while (lo > 0 && s.step[lo] != 0.f) --lo;
           if (lo > 0 || s.step[0] == 0.f) first = lo;
         }
-        solve(x, kd, masked, lo, hi, z);
+        solve(c, x, kd, masked, lo, hi, z);
         hi = lo;
       } while (hi > 0);
       float test = 0.f;
@@ -205,13 +202,20 @@ struct Backward : Team<T, DK> {
       if (masked || !bad) break;
       masked = true;
       if (threadIdx.x < kChunk) s.step[threadIdx.x] = a.w.rows[(chunk_index(a, F::bh, c) * 4 + 3) * kChunk + threadIdx.x];
+      wait_for_memory();
       __syncthreads();
     }
-    move(x.stay, masked, first);
-    store(c, x, z);
     F::template load_matrix<true>(a.w.solve_t, next, x.solve);
     F::template load_matrix<true>(a.w.read_t, next, x.read);
-    fetch_gates(next, x);
+    move(x.g.stay, masked, first);
+    // stores come after the loads of the next chunk (see delta_fwd.h)
+    store(c, x.g.beta, z);
+    keep_state(c - 1);
+    x.g = gates;
+  }
+  // The gradient of the state after chunk c.
+  __device__ __forceinline__ void keep_state(int c) const {
+    F::store_state(c >= 0 ? a.w.dstate + chunk_index(a, F::bh, c) * a.dk * a.dvp : nullptr, a.dvp, a.dvp, state);
   }
 };
 
@@ -226,13 +230,13 @@ __global__ __launch_bounds__(kTeam, 2) void delta_bwd_kernel(DeltaArgs a, int bl
   f.load_state(a.dh_last ? a.dh_last + bh * size : nullptr, f.state);
   if (threadIdx.x == 0) s.bad[0] = s.bad[1] = 0;
   f.put_state(s.state, f.state);
-  typename F::Chunk x;
-  if (a.chunks > 0) f.fetch(a.chunks - 1, x);
-  for (int c = a.chunks - 1; c >= 0; --c) {
-    f.store_state(a.w.dstate + chunk_index(a, bh, c) * a.dk * a.dvp, a.dvp, f.col < a.dvp, f.state);
-    f.chunk(c, max(c - 1, 0), x);
+  if (a.chunks > 0) {
+    typename F::Chunk x;
+    f.fetch(a.chunks - 1, x);
+    f.keep_state(a.chunks - 1);
+    for (int c = a.chunks - 1; c >= 0; --c) f.chunk(c, max(c - 1, 0), x);
   }
-  f.store_state(a.dh0 + bh * size, a.dv, f.live, f.state);
+  f.store_state(a.dh0 + bh * size, a.dv, a.dv, f.state);
 }
 
 }  // namespace

@@ -107,46 +107,72 @@ template <typename P>
 __device__ __forceinline__ P load_at(const void* base, uint32_t offset) {
   return *(const P*)((const char*)base + offset);
 }
-template <typename P>
-__device__ __forceinline__ void store_at(void* base, uint32_t offset, const P& v) {
-  *(P*)((char*)base + offset) = v;
+
+// Accesses whose range the hardware checks: what lies past `bytes` is read as zero and not written.  No
+// access needs a branch then, and the compiler knows how many are in flight at every wait (it counts them in the
+// order of issue, and would take each that a branch may skip for one that was).
+constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every range
+struct Range {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Range(const void* base, int64_t bytes)
+      : r(__builtin_amdgcn_make_buffer_rsrc((void*)base, (short)0, (int)bytes, 0x00027000)) {}
+  template <typename T>
+  __device__ __forceinline__ T load(uint32_t offset) const {
+    if constexpr (sizeof(T) == 2) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, offset, 0, 0));
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, offset, 0, 0));
+    if constexpr (sizeof(T) == 16) return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
+  }
+  template <typename T>
+  __device__ __forceinline__ void store(uint32_t offset, T v) const {
+    if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, offset, 0, 0);
+    if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned int, v), r, offset, 0, 0);
+  }
+};
+// At the end of a path that is hardly ever taken: with nothing of it in flight, the waits after it are those of the
+// usual path.
+__device__ __forceinline__ void wait_for_memory() { __builtin_amdgcn_s_waitcnt(0x0f70); }  // vmcnt(0)
+
+// The rows [t0, t) of one head, at most 64, of d elements.
+template <typename T>
+__device__ __forceinline__ Range rows_range(const Heads& h, int b, int head, int t0, int t, int d) {
+  return Range((const T*)h.p + b * h.sb + head * h.sh + t0 * h.st, ((int64_t)(min(kChunk, t - t0) - 1) * h.st + d) * (int64_t)sizeof(T));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t row_bytes(const Heads& h) {
+  return (uint32_t)h.st * (uint32_t)sizeof(T);
 }
 
 // 8 elements of a row as they come from memory; they stay raw until they are used, so
 // that a load in flight is not waited for.  The row is 16-byte aligned and has d elements, a
-// multiple of 8; past its end they are any of its elements, and `parts` selects zero.
+// multiple of 8; past its end they are zero.
 template <typename T>
 struct Raw8 {
   convfwd::u32x4_t w[sizeof(T) / 2];
-  __device__ __forceinline__ void load(const void* base, uint32_t row, int d0, int d) {
-    const uint32_t at = row + (uint32_t)min(d0, d - 8) * (uint32_t)sizeof(T);
+  __device__ __forceinline__ void load(const Range& x, uint32_t row, int d0, int d) {
+    const uint32_t at = d0 < d ? row + (uint32_t)d0 * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
-    for (unsigned k = 0; k < sizeof(T) / 2; ++k) w[k] = load_at<convfwd::u32x4_t>(base, at + 16 * k);
+    for (unsigned k = 0; k < sizeof(T) / 2; ++k) w[k] = x.load<convfwd::u32x4_t>(at + 16 * k);
   }
-  __device__ __forceinline__ void get(float (&x)[8], bool in) const {
+  __device__ __forceinline__ void get(float (&x)[8]) const {
     T v[8];
     __builtin_memcpy(v, w, sizeof(v));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = in ? to_f32(v[e]) : 0.f;
+    for (int e = 0; e < 8; ++e) x[e] = to_f32(v[e]);
   }
-  __device__ __forceinline__ Parts<InParts<T>::n> parts(bool in) const {
+  __device__ __forceinline__ Parts<InParts<T>::n> parts() const {
     float x[8];
-    get(x, in);
+    get(x);
     return split<InParts<T>::n>(x);
   }
 };
 template <>
-__device__ __forceinline__ Parts<1> Raw8<__bf16>::parts(bool in) const {
+__device__ __forceinline__ Parts<1> Raw8<__bf16>::parts() const {
   Parts<1> r;
-  convfwd::u32x4_t v = w[0];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) v[k] = in ? v[k] : 0u;
-  __builtin_memcpy(&r.p[0], &v, 16);
+  __builtin_memcpy(&r.p[0], w, 16);
   return r;
 }
 
-// Pieces of a chunk's rows that a thread of `threads` holds on their way to LDS.  Rows past T
-// repeat the last one: what is made of them meets a beta or a gradient of zero.
+// Pieces of a chunk's rows that a thread of `threads` holds on their way to LDS.
 template <typename T, int DK, int THREADS>
 struct Rows64 {
   static constexpr int pieces = kChunk * (DK / 8), each = (pieces + THREADS - 1) / THREADS;
@@ -155,26 +181,25 @@ struct Rows64 {
   __device__ __forceinline__ static int row(int k) { return at(k) / (DK / 8); }
   __device__ __forceinline__ static int d0(int k) { return at(k) % (DK / 8) * 8; }
   __device__ __forceinline__ void load(const Heads& h, int b, int head, int t0, int t, int d) {
-    const T* base = (const T*)h.p + b * h.sb + head * h.sh + t0 * h.st;
-    const uint32_t ld = (uint32_t)h.st * (uint32_t)sizeof(T);
+    const Range x = rows_range<T>(h, b, head, t0, t, d);
 #pragma unroll
-    for (int k = 0; k < each; ++k) p[k].load(base, (uint32_t)min(row(k), t - 1 - t0) * ld, d0(k), d);
+    for (int k = 0; k < each; ++k) p[k].load(x, row(k) * row_bytes<T>(h), d0(k), d);
   }
   __device__ __forceinline__ bool finite() const {
     bool all = true;
 #pragma unroll
     for (int k = 0; k < each; ++k) {
       float x[8];
-      p[k].get(x, true);
+      p[k].get(x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) all = all && convdelta::finite(x[e]);
     }
     return all;
   }
-  __device__ __forceinline__ void put(__bf16* lds, int d) const {
+  __device__ __forceinline__ void put(__bf16* lds) const {
 #pragma unroll
     for (int k = 0; k < each; ++k) {
-      const auto q = p[k].parts(d0(k) < d);
+      const auto q = p[k].parts();
 #pragma unroll
       for (int n = 0; n < InParts<T>::n; ++n)
         *(bf168_t*)(lds + n * RowsAt<DK>::part + row(k) * RowsAt<DK>::stride + d0(k)) = q.p[n];

@@ -37,8 +37,7 @@ struct Forward : Team<T, DK> {
     Raw8<T> k[KS], q[KS];
     Parts<kParts> solve[2];
     Parts<YP> read[2];
-    f32x4_t enter, leave, beta;
-    float stay;
+    Gates g;
     T v[4];
   };
 
@@ -48,18 +47,12 @@ struct Forward : Team<T, DK> {
 
   __device__ __forceinline__ Forward(const DeltaArgs& a_, Lds& s_, int bh_, int cb) : F(a_, bh_, cb), s(s_) {}
 
-  __device__ __forceinline__ void fetch_gates(int c, Chunk& x) const {
-    x.enter = F::load_gate(0, c);
-    x.leave = F::load_gate(1, c);
-    x.beta = F::load_gate(2, c);
-    x.stay = a.w.rows[chunk_index(a, F::bh, c) * 4 * kChunk + kChunk - 1];
-  }
   __device__ __forceinline__ void fetch(int c, Chunk& x) const {
     F::load_rows(a.k, c, x.k);
     F::load_rows(a.q, c, x.q);
     F::template load_matrix<false>(a.w.solve, c, x.solve);
     F::template load_matrix<false>(a.w.read, c, x.read);
-    fetch_gates(c, x);
+    x.g = F::load_gates(c);
     F::load_col(a.v, c, x.v);
   }
 
@@ -69,12 +62,21 @@ struct Forward : Team<T, DK> {
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     if (alone) {
       // a row by itself: its own decay takes the place of the sums', and only its products count
-      x.enter = F::load_gate(3, c);
-      x.stay = a.w.rows[(chunk_index(a, F::bh, c) * 4 + 3) * kChunk + only];
+      x.g.enter = F::load_gate(3, c);
+      x.g.stay = a.w.rows[(chunk_index(a, F::bh, c) * 4 + 3) * kChunk + only];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x.leave[i] = row() + i == only ? 1.f : 0.f;
+      for (int i = 0; i < 4; ++i) x.g.leave[i] = row() + i == only ? 1.f : 0.f;
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (unsigned n = 0; n < sizeof(T) / 2; ++n)
+          if (16 * wave + m != only) x.k[k].w[n] = convfwd::u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) keep(x.read[k], 32 * k + 8 * q4, only, only + 1);
+      wait_for_memory();
     }
     __syncthreads();  // the state's parts are there
+    const Gates gates = F::load_gates(next);
     F::put_rows(s.k, x.k);
     f32x4_t ks = zero, qs = zero;
 #pragma unroll
@@ -86,8 +88,8 @@ struct Forward : Team<T, DK> {
     f32x4_t xs, u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      xs[i] = to_f32(x.v[i]) - times(x.enter[i], ks[i]);
-      u[i] = alone && row() + i != only ? 0.f : x.beta[i] * xs[i];
+      xs[i] = to_f32(x.v[i]) - times(x.g.enter[i], ks[i]);
+      u[i] = alone && row() + i != only ? 0.f : x.g.beta[i] * xs[i];
     }
     F::load_rows(a.k, next, x.k);
     F::load_rows(a.q, next, x.q);
@@ -104,14 +106,14 @@ struct Forward : Team<T, DK> {
         }
       xs += more;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = x.beta[i] * xs[i];
+      for (int i = 0; i < 4; ++i) u[i] = x.g.beta[i] * xs[i];
     }
     F::template load_matrix<false>(a.w.solve, next, x.solve);
     f32x4_t lu;
     float test = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      lu[i] = times(x.leave[i], u[i]);
+      lu[i] = times(x.g.leave[i], u[i]);
       test = fmaf(u[i], 0.f, test);
     }
     F::template put<YP, typename F::Rows>(s.out, row(), u);
@@ -132,11 +134,10 @@ struct Forward : Team<T, DK> {
       if (F::tile(j) < F::DT) {
         f32x4_t n, more = zero;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) n[i] = times(x.stay, state[j][i]);
+        for (int i = 0; i < 4; ++i) n[i] = times(x.g.stay, state[j][i]);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          Parts<NP> kt = F::cols_of(s.k, F::tile(j), k);
-          if (alone) keep(kt, 32 * k + 8 * q4, only, only + 1);
+          const auto kt = F::cols_of(s.k, F::tile(j), k);
           (k ? more : n) = mma(kt, up[k], k ? more : n);
         }
         state[j] = n + more;
@@ -144,7 +145,7 @@ struct Forward : Team<T, DK> {
     F::put_state(s.state, state);
     f32x4_t o, more = zero;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = times(x.enter[i], qs[i]);
+    for (int i = 0; i < 4; ++i) o[i] = times(x.g.enter[i], qs[i]);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       if (F::template has<false>(k)) {
@@ -152,39 +153,42 @@ struct Forward : Team<T, DK> {
         const auto op = F::template get<YP, typename F::Rows>(s.out, k);
         (k ? more : o) = mma_first<YP>(x.read[k], op, k ? more : o);
       }
-    const int64_t ld = (int64_t)a.hv * a.dv;
-    T* y = (T*)a.y + ((int64_t)F::b * a.t + c * kChunk) * ld + (int64_t)F::h * a.dv;
-    const uint32_t to = (uint32_t)(row() * (uint32_t)ld + col) * (uint32_t)sizeof(T);
-    const int n = a.t - c * kChunk;
-    if (F::live)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (row() + i < n && (!alone || row() + i == only)) store_at(y + i * ld, to, from_f32<T>(a.scale * (o[i] + more[i])));
+    // Stores come after the loads of the next chunk: waits for memory are counted in the order of issue, and a load
+    // issued after a store would be waited for together with it.
     F::template load_matrix<false>(a.w.read, next, x.read);
-    fetch_gates(next, x);
+    x.g = gates;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = a.scale * (o[i] + more[i]);
+    F::store_col(a.y, c, o, alone ? only : 0, alone ? only + 1 : kChunk);
     return true;
   }
 
-  // The chunks [c, end), x holding chunk c.  One in which something is not finite goes row by row, so that it reaches
-  // only what comes after it.
-  template <typename Before>
-  __device__ __forceinline__ void run(int c, int end, Chunk& x, const Before& before) {
+  // The state before chunk c, kept for the backward pass.
+  __device__ __forceinline__ void keep_state(int c) const {
+    float* to = a.states && c < a.chunks ? a.states + (((int64_t)F::b * a.chunks + c) * a.hv + F::h) * a.dk * a.dv : nullptr;
+    F::store_state(to, a.dv, a.dv, state);
+  }
+
+  // All chunks, x holding the first.  One in which something is not finite goes row by row, so that it reaches only
+  // what comes after it.
+  __device__ __forceinline__ void run(Chunk& x) {
     bool alone = false;
-    int only = 0;
+    int c = 0, only = 0;
+    keep_state(0);
 #pragma clang loop unroll(disable)
-    while (c < end) {
-      const int n = min(kChunk, a.t - c * kChunk);
-      const bool last = !alone || only + 1 >= n;
-      if (!alone) before(c);
-      if (!chunk(c, last ? min(c + 1, end - 1) : c, x, alone, only)) {
+    while (c < a.chunks) {
+      const bool last = !alone || only + 1 >= min(kChunk, a.t - c * kChunk);
+      if (!chunk(c, last ? min(c + 1, a.chunks - 1) : c, x, alone, only)) {
         alone = true;
         only = 0;
         fetch(c, x);
+        wait_for_memory();
         continue;
       }
       if (last) {
         ++c;
         alone = false;
+        keep_state(c);
       } else {
         ++only;
       }
@@ -203,12 +207,12 @@ __global__ __launch_bounds__(kTeam, 2) void delta_fwd_kernel(DeltaArgs a, int bl
   f.load_state(a.h0 ? a.h0 + bh * size : nullptr, f.state);
   if (threadIdx.x == 0) s.bad[0] = s.bad[1] = 0;
   f.put_state(s.state, f.state);
-  typename F::Chunk x;
-  if (a.chunks > 0) f.fetch(0, x);
-  f.run(0, a.chunks, x, [&](int c) {
-    if (a.states) f.store_state(a.states + (((int64_t)f.b * a.chunks + c) * a.hv + f.h) * size, a.dv, f.live, f.state);
-  });
-  f.store_state(a.h_last + bh * size, a.dv, f.live, f.state);
+  if (a.chunks > 0) {
+    typename F::Chunk x;
+    f.fetch(0, x);
+    f.run(x);
+  }
+  f.store_state(a.h_last + bh * size, a.dv, a.dv, f.state);
 }
 
 }  // namespace

@@ -241,26 +241,26 @@ struct Grad {
     const float* before = c ? dstate - (int64_t)a.dk * a.dvp : a.dh0 + bh * a.dk * a.dv;
     const int ldb = c ? a.dvp : a.dv;
     const float* zs = a.w.z + at * kChunk * a.dvp;
-    const T* vs = (const T*)a.v.p + b * a.v.sb + h * a.v.sh + (int64_t)c * kChunk * a.v.st;
-    const T* dys = (const T*)a.dy.p + b * a.dy.sb + h * a.dy.sh + (int64_t)c * kChunk * a.dy.st;
-    const int last = a.t - 1 - c * kChunk;
+    const Range vs = rows_range<T>(a.v, b, h, c * kChunk, a.t, a.dv), dys = rows_range<T>(a.dy, b, h, c * kChunk, a.t, a.dv);
     const auto fetch = [&](int v0, Slice& x) {
       load_state(states, v0, a.dv, x.s);
       load_state(dstate, v0, a.dvp, x.ds);
       load_state(before, v0, ldb, x.before);
-      const uint32_t col = min(v0 + 16 * half + m, a.dv - 1) * (uint32_t)sizeof(T), ld = (uint32_t)a.v.st * (uint32_t)sizeof(T);
+      const int col = v0 + 16 * half + m;
+      const uint32_t ld = row_bytes<T>(a.v), at_v = col < a.dv ? own * ld + (uint32_t)col * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         x.z[i] = load_at<float>(zs + (int64_t)i * a.dvp + v0, (uint32_t)(own * a.dvp + 16 * half + m) * 4u);
-        x.v[i] = load_at<T>(vs, (uint32_t)min(own + i, last) * ld + col);
+        x.v[i] = vs.load<T>(at_v + i * ld);
       }
-      const uint32_t dy_row = (uint32_t)min(row(), last) * ((uint32_t)a.dy.st * (uint32_t)sizeof(T));
+      const uint32_t dy_row = row() * row_bytes<T>(a.dy);
       if (a.vec_dy) {
         x.dy.load(dys, dy_row, v0 + 8 * q4, a.dv);
       } else {
         T e8[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) e8[e] = load_at<T>(dys, dy_row + min(v0 + 8 * q4 + e, a.dv - 1) * (uint32_t)sizeof(T));
+        for (int e = 0; e < 8; ++e)
+          e8[e] = dys.load<T>(v0 + 8 * q4 + e < a.dv ? dy_row + (uint32_t)(v0 + 8 * q4 + e) * (uint32_t)sizeof(T) : kNowhere);
         __builtin_memcpy(x.dy.w, e8, sizeof(e8));
       }
     };
@@ -273,7 +273,7 @@ struct Grad {
       s.seq[tid] = a.w.seq[at * kChunk + tid];
     }
     if (tid < 2) s.bad[tid] = 0;
-    k.put(s.rows, a.dkp);
+    k.put(s.rows);
     bool wild = !k.finite() || !q.finite();
     wild = __syncthreads_or(wild);
     const f32x4_t enter = *(const f32x4_t*)(s.gates + own), leave = *(const f32x4_t*)(s.gates + kChunk + own);
@@ -298,17 +298,14 @@ struct Grad {
           for (int e = 0; e < 4; ++e) dot = fmaf(x.s[n][e], x.before[n][e], dot);  // S is zero outside
       // r and dx; rows past T and columns past Dv hold nothing
       f32x4_t r, z = x.z, dx;
-      Parts<NP> yp;
-      {
-        float e8[8], t8[8];
-        x.dy.get(t8, c * kChunk + row() < a.t);
+      float e8[8];
+      x.dy.get(e8);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) e8[e] = v0 + 8 * q4 + e < a.dv ? t8[e] : 0.f;
-        yp = split<NP>(e8);
-      }
+      for (int e = 0; e < 8; ++e) e8[e] = c * kChunk + row() < a.t ? e8[e] : 0.f;
+      const Parts<NP> yp = split<NP>(e8);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        r[i] = v0 + 16 * half + m < a.dv && c * kChunk + own + i < a.t ? to_f32(x.v[i]) : 0.f;
+        r[i] = c * kChunk + own + i < a.t ? to_f32(x.v[i]) : 0.f;
         dx[i] = beta[i] * z[i];
         dxv[i] = fmaf(dx[i], r[i], dxv[i]);
       }
@@ -426,7 +423,7 @@ struct Grad {
     add<true, GP>(s.l, dk, wild);
     renew();
     __syncthreads();
-    q.put(s.rows, a.dkp);
+    q.put(s.rows);
     __syncthreads();
     renew();
     add<true, GP>(s.p, dk, wild);

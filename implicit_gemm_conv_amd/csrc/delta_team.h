@@ -15,6 +15,12 @@ struct ColsAt {
   static constexpr int ld = LEN + 8, part = 16 * ld;
 };
 
+// Gates of the lane's four rows, and the last row's enter.
+struct Gates {
+  f32x4_t enter, leave, beta;
+  float stay;
+};
+
 template <typename T, int DK>
 struct Team {
   static constexpr int NP = InParts<T>::n, KS = DK / 32, DT = DK / 16;
@@ -24,7 +30,7 @@ struct Team {
   typedef ColsAt<kChunk> Rows;
 
   const DeltaArgs& a;
-  int wave, m, q4, lane, b, h, hk, bh, col, vcol;
+  int wave, m, q4, lane, b, h, hk, bh, col;
   bool live;
 
   __device__ __forceinline__ Team(const DeltaArgs& a_, int bh_, int cb) : a(a_), bh(bh_) {
@@ -37,7 +43,6 @@ struct Team {
     hk = h / (a.hv / a.hk);
     col = cb * 16 + m;
     live = col < a.dv;
-    vcol = min(col, a.dv - 1);
   }
   __device__ __forceinline__ int tile(int j) const { return wave * own + j; }       // of the state
   __device__ __forceinline__ int row() const { return 16 * wave + 4 * q4; }         // the first of the lane's four
@@ -52,15 +57,14 @@ struct Team {
         s[j][r] = from && live && d < a.dk ? from[(int64_t)d * a.dv + col] : 0.f;
       }
   }
-  // (a state's rows are below 2^25 bytes apart, so that 128 of them have offsets of 32 bits)
-  __device__ __forceinline__ void store_state(float* to, int ld, bool in, const f32x4_t (&s)[own]) const {
-    if (!in) return;
+  // ... into a (Dk, ld) state of which the columns below `width` are there; nowhere if `to` is NULL
+  __device__ __forceinline__ void store_state(float* to, int ld, int width, const f32x4_t (&s)[own]) const {
+    const Range x(to, to ? (int64_t)a.dk * ld * 4 : 0);
+    const uint32_t at = col < width ? (uint32_t)(4 * q4 * ld + col) * 4u : kNowhere;
 #pragma unroll
     for (int j = 0; j < own; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (16 * tile(j) + 4 * q4 + r < a.dk)
-          store_at(to + (int64_t)(16 * tile(j) + r) * ld, (uint32_t)(4 * q4 * ld + col) * 4u, s[j][r]);
+      for (int r = 0; r < 4; ++r) x.store(at + (uint32_t)((16 * tile(j) + r) * ld) * 4u, s[j][r]);
   }
   // four neighbouring rows of the lane's column, as parts
   template <int N, typename AT>
@@ -93,12 +97,11 @@ struct Team {
   }
   // this wave's rows of q or k
   __device__ __forceinline__ void load_rows(const Heads& x, int c, Raw8<T> (&to)[KS]) const {
-    const T* p = (const T*)x.p + b * x.sb + hk * x.sh + (int64_t)c * kChunk * x.st;
-    const uint32_t at = (uint32_t)min(16 * wave + m, a.t - 1 - c * kChunk) * ((uint32_t)x.st * (uint32_t)sizeof(T));
+    const Range p = rows_range<T>(x, b, hk, c * kChunk, a.t, a.dkp);
 #pragma unroll
-    for (int k = 0; k < KS; ++k) to[k].load(p, at, 32 * k + 8 * q4, a.dkp);
+    for (int k = 0; k < KS; ++k) to[k].load(p, (16 * wave + m) * row_bytes<T>(x), 32 * k + 8 * q4, a.dkp);
   }
-  __device__ __forceinline__ Parts<NP> rows_of(const Raw8<T> (&x)[KS], int k) const { return x[k].parts(32 * k + 8 * q4 < a.dkp); }
+  __device__ __forceinline__ Parts<NP> rows_of(const Raw8<T> (&x)[KS], int k) const { return x[k].parts(); }
   // ... into LDS, row by row
   __device__ __forceinline__ void put_rows(__bf16* to, const Raw8<T> (&x)[KS]) const {
 #pragma unroll
@@ -108,21 +111,27 @@ struct Team {
       for (int n = 0; n < NP; ++n) *(bf168_t*)(to + n * RowsAt<DK>::part + (16 * wave + m) * RowsAt<DK>::stride + 32 * k + 8 * q4) = p.p[n];
     }
   }
-  // the lane's four rows of its column of v or of y's gradient
+  // the lane's four rows of its column of v or of y's gradient; zero past Dv (and past T, if rows do not overlap)
   __device__ __forceinline__ void load_col(const Heads& x, int c, T (&to)[4]) const {
-    const T* p = (const T*)x.p + b * x.sb + h * x.sh + (int64_t)c * kChunk * x.st;
-    const uint32_t ld = (uint32_t)x.st * (uint32_t)sizeof(T), at = (uint32_t)vcol * (uint32_t)sizeof(T);
-    const int last = a.t - 1 - c * kChunk;
-    if (last >= kChunk - 1) {
+    const Range p = rows_range<T>(x, b, h, c * kChunk, a.t, a.dv);
+    const uint32_t ld = row_bytes<T>(x), at = live ? row() * ld + (uint32_t)col * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) to[r] = load_at<T>(p + (int64_t)r * x.st, row() * ld + at);
-    } else {
+    for (int r = 0; r < 4; ++r) to[r] = p.load<T>(at + r * ld);
+  }
+  // ... and of y or of v's gradient, dense, rows past T left out
+  __device__ __forceinline__ void store_col(void* to, int c, const f32x4_t& v, int first = 0, int end = kChunk) const {
+    const uint32_t ld = (uint32_t)(a.hv * a.dv) * (uint32_t)sizeof(T);
+    const Range p((T*)to + ((int64_t)b * a.t + c * kChunk) * (a.hv * a.dv) + (int64_t)h * a.dv, (int64_t)min(kChunk, a.t - c * kChunk) * ld);
+    const uint32_t at = live ? row() * ld + (uint32_t)col * (uint32_t)sizeof(T) : kNowhere;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) to[r] = load_at<T>(p, min(row() + r, last) * ld + at);
-    }
+    for (int r = 0; r < 4; ++r) p.store(row() + r >= first && row() + r < end ? at + r * ld : kNowhere, from_f32<T>(v[r]));
   }
   __device__ __forceinline__ f32x4_t load_gate(int which, int c) const {
     return load_at<f32x4_t>(a.w.rows + (chunk_index(a, bh, c) * 4 + which) * kChunk, 4u * row());
+  }
+  __device__ __forceinline__ Gates load_gates(int c) const {
+    return Gates{load_gate(0, c), load_gate(1, c), load_gate(2, c),
+                 load_at<float>(a.w.rows + chunk_index(a, bh, c) * 4 * kChunk, 4u * (kChunk - 1))};
   }
   // this wave's operands of a triangular matrix: of a lower one steps 0 and, from wave 2 on, 1; of an
   // upper one (UP) step 1 and, up to wave 1, 0
