@@ -22,12 +22,12 @@ int check(const convdelta_desc* d) {
   if (d->hv % d->hk || !isfinite(d->scale)) return CONVFWD_ERR_BAD_DESC;
   if (d->dtype != CONVFWD_F32 && d->dtype != CONVFWD_F16 && d->dtype != CONVFWD_BF16) return CONVFWD_ERR_UNSUPPORTED;
   if (d->dk > CONVDELTA_MAX_DK) return CONVFWD_ERR_UNSUPPORTED;
-  // workgroups of 256 threads: at most one for each chunk, value head and 16 columns (rounded up to 32), and the
-  // heads are rounded up to 8; a grid holds less than 2^32 threads
-  const int64_t lim = (int64_t)1 << 24, chunks = ((int64_t)d->t + kChunk - 1) / kChunk, blocks = ((int64_t)d->dv + 31) / 32 * 2;
+  // workgroups of up to 512 threads: one for each value head and 16 columns (rounded up to 32), where the heads are
+  // rounded up to 8, or for each chunk and value head; a grid holds less than 2^32 threads
+  const int64_t lim = (int64_t)1 << 23, chunks = ((int64_t)d->t + kChunk - 1) / kChunk, blocks = ((int64_t)d->dv + 31) / 32 * 2;
   const int64_t heads = ((int64_t)d->b * d->hv + 7) / 8 * 8;
   if (d->t >= 1 << 30 || d->hv >= lim || blocks >= lim || heads >= lim || heads * blocks >= lim) return CONVFWD_ERR_TOO_LARGE;
-  if (chunks * heads >= lim || chunks * heads * blocks >= lim) return CONVFWD_ERR_TOO_LARGE;
+  if (chunks * heads >= lim) return CONVFWD_ERR_TOO_LARGE;
   // offsets of 32 bits: 64 rows of v or y, 128 rows of a state
   if ((int64_t)d->hv * d->dv >= (int64_t)1 << 23 || d->dv >= 1 << 22) return CONVFWD_ERR_TOO_LARGE;
   // ... and one for each 2048 elements of q and k

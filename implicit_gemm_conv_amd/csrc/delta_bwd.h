@@ -8,7 +8,8 @@
 //
 // z and each chunk's dS are left for the gradients that add over all columns
 // (delta_grad.h).  The steps between barriers are those of delta_fwd.h: (1) du, (2) z,
-// (3) the state's gradient.  Included by one source for each type.
+// (3) the state's gradient.  The waves of the first role go the way from state to state,
+// those of the second bring q and dy.  Included by one source for each type.
 #include "delta_team.h"
 
 namespace convdelta {
@@ -25,7 +26,7 @@ struct BwdLds {
   int bad[2];
 };
 
-template <typename T, int DK>
+template <typename T, int DK, bool FIRST>
 struct Backward : Team<T, DK> {
   typedef Team<T, DK> F;
   typedef BwdLds<T, DK> Lds;
@@ -36,140 +37,109 @@ struct Backward : Team<T, DK> {
   using F::col;
   using F::row;
   static constexpr int NP = F::NP, KS = F::KS;
+  typedef typename F::Rows Rows;
 
   struct Chunk {
-    Raw8<T> k[KS], q[KS];
-    Parts<kParts> solve[2], read[2];
-    Gates g;
-    T dy[4];
+    Raw8<T> rows[KS];                // of k, or of q
+    Parts<kParts> solve[2], read[2]; // first role
+    f32x4_t enter, leave, beta;
+    float stay;
+    T dy[4];                         // second role
   };
 
   Lds& s;
-  f32x4_t state[F::own];
+  f32x4_t state;
   int turn = 0;
 
   __device__ __forceinline__ Backward(const DeltaArgs& a_, Lds& s_, int bh_, int cb) : F(a_, bh_, cb), s(s_) {}
 
   __device__ __forceinline__ void fetch_rows(int c, Chunk& x) const {
-    F::load_rows(a.k, c, x.k);
-    F::load_rows(a.q, c, x.q);
-    F::load_col(a.dy, c, x.dy);
+    F::load_rows(FIRST ? a.k : a.q, c, x.rows);
+    if (!FIRST) F::load_col(a.dy, c, x.dy);
   }
-  __device__ __forceinline__ void fetch(int c, Chunk& x) const {
-    fetch_rows(c, x);
+  __device__ __forceinline__ void fetch_matrices(int c, Chunk& x) const {
+    if (!FIRST) return;
     F::template load_matrix<true>(a.w.solve_t, c, x.solve);
     F::template load_matrix<true>(a.w.read_t, c, x.read);
-    x.g = F::load_gates(c);
   }
-  __device__ __forceinline__ f32x4_t dy_of(int c, const Chunk& x) const {
+  __device__ __forceinline__ void fetch_gates(int c, Chunk& x) const {
+    x.enter = F::load_gate(0, c);
+    if (FIRST) x.leave = F::load_gate(1, c), x.beta = F::load_gate(2, c);
+    x.stay = F::load_stay(c);
+  }
+  // dy of chunk c into LDS (second role)
+  __device__ __forceinline__ f32x4_t put_dy(int c, const Chunk& x) const {
     f32x4_t d;
 #pragma unroll
     for (int i = 0; i < 4; ++i) d[i] = c * kChunk + row() + i < a.t ? to_f32(x.dy[i]) : 0.f;
+    F::template put<NP, Rows>(s.dy, row(), d);
     return d;
   }
 
   // (1) and (2) for all rows, or (masked) the rows [lo, hi) of one sequence, into z; kd is k dS.
   __device__ __forceinline__ void solve(int c, Chunk& x, const f32x4_t& kd, bool masked, int lo, int hi, f32x4_t& z) {
-    if (masked) {
-      F::template load_matrix<true>(a.w.solve_t, c, x.solve);
-      F::template load_matrix<true>(a.w.read_t, c, x.read);
+    f32x4_t du, more = {0.f, 0.f, 0.f, 0.f};
+    if (FIRST) {
+      if (masked) {
+        fetch_matrices(c, x);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) keep(x.solve[k], 32 * k + 8 * q4, lo, hi), keep(x.read[k], 32 * k + 8 * q4, lo, hi);
-      wait_for_memory();
-    }
-    f32x4_t ry = {0.f, 0.f, 0.f, 0.f}, more = ry;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (F::template has<true>(k)) {
-        Parts<NP> d = F::template get<NP, typename F::Rows>(s.dy, k);
-        if (masked) keep(d, 32 * k + 8 * q4, lo, hi);
-        (k ? more : ry) = mma(x.read[k], d, k ? more : ry);
+        for (int k = 0; k < 2; ++k) keep(x.solve[k], 32 * k + 8 * q4, lo, hi), keep(x.read[k], 32 * k + 8 * q4, lo, hi);
+        wait_for_memory();
       }
-    f32x4_t du, bd;
+      f32x4_t ry = more, bd;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool out = row() + i < lo || row() + i >= hi;
-      du[i] = out ? 0.f : times(x.g.leave[i], kd[i]) + a.scale * (ry[i] + more[i]);
-      bd[i] = out ? 0.f : x.g.beta[i] * du[i];
-    }
-    if (masked) __syncthreads();  // what is read of the sequence before
-    F::template put<kParts, typename F::Rows>(s.bd, row(), bd);
-    __syncthreads();
-    more = f32x4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (F::template has<true>(k)) {
-        const auto bp = F::template get<kParts, typename F::Rows>(s.bd, k);
-        (k ? more : du) = mma(x.solve[k], bp, k ? more : du);
-      }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (row() + i >= lo && row() + i < hi) z[i] = du[i] + more[i];
-  }
-
-  // What a wave gives to (3).
-  __device__ __forceinline__ void give(int c, const Chunk& x, f32x4_t& z, const f32x4_t& dy) {
-    f32x4_t in, out;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (c * kChunk + row() + i >= a.t) z[i] = 0.f;  // rows past T hold nothing, whatever the state's gradient is
-      in[i] = times(x.g.enter[i], a.scale * dy[i]);
-      out[i] = -times(x.g.enter[i], x.g.beta[i] * z[i]);
-    }
-    F::template put<kParts, typename F::Rows>(s.in, row(), in);
-    F::template put<kParts, typename F::Rows>(s.out, row(), out);
-  }
-  __device__ __forceinline__ void store(int c, const f32x4_t& beta, const f32x4_t& z) const {
-    const Range zs(a.w.z + chunk_index(a, F::bh, c) * kChunk * a.dvp, (int64_t)kChunk * a.dvp * 4);
-    const uint32_t at = col < a.dvp ? (uint32_t)(row() * a.dvp + col) * 4u : kNowhere;
-    f32x4_t dx;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dx[i] = beta[i] * z[i];
-      zs.store(at + (uint32_t)(i * a.dvp) * 4u, F::live ? z[i] : 0.f);
-    }
-    F::store_col(a.dv_, c, dx);
-  }
-  // (3), from the rows [0, first) where masked
-  __device__ __forceinline__ void move(float stay, bool masked, int first) {
-    Parts<kParts> ip[2], op[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      ip[k] = F::template get<kParts, typename F::Rows>(s.in, k);
-      op[k] = F::template get<kParts, typename F::Rows>(s.out, k);
-    }
-#pragma unroll
-    for (int j = 0; j < F::own; ++j)
-      if (F::tile(j) < F::DT) {
-        f32x4_t n, more = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) n[i] = times(stay, state[j][i]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          Parts<NP> qt = F::cols_of(s.q, F::tile(j), k), kt = F::cols_of(s.k, F::tile(j), k);
-          if (masked) keep(qt, 32 * k + 8 * q4, 0, first), keep(kt, 32 * k + 8 * q4, 0, first);
-          n = mma(qt, ip[k], n);
-          more = mma(kt, op[k], more);
+      for (int k = 0; k < 2; ++k)
+        if (F::template has<true>(k)) {
+          Parts<NP> d = F::template get<NP, Rows>(s.dy, k);
+          if (masked) keep(d, 32 * k + 8 * q4, lo, hi);
+          (k ? more : ry) = mma(x.read[k], d, k ? more : ry);
         }
-        state[j] = n + more;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool out = row() + i < lo || row() + i >= hi;
+        du[i] = out ? 0.f : times(x.leave[i], kd[i]) + a.scale * (ry[i] + more[i]);
+        bd[i] = out ? 0.f : x.beta[i] * du[i];
       }
-    F::put_state(s.state, state);
+      if (masked) __syncthreads();  // what is read of the sequence before
+      F::template put<kParts, Rows>(s.bd, row(), bd);
+    } else if (masked) {
+      __syncthreads();
+    }
+    __syncthreads();
+    if (FIRST) {
+      more = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (F::template has<true>(k)) {
+          const auto bp = F::template get<kParts, Rows>(s.bd, k);
+          (k ? more : du) = mma(x.solve[k], bp, k ? more : du);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (row() + i >= lo && row() + i < hi) z[i] = du[i] + more[i];
+    }
   }
 
-  __device__ __forceinline__ void chunk(int c, int next, Chunk& x) {
-    f32x4_t dy = dy_of(c, x);
-    F::template put<NP, typename F::Rows>(s.dy, row(), dy);
+  __device__ __forceinline__ void chunk(int c, int next, Chunk& x, f32x4_t& dy) {
     __syncthreads();  // the state's parts and dy are there
-    const Gates gates = F::load_gates(next);
-    F::put_rows(s.k, x.k);
-    F::put_rows(s.q, x.q);
-    f32x4_t kd = {0.f, 0.f, 0.f, 0.f}, more = kd;
+    Chunk ahead;
+    fetch_gates(next, ahead);
+    F::put_rows(FIRST ? s.k : s.q, x.rows);
+    f32x4_t kd = {0.f, 0.f, 0.f, 0.f};
+    if (FIRST) {
+      f32x4_t more = kd;
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const auto sp = F::template get<kParts, typename F::State>(s.state, k);
-      (k & 1 ? more : kd) = mma(F::rows_of(x.k, k), sp, k & 1 ? more : kd);
+      for (int k = 0; k < KS; ++k) {
+        const auto sp = F::template get<kParts, typename F::State>(s.state, k);
+        (k & 1 ? more : kd) = mma(F::rows_of(x.rows, k), sp, k & 1 ? more : kd);
+      }
+      kd += more;
+    } else {
+      f32x4_t in;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) in[i] = times(x.enter[i], a.scale * dy[i]);
+      F::template put<kParts, Rows>(s.in, row(), in);
     }
-    kd += more;
     fetch_rows(next, x);
     // All rows at once, and where something is not finite once more, each sequence by itself, so that nothing crosses a
     // start.  `first`: the rows that the state before the chunk reaches are those of the first sequence.
@@ -190,11 +160,18 @@ struct Backward : Team<T, DK> {
         solve(c, x, kd, masked, lo, hi, z);
         hi = lo;
       } while (hi > 0);
-      float test = 0.f;
+      if (FIRST) {
+        float test = 0.f;
+        f32x4_t out;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) test = fmaf(z[i], 0.f, test);
-      give(c, x, z, dy);
-      if (__any(test != 0.f)) s.bad[turn & 1] = 1;  // NaN
+        for (int i = 0; i < 4; ++i) {
+          test = fmaf(z[i], 0.f, test);
+          if (c * kChunk + row() + i >= a.t) z[i] = 0.f;  // rows past T hold nothing, whatever the state's gradient is
+          out[i] = -times(x.enter[i], x.beta[i] * z[i]);
+        }
+        F::template put<kParts, Rows>(s.out, row(), out);
+        if (__any(test != 0.f)) s.bad[turn & 1] = 1;  // NaN
+      }
       __syncthreads();
       const bool bad = s.bad[turn & 1];
       if (threadIdx.x == 0) s.bad[~turn & 1] = 0;
@@ -205,38 +182,75 @@ struct Backward : Team<T, DK> {
       wait_for_memory();
       __syncthreads();
     }
-    F::template load_matrix<true>(a.w.solve_t, next, x.solve);
-    F::template load_matrix<true>(a.w.read_t, next, x.read);
-    move(x.g.stay, masked, first);
+    fetch_matrices(next, x);
+    // (3), from the rows [0, first) where masked
+    if (F::has_tile()) {
+      f32x4_t n, more = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n[i] = times(x.stay, state[i]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const auto ip = F::template get<kParts, Rows>(s.in, k), op = F::template get<kParts, Rows>(s.out, k);
+        Parts<NP> qt = F::cols_of(s.q, F::tile, k), kt = F::cols_of(s.k, F::tile, k);
+        if (masked) keep(qt, 32 * k + 8 * q4, 0, first), keep(kt, 32 * k + 8 * q4, 0, first);
+        n = mma(qt, ip, n);
+        more = mma(kt, op, more);
+      }
+      state = n + more;
+      F::put_state(s.state, state);
+    }
     // stores come after the loads of the next chunk (see delta_fwd.h)
-    store(c, x.g.beta, z);
+    if (FIRST) {
+      const Range zs(a.w.z + chunk_index(a, F::bh, c) * kChunk * a.dvp, (int64_t)kChunk * a.dvp * 4);
+      const uint32_t at = col < a.dvp ? (uint32_t)(row() * a.dvp + col) * 4u : kNowhere;
+      f32x4_t dx;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dx[i] = x.beta[i] * z[i];
+        zs.store(at + (uint32_t)(i * a.dvp) * 4u, F::live ? z[i] : 0.f);
+      }
+      F::store_col(a.dv_, c, dx);
+    } else {
+      dy = put_dy(next, x);
+    }
     keep_state(c - 1);
-    x.g = gates;
+    x.enter = ahead.enter;
+    if (FIRST) x.leave = ahead.leave, x.beta = ahead.beta;
+    x.stay = ahead.stay;
   }
   // The gradient of the state after chunk c.
   __device__ __forceinline__ void keep_state(int c) const {
     F::store_state(c >= 0 ? a.w.dstate + chunk_index(a, F::bh, c) * a.dk * a.dvp : nullptr, a.dvp, a.dvp, state);
   }
+
+  __device__ __forceinline__ void run() {
+    const int64_t size = (int64_t)a.dk * a.dv;
+    state = F::load_state(a.dh_last ? a.dh_last + F::bh * size : nullptr);
+    F::put_state(s.state, state);
+    if (a.chunks > 0) {
+      Chunk x;
+      fetch_rows(a.chunks - 1, x);
+      fetch_matrices(a.chunks - 1, x);
+      fetch_gates(a.chunks - 1, x);
+      keep_state(a.chunks - 1);
+      f32x4_t dy;
+      if (!FIRST) dy = put_dy(a.chunks - 1, x);
+      for (int c = a.chunks - 1; c >= 0; --c) chunk(c, max(c - 1, 0), x, dy);
+    }
+    F::store_state(a.dh0 + F::bh * size, a.dv, a.dv, state);
+  }
 };
 
 template <typename T, int DK>
 __global__ __launch_bounds__(kTeam, 2) void delta_bwd_kernel(DeltaArgs a, int blocks) {
-  typedef Backward<T, DK> F;
-  __shared__ __attribute__((aligned(16))) typename F::Lds s;
+  __shared__ __attribute__((aligned(16))) BwdLds<T, DK> s;
   int bh, cb;
   if (!head_of(a.b * a.hv, blocks, bh, cb)) return;
-  F f(a, s, bh, cb);
-  const int64_t size = (int64_t)a.dk * a.dv;
-  f.load_state(a.dh_last ? a.dh_last + bh * size : nullptr, f.state);
-  if (threadIdx.x == 0) s.bad[0] = s.bad[1] = 0;
-  f.put_state(s.state, f.state);
-  if (a.chunks > 0) {
-    typename F::Chunk x;
-    f.fetch(a.chunks - 1, x);
-    f.keep_state(a.chunks - 1);
-    for (int c = a.chunks - 1; c >= 0; --c) f.chunk(c, max(c - 1, 0), x);
-  }
-  f.store_state(a.dh0 + bh * size, a.dv, a.dv, f.state);
+  if (threadIdx.x < 2) s.bad[threadIdx.x] = 0;
+  if (wave_id() < 4)
+    Backward<T, DK, true>(a, s, bh, cb).run();
+  else
+    Backward<T, DK, false>(a, s, bh, cb).run();
 }
 
 }  // namespace

@@ -17,10 +17,11 @@
 // those that matter to 24 bits are added in fp32.  A bf16 input is one part, an
 // fp16 input two.  bf16 has fp32's range, so nothing overflows on the way.
 //
-// A workgroup of four waves carries 16 columns of one head's state (or of its
-// gradient).  Wave w computes rows 16 w .. + 15 of r, x and y, and a quarter of the
-// state's rows; the parts of what one step makes and the next one contracts over go
-// through LDS, column by column, so that an operand is one 16-byte read.
+// A workgroup of eight waves carries 16 columns of one head's state (or of its
+// gradient), four of them in each of two roles.  Wave w of a role computes rows 16 w
+// .. + 15 of a chunk's r, x and y, and each wave 16 rows of the state; the parts of what
+// one step makes and the next one contracts over go through LDS, column by column, so
+// that an operand is one 16-byte read.
 #pragma once
 
 #include "conv_device.h"

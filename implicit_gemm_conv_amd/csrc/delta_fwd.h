@@ -1,10 +1,11 @@
 // delta_fwd.h -- gated delta rule forward: a workgroup carries 16 columns of one
 // head's state through the chunks.  Included by one source for each type.
 //
-// A chunk takes three steps between barriers: (1) k S and q S, r; (2) x = r + H (beta r),
-// u; (3) the state, y.  Each wave has its own rows (1, 2, y) or rows of the state (3), and
-// fetches the next chunk's operands, each of which no other wave needs, as soon as this
-// chunk's are used.
+// A chunk takes three steps between barriers: (1) k S, r, and q S; (2) x = r + H (beta r),
+// u; (3) the state, and y.  The waves of the first role go the way from state to state (k S,
+// r, x, u), those of the second compute y beside it; the state's rows are all waves'.  Each
+// wave fetches what it needs of the next chunk, which no other wave needs, as soon as this
+// chunk's is used.
 #include "delta_team.h"
 
 namespace convdelta {
@@ -20,7 +21,7 @@ struct FwdLds {
   int bad[2];
 };
 
-template <typename T, int DK>
+template <typename T, int DK, bool FIRST>
 struct Forward : Team<T, DK> {
   typedef Team<T, DK> F;
   typedef FwdLds<T, DK> Lds;
@@ -28,32 +29,36 @@ struct Forward : Team<T, DK> {
   using F::q4;
   using F::m;
   using F::wave;
-  using F::col;
   using F::row;
   static constexpr int NP = F::NP, KS = F::KS, YP = F::YP;
+  typedef typename F::Rows Rows;
 
   // what a chunk needs
   struct Chunk {
-    Raw8<T> k[KS], q[KS];
-    Parts<kParts> solve[2];
-    Parts<YP> read[2];
-    Gates g;
+    Raw8<T> rows[KS];                   // of k, or of q
+    Parts<FIRST ? kParts : YP> mat[2];  // of H, or of the decayed q k^T
+    f32x4_t enter, leave, beta;
+    float stay;
     T v[4];
   };
 
   Lds& s;
-  f32x4_t state[F::own];
+  f32x4_t state;
   int turn = 0;
 
   __device__ __forceinline__ Forward(const DeltaArgs& a_, Lds& s_, int bh_, int cb) : F(a_, bh_, cb), s(s_) {}
 
-  __device__ __forceinline__ void fetch(int c, Chunk& x) const {
-    F::load_rows(a.k, c, x.k);
-    F::load_rows(a.q, c, x.q);
-    F::template load_matrix<false>(a.w.solve, c, x.solve);
-    F::template load_matrix<false>(a.w.read, c, x.read);
-    x.g = F::load_gates(c);
-    F::load_col(a.v, c, x.v);
+  __device__ __forceinline__ void fetch_rows(int c, Chunk& x) const {
+    F::load_rows(FIRST ? a.k : a.q, c, x.rows);
+    if (FIRST) F::load_col(a.v, c, x.v);
+  }
+  __device__ __forceinline__ void fetch_matrix(int c, Chunk& x) const {
+    F::template load_matrix<false>(FIRST ? a.w.solve : a.w.read, c, x.mat);
+  }
+  __device__ __forceinline__ void fetch_gates(int c, Chunk& x) const {
+    x.enter = F::load_gate(0, c);
+    if (FIRST) x.leave = F::load_gate(1, c), x.beta = F::load_gate(2, c);
+    x.stay = F::load_stay(c);
   }
 
   // One chunk, all of its rows, or (`alone`) row `only` of it.  False where u is not finite: the state is then as it
@@ -62,63 +67,78 @@ struct Forward : Team<T, DK> {
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     if (alone) {
       // a row by itself: its own decay takes the place of the sums', and only its products count
-      x.g.enter = F::load_gate(3, c);
-      x.g.stay = a.w.rows[(chunk_index(a, F::bh, c) * 4 + 3) * kChunk + only];
+      x.enter = F::load_gate(3, c);
+      x.stay = a.w.rows[(chunk_index(a, F::bh, c) * 4 + 3) * kChunk + only];
+      if (FIRST) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x.g.leave[i] = row() + i == only ? 1.f : 0.f;
+        for (int i = 0; i < 4; ++i) x.leave[i] = row() + i == only ? 1.f : 0.f;
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+        for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (unsigned n = 0; n < sizeof(T) / 2; ++n)
-          if (16 * wave + m != only) x.k[k].w[n] = convfwd::u32x4_t{0u, 0u, 0u, 0u};
+          for (unsigned n = 0; n < sizeof(T) / 2; ++n)
+            if (16 * wave + m != only) x.rows[k].w[n] = convfwd::u32x4_t{0u, 0u, 0u, 0u};
+      } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) keep(x.read[k], 32 * k + 8 * q4, only, only + 1);
+        for (int k = 0; k < 2; ++k) keep(x.mat[k], 32 * k + 8 * q4, only, only + 1);
+      }
       wait_for_memory();
     }
     __syncthreads();  // the state's parts are there
-    const Gates gates = F::load_gates(next);
-    F::put_rows(s.k, x.k);
-    f32x4_t ks = zero, qs = zero;
+    Chunk ahead;
+    fetch_gates(next, ahead);
+    if (FIRST) F::put_rows(s.k, x.rows);
+    f32x4_t xs = zero, more = zero;  // k S, or q S; then r, x
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const auto sp = F::template get<kParts, typename F::State>(s.state, k);
-      ks = mma(F::rows_of(x.k, k), sp, ks);
-      qs = mma_first<YP>(F::rows_of(x.q, k), sp, qs);
+      if (FIRST)
+        (k & 1 ? more : xs) = mma(F::rows_of(x.rows, k), sp, k & 1 ? more : xs);
+      else
+        (k & 1 ? more : xs) = mma_first<YP>(F::rows_of(x.rows, k), sp, k & 1 ? more : xs);
     }
-    f32x4_t xs, u;
+    xs += more;
+    if (alone) {
+      // a state that is not finite, behind a start (with all rows such a chunk comes to nothing)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      xs[i] = to_f32(x.v[i]) - times(x.g.enter[i], ks[i]);
-      u[i] = alone && row() + i != only ? 0.f : x.g.beta[i] * xs[i];
+      for (int i = 0; i < 4; ++i) {
+        if (x.enter[i] == 0.f) xs[i] = 0.f;
+        if (x.stay == 0.f) state[i] = 0.f;
+      }
     }
-    F::load_rows(a.k, next, x.k);
-    F::load_rows(a.q, next, x.q);
-    F::load_col(a.v, next, x.v);
-    F::template put<kParts, typename F::Rows>(s.br, row(), u);
+    f32x4_t u, lu;
+    if (FIRST) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xs[i] = to_f32(x.v[i]) - x.enter[i] * xs[i];
+        u[i] = alone && row() + i != only ? 0.f : x.beta[i] * xs[i];
+      }
+      F::template put<kParts, Rows>(s.br, row(), u);
+    }
+    fetch_rows(next, x);
     __syncthreads();
-    if (!alone) {
-      f32x4_t more = zero;
+    if (FIRST) {
+      if (!alone) {
+        more = zero;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (F::template has<false>(k)) {
-          const auto bp = F::template get<kParts, typename F::Rows>(s.br, k);
-          (k ? more : xs) = mma(x.solve[k], bp, k ? more : xs);
-        }
-      xs += more;
+        for (int k = 0; k < 2; ++k)
+          if (F::template has<false>(k)) {
+            const auto bp = F::template get<kParts, Rows>(s.br, k);
+            (k ? more : xs) = mma(x.mat[k], bp, k ? more : xs);
+          }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = x.g.beta[i] * xs[i];
+        for (int i = 0; i < 4; ++i) u[i] = x.beta[i] * (xs[i] + more[i]);
+      }
+      float test = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lu[i] = x.leave[i] * u[i];
+        test = fmaf(u[i], 0.f, test);
+      }
+      F::template put<kParts, Rows>(s.u, row(), lu);
+      F::template put<YP, Rows>(s.out, row(), u);
+      if (__any(test != 0.f)) s.bad[turn & 1] = 1;  // NaN
+      fetch_matrix(next, x);
     }
-    F::template load_matrix<false>(a.w.solve, next, x.solve);
-    f32x4_t lu;
-    float test = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      lu[i] = times(x.g.leave[i], u[i]);
-      test = fmaf(u[i], 0.f, test);
-    }
-    F::template put<YP, typename F::Rows>(s.out, row(), u);
-    F::template put<kParts, typename F::Rows>(s.u, row(), lu);
-    if (__any(test != 0.f)) s.bad[turn & 1] = 1;  // NaN
     __syncthreads();
     const bool bad = s.bad[turn & 1];
     // the other flag: read before the last barrier, set after the next one but one
@@ -126,40 +146,39 @@ struct Forward : Team<T, DK> {
     ++turn;
     if (!alone && bad) return false;
     // the state moves on
-    Parts<kParts> up[2];
+    if (F::has_tile()) {
+      f32x4_t n;
+      more = zero;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) up[k] = F::template get<kParts, typename F::Rows>(s.u, k);
+      for (int i = 0; i < 4; ++i) n[i] = x.stay * state[i];
 #pragma unroll
-    for (int j = 0; j < F::own; ++j)
-      if (F::tile(j) < F::DT) {
-        f32x4_t n, more = zero;
+      for (int k = 0; k < 2; ++k) {
+        const auto up = F::template get<kParts, Rows>(s.u, k);
+        (k ? more : n) = mma(F::cols_of(s.k, F::tile, k), up, k ? more : n);
+      }
+      state = n + more;
+      F::put_state(s.state, state);
+    }
+    if (!FIRST) {
+      more = zero;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) n[i] = times(x.g.stay, state[j][i]);
+      for (int i = 0; i < 4; ++i) xs[i] = x.enter[i] * xs[i];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const auto kt = F::cols_of(s.k, F::tile(j), k);
-          (k ? more : n) = mma(kt, up[k], k ? more : n);
+      for (int k = 0; k < 2; ++k)
+        if (F::template has<false>(k)) {
+          const auto op = F::template get<YP, Rows>(s.out, k);
+          (k ? more : xs) = mma_first<YP>(x.mat[k], op, k ? more : xs);
         }
-        state[j] = n + more;
-      }
-    F::put_state(s.state, state);
-    f32x4_t o, more = zero;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = times(x.g.enter[i], qs[i]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (F::template has<false>(k)) {
-        if (alone) keep(x.read[k], 32 * k + 8 * q4, only, only + 1);
-        const auto op = F::template get<YP, typename F::Rows>(s.out, k);
-        (k ? more : o) = mma_first<YP>(x.read[k], op, k ? more : o);
-      }
-    // Stores come after the loads of the next chunk: waits for memory are counted in the order of issue, and a load
-    // issued after a store would be waited for together with it.
-    F::template load_matrix<false>(a.w.read, next, x.read);
-    x.g = gates;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = a.scale * (o[i] + more[i]);
-    F::store_col(a.y, c, o, alone ? only : 0, alone ? only + 1 : kChunk);
+      for (int i = 0; i < 4; ++i) xs[i] = a.scale * (xs[i] + more[i]);
+      fetch_matrix(next, x);
+      // Stores come after the loads of the next chunk: waits for memory are counted in the order of issue, and a load
+      // issued after a store would be waited for together with it.
+      F::store_col(a.y, c, xs, alone ? only : 0, alone ? only + 1 : kChunk);
+    }
+    x.enter = ahead.enter;
+    if (FIRST) x.leave = ahead.leave, x.beta = ahead.beta;
+    x.stay = ahead.stay;
     return true;
   }
 
@@ -168,51 +187,57 @@ struct Forward : Team<T, DK> {
     float* to = a.states && c < a.chunks ? a.states + (((int64_t)F::b * a.chunks + c) * a.hv + F::h) * a.dk * a.dv : nullptr;
     F::store_state(to, a.dv, a.dv, state);
   }
+  __device__ __forceinline__ void fetch(int c, Chunk& x) const {
+    fetch_rows(c, x);
+    fetch_matrix(c, x);
+    fetch_gates(c, x);
+  }
 
-  // All chunks, x holding the first.  One in which something is not finite goes row by row, so that it reaches only
-  // what comes after it.
-  __device__ __forceinline__ void run(Chunk& x) {
-    bool alone = false;
-    int c = 0, only = 0;
-    keep_state(0);
+  // All chunks.  One in which something is not finite goes row by row, so that it reaches only what comes after it.
+  // (Both roles take the same turns: they wait for each other at every barrier.)
+  __device__ __forceinline__ void run() {
+    const int64_t size = (int64_t)a.dk * a.dv;
+    state = F::load_state(a.h0 ? a.h0 + F::bh * size : nullptr);
+    F::put_state(s.state, state);
+    if (a.chunks > 0) {
+      Chunk x;
+      fetch(0, x);
+      bool alone = false;
+      int c = 0, only = 0;
+      keep_state(0);
 #pragma clang loop unroll(disable)
-    while (c < a.chunks) {
-      const bool last = !alone || only + 1 >= min(kChunk, a.t - c * kChunk);
-      if (!chunk(c, last ? min(c + 1, a.chunks - 1) : c, x, alone, only)) {
-        alone = true;
-        only = 0;
-        fetch(c, x);
-        wait_for_memory();
-        continue;
-      }
-      if (last) {
-        ++c;
-        alone = false;
-        keep_state(c);
-      } else {
-        ++only;
+      while (c < a.chunks) {
+        const bool last = !alone || only + 1 >= min(kChunk, a.t - c * kChunk);
+        if (!chunk(c, last ? min(c + 1, a.chunks - 1) : c, x, alone, only)) {
+          alone = true;
+          only = 0;
+          fetch(c, x);
+          wait_for_memory();
+          continue;
+        }
+        if (last) {
+          ++c;
+          alone = false;
+          keep_state(c);
+        } else {
+          ++only;
+        }
       }
     }
+    F::store_state(a.h_last + F::bh * size, a.dv, a.dv, state);
   }
 };
 
 template <typename T, int DK>
 __global__ __launch_bounds__(kTeam, 2) void delta_fwd_kernel(DeltaArgs a, int blocks) {
-  typedef Forward<T, DK> F;
-  __shared__ __attribute__((aligned(16))) typename F::Lds s;
+  __shared__ __attribute__((aligned(16))) FwdLds<T, DK> s;
   int bh, cb;
   if (!head_of(a.b * a.hv, blocks, bh, cb)) return;
-  F f(a, s, bh, cb);
-  const int64_t size = (int64_t)a.dk * a.dv;
-  f.load_state(a.h0 ? a.h0 + bh * size : nullptr, f.state);
-  if (threadIdx.x == 0) s.bad[0] = s.bad[1] = 0;
-  f.put_state(s.state, f.state);
-  if (a.chunks > 0) {
-    typename F::Chunk x;
-    f.fetch(0, x);
-    f.run(x);
-  }
-  f.store_state(a.h_last + bh * size, a.dv, a.dv, f.state);
+  if (threadIdx.x < 2) s.bad[threadIdx.x] = 0;
+  if (wave_id() < 4)
+    Forward<T, DK, true>(a, s, bh, cb).run();
+  else
+    Forward<T, DK, false>(a, s, bh, cb).run();
 }
 
 }  // namespace

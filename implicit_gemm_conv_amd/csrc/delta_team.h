@@ -1,5 +1,5 @@
 // delta_team.h -- what the forward and the backward recurrence of the gated delta
-// rule share: where a lane of the four waves stands, the columns of parts in LDS, and
+// rule share: where a lane of the eight waves stands, the columns of parts in LDS, and
 // the operands that a wave fetches for a chunk.
 #pragma once
 
@@ -7,7 +7,7 @@
 
 namespace convdelta {
 
-constexpr int kTeam = 256;  // four waves
+constexpr int kTeam = 512;  // two roles of four waves
 
 // Columns of parts: [part][16 columns][ld].  The 8 spare elements spread the columns over the banks.
 template <int LEN>
@@ -15,27 +15,22 @@ struct ColsAt {
   static constexpr int ld = LEN + 8, part = 16 * ld;
 };
 
-// Gates of the lane's four rows, and the last row's enter.
-struct Gates {
-  f32x4_t enter, leave, beta;
-  float stay;
-};
-
 template <typename T, int DK>
 struct Team {
   static constexpr int NP = InParts<T>::n, KS = DK / 32, DT = DK / 16;
   static constexpr int YP = NP == 3 ? 3 : 2;                // parts that an output of type T can tell apart
-  static constexpr int own = (DT + 3) / 4;                  // 16-row tiles of the state a wave holds
   typedef ColsAt<DK> State;
   typedef ColsAt<kChunk> Rows;
 
   const DeltaArgs& a;
-  int wave, m, q4, lane, b, h, hk, bh, col;
+  int wave, tile, m, q4, lane, b, h, hk, bh, col;  // tile: the wave's 16 rows of the state, where it is below DT
   bool live;
 
   __device__ __forceinline__ Team(const DeltaArgs& a_, int bh_, int cb) : a(a_), bh(bh_) {
     lane = threadIdx.x % 64;
-    wave = wave_id();
+    wave = wave_id() % 4;
+    // the second role has less to do before the state: with few tiles it takes them
+    tile = DT == 8 ? wave_id() : wave_id() - 4;
     m = lane % 16;
     q4 = lane / 16;
     b = bh / a.hv;
@@ -44,27 +39,25 @@ struct Team {
     col = cb * 16 + m;
     live = col < a.dv;
   }
-  __device__ __forceinline__ int tile(int j) const { return wave * own + j; }       // of the state
-  __device__ __forceinline__ int row() const { return 16 * wave + 4 * q4; }         // the first of the lane's four
+  __device__ __forceinline__ int row() const { return 16 * wave + 4 * q4; }  // the first of the lane's four
+  __device__ __forceinline__ bool has_tile() const { return tile >= 0 && tile < DT; }
 
-  // the lane's 4 x own values of a (Dk, Dv) state, zero outside
-  __device__ __forceinline__ void load_state(const float* from, f32x4_t (&s)[own]) const {
+  // the lane's 4 values of a (Dk, Dv) state, zero outside
+  __device__ __forceinline__ f32x4_t load_state(const float* from) const {
+    f32x4_t s;
 #pragma unroll
-    for (int j = 0; j < own; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int d = 16 * tile(j) + 4 * q4 + r;
-        s[j][r] = from && live && d < a.dk ? from[(int64_t)d * a.dv + col] : 0.f;
-      }
+    for (int r = 0; r < 4; ++r) {
+      const int d = 16 * tile + 4 * q4 + r;
+      s[r] = from && live && has_tile() && d < a.dk ? from[(int64_t)d * a.dv + col] : 0.f;
+    }
+    return s;
   }
   // ... into a (Dk, ld) state of which the columns below `width` are there; nowhere if `to` is NULL
-  __device__ __forceinline__ void store_state(float* to, int ld, int width, const f32x4_t (&s)[own]) const {
+  __device__ __forceinline__ void store_state(float* to, int ld, int width, const f32x4_t& s) const {
     const Range x(to, to ? (int64_t)a.dk * ld * 4 : 0);
-    const uint32_t at = col < width ? (uint32_t)(4 * q4 * ld + col) * 4u : kNowhere;
+    const uint32_t at = col < width && has_tile() ? (uint32_t)((16 * tile + 4 * q4) * ld + col) * 4u : kNowhere;
 #pragma unroll
-    for (int j = 0; j < own; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) x.store(at + (uint32_t)((16 * tile(j) + r) * ld) * 4u, s[j][r]);
+    for (int r = 0; r < 4; ++r) x.store(at + (uint32_t)(r * ld) * 4u, s[r]);
   }
   // four neighbouring rows of the lane's column, as parts
   template <int N, typename AT>
@@ -80,10 +73,8 @@ struct Team {
 #pragma unroll
     for (int n = 0; n < N; ++n) *(bf164_t*)(cols + n * AT::part + m * AT::ld + at) = o[n];
   }
-  __device__ __forceinline__ void put_state(__bf16* cols, const f32x4_t (&s)[own]) const {
-#pragma unroll
-    for (int j = 0; j < own; ++j)
-      if (tile(j) < DT) put<kParts, State>(cols, 16 * tile(j) + 4 * q4, s[j]);
+  __device__ __forceinline__ void put_state(__bf16* cols, const f32x4_t& s) const {
+    if (has_tile()) put<kParts, State>(cols, 16 * tile + 4 * q4, s);
   }
   // the operand of step k of a contraction over the state's rows, or over the chunk's
   template <int N, typename AT>
@@ -129,9 +120,9 @@ struct Team {
   __device__ __forceinline__ f32x4_t load_gate(int which, int c) const {
     return load_at<f32x4_t>(a.w.rows + (chunk_index(a, bh, c) * 4 + which) * kChunk, 4u * row());
   }
-  __device__ __forceinline__ Gates load_gates(int c) const {
-    return Gates{load_gate(0, c), load_gate(1, c), load_gate(2, c),
-                 load_at<float>(a.w.rows + chunk_index(a, bh, c) * 4 * kChunk, 4u * (kChunk - 1))};
+  // the last row's enter
+  __device__ __forceinline__ float load_stay(int c) const {
+    return load_at<float>(a.w.rows + chunk_index(a, bh, c) * 4 * kChunk, 4u * (kChunk - 1));
   }
   // this wave's operands of a triangular matrix: of a lower one steps 0 and, from wave 2 on, 1; of an
   // upper one (UP) step 1 and, up to wave 1, 0

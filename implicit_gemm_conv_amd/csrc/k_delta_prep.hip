@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
   __shared__ __attribute__((aligned(16))) PrepLds<T, DK> s;
   const int c = blockIdx.x % a.chunks, t0 = c * kChunk;
   const F f(a, blockIdx.x / a.chunks, 0);
-  const int wave = f.wave, lane = f.lane, m = f.m, q4 = f.q4;
+  const int wave = wave_id(), lane = f.lane, m = f.m, q4 = f.q4;
   const int64_t at = chunk_index(a, f.bh, c);
   Raw8<T> k[KS], q[KS];
   f.load_rows(a.k, c, k);
