@@ -330,4 +330,4 @@ def from_torch_weight(w_oc_first: torch.Tensor) -> torch.Tensor:
 from .sequence import (Packed8, gated_scan, gated_scan_bwd, gated_scan_step, pack8, seq_conv,  # noqa: E402
                        seq_conv_bwd, seq_conv_step, unpack8)
 from .norm import GroupNorm, GroupNormGrad, group_norm, group_norm_bwd  # noqa: E402
-from .delta import DeltaRule, DeltaRuleGrad, delta_rule, delta_rule_bwd, delta_rule_step  # noqa: E402
+from .delta import DeltaRule, DeltaRuleGrad, DeltaStates, delta_rule, delta_rule_bwd, delta_rule_step  # noqa: E402

@@ -134,10 +134,11 @@ int64_t convdelta_bwd_workspace(const convdelta_desc* d) { return work_bytes(d, 
 
 int convdelta_fwd(const convdelta_desc* d, const convdelta_heads* q, const convdelta_heads* k,
                   const convdelta_heads* v, const void* log_decay, const void* beta, const void* h0,
-                  const void* starts, void* y, void* h_last, void* states, void* workspace, void* stream) {
+                  const void* starts, void* y, void* h_last, void* states, void* x, void* workspace, void* stream) {
   const int64_t work = work_bytes(d, false);
   if (work < 0) return (int)work;
   const int eb = elem_bytes(d->dtype);
+  if (!states != !x && d->b > 0 && d->t > 0) return CONVFWD_ERR_NULL;
   const int64_t rows = (int64_t)d->b * d->t, size = (int64_t)d->b * d->hv * d->dk * d->dv * 4;
   DeltaArgs a{};
   Buffers buf;
@@ -151,6 +152,7 @@ int convdelta_fwd(const convdelta_desc* d, const convdelta_heads* q, const convd
   buf.out(y, rows * d->hv * d->dv * eb, eb);
   buf.out(h_last, size, 4);
   buf.out(states, size * chunks_of(d), 4, false);
+  buf.out(x, rows * d->hv * d->dv * 4, 4, false);
   buf.out(workspace, work, 16);
   if (buf.result() < 0) return buf.result();
   if (!near_rows(a.v)) return CONVFWD_ERR_TOO_LARGE;
@@ -158,6 +160,7 @@ int convdelta_fwd(const convdelta_desc* d, const convdelta_heads* q, const convd
   fill(&a, d);
   a.log_decay = (const float*)log_decay; a.beta = (const float*)beta; a.h0 = (const float*)h0;
   a.starts = (const uint8_t*)starts; a.y = y; a.h_last = (float*)h_last; a.states = (float*)states;
+  a.x = (float*)x;
   lay_out(d, false, (char*)workspace, &a.w);
   const hipStream_t s = (hipStream_t)stream;
   if (a.chunks > 0) {
@@ -170,8 +173,8 @@ int convdelta_fwd(const convdelta_desc* d, const convdelta_heads* q, const convd
 
 int convdelta_bwd(const convdelta_desc* d, const convdelta_heads* dy, const convdelta_heads* q,
                   const convdelta_heads* k, const convdelta_heads* v, const void* log_decay, const void* beta,
-                  const void* states, const void* starts, const void* dh_last, void* dq, void* dk, void* dv,
-                  void* dlog_decay, void* dbeta, void* dh0, void* workspace, void* stream) {
+                  const void* states, const void* x, const void* starts, const void* dh_last, void* dq, void* dk,
+                  void* dv, void* dlog_decay, void* dbeta, void* dh0, void* workspace, void* stream) {
   const int64_t work = work_bytes(d, true);
   if (work < 0) return (int)work;
   const int eb = elem_bytes(d->dtype);
@@ -185,6 +188,7 @@ int convdelta_bwd(const convdelta_desc* d, const convdelta_heads* dy, const conv
   buf.in(log_decay, rows * d->hv * 4, 4);
   buf.in(beta, rows * d->hv * 4, 4);
   buf.in(states, size * chunks_of(d), 4);
+  buf.in(x, rows * d->hv * d->dv * 4, 4);
   buf.in(starts, rows, 1, false);
   buf.in(dh_last, size, 4, false);
   buf.out(dq, rows * d->hk * d->dk * eb, eb);
@@ -199,9 +203,15 @@ int convdelta_bwd(const convdelta_desc* d, const convdelta_heads* dy, const conv
   if (d->b == 0) return CONVFWD_OK;
   fill(&a, d);
   a.log_decay = (const float*)log_decay; a.beta = (const float*)beta; a.states_in = (const float*)states;
+  a.x_in = (const float*)x;
   a.starts = (const uint8_t*)starts; a.dh_last = (const float*)dh_last;
   a.dq = dq; a.dk_ = dk; a.dv_ = dv; a.dlog_decay = (float*)dlog_decay; a.dbeta = (float*)dbeta; a.dh0 = (float*)dh0;
+  const auto fours = [&](const Heads& h, int e) {
+    return d->dv % 4 == 0 && ((uintptr_t)h.p | (uint64_t)(h.sb * e) | (uint64_t)(h.st * e) | (uint64_t)(h.sh * e)) % (4 * e) == 0;
+  };
   a.vec_dy = pieces(a.dy, d->dv, eb);
+  a.vec_v = fours(a.v, eb);
+  a.vec_x = fours(Heads{x, 0, 0, 0}, 4);
   lay_out(d, true, (char*)workspace, &a.w);
   const hipStream_t s = (hipStream_t)stream;
   static const Launch bwd[3] = {launch_delta_bwd_f32, launch_delta_bwd_f16, launch_delta_bwd_bf16};

@@ -9,19 +9,24 @@
 // z and each chunk's dS are left for the gradients that add over all columns
 // (delta_grad.h).  The steps between barriers are those of delta_fwd.h: (1) du, (2) z,
 // (3) the state's gradient.  The waves of the first role go the way from state to state,
-// those of the second bring q and dy.  Included by one source for each type.
+// those of the second bring q and
+// dy, and R^T dy a chunk ahead.  Included by one source for each type.
 #include "delta_team.h"
 
 namespace convdelta {
 
 namespace {
 
+constexpr int kReadLd = kChunk + 4;  // spreads the columns over the banks
+
 template <typename T, int DK>
 struct BwdLds {
   typedef Team<T, DK> F;
   __bf16 k[F::NP * RowsAt<DK>::part], q[F::NP * RowsAt<DK>::part];
   __bf16 state[kParts * F::State::part];
-  __bf16 dy[F::NP * F::Rows::part], bd[kParts * F::Rows::part], in[kParts * F::Rows::part], out[kParts * F::Rows::part];
+  __bf16 dy[2][F::NP * F::Rows::part];  // of the chunk, and of the one it goes on to
+  float ry[16 * kReadLd];               // scale * R^T dy by columns
+  __bf16 bd[kParts * F::Rows::part], in[kParts * F::Rows::part], out[kParts * F::Rows::part];
   float step[kChunk];
   int bad[2];
 };
@@ -40,11 +45,11 @@ struct Backward : Team<T, DK> {
   typedef typename F::Rows Rows;
 
   struct Chunk {
-    Raw8<T> rows[KS];                // of k, or of q
-    Parts<kParts> solve[2], read[2]; // first role
+    Raw8<T> rows[KS];      // of k, or of q
+    Parts<kParts> mat[2];  // of H^T, or the next chunk's R^T
     f32x4_t enter, leave, beta;
     float stay;
-    T dy[4];                         // second role
+    T dy[4];               // second role, the next chunk's
   };
 
   Lds& s;
@@ -53,14 +58,8 @@ struct Backward : Team<T, DK> {
 
   __device__ __forceinline__ Backward(const DeltaArgs& a_, Lds& s_, int bh_, int cb) : F(a_, bh_, cb), s(s_) {}
 
-  __device__ __forceinline__ void fetch_rows(int c, Chunk& x) const {
-    F::load_rows(FIRST ? a.k : a.q, c, x.rows);
-    if (!FIRST) F::load_col(a.dy, c, x.dy);
-  }
-  __device__ __forceinline__ void fetch_matrices(int c, Chunk& x) const {
-    if (!FIRST) return;
-    F::template load_matrix<true>(a.w.solve_t, c, x.solve);
-    F::template load_matrix<true>(a.w.read_t, c, x.read);
+  __device__ __forceinline__ void fetch_matrix(int c, Parts<kParts> (&to)[2]) const {
+    F::template load_matrix<true>(FIRST ? a.w.solve_t : a.w.read_t, c, to);
   }
   __device__ __forceinline__ void fetch_gates(int c, Chunk& x) const {
     x.enter = F::load_gate(0, c);
@@ -72,47 +71,61 @@ struct Backward : Team<T, DK> {
     f32x4_t d;
 #pragma unroll
     for (int i = 0; i < 4; ++i) d[i] = c * kChunk + row() + i < a.t ? to_f32(x.dy[i]) : 0.f;
-    F::template put<NP, Rows>(s.dy, row(), d);
+    F::template put<NP, Rows>(s.dy[c & 1], row(), d);
     return d;
+  }
+  // scale * R^T dy of chunk c (second role), from the rows [lo, hi) where masked
+  __device__ __forceinline__ void put_read(int c, const Parts<kParts> (&read)[2], bool masked, int lo, int hi) const {
+    f32x4_t ry = {0.f, 0.f, 0.f, 0.f}, more = ry;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (F::template has<true>(k)) {
+        Parts<NP> d = F::template get<NP, Rows>(s.dy[c & 1], k);
+        if (masked) keep(d, 32 * k + 8 * q4, lo, hi);
+        (k ? more : ry) = mma(read[k], d, k ? more : ry);
+      }
+    *(f32x4_t*)(s.ry + m * kReadLd + row()) = a.scale * (ry + more);
   }
 
   // (1) and (2) for all rows, or (masked) the rows [lo, hi) of one sequence, into z; kd is k dS.
   __device__ __forceinline__ void solve(int c, Chunk& x, const f32x4_t& kd, bool masked, int lo, int hi, f32x4_t& z) {
-    f32x4_t du, more = {0.f, 0.f, 0.f, 0.f};
-    if (FIRST) {
-      if (masked) {
-        fetch_matrices(c, x);
+    if (masked) {
+      __syncthreads();  // what is read of the sequence before
+      if (FIRST) {
+        fetch_matrix(c, x.mat);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) keep(x.solve[k], 32 * k + 8 * q4, lo, hi), keep(x.read[k], 32 * k + 8 * q4, lo, hi);
-        wait_for_memory();
+        for (int k = 0; k < 2; ++k) keep(x.mat[k], 32 * k + 8 * q4, lo, hi);
+      } else {
+        Parts<kParts> read[2];
+        fetch_matrix(c, read);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) keep(read[k], 32 * k + 8 * q4, lo, hi);
+        put_read(c, read, true, lo, hi);
       }
-      f32x4_t ry = more, bd;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (F::template has<true>(k)) {
-          Parts<NP> d = F::template get<NP, Rows>(s.dy, k);
-          if (masked) keep(d, 32 * k + 8 * q4, lo, hi);
-          (k ? more : ry) = mma(x.read[k], d, k ? more : ry);
-        }
+      wait_for_memory();
+      __syncthreads();
+    }
+    f32x4_t du, more;
+    if (FIRST) {
+      f32x4_t bd;
+      const f32x4_t ry = *(const f32x4_t*)(s.ry + m * kReadLd + row());
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool out = row() + i < lo || row() + i >= hi;
-        du[i] = out ? 0.f : times(x.leave[i], kd[i]) + a.scale * (ry[i] + more[i]);
+        du[i] = out ? 0.f : times(x.leave[i], kd[i]) + ry[i];
         bd[i] = out ? 0.f : x.beta[i] * du[i];
       }
-      if (masked) __syncthreads();  // what is read of the sequence before
       F::template put<kParts, Rows>(s.bd, row(), bd);
-    } else if (masked) {
-      __syncthreads();
     }
     __syncthreads();
+    F::renew();
     if (FIRST) {
       more = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         if (F::template has<true>(k)) {
           const auto bp = F::template get<kParts, Rows>(s.bd, k);
-          (k ? more : du) = mma(x.solve[k], bp, k ? more : du);
+          (k ? more : du) = mma(x.mat[k], bp, k ? more : du);
         }
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -120,10 +133,10 @@ struct Backward : Team<T, DK> {
     }
   }
 
-  __device__ __forceinline__ void chunk(int c, int next, Chunk& x, f32x4_t& dy) {
+  __device__ __forceinline__ void chunk(int c, Chunk& x, f32x4_t& dy) {
+    const int next = max(c - 1, 0), then = max(c - 2, 0);
     __syncthreads();  // the state's parts and dy are there
-    Chunk ahead;
-    fetch_gates(next, ahead);
+    F::renew();
     F::put_rows(FIRST ? s.k : s.q, x.rows);
     f32x4_t kd = {0.f, 0.f, 0.f, 0.f};
     if (FIRST) {
@@ -140,7 +153,13 @@ struct Backward : Team<T, DK> {
       for (int i = 0; i < 4; ++i) in[i] = times(x.enter[i], a.scale * dy[i]);
       F::template put<kParts, Rows>(s.in, row(), in);
     }
-    fetch_rows(next, x);
+    F::renew();
+    F::load_rows(FIRST ? a.k : a.q, next, x.rows);
+    f32x4_t ahead;
+    if (!FIRST) {
+      ahead = put_dy(next, x);
+      F::load_col(a.dy, then, x.dy);
+    }
     // All rows at once, and where something is not finite once more, each sequence by itself, so that nothing crosses a
     // start.  `first`: the rows that the state before the chunk reaches are those of the first sequence.
     f32x4_t z;
@@ -182,7 +201,13 @@ struct Backward : Team<T, DK> {
       wait_for_memory();
       __syncthreads();
     }
-    fetch_matrices(next, x);
+    F::renew();
+    if (FIRST) {
+      fetch_matrix(next, x.mat);
+    } else {
+      put_read(next, x.mat, false, 0, kChunk);
+      fetch_matrix(then, x.mat);
+    }
     // (3), from the rows [0, first) where masked
     if (F::has_tile()) {
       f32x4_t n, more = {0.f, 0.f, 0.f, 0.f};
@@ -207,16 +232,17 @@ struct Backward : Team<T, DK> {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         dx[i] = x.beta[i] * z[i];
-        zs.store(at + (uint32_t)(i * a.dvp) * 4u, F::live ? z[i] : 0.f);
+        z[i] = F::live ? z[i] : 0.f;
       }
-      F::store_col(a.dv_, c, dx);
+      fetch_gates(next, x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) zs.store(at + (uint32_t)(i * a.dvp) * 4u, z[i]);
+      F::template store_col<T>(a.dv_, c, dx);
     } else {
-      dy = put_dy(next, x);
+      fetch_gates(next, x);
+      dy = ahead;
     }
     keep_state(c - 1);
-    x.enter = ahead.enter;
-    if (FIRST) x.leave = ahead.leave, x.beta = ahead.beta;
-    x.stay = ahead.stay;
   }
   // The gradient of the state after chunk c.
   __device__ __forceinline__ void keep_state(int c) const {
@@ -229,13 +255,23 @@ struct Backward : Team<T, DK> {
     F::put_state(s.state, state);
     if (a.chunks > 0) {
       Chunk x;
-      fetch_rows(a.chunks - 1, x);
-      fetch_matrices(a.chunks - 1, x);
-      fetch_gates(a.chunks - 1, x);
-      keep_state(a.chunks - 1);
+      const int last = a.chunks - 1, next = max(last - 1, 0);
       f32x4_t dy;
-      if (!FIRST) dy = put_dy(a.chunks - 1, x);
-      for (int c = a.chunks - 1; c >= 0; --c) chunk(c, max(c - 1, 0), x, dy);
+      if (!FIRST) {
+        F::load_col(a.dy, last, x.dy);
+        dy = put_dy(last, x);
+      }
+      fetch_matrix(last, x.mat);
+      __syncthreads();
+      if (!FIRST) {
+        put_read(last, x.mat, false, 0, kChunk);
+        fetch_matrix(next, x.mat);
+        F::load_col(a.dy, next, x.dy);
+      }
+      F::load_rows(FIRST ? a.k : a.q, last, x.rows);
+      fetch_gates(last, x);
+      keep_state(last);
+      for (int c = last; c >= 0; --c) chunk(c, x, dy);
     }
     F::store_state(a.dh0 + F::bh * size, a.dv, a.dv, state);
   }

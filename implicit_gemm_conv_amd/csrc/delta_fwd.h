@@ -1,11 +1,11 @@
 // delta_fwd.h -- gated delta rule forward: a workgroup carries 16 columns of one
 // head's state through the chunks.  Included by one source for each type.
 //
-// A chunk takes three steps between barriers: (1) k S, r, and q S; (2) x = r + H (beta r),
-// u; (3) the state, and y.  The waves of the first role go the way from state to state (k S,
-// r, x, u), those of the second compute y beside it; the state's rows are all waves'.  Each
-// wave fetches what it needs of the next chunk, which no other wave needs, as soon as this
-// chunk's is used.
+// A chunk takes three steps between barriers: (1) k S and r; (2) x = r + H (beta r), u;
+// (3) the state.  The waves of the first role go the way from state to state (k S, r, x, u);
+// those of the second compute q S in step (2) and finish y in step (1) of the next chunk, while
+// the first role is at work; the state's rows are all waves'.  Each wave fetches what it needs
+// of the next chunk, which no other wave needs, as soon as this chunk's is used.
 #include "delta_team.h"
 
 namespace convdelta {
@@ -17,11 +17,11 @@ struct FwdLds {
   typedef Team<T, DK> F;
   __bf16 k[F::NP * RowsAt<DK>::part];
   __bf16 state[kParts * F::State::part];
-  __bf16 br[kParts * F::Rows::part], u[kParts * F::Rows::part], out[F::YP * F::Rows::part];
+  __bf16 br[kParts * F::Rows::part], u[kParts * F::Rows::part], out[2][F::YP * F::Rows::part];
   int bad[2];
 };
 
-template <typename T, int DK, bool FIRST>
+template <typename T, int DK, bool FIRST, bool TRAIN>
 struct Forward : Team<T, DK> {
   typedef Team<T, DK> F;
   typedef FwdLds<T, DK> Lds;
@@ -36,15 +36,15 @@ struct Forward : Team<T, DK> {
   // what a chunk needs
   struct Chunk {
     Raw8<T> rows[KS];                   // of k, or of q
-    Parts<FIRST ? kParts : YP> mat[2];  // of H, or of the decayed q k^T
+    Parts<FIRST ? kParts : YP> mat[2];  // of H; of the decayed q k^T of the chunk whose y is next
     f32x4_t enter, leave, beta;
     float stay;
     T v[4];
   };
 
   Lds& s;
-  f32x4_t state;
-  int turn = 0;
+  f32x4_t state, read;
+  int turn = 0, was = 0, was_first = 0, was_end = 0;  // the chunk whose y is to be finished
 
   __device__ __forceinline__ Forward(const DeltaArgs& a_, Lds& s_, int bh_, int cb) : F(a_, bh_, cb), s(s_) {}
 
@@ -56,9 +56,28 @@ struct Forward : Team<T, DK> {
     F::template load_matrix<false>(FIRST ? a.w.solve : a.w.read, c, x.mat);
   }
   __device__ __forceinline__ void fetch_gates(int c, Chunk& x) const {
-    x.enter = F::load_gate(0, c);
     if (FIRST) x.leave = F::load_gate(1, c), x.beta = F::load_gate(2, c);
     x.stay = F::load_stay(c);
+  }
+
+  // What is loaded next takes its registers over: a load that moves up, past the last use of what they hold, takes
+  // others, and its result has to be waited for and moved at the turn's end.
+  static __device__ __forceinline__ void used() { __builtin_amdgcn_sched_barrier(0); }
+
+  // y of the chunk before, of its rows [first, end): what q S was is in `read`, u in LDS.
+  __device__ __forceinline__ void finish(int c, const Chunk& x, int first, int end) const {
+    f32x4_t y = read, more = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (F::template has<false>(k)) {
+        Parts<YP> mat = x.mat[k];
+        if (end - first < kChunk) keep(mat, 32 * k + 8 * q4, first, end);
+        const auto op = F::template get<YP, Rows>(s.out[~turn & 1], k);
+        (k ? more : y) = mma_first<YP>(mat, op, k ? more : y);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = a.scale * (y[i] + more[i]);
+    F::template store_col<T>(a.y, c, y, first, end);
   }
 
   // One chunk, all of its rows, or (`alone`) row `only` of it.  False where u is not finite: the state is then as it
@@ -67,8 +86,6 @@ struct Forward : Team<T, DK> {
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     if (alone) {
       // a row by itself: its own decay takes the place of the sums', and only its products count
-      x.enter = F::load_gate(3, c);
-      x.stay = a.w.rows[(chunk_index(a, F::bh, c) * 4 + 3) * kChunk + only];
       if (FIRST) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) x.leave[i] = row() + i == only ? 1.f : 0.f;
@@ -77,45 +94,58 @@ struct Forward : Team<T, DK> {
 #pragma unroll
           for (unsigned n = 0; n < sizeof(T) / 2; ++n)
             if (16 * wave + m != only) x.rows[k].w[n] = convfwd::u32x4_t{0u, 0u, 0u, 0u};
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) keep(x.mat[k], 32 * k + 8 * q4, only, only + 1);
       }
       wait_for_memory();
     }
     __syncthreads();  // the state's parts are there
-    Chunk ahead;
-    fetch_gates(next, ahead);
+    if (TRAIN) F::renew();
     if (FIRST) F::put_rows(s.k, x.rows);
     f32x4_t xs = zero, more = zero;  // k S, or q S; then r, x
+    const auto times_state = [&] {
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const auto sp = F::template get<kParts, typename F::State>(s.state, k);
-      if (FIRST)
-        (k & 1 ? more : xs) = mma(F::rows_of(x.rows, k), sp, k & 1 ? more : xs);
-      else
-        (k & 1 ? more : xs) = mma_first<YP>(F::rows_of(x.rows, k), sp, k & 1 ? more : xs);
-    }
-    xs += more;
-    if (alone) {
-      // a state that is not finite, behind a start (with all rows such a chunk comes to nothing)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (x.enter[i] == 0.f) xs[i] = 0.f;
-        if (x.stay == 0.f) state[i] = 0.f;
+      for (int k = 0; k < KS; ++k) {
+        const auto sp = F::template get<kParts, typename F::State>(s.state, k);
+        if (FIRST)
+          (k & 1 ? more : xs) = mma(F::rows_of(x.rows, k), sp, k & 1 ? more : xs);
+        else
+          (k & 1 ? more : xs) = mma_first<YP>(F::rows_of(x.rows, k), sp, k & 1 ? more : xs);
       }
-    }
+      xs += more;
+      f32x4_t enter = x.enter;
+      if (alone) {
+        enter = F::load_gate(3, c);
+        x.stay = a.w.rows[(chunk_index(a, F::bh, c) * 4 + 3) * kChunk + only];
+        wait_for_memory();
+        // a state that is not finite, behind a start (with all rows such a chunk comes to nothing)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (enter[i] == 0.f) xs[i] = 0.f;
+          if (x.stay == 0.f) state[i] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xs[i] *= enter[i];
+    };
     f32x4_t u, lu;
-    if (FIRST) {
+    if constexpr (FIRST) {
+      times_state();
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        xs[i] = to_f32(x.v[i]) - x.enter[i] * xs[i];
+        xs[i] = to_f32(x.v[i]) - xs[i];
         u[i] = alone && row() + i != only ? 0.f : x.beta[i] * xs[i];
       }
       F::template put<kParts, Rows>(s.br, row(), u);
+      if (TRAIN) F::renew();
+      used();
+      x.enter = F::load_gate(0, next);
+      fetch_rows(next, x);
+    } else {
+      finish(was, x, was_first, was_end);
+      used();
+      fetch_matrix(c, x);
     }
-    fetch_rows(next, x);
     __syncthreads();
+    if (TRAIN) F::renew();
     if (FIRST) {
       if (!alone) {
         more = zero;
@@ -125,8 +155,9 @@ struct Forward : Team<T, DK> {
             const auto bp = F::template get<kParts, Rows>(s.br, k);
             (k ? more : xs) = mma(x.mat[k], bp, k ? more : xs);
           }
+        xs += more;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = x.beta[i] * (xs[i] + more[i]);
+        for (int i = 0; i < 4; ++i) u[i] = x.beta[i] * xs[i];
       }
       float test = 0.f;
 #pragma unroll
@@ -135,62 +166,73 @@ struct Forward : Team<T, DK> {
         test = fmaf(u[i], 0.f, test);
       }
       F::template put<kParts, Rows>(s.u, row(), lu);
-      F::template put<YP, Rows>(s.out, row(), u);
+      F::template put<YP, Rows>(s.out[turn & 1], row(), u);
       if (__any(test != 0.f)) s.bad[turn & 1] = 1;  // NaN
-      fetch_matrix(next, x);
+    } else {
+      times_state();
+      read = xs;
+      used();
+      x.enter = F::load_gate(0, next);
+      fetch_rows(next, x);
     }
+    // Serving, as early as possible: what the state's step has of k, and all that is left to load for the next chunk.
+    // Training, where that is used: with 128 registers two workgroups share a CU.
+    Parts<NP> kt[2];
+    const auto get_kt = [&] {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) kt[k] = F::cols_of(s.k, F::tile, k);
+    };
+    const float stay = x.stay;
+    if (!TRAIN) {
+      if (F::has_tile()) get_kt();
+      used();
+      fetch_gates(next, x);
+    }
+    if (FIRST) fetch_matrix(next, x);
     __syncthreads();
+    if (TRAIN) F::renew();
     const bool bad = s.bad[turn & 1];
     // the other flag: read before the last barrier, set after the next one but one
     if (threadIdx.x == 0) s.bad[~turn & 1] = 0;
     ++turn;
+    was_end = was_first;
     if (!alone && bad) return false;
+    was = c;
+    was_first = alone ? only : 0;
+    was_end = alone ? only + 1 : kChunk;
     // the state moves on
     if (F::has_tile()) {
       f32x4_t n;
+      if (TRAIN) get_kt();
       more = zero;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n[i] = x.stay * state[i];
+      for (int i = 0; i < 4; ++i) n[i] = stay * state[i];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const auto up = F::template get<kParts, Rows>(s.u, k);
-        (k ? more : n) = mma(F::cols_of(s.k, F::tile, k), up, k ? more : n);
+        (k ? more : n) = mma(kt[k], up, k ? more : n);
       }
       state = n + more;
       F::put_state(s.state, state);
     }
-    if (!FIRST) {
-      more = zero;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) xs[i] = x.enter[i] * xs[i];
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (F::template has<false>(k)) {
-          const auto op = F::template get<YP, Rows>(s.out, k);
-          (k ? more : xs) = mma_first<YP>(x.mat[k], op, k ? more : xs);
-        }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) xs[i] = a.scale * (xs[i] + more[i]);
-      fetch_matrix(next, x);
-      // Stores come after the loads of the next chunk: waits for memory are counted in the order of issue, and a load
-      // issued after a store would be waited for together with it.
-      F::store_col(a.y, c, xs, alone ? only : 0, alone ? only + 1 : kChunk);
-    }
-    x.enter = ahead.enter;
-    if (FIRST) x.leave = ahead.leave, x.beta = ahead.beta;
-    x.stay = ahead.stay;
+    // Stores come after the loads of the next chunk: waits for memory are counted in the order of issue, and a load
+    // issued after a store would be waited for together with it.
+    if (TRAIN) fetch_gates(next, x);
+    if (FIRST && TRAIN) F::template store_col<float>(a.x, c, xs, was_first, was_end);
     return true;
   }
 
   // The state before chunk c, kept for the backward pass.
   __device__ __forceinline__ void keep_state(int c) const {
-    float* to = a.states && c < a.chunks ? a.states + (((int64_t)F::b * a.chunks + c) * a.hv + F::h) * a.dk * a.dv : nullptr;
+    if (!TRAIN) return;
+    float* to = c < a.chunks ? a.states + (((int64_t)F::b * a.chunks + c) * a.hv + F::h) * a.dk * a.dv : nullptr;
     F::store_state(to, a.dv, a.dv, state);
   }
   __device__ __forceinline__ void fetch(int c, Chunk& x) const {
     fetch_rows(c, x);
-    fetch_matrix(c, x);
+    if (FIRST) fetch_matrix(c, x);
     fetch_gates(c, x);
+    x.enter = F::load_gate(0, c);
   }
 
   // All chunks.  One in which something is not finite goes row by row, so that it reaches only what comes after it.
@@ -202,6 +244,8 @@ struct Forward : Team<T, DK> {
     if (a.chunks > 0) {
       Chunk x;
       fetch(0, x);
+      if (!FIRST) fetch_matrix(0, x);
+      read = f32x4_t{0.f, 0.f, 0.f, 0.f};
       bool alone = false;
       int c = 0, only = 0;
       keep_state(0);
@@ -223,21 +267,22 @@ struct Forward : Team<T, DK> {
           ++only;
         }
       }
+      if constexpr (!FIRST) finish(was, x, was_first, was_end);
     }
     F::store_state(a.h_last + F::bh * size, a.dv, a.dv, state);
   }
 };
 
-template <typename T, int DK>
+template <typename T, int DK, bool TRAIN>
 __global__ __launch_bounds__(kTeam, 2) void delta_fwd_kernel(DeltaArgs a, int blocks) {
   __shared__ __attribute__((aligned(16))) FwdLds<T, DK> s;
   int bh, cb;
   if (!head_of(a.b * a.hv, blocks, bh, cb)) return;
   if (threadIdx.x < 2) s.bad[threadIdx.x] = 0;
   if (wave_id() < 4)
-    Forward<T, DK, true>(a, s, bh, cb).run();
+    Forward<T, DK, true, TRAIN>(a, s, bh, cb).run();
   else
-    Forward<T, DK, false>(a, s, bh, cb).run();
+    Forward<T, DK, false, TRAIN>(a, s, bh, cb).run();
 }
 
 }  // namespace
@@ -246,8 +291,9 @@ template <typename T>
 hipError_t delta_fwd_of(const DeltaArgs& a, hipStream_t s) {
   return for_dk(a.dk, [&](auto dk) {
     const int blocks = (a.dv + 15) / 16;
-    hipLaunchKernelGGL((delta_fwd_kernel<T, decltype(dk)::value>), dim3((a.b * a.hv + 7) / 8 * 8 * blocks), dim3(kTeam), 0, s, a,
-                       blocks);
+    constexpr int DK = decltype(dk)::value;
+    hipLaunchKernelGGL((a.states ? delta_fwd_kernel<T, DK, true> : delta_fwd_kernel<T, DK, false>),
+                       dim3((a.b * a.hv + 7) / 8 * 8 * blocks), dim3(kTeam), 0, s, a, blocks);
     return hipGetLastError();
   });
 }

@@ -1,7 +1,7 @@
 // delta_grad.h -- gated delta rule, the gradients that add over all columns of v: one
 // workgroup of eight waves a chunk and key head, all chunks at once.  With S the state
-// before the chunk, dS the gradient of the one after it, x as in the forward pass (computed
-// again from S), u = beta x, dx = beta z,
+// before the chunk, dS the gradient of the one after it, x what the forward pass kept,
+// u = beta x, dx = beta z,
 //
 //   dP = scale * D * (dy u^T) (j <= i),  dL = -D * (dx u^T) (j < i)
 //   dq = scale * enter * (dy S^T) + dP k
@@ -15,8 +15,8 @@
 //
 // and from zero at a start, where the decay acts on nothing.
 //
-// The columns are taken 32 at a time; wave (w, half) owns rows 16 w .. + 15 and half of
-// the columns (of x) or of dq's and dk's.  What dlog_decay and dbeta are made of has fp32's
+// The columns are taken 32 at a time, through LDS; wave (w, half) owns rows 16 w .. + 15
+// and half of dq's and dk's columns.  What dlog_decay and dbeta are made of has fp32's
 // precision (three parts); what ends in a 16-bit dk alone has two parts, 2^-17.
 // Included by one source for each type.
 #include "delta_team.h"
@@ -31,34 +31,33 @@ template <typename T, int DK>
 struct GradLds {
   typedef Team<T, DK> F;
   static constexpr int NP = F::NP, GP = F::YP;
-  __bf16 rows[NP * RowsAt<DK>::part];  // k, and at the end q
   union {
     struct {
       __bf16 s[kParts * DK * kSlice], ds[GP * DK * kSlice];          // 32 columns of both states, rows d
       __bf16 u[kParts * kChunk * kSlice], dx[GP * kChunk * kSlice];  // rows of the chunk
-      __bf16 br[2 * kParts * F::Rows::part];                         // columns of beta r, 16 at a time
     };
     struct {
       __bf16 p[kParts * kChunk * kLdM], l[GP * kChunk * kLdM];       // dP and dL
+      __bf16 rows[NP * RowsAt<DK>::part];                            // k, then q
     };
   };
-  float gates[3 * kChunk], red[2][kChunk][3];  // enter, leave, beta; sums of both halves
+  float gates[3 * kChunk], red[kChunk][4];  // enter, leave, beta; dx.v, z.x and both halves of q.dq
   double sums[kChunk], a[kT / 64];
-  int seq[kChunk], bad[2];
+  int seq[kChunk];
 };
 
 template <typename T, int DK>
 struct Grad {
   typedef Team<T, DK> F;
   typedef GradLds<T, DK> Lds;
-  static constexpr int NP = F::NP, GP = F::YP, KS = DK / 32, DT = DK / 32;  // DT: 16-row tiles of a half of dq's columns
+  static constexpr int NP = F::NP, GP = F::YP, DT = DK / 32;  // DT: 16-row tiles of a half of dq's columns
   static constexpr int each = DK * kCols / 4 / kT;                          // pieces of 4 floats of a slice a thread
   static_assert(each >= 1 || DK == 32, "slices");
   static constexpr int held = each ? each : 1;
 
   const DeltaArgs& a;
   Lds& s;
-  int wave, half, lane, m, q4, b, c, own, tid, turn = 0;  // own: the lane's first row of accumulators
+  int wave, half, lane, m, q4, b, c, own, tid;  // own: the lane's first row of accumulators
 
   __device__ __forceinline__ Grad(const DeltaArgs& a_, Lds& s_, int b_, int c_) : a(a_), s(s_), b(b_), c(c_) {
     const int w = wave_id();
@@ -119,16 +118,19 @@ struct Grad {
       for (int n = 0; n < N; ++n) *(bf164_t*)(to + (n * DK + d) * kSlice + v) = o[n];
     }
   }
-  // four rows of the lane's column, as parts, into rows of a slice
+  // 4 columns of a row of the chunk, as parts, into a slice
   template <int N>
-  __device__ __forceinline__ void put_rows(__bf16* to, const f32x4_t& x) const {
+  __device__ __forceinline__ void put_row(__bf16* to, const f32x4_t& x) const {
+    bf164_t o[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int e = 0; e < 4; ++e) {
       __bf16 w[N];
-      split_one<N>(x[i], w);
+      split_one<N>(x[e], w);
 #pragma unroll
-      for (int n = 0; n < N; ++n) to[(n * kChunk + own + i) * kSlice + 16 * half + m] = w[n];
+      for (int n = 0; n < N; ++n) o[n][e] = w[n];
     }
+#pragma unroll
+    for (int n = 0; n < N; ++n) *(bf164_t*)(to + (n * kChunk + tid / 8) * kSlice + tid % 8 * 4) = o[n];
   }
   // rows of a slice as an operand
   template <int N>
@@ -212,175 +214,92 @@ struct Grad {
     return v;
   }
 
-  // What a slice of 32 columns needs.
-  struct Slice {
-    f32x4_t s[held], ds[held], before[held], z;
-    T v[4];
-    Raw8<T> dy;
-  };
+  // 4 neighbouring elements of a row, zero outside; `whole`: as one access
+  template <typename E>
+  __device__ __forceinline__ f32x4_t load4(const Range& x, uint32_t row, int col, int width, bool whole) const {
+    struct alignas(4 * sizeof(E)) Four { E v[4]; } f;
+    if (whole) {
+      f = x.load<Four>(col < width ? row + (uint32_t)col * (uint32_t)sizeof(E) : kNowhere);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f.v[e] = x.load<E>(col + e < width ? row + (uint32_t)(col + e) * (uint32_t)sizeof(E) : kNowhere);
+    }
+    return f32x4_t{to_f32(f.v[0]), to_f32(f.v[1]), to_f32(f.v[2]), to_f32(f.v[3])};
+  }
 
   // The gradients of one value head; its share of dq and dk.
   __device__ __forceinline__ void head(int hk, int h, f32x4_t (&dq)[DT], f32x4_t (&dk)[DT]) {
     const int64_t bh = (int64_t)b * a.hv + h, at = bh * a.chunks + c;
     const auto row = [&] { return 16 * wave + m; };  // the lane's row as an operand
-    Rows64<T, DK, kT> k, q;
-    k.load(a.k, b, hk, c * kChunk, a.t, a.dkp);
-    q.load(a.q, b, hk, c * kChunk, a.t, a.dkp);
-    Parts<kParts> solve[2];
-    {
-      const char* p = a.w.solve + at * kMatrix + lane * 16;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int f = wave < 2 ? wave : 2 * wave - 2 + e;
-#pragma unroll
-        for (int n = 0; n < kParts; ++n) solve[e].p[n] = *(const bf168_t*)(p + (f * kParts + n) * kFrag);
-      }
-    }
+    const int rows = min(kChunk, a.t - c * kChunk);
     const float* states = a.states_in + (((int64_t)b * a.chunks + c) * a.hv + h) * a.dk * a.dv;
     const float* dstate = a.w.dstate + at * a.dk * a.dvp;
     const float* before = c ? dstate - (int64_t)a.dk * a.dvp : a.dh0 + bh * a.dk * a.dv;
     const int ldb = c ? a.dvp : a.dv;
-    const float* zs = a.w.z + at * kChunk * a.dvp;
+    const Range zs(a.w.z + at * kChunk * a.dvp, (int64_t)kChunk * a.dvp * 4);
+    const Range xs(a.x_in + ((int64_t)b * a.t + c * kChunk) * a.hv * a.dv + (int64_t)h * a.dv, (int64_t)rows * a.hv * a.dv * 4);
     const Range vs = rows_range<T>(a.v, b, h, c * kChunk, a.t, a.dv), dys = rows_range<T>(a.dy, b, h, c * kChunk, a.t, a.dv);
-    const auto fetch = [&](int v0, Slice& x) {
-      load_state(states, v0, a.dv, x.s);
-      load_state(dstate, v0, a.dvp, x.ds);
-      load_state(before, v0, ldb, x.before);
-      const int col = v0 + 16 * half + m;
-      const uint32_t ld = row_bytes<T>(a.v), at_v = col < a.dv ? own * ld + (uint32_t)col * (uint32_t)sizeof(T) : kNowhere;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x.z[i] = load_at<float>(zs + (int64_t)i * a.dvp + v0, (uint32_t)(own * a.dvp + 16 * half + m) * 4u);
-        x.v[i] = vs.load<T>(at_v + i * ld);
-      }
-      const uint32_t dy_row = row() * row_bytes<T>(a.dy);
-      if (a.vec_dy) {
-        x.dy.load(dys, dy_row, v0 + 8 * q4, a.dv);
-      } else {
-        T e8[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          e8[e] = dys.load<T>(v0 + 8 * q4 + e < a.dv ? dy_row + (uint32_t)(v0 + 8 * q4 + e) * (uint32_t)sizeof(T) : kNowhere);
-        __builtin_memcpy(x.dy.w, e8, sizeof(e8));
-      }
-    };
-    Slice x;
-    fetch(0, x);
     __syncthreads();  // what is read of the head before
     for (int i = tid; i < 3 * kChunk; i += kT) s.gates[i] = a.w.rows[at * 4 * kChunk + i];
     if (tid < kChunk) {
       s.sums[tid] = a.w.sums[at * kChunk + tid];
       s.seq[tid] = a.w.seq[at * kChunk + tid];
     }
-    if (tid < 2) s.bad[tid] = 0;
-    k.put(s.rows);
-    bool wild = !k.finite() || !q.finite();
-    wild = __syncthreads_or(wild);
-    const f32x4_t enter = *(const f32x4_t*)(s.gates + own), leave = *(const f32x4_t*)(s.gates + kChunk + own);
-    const f32x4_t beta = *(const f32x4_t*)(s.gates + 2 * kChunk + own);
+    const float my_beta = load_at<float>(a.w.rows + (at * 4 + 2) * kChunk, (uint32_t)(tid / 8) * 4u);
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4_t dkr[DT], dkc[DT], dp[2] = {zero, zero}, dl[2] = {zero, zero}, db = zero, dxv = zero;
-    float dot = 0.f;
+    f32x4_t dkr[DT], dkc[DT], dp[2] = {zero, zero}, dl[2] = {zero, zero};
+    float dot = 0.f, db = 0.f, dxv = 0.f;
 #pragma unroll
     for (int t = 0; t < DT; ++t) dq[t] = dkr[t] = dkc[t] = zero;
 #pragma clang loop unroll(disable)
     for (int v0 = 0; v0 < a.dvp; v0 += kCols) {
       renew();
+      f32x4_t st[held], ds[held], be[held];
+      load_state(states, v0, a.dv, st);
+      load_state(dstate, v0, a.dvp, ds);
+      load_state(before, v0, ldb, be);
+      const int col = v0 + tid % 8 * 4;
+      const f32x4_t z = load4<float>(zs, (uint32_t)(tid / 8 * a.dvp) * 4u, col, a.dvp, true);
+      const f32x4_t x = load4<float>(xs, (uint32_t)(tid / 8 * a.hv * a.dv) * 4u, col, a.dv, a.vec_x);
+      const f32x4_t v = load4<T>(vs, tid / 8 * row_bytes<T>(a.v), col, a.dv, a.vec_v);
+      Raw8<T> dy;
+      if (a.vec_dy) {
+        dy.load(dys, row() * row_bytes<T>(a.dy), v0 + 8 * q4, a.dv);
+      } else {
+        T e8[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          e8[e] = dys.load<T>(v0 + 8 * q4 + e < a.dv ? row() * row_bytes<T>(a.dy) + (uint32_t)(v0 + 8 * q4 + e) * (uint32_t)sizeof(T)
+                                                     : kNowhere);
+        __builtin_memcpy(dy.w, e8, sizeof(e8));
+      }
       if (v0) __syncthreads();  // what is read of the slice before
-      within(x.s, v0, a.dv);
-      within(x.ds, v0, a.dvp);
-      put_state<kParts>(s.s, x.s);
-      put_state<GP>(s.ds, x.ds);
+      within(st, v0, a.dv);
+      within(ds, v0, a.dvp);
+      put_state<kParts>(s.s, st);
+      put_state<GP>(s.ds, ds);
       if (each || tid < DK * kCols / 4)
 #pragma unroll
         for (int n = 0; n < held; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dot = fmaf(x.s[n][e], x.before[n][e], dot);  // S is zero outside
-      // r and dx; rows past T and columns past Dv hold nothing
-      f32x4_t r, z = x.z, dx;
+          for (int e = 0; e < 4; ++e) dot = fmaf(st[n][e], be[n][e], dot);  // S is zero outside
+      f32x4_t u, dx;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u[e] = my_beta * x[e];
+        dx[e] = my_beta * z[e];
+        db = fmaf(x[e], z[e], db);
+        dxv = fmaf(dx[e], v[e], dxv);
+      }
+      put_row<kParts>(s.u, u);
+      put_row<GP>(s.dx, dx);
       float e8[8];
-      x.dy.get(e8);
+      dy.get(e8);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) e8[e] = c * kChunk + row() < a.t ? e8[e] : 0.f;
+      for (int e = 0; e < 8; ++e) e8[e] = row() < rows ? e8[e] : 0.f;
       const Parts<NP> yp = split<NP>(e8);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        r[i] = c * kChunk + own + i < a.t ? to_f32(x.v[i]) : 0.f;
-        dx[i] = beta[i] * z[i];
-        dxv[i] = fmaf(dx[i], r[i], dxv[i]);
-      }
-      if (v0 + kCols < a.dvp) fetch(v0 + kCols, x);
-      put_rows<GP>(s.dx, dx);
       __syncthreads();
       renew();
-      {
-        f32x4_t ks = zero, more = zero;
-#pragma unroll
-        for (int e = 0; e < KS; ++e) {
-          const auto kp = natural<NP>(s.rows + row() * RowsAt<DK>::stride + 32 * e + 8 * q4, RowsAt<DK>::part);
-          const auto sp = transposed<kParts>(s.s + (32 * e + 8 * q4 + m / 4) * kSlice + 16 * half + 4 * (m % 4), kSlice, DK * kSlice);
-          (e & 1 ? more : ks) = mma(kp, sp, e & 1 ? more : ks);
-          if (e & 1) __builtin_amdgcn_sched_barrier(0);
-        }
-        bf164_t o[kParts];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          r[i] -= times(enter[i], ks[i] + more[i]);
-          __bf16 w[kParts];
-          split_one<kParts>(beta[i] * r[i], w);
-#pragma unroll
-          for (int n = 0; n < kParts; ++n) o[n][i] = w[n];
-        }
-#pragma unroll
-        for (int n = 0; n < kParts; ++n)
-          *(bf164_t*)(s.br + (half * kParts + n) * F::Rows::part + m * F::Rows::ld + own) = o[n];
-      }
-      __syncthreads();
-      renew();
-      f32x4_t xs;
-      bool masked = false;
-#pragma clang loop unroll(disable)
-      for (;;) {
-        int hi = kChunk;
-#pragma clang loop unroll(disable)
-        do {
-          int lo = 0;
-          if (masked)
-            for (lo = hi - 1; lo > 0 && s.seq[lo] == s.seq[lo - 1];) --lo;
-          f32x4_t n = r, more = zero;
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (e <= wave / 2) {
-              Parts<kParts> hp = solve[e];
-              auto bp = natural<kParts>(s.br + half * kParts * F::Rows::part + m * F::Rows::ld + 32 * e + 8 * q4, F::Rows::part);
-              if (masked) keep(hp, 32 * e + 8 * q4, lo, hi), keep(bp, 32 * e + 8 * q4, lo, hi);
-              (e ? more : n) = mma(hp, bp, e ? more : n);
-            }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (own + i >= lo && own + i < hi) xs[i] = n[i] + more[i];
-          hi = lo;
-        } while (hi > 0);
-        float test = 0.f;
-        f32x4_t u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          u[i] = beta[i] * xs[i];
-          test = fmaf(xs[i], 0.f, test);
-        }
-        put_rows<kParts>(s.u, u);
-        if (__any(test != 0.f)) s.bad[turn & 1] = 1;  // NaN
-        __syncthreads();
-        const bool bad = s.bad[turn & 1];
-        if (tid == 0) s.bad[~turn & 1] = 0;
-        ++turn;
-        if (masked || !bad) break;
-        masked = true;
-        __syncthreads();  // the flags, and u, are read before they are written again
-      }
-      renew();
-#pragma unroll
-      for (int i = 0; i < 4; ++i) db[i] = fmaf(xs[i], z[i], db[i]);
       const auto up = slice<kParts>(s.u, row(), kChunk);
       const auto xp = slice<GP>(s.dx, row(), kChunk);
 #pragma unroll
@@ -391,7 +310,6 @@ struct Grad {
         dq[t] = mma(yp, sp, dq[t]);
         dkr[t] = mma_first<GP>(xp, sp, dkr[t]);
         dkc[t] = mma_first<GP>(up, dsp, dkc[t]);
-        __builtin_amdgcn_sched_barrier(0);  // or the operands of all tiles are held at once
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
@@ -401,6 +319,11 @@ struct Grad {
           dl[n] = mma_first<GP>(xp, uj, dl[n]);
         }
     }
+    renew();
+    Rows64<T, DK, kT> k, q;
+    k.load(a.k, b, hk, c * kChunk, a.t, a.dkp);
+    q.load(a.q, b, hk, c * kChunk, a.t, a.dkp);
+    const f32x4_t enter = *(const f32x4_t*)(s.gates + own), leave = *(const f32x4_t*)(s.gates + kChunk + own);
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -410,10 +333,19 @@ struct Grad {
       }
     for (int o = 1; o < 64; o <<= 1) dot += __shfl_xor(dot, o);
     if (lane == 0) s.a[4 * half + wave] = dot;
+    for (int o = 1; o < 8; o <<= 1) {
+      db += __shfl_xor(db, o);
+      dxv += __shfl_xor(dxv, o);
+    }
+    if (tid % 8 == 0) {
+      s.red[tid / 8][0] = dxv;
+      s.red[tid / 8][1] = db;
+    }
+    const bool wild = __syncthreads_or(!k.finite() || !q.finite());  // the slices are read: their room is the matrices' now
     renew();
-    __syncthreads();  // the slices are read: their room is the matrices' now
     put_matrix<true, kParts>(s.p, dp, a.scale);
     put_matrix<false, GP>(s.l, dl, -1.f);
+    k.put(s.rows);
     __syncthreads();
     renew();
     add<false, kParts>(s.p, dq, wild);
@@ -421,7 +353,6 @@ struct Grad {
     add<false, GP>(s.l, dk, wild);
     renew();
     add<true, GP>(s.l, dk, wild);
-    renew();
     __syncthreads();
     q.put(s.rows);
     __syncthreads();
@@ -433,17 +364,13 @@ struct Grad {
       float g = 0.f;
 #pragma unroll
       for (int t = 0; t < DT; ++t) g = fmaf(value(s.rows, own + r, 16 * (half * DT + t) + m), dq[t][r], g);
-      const float qdq = over_lanes(g), xv = over_lanes(dxv[r]), dbr = over_lanes(db[r]);
-      if (m == 0) {
-        s.red[half][own + r][0] = qdq;
-        s.red[half][own + r][1] = xv;
-        s.red[half][own + r][2] = dbr;
-      }
+      g = over_lanes(g);
+      if (m == 0) s.red[own + r][2 + half] = g;
     }
     __syncthreads();
     if (tid < kChunk) {
       const int mine = s.seq[lane], t = c * kChunk + lane;
-      double sum = ((double)s.red[0][lane][1] + s.red[1][lane][1]) - ((double)s.red[0][lane][0] + s.red[1][lane][0]), g = 0;
+      double sum = (double)s.red[lane][0] - ((double)s.red[lane][2] + s.red[lane][3]), g = 0;
       if (mine == 0)
         for (int w = 0; w < kT / 64; ++w) g += s.a[w];
       // the rows before, of the same sequence
@@ -458,14 +385,17 @@ struct Grad {
       if (t < a.t) {
         const int64_t to = ((int64_t)b * a.t + t) * a.hv + h;
         a.dlog_decay[to] = (float)g;
-        a.dbeta[to] = s.red[0][lane][2] + s.red[1][lane][2];
+        a.dbeta[to] = s.red[lane][1];
       }
     }
   }
 };
 
+template <typename T>
+constexpr int kGradWaves = 2;  // waves a SIMD
+
 template <typename T, int DK>
-__global__ __launch_bounds__(kT, 1) void delta_grad_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(kT, kGradWaves<T>) void delta_grad_kernel(DeltaArgs a) {
   typedef Grad<T, DK> F;
   __shared__ __attribute__((aligned(16))) typename F::Lds s;
   // neighbouring chunks on one die: each reads the gradient of a state that its neighbour reads too

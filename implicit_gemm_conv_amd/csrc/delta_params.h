@@ -39,13 +39,13 @@ struct DeltaArgs {
   int b, t, hk, hv, dk, dv, dtype;
   int chunks, dvp;  // ceil(T / 64); Dv rounded up to 32
   int dkp;          // elements of a row of q and k as the kernels read them: Dk rounded up to 8
-  int vec_dy;       // dy's rows are 16-byte aligned and whole pieces of 8 elements
+  int vec_dy, vec_v, vec_x;  // rows are aligned and whole pieces of 8 (dy) or 4 (v, x) elements
   float scale;
   Heads q, k, v, dy;
-  const float *log_decay, *beta, *h0, *states_in, *dh_last;
+  const float *log_decay, *beta, *h0, *states_in, *x_in, *dh_last;
   const uint8_t* starts;
   void *y, *dq, *dk_, *dv_;
-  float *h_last, *states, *dlog_decay, *dbeta, *dh0;
+  float *h_last, *states, *x, *dlog_decay, *dbeta, *dh0;
   Work w;
 };
 

@@ -23,20 +23,27 @@ struct Team {
   typedef ColsAt<kChunk> Rows;
 
   const DeltaArgs& a;
-  int wave, tile, m, q4, lane, b, h, hk, bh, col;  // tile: the wave's 16 rows of the state, where it is below DT
+  int wave, tile, m, q4, lane, b, h, hk, bh, block, col;  // tile: the wave's 16 rows of the state, where it is below DT
   bool live;
 
   __device__ __forceinline__ Team(const DeltaArgs& a_, int bh_, int cb) : a(a_), bh(bh_) {
-    lane = threadIdx.x % 64;
     wave = wave_id() % 4;
     // the second role has less to do before the state: with few tiles it takes them
     tile = DT == 8 ? wave_id() : wave_id() - 4;
-    m = lane % 16;
-    q4 = lane / 16;
+    block = cb * 16;
     b = bh / a.hv;
     h = bh % a.hv;
     hk = h / (a.hv / a.hk);
-    col = cb * 16 + m;
+    renew();
+  }
+  // Where the lane stands, as something new: what the compiler makes of it (addresses, mostly) is made again
+  // where it is needed next, and not held in registers, or spilled, from the kernel's start on.
+  __device__ __forceinline__ void renew() {
+    lane = threadIdx.x % 64;
+    asm volatile("" : "+v"(lane));
+    m = lane % 16;
+    q4 = lane / 16;
+    col = block + m;
     live = col < a.dv;
   }
   __device__ __forceinline__ int row() const { return 16 * wave + 4 * q4; }  // the first of the lane's four
@@ -109,13 +116,15 @@ struct Team {
 #pragma unroll
     for (int r = 0; r < 4; ++r) to[r] = p.load<T>(at + r * ld);
   }
-  // ... and of y or of v's gradient, dense, rows past T left out
+  // ... and of y, x or v's gradient, dense, rows past T left out; nowhere if `to` is NULL
+  template <typename E>
   __device__ __forceinline__ void store_col(void* to, int c, const f32x4_t& v, int first = 0, int end = kChunk) const {
-    const uint32_t ld = (uint32_t)(a.hv * a.dv) * (uint32_t)sizeof(T);
-    const Range p((T*)to + ((int64_t)b * a.t + c * kChunk) * (a.hv * a.dv) + (int64_t)h * a.dv, (int64_t)min(kChunk, a.t - c * kChunk) * ld);
-    const uint32_t at = live ? row() * ld + (uint32_t)col * (uint32_t)sizeof(T) : kNowhere;
+    const uint32_t ld = (uint32_t)(a.hv * a.dv) * (uint32_t)sizeof(E);
+    const Range p((E*)to + ((int64_t)b * a.t + c * kChunk) * (a.hv * a.dv) + (int64_t)h * a.dv,
+                  to ? (int64_t)min(kChunk, a.t - c * kChunk) * ld : 0);
+    const uint32_t at = live ? row() * ld + (uint32_t)col * (uint32_t)sizeof(E) : kNowhere;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) p.store(row() + r >= first && row() + r < end ? at + r * ld : kNowhere, from_f32<T>(v[r]));
+    for (int r = 0; r < 4; ++r) p.store(row() + r >= first && row() + r < end ? at + r * ld : kNowhere, from_f32<E>(v[r]));
   }
   __device__ __forceinline__ f32x4_t load_gate(int which, int c) const {
     return load_at<f32x4_t>(a.w.rows + (chunk_index(a, bh, c) * 4 + which) * kChunk, 4u * row());

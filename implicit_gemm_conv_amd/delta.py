@@ -38,9 +38,9 @@ _HP, _DD = ctypes.POINTER(Heads), ctypes.POINTER(DeltaDesc)
 # Every entry point include/convdelta.h declares: (name, restype, argtypes).
 EXPORTS = [
     ("convdelta_fwd_workspace", _I64, [_DD]),
-    ("convdelta_fwd", ctypes.c_int, [_DD, _HP, _HP, _HP, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    ("convdelta_fwd", ctypes.c_int, [_DD, _HP, _HP, _HP] + [_P] * 10),
     ("convdelta_bwd_workspace", _I64, [_DD]),
-    ("convdelta_bwd", ctypes.c_int, [_DD, _HP, _HP, _HP, _HP] + [_P] * 13),
+    ("convdelta_bwd", ctypes.c_int, [_DD, _HP, _HP, _HP, _HP] + [_P] * 14),
     ("convdelta_step", ctypes.c_int, [_DD, _HP, _HP, _HP, _P, _P, _P, _P, _P, _I32, _P, _P]),
 ]
 
@@ -60,10 +60,16 @@ def _delta():
     return _lib
 
 
+class DeltaStates(NamedTuple):
+    """What the forward pass keeps for the backward pass."""
+    states: torch.Tensor             # (B, ceil(T/64), Hv, Dk, Dv) fp32: the state before rows 0, 64, 128, ...
+    x: torch.Tensor                  # (B, T, Hv, Dv) fp32: v less what the state held for k
+
+
 class DeltaRule(NamedTuple):
     y: torch.Tensor
     h: torch.Tensor                  # (B, Hv, Dk, Dv) fp32: the state after the last row
-    states: Optional[torch.Tensor]   # (B, ceil(T/64), Hv, Dk, Dv) fp32, for the backward pass
+    states: Optional[DeltaStates]    # for the backward pass
 
 
 class DeltaRuleGrad(NamedTuple):
@@ -124,7 +130,7 @@ def delta_rule(q, k, v, log_decay, beta, scale=None, h0=None, starts=None, train
     S' = a S, S = S' + k (beta (v - S'^T k))^T, y = scale S^T q; scale is Dk^-0.5 if None.  q and k are
     taken as they are: a layer brings them to length one itself.  h0 (B, Hv, Dk, Dv) fp32 is the state
     before the first row (zeros if None); starts (B, T), bool or uint8, marks rows that begin a new
-    sequence.  train returns the states that delta_rule_bwd needs."""
+    sequence.  train returns what delta_rule_bwd needs in `states`."""
     q, k, v, log_decay, beta, scale = _inputs(q, k, v, log_decay, beta, scale, 4)
     b, t, hv, dv = v.shape
     dk, device = k.shape[-1], v.device
@@ -132,11 +138,13 @@ def delta_rule(q, k, v, log_decay, beta, scale=None, h0=None, starts=None, train
     starts = _starts(starts, b, t, device)
     y = v.new_empty((b, t, hv, dv)) if out is None else _out(out, (b, t, hv, dv), v.dtype, device, "out")
     h = v.new_empty((b, hv, dk, dv), dtype=torch.float32)
-    states = v.new_empty((b, -(-t // STATE_ROWS), hv, dk, dv), dtype=torch.float32) if train else None
+    states = DeltaStates(v.new_empty((b, -(-t // STATE_ROWS), hv, dk, dv), dtype=torch.float32),
+                         v.new_empty((b, t, hv, dv), dtype=torch.float32)) if train else None
+    kept = states if train else (None, None)
     d = _describe(k, v, t, scale)
     work = _workspace(_delta().convdelta_fwd_workspace(d), v)
     _call(v, _delta().convdelta_fwd, d, _view(q), _view(k), _view(v), log_decay.data_ptr(), beta.data_ptr(), _ptr(h0),
-          _ptr(starts), y.data_ptr(), h.data_ptr(), _ptr(states), _ptr(work))
+          _ptr(starts), y.data_ptr(), h.data_ptr(), *map(_ptr, kept), _ptr(work))
     return DeltaRule(y, h, states)
 
 
@@ -149,9 +157,10 @@ def delta_rule_bwd(dy, q, k, v, log_decay, beta, states, scale=None, starts=None
     dy = _heads(dy, "dy", 4)
     if dy.shape != v.shape or dy.dtype is not v.dtype or dy.device != device:
         raise ValueError(f"dy must be {v.dtype} of shape {tuple(v.shape)} on {device}, got {dy.dtype} {tuple(dy.shape)} on {dy.device}")
-    states = _dense(states, (b, -(-t // STATE_ROWS), hv, dk, dv), torch.float32, device, "states")
-    if states is None:
-        raise ValueError("states is needed: call delta_rule with train=True")
+    if not isinstance(states, DeltaStates):
+        raise ValueError("states is needed, as delta_rule returned it: call it with train=True")
+    x = _dense(states.x, (b, t, hv, dv), torch.float32, device, "states.x")
+    states = _dense(states.states, (b, -(-t // STATE_ROWS), hv, dk, dv), torch.float32, device, "states.states")
     dh = _dense(dh, (b, hv, dk, dv), torch.float32, device, "dh")
     starts = _starts(starts, b, t, device)
     dq, dk_ = (v.new_empty((b, t, hk, dk)) for _ in range(2))
@@ -161,7 +170,7 @@ def delta_rule_bwd(dy, q, k, v, log_decay, beta, states, scale=None, starts=None
     d = _describe(k, v, t, scale)
     work = _workspace(_delta().convdelta_bwd_workspace(d), v)
     _call(v, _delta().convdelta_bwd, d, _view(dy), _view(q), _view(k), _view(v), log_decay.data_ptr(), beta.data_ptr(),
-          states.data_ptr(), _ptr(starts), _ptr(dh), dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), dg.data_ptr(),
+          states.data_ptr(), x.data_ptr(), _ptr(starts), _ptr(dh), dq.data_ptr(), dk_.data_ptr(), dv_.data_ptr(), dg.data_ptr(),
           db.data_ptr(), dh0.data_ptr(), _ptr(work))
     return DeltaRuleGrad(dq, dk_, dv_, dg, db, dh0)
 

@@ -63,23 +63,23 @@ typedef struct {
 } convdelta_heads;
 
 /* y (B, T, Hv, Dv), h_last (B, Hv, Dk, Dv) fp32.  h0 (B, Hv, Dk, Dv) fp32 may be
- * NULL: zeros.  states (B, ceil(T/64), Hv, Dk, Dv) fp32, may be NULL: the S
- * before rows 0, 64, 128, ..., from which the backward pass starts. */
+ * NULL: zeros.  For the backward pass, both or neither NULL: states (B, ceil(T/64),
+ * Hv, Dk, Dv) fp32, the S before rows 0, 64, 128, ..., and x (B, T, Hv, Dv) fp32. */
 int64_t convdelta_fwd_workspace(const convdelta_desc* desc); /* bytes, or a negative error */
 int convdelta_fwd(const convdelta_desc* desc, const convdelta_heads* q, const convdelta_heads* k,
                   const convdelta_heads* v, const void* log_decay, const void* beta, const void* h0,
-                  const void* starts, void* y, void* h_last, void* states, void* workspace, void* stream);
+                  const void* starts, void* y, void* h_last, void* states, void* x, void* workspace, void* stream);
 
 /* Gradients of convdelta_fwd.  dy is the gradient of y, dh_last (B, Hv, Dk, Dv)
  * fp32 (may be NULL) that of h_last; the other inputs are the forward pass's, and
- * states what it kept.  Outputs: dq, dk (B, T, Hk, Dk), added over the value heads
+ * states and x what it kept.  Outputs: dq, dk (B, T, Hk, Dk), added over the value heads
  * that share a key head before they are rounded, dv (B, T, Hv, Dv) (dtype),
  * dlog_decay and dbeta (B, T, Hv), dh0 (B, Hv, Dk, Dv) (fp32). */
 int64_t convdelta_bwd_workspace(const convdelta_desc* desc); /* bytes, or a negative error */
 int convdelta_bwd(const convdelta_desc* desc, const convdelta_heads* dy, const convdelta_heads* q,
                   const convdelta_heads* k, const convdelta_heads* v, const void* log_decay, const void* beta,
-                  const void* states, const void* starts, const void* dh_last, void* dq, void* dk, void* dv,
-                  void* dlog_decay, void* dbeta, void* dh0, void* workspace, void* stream);
+                  const void* states, const void* x, const void* starts, const void* dh_last, void* dq, void* dk,
+                  void* dv, void* dlog_decay, void* dbeta, void* dh0, void* workspace, void* stream);
 
 /* One row of each of B streams (desc->t is not used; row strides are not used):
  * y (B, Hv, Dv) and the moved-on state.  Stream b's state is state[slot], slot =

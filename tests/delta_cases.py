@@ -64,7 +64,7 @@ def definition(x, scale=None, starts=None, use_h0=True, use_dh=True):
         size = torch.maximum(size, frob(S) + _norm(err) + _norm(v[:, i]))
         olds.append(old), errs.append(err), us.append(u), news.append(S)
     last = S
-    out = {"y": y, "h": last, "states": torch.stack(kept, 1) if kept else torch.zeros((b, 0, hv, dk, dv), dtype=torch.float64)}
+    out = {"y": y, "h": last, "x": torch.stack(errs, 1) if errs else torch.zeros_like(v), "states": torch.stack(kept, 1) if kept else torch.zeros((b, 0, hv, dk, dv), dtype=torch.float64)}
     dy = d["dy"]
     dS = d["dh"] if use_dh else torch.zeros_like(S)
     back = torch.maximum(back, frob(dS))
@@ -86,7 +86,7 @@ def definition(x, scale=None, starts=None, use_h0=True, use_dh=True):
     tol = U * CHUNK_SUMS * max(1, -(-t // 64) + 1)
     both = size * back
     rows = lambda a: a[:, None, :, None]  # noqa: E731
-    bound = {"y": tol * rows(size) * scale * _norm(q)[..., None], "h": tol * size[..., None, None],
+    bound = {"y": tol * rows(size) * scale * _norm(q)[..., None], "h": tol * size[..., None, None], "x": tol * rows(size) * torch.ones_like(v),
              "states": tol * size[:, None, :, None, None], "dv": tol * rows(back) * torch.ones_like(v),
              "dq": fold(tol * rows(size) * scale * _norm(dy)[..., None].expand_as(q)),
              "dk": fold((4 * tol * rows(both)).expand_as(k)),

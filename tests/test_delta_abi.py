@@ -39,13 +39,13 @@ def _heads(at, h=2, d=32, **kw):
 
 def _fwd(d, **kw):
     p = dict(q=_heads(1 * MB), k=_heads(2 * MB), v=_heads(3 * MB, 4), g=4 * MB, beta=5 * MB, h0=None, starts=None, y=6 * MB,
-             h=7 * MB, states=None, work=64 * MB)
+             h=7 * MB, states=None, x=None, work=64 * MB)
     p.update(kw)
     return dl._delta().convdelta_fwd(d, *p.values(), None)
 
 
 def _bwd(d, **kw):
-    p = dict(dy=_heads(1 * MB, 4), q=_heads(2 * MB), k=_heads(3 * MB), v=_heads(4 * MB, 4), g=5 * MB, beta=6 * MB, states=7 * MB,
+    p = dict(dy=_heads(1 * MB, 4), q=_heads(2 * MB), k=_heads(3 * MB), v=_heads(4 * MB, 4), g=5 * MB, beta=6 * MB, states=7 * MB, x=14 * MB,
              starts=None, dh=None, dq=8 * MB, dk=9 * MB, dv=10 * MB, dg=11 * MB, db=12 * MB, dh0=13 * MB, work=64 * MB)
     p.update(kw)
     return dl._delta().convdelta_bwd(d, *p.values(), None)
@@ -75,7 +75,7 @@ def test_missing_and_misplaced_buffers():
     assert _fwd(None) == NULL and _bwd(None) == NULL and _step(None) == NULL
     for n in ("q", "k", "v", "g", "beta", "y", "h", "work"):
         assert _fwd(d, **{n: None}) == NULL, n
-    for n in ("dy", "q", "k", "v", "g", "beta", "states", "dq", "dk", "dv", "dg", "db", "dh0", "work"):
+    for n in ("dy", "q", "k", "v", "g", "beta", "states", "x", "dq", "dk", "dv", "dg", "db", "dh0", "work"):
         assert _bwd(d, **{n: None}) == NULL, n
     for n in ("q", "k", "v", "g", "beta", "state", "out", "y"):
         assert _step(d, **{n: None}) == NULL, n
@@ -86,7 +86,8 @@ def test_missing_and_misplaced_buffers():
     n = 2 * 100 * 4 * 32 * 2
     for y in (MB, 3 * MB + n - 2, 4 * MB, 7 * MB, 64 * MB):
         assert _fwd(d, y=y) == ALIAS, y
-    assert _fwd(d, h0=7 * MB) == ALIAS and _fwd(d, states=7 * MB + 4) == ALIAS
+    assert _fwd(d, h0=7 * MB) == ALIAS and _fwd(d, states=7 * MB + 4, x=20 * MB) == ALIAS and _fwd(d, states=20 * MB, x=6 * MB) == ALIAS
+    assert _fwd(d, states=20 * MB) == NULL and _fwd(d, x=20 * MB) == NULL
     for k in ("dq", "dk", "dv", "dg", "db", "dh0"):
         assert _bwd(d, **{k: 7 * MB}) == ALIAS
     assert _bwd(d, dk=8 * MB) == ALIAS and _bwd(d, dv=9 * MB) == ALIAS
@@ -97,7 +98,7 @@ def test_an_empty_batch_launches_nothing():
     none = dl.Heads(None, 0, 0, 0)
     d = _desc(b=0)
     assert _fwd(d, q=none, k=none, v=none, g=None, beta=None, y=None, h=None, work=None) == OK
-    assert _bwd(d, dy=none, q=none, k=none, v=none, g=None, beta=None, states=None, dq=None, dk=None, dv=None, dg=None, db=None,
+    assert _bwd(d, dy=none, q=none, k=none, v=none, g=None, beta=None, states=None, x=None, dq=None, dk=None, dv=None, dg=None, db=None,
                 dh0=None, work=None) == OK
     assert _step(d, q=none, k=none, v=none, g=None, beta=None, state=None, out=None, n=0, y=None) == OK
 
@@ -110,7 +111,7 @@ def test_the_workspace_grows_with_the_problem():
 
 def test_the_binding_needs_device_tensors():
     q, g, h = torch.zeros(1, 4, 2, 8), torch.zeros(1, 4, 2), torch.zeros(1, 2, 8, 8)
-    for call in (lambda: igc.delta_rule(q, q, q, g, g), lambda: igc.delta_rule_bwd(q, q, q, q, g, g, h[:, None]),
+    for call in (lambda: igc.delta_rule(q, q, q, g, g), lambda: igc.delta_rule_bwd(q, q, q, q, g, g, igc.DeltaStates(h[:, None], q)),
                  lambda: igc.delta_rule_step(q[:, 0], q[:, 0], q[:, 0], g[:, 0], g[:, 0], h)):
         with pytest.raises(ValueError, match="GPU only"):
             call()
@@ -121,7 +122,7 @@ def test_the_binding_refuses_what_does_not_fit():
     dev = "cuda:0"
     q, v = torch.zeros(2, 20, 2, 8, device=dev), torch.zeros(2, 20, 4, 6, device=dev)
     g, h = torch.zeros(2, 20, 4, device=dev), torch.zeros(2, 4, 8, 6, device=dev)
-    st = h[:, None].contiguous()
+    st = igc.DeltaStates(h[:, None].contiguous(), v)
     one = (q[:, 0], q[:, 0], v[:, 0], g[:, 0], g[:, 0])
     for error, call in (
             (ValueError, lambda: igc.delta_rule(q[0], q, v, g, g)), (TypeError, lambda: igc.delta_rule(q.double(), q, v, g, g)),
@@ -137,7 +138,9 @@ def test_the_binding_refuses_what_does_not_fit():
             (ValueError, lambda: igc.delta_rule_bwd(v[:, :19], q, q, v, g, g, st)),
             (ValueError, lambda: igc.delta_rule_bwd(v.half(), q, q, v, g, g, st)),
             (ValueError, lambda: igc.delta_rule_bwd(v, q, q, v, g, g, None)),
-            (ValueError, lambda: igc.delta_rule_bwd(v, q, q, v, g, g, torch.zeros(2, 2, 4, 8, 6, device=dev))),
+            (ValueError, lambda: igc.delta_rule_bwd(v, q, q, v, g, g, st.states)),
+            (ValueError, lambda: igc.delta_rule_bwd(v, q, q, v, g, g, st._replace(states=torch.zeros(2, 2, 4, 8, 6, device=dev)))),
+            (ValueError, lambda: igc.delta_rule_bwd(v, q, q, v, g, g, st._replace(x=v[:, :19]))),
             (ValueError, lambda: igc.delta_rule_bwd(v, q, q, v, g, g, st, dh=h.half())),
             (ValueError, lambda: igc.delta_rule_step(*one, h[:, :2])), (ValueError, lambda: igc.delta_rule_step(*one, torch.zeros(3, 4, 8, 6, device=dev))),
             (TypeError, lambda: igc.delta_rule_step(*one, h, slots=torch.zeros(2, dtype=torch.int64, device=dev))),

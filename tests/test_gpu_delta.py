@@ -22,7 +22,7 @@ def _ins(x):
 def _both(x, scale=None, starts=None, use_h0=True, use_dh=True):
     f = igc.delta_rule(*_ins(x), scale=scale, h0=x["h0"] if use_h0 else None, starts=starts, train=True)
     g = igc.delta_rule_bwd(x["dy"], *_ins(x), f.states, scale=scale, starts=starts, dh=x["dh"] if use_dh else None)
-    return {**f._asdict(), **g._asdict()}
+    return {**f._asdict(), **f.states._asdict(), **g._asdict()}
 
 
 def _check_all(got, ref, names=None, where=None):
