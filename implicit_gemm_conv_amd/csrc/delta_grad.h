@@ -35,7 +35,7 @@ struct GradLds {
     struct {
       __bf16 s[kParts * DK * kSlice], ds[GP * DK * kSlice];          // 32 columns of both states, rows d
       __bf16 u[kParts * kChunk * kSlice], dx[GP * kChunk * kSlice];  // rows of the chunk
-    };
+    } slice[NP == 3 ? 1 : 2];
     struct {
       __bf16 p[kParts * kChunk * kLdM], l[GP * kChunk * kLdM];       // dP and dL
       __bf16 rows[NP * RowsAt<DK>::part];                            // k, then q
@@ -43,10 +43,10 @@ struct GradLds {
   };
   float gates[3 * kChunk], red[kChunk][4];  // enter, leave, beta; dx.v, z.x and both halves of q.dq
   double sums[kChunk], a[kT / 64];
-  int seq[kChunk];
+  int seq[kChunk], wild;
 };
 
-template <typename T, int DK>
+template <typename T, int DK, bool WHOLE>
 struct Grad {
   typedef Team<T, DK> F;
   typedef GradLds<T, DK> Lds;
@@ -76,28 +76,31 @@ struct Grad {
     own = 16 * wave + 4 * q4;
   }
 
-  // 4 columns of row d of a (Dk, ld) state from column v0 on, whatever is there where it ends
-  __device__ __forceinline__ void load_state(const float* from, int v0, int ld, f32x4_t (&x)[held]) const {
+  // What a slice of 32 columns is made of: pieces of both states and of the gradient before the chunk; 4 columns of a
+  // row of z, x and v; 8 of the lane's row of dy, an operand.
+  struct Slice {
+    f32x4_t st[held], ds[held], be[held], z, x;
+    typedef uint32_t V __attribute__((ext_vector_type(sizeof(T))));
+    V v;  // as it is in memory
+    Raw8<T> dy;
+  };
+  // N neighbouring elements of a row, zero past its end: as pieces of at most 16 bytes, where rows are whole ones (WHOLE)
+  template <typename E, int N>
+  __device__ __forceinline__ void load(const Range& x, uint32_t row, int col, int width, void* to) const {
+    constexpr int n = WHOLE ? (N * sizeof(E) > 16 ? 16 / sizeof(E) : N) : 1;
+    struct alignas(n * sizeof(E)) Piece { E e[n]; };
 #pragma unroll
-    for (int k = 0; k < held; ++k) {
-      const int d = min(tid / (kCols / 4), a.dk - 1 - k * kT / (kCols / 4)), v = v0 + tid % (kCols / 4) * 4;
-      const float* p = from + (int64_t)k * (kT / (kCols / 4)) * ld;
-      if (k * kT / (kCols / 4) >= a.dk) continue;
-      if (ld % 4 == 0) {
-        x[k] = load_at<f32x4_t>(p, (uint32_t)(d * ld + min(v, ld - 4)) * 4u);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[k][e] = load_at<float>(p, (uint32_t)(d * ld + min(v + e, ld - 1)) * 4u);
-      }
+    for (int k = 0; k < N / n; ++k) {
+      const int at = col + k * n;
+      const Piece p = x.load<Piece>(at < width ? row + (uint32_t)at * (uint32_t)sizeof(E) : kNowhere);
+      __builtin_memcpy((E*)to + k * n, &p, sizeof(p));
     }
   }
-  // ... and zeros there
-  __device__ __forceinline__ void within(f32x4_t (&x)[held], int v0, int width) const {
+  __device__ __forceinline__ void load_state(const Range& from, int v0, int ld, f32x4_t (&x)[held]) const {
 #pragma unroll
     for (int k = 0; k < held; ++k) {
-      const int i = tid + k * kT, d = i / (kCols / 4), v = v0 + i % (kCols / 4) * 4;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[k][e] = d < a.dk && v + e < width ? x[k][e] : 0.f;
+      const int i = tid + k * kT;
+      load<float, 4>(from, (uint32_t)(i / 8 * ld) * 4u, v0 + i % 8 * 4, ld, &x[k]);  // rows past Dk are past the range
     }
   }
   template <int N>
@@ -192,19 +195,31 @@ struct Grad {
 
   // M = factor * D * acc below (and, EDGE, on) the diagonal, as N parts into LDS.  A half has the columns' tiles half, half + 2.
   template <bool EDGE, int N>
-  __device__ __forceinline__ void put_matrix(__bf16* to, const f32x4_t (&acc)[2], float factor) const {
+  __device__ __forceinline__ void put_matrix(__bf16* to, const f32x4_t (&acc)[2], const f32x4_t (&decay)[2], float factor) const {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int j = 16 * (half + 2 * n) + m;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = own + r;
-        const bool in = (EDGE ? j <= i : j < i) && s.seq[i] == s.seq[j];
-        const float x = in ? factor * expf((float)(s.sums[i] - s.sums[j])) * acc[n][r] : 0.f;
+        const bool in = decay[n][r] >= 0.f && (EDGE ? j <= i : j < i);
         __bf16 w[N];
-        split_one<N>(x, w);
+        split_one<N>(in ? factor * decay[n][r] * acc[n][r] : 0.f, w);
 #pragma unroll
         for (int p = 0; p < N; ++p) to[(p * kChunk + i) * kLdM + j] = w[p];
+      }
+    }
+  }
+  // D of those tiles, -1 where the rows are not of one sequence
+  __device__ __forceinline__ void get_decay(f32x4_t (&decay)[2]) const {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int j = 16 * (half + 2 * n) + m;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = own + r;
+        const float d = expf((float)fmin(s.sums[i] - s.sums[j], 0.));
+        decay[n][r] = s.seq[i] == s.seq[j] ? d : -1.f;
       }
     }
   }
@@ -214,115 +229,115 @@ struct Grad {
     return v;
   }
 
-  // 4 neighbouring elements of a row, zero outside; `whole`: as one access
-  template <typename E>
-  __device__ __forceinline__ f32x4_t load4(const Range& x, uint32_t row, int col, int width, bool whole) const {
-    struct alignas(4 * sizeof(E)) Four { E v[4]; } f;
-    if (whole) {
-      f = x.load<Four>(col < width ? row + (uint32_t)col * (uint32_t)sizeof(E) : kNowhere);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f.v[e] = x.load<E>(col + e < width ? row + (uint32_t)(col + e) * (uint32_t)sizeof(E) : kNowhere);
-    }
-    return f32x4_t{to_f32(f.v[0]), to_f32(f.v[1]), to_f32(f.v[2]), to_f32(f.v[3])};
-  }
-
   // The gradients of one value head; its share of dq and dk.
   __device__ __forceinline__ void head(int hk, int h, f32x4_t (&dq)[DT], f32x4_t (&dk)[DT]) {
     const int64_t bh = (int64_t)b * a.hv + h, at = bh * a.chunks + c;
     const auto row = [&] { return 16 * wave + m; };  // the lane's row as an operand
     const int rows = min(kChunk, a.t - c * kChunk);
-    const float* states = a.states_in + (((int64_t)b * a.chunks + c) * a.hv + h) * a.dk * a.dv;
-    const float* dstate = a.w.dstate + at * a.dk * a.dvp;
-    const float* before = c ? dstate - (int64_t)a.dk * a.dvp : a.dh0 + bh * a.dk * a.dv;
+    const int64_t size = (int64_t)a.dk * a.dv, size_p = (int64_t)a.dk * a.dvp;
+    const Range states(a.states_in + (((int64_t)b * a.chunks + c) * a.hv + h) * size, size * 4);
+    const Range dstate(a.w.dstate + at * size_p, size_p * 4);
+    const Range before(c ? a.w.dstate + (at - 1) * size_p : a.dh0 + bh * size, (c ? size_p : size) * 4);
     const int ldb = c ? a.dvp : a.dv;
     const Range zs(a.w.z + at * kChunk * a.dvp, (int64_t)kChunk * a.dvp * 4);
     const Range xs(a.x_in + ((int64_t)b * a.t + c * kChunk) * a.hv * a.dv + (int64_t)h * a.dv, (int64_t)rows * a.hv * a.dv * 4);
     const Range vs = rows_range<T>(a.v, b, h, c * kChunk, a.t, a.dv), dys = rows_range<T>(a.dy, b, h, c * kChunk, a.t, a.dv);
     __syncthreads();  // what is read of the head before
-    for (int i = tid; i < 3 * kChunk; i += kT) s.gates[i] = a.w.rows[at * 4 * kChunk + i];
+    const float my_beta = load_at<float>(a.w.rows + (at * 4 + 2) * kChunk, (uint32_t)(tid / 8) * 4u);
+    Slice x;
+    const auto fetch = [&](int v0) {
+      load_state(states, v0, a.dv, x.st);
+      load_state(dstate, v0, a.dvp, x.ds);
+      load_state(before, v0, ldb, x.be);
+      const int col = v0 + tid % 8 * 4;
+      load<float, 4>(zs, (uint32_t)(tid / 8 * a.dvp) * 4u, col, a.dvp, &x.z);
+      load<float, 4>(xs, (uint32_t)(tid / 8 * a.hv * a.dv) * 4u, col, a.dv, &x.x);
+      load<T, 4>(vs, tid / 8 * row_bytes<T>(a.v), col, a.dv, &x.v);
+      load<T, 8>(dys, row() * row_bytes<T>(a.dy), v0 + 8 * q4, a.dv, x.dy.w);
+    };
+    Parts<NP> yp;
+    float dot = 0.f, db = 0.f, dxv = 0.f;
+    // what was fetched, into LDS, and dy into yp
+    const auto put = [&](auto& to) {
+      put_state<kParts>(to.s, x.st);
+      put_state<GP>(to.ds, x.ds);
+#pragma unroll
+      for (int n = 0; n < held; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dot = fmaf(x.st[n][e], x.be[n][e], dot);
+      f32x4_t u, dx;
+      T v[4];
+      __builtin_memcpy(v, &x.v, sizeof(v));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u[e] = my_beta * x.x[e];
+        dx[e] = my_beta * x.z[e];
+        db = fmaf(x.x[e], x.z[e], db);
+        dxv = fmaf(dx[e], to_f32(v[e]), dxv);
+      }
+      put_row<kParts>(to.u, u);
+      put_row<GP>(to.dx, dx);
+      float e8[8];
+      x.dy.get(e8);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) e8[e] = row() < rows ? e8[e] : 0.f;
+      yp = split<NP>(e8);
+    };
+    fetch(0);
+    if (tid == 0) s.wild = 0;
+    if (tid < 3 * kChunk) s.gates[tid] = a.w.rows[at * 4 * kChunk + tid];
     if (tid < kChunk) {
       s.sums[tid] = a.w.sums[at * kChunk + tid];
       s.seq[tid] = a.w.seq[at * kChunk + tid];
     }
-    const float my_beta = load_at<float>(a.w.rows + (at * 4 + 2) * kChunk, (uint32_t)(tid / 8) * 4u);
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     f32x4_t dkr[DT], dkc[DT], dp[2] = {zero, zero}, dl[2] = {zero, zero};
-    float dot = 0.f, db = 0.f, dxv = 0.f;
 #pragma unroll
     for (int t = 0; t < DT; ++t) dq[t] = dkr[t] = dkc[t] = zero;
+    put(s.slice[0]);
+    fetch(kCols);
+    __syncthreads();
+    Rows64<T, DK, kT> k, q;
+    constexpr int kTurns = NP == 3 ? 1 : 2;
+    int turn = 0;
 #pragma clang loop unroll(disable)
     for (int v0 = 0; v0 < a.dvp; v0 += kCols) {
       renew();
-      f32x4_t st[held], ds[held], be[held];
-      load_state(states, v0, a.dv, st);
-      load_state(dstate, v0, a.dvp, ds);
-      load_state(before, v0, ldb, be);
-      const int col = v0 + tid % 8 * 4;
-      const f32x4_t z = load4<float>(zs, (uint32_t)(tid / 8 * a.dvp) * 4u, col, a.dvp, true);
-      const f32x4_t x = load4<float>(xs, (uint32_t)(tid / 8 * a.hv * a.dv) * 4u, col, a.dv, a.vec_x);
-      const f32x4_t v = load4<T>(vs, tid / 8 * row_bytes<T>(a.v), col, a.dv, a.vec_v);
-      Raw8<T> dy;
-      if (a.vec_dy) {
-        dy.load(dys, row() * row_bytes<T>(a.dy), v0 + 8 * q4, a.dv);
-      } else {
-        T e8[8];
+      {
+        auto& at = s.slice[turn];
+        const auto up = slice<kParts>(at.u, row(), kChunk);
+        const auto xp = slice<GP>(at.dx, row(), kChunk);
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          e8[e] = dys.load<T>(v0 + 8 * q4 + e < a.dv ? row() * row_bytes<T>(a.dy) + (uint32_t)(v0 + 8 * q4 + e) * (uint32_t)sizeof(T)
-                                                     : kNowhere);
-        __builtin_memcpy(dy.w, e8, sizeof(e8));
-      }
-      if (v0) __syncthreads();  // what is read of the slice before
-      within(st, v0, a.dv);
-      within(ds, v0, a.dvp);
-      put_state<kParts>(s.s, st);
-      put_state<GP>(s.ds, ds);
-      if (each || tid < DK * kCols / 4)
-#pragma unroll
-        for (int n = 0; n < held; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dot = fmaf(st[n][e], be[n][e], dot);  // S is zero outside
-      f32x4_t u, dx;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        u[e] = my_beta * x[e];
-        dx[e] = my_beta * z[e];
-        db = fmaf(x[e], z[e], db);
-        dxv = fmaf(dx[e], v[e], dxv);
-      }
-      put_row<kParts>(s.u, u);
-      put_row<GP>(s.dx, dx);
-      float e8[8];
-      dy.get(e8);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) e8[e] = row() < rows ? e8[e] : 0.f;
-      const Parts<NP> yp = split<NP>(e8);
-      __syncthreads();
-      renew();
-      const auto up = slice<kParts>(s.u, row(), kChunk);
-      const auto xp = slice<GP>(s.dx, row(), kChunk);
-#pragma unroll
-      for (int t = 0; t < DT; ++t) {
-        const int d = 16 * (half * DT + t) + m;
-        const auto sp = slice<kParts>(s.s, d, DK);
-        const auto dsp = slice<GP>(s.ds, d, DK);
-        dq[t] = mma(yp, sp, dq[t]);
-        dkr[t] = mma_first<GP>(xp, sp, dkr[t]);
-        dkc[t] = mma_first<GP>(up, dsp, dkc[t]);
-      }
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-        if (half + 2 * n <= wave) {
-          const auto uj = slice<kParts>(s.u, 16 * (half + 2 * n) + m, kChunk);
-          dp[n] = mma(yp, uj, dp[n]);
-          dl[n] = mma_first<GP>(xp, uj, dl[n]);
+        for (int t = 0; t < DT; ++t) {
+          const int d = 16 * (half * DT + t) + m;
+          const auto sp = slice<kParts>(at.s, d, DK);
+          const auto dsp = slice<GP>(at.ds, d, DK);
+          dq[t] = mma(yp, sp, dq[t]);
+          dkr[t] = mma_first<GP>(xp, sp, dkr[t]);
+          dkc[t] = mma_first<GP>(up, dsp, dkc[t]);
         }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          if (half + 2 * n <= wave) {
+            const auto uj = slice<kParts>(at.u, 16 * (half + 2 * n) + m, kChunk);
+            dp[n] = mma(yp, uj, dp[n]);
+            dl[n] = mma_first<GP>(xp, uj, dl[n]);
+          }
+      }
+      turn = (turn + 1) % kTurns;
+      if (v0 + kCols < a.dvp) {
+        if (kTurns == 1) __syncthreads();  // what is read of the slice
+        renew();
+        put(s.slice[turn]);
+        __builtin_amdgcn_sched_barrier(0);  // the next slice takes this one's registers over
+        fetch(v0 + 2 * kCols);
+      } else {
+        k.load(a.k, b, hk, c * kChunk, a.t, a.dkp);
+        q.load(a.q, b, hk, c * kChunk, a.t, a.dkp);
+      }
+      __syncthreads();
     }
     renew();
-    Rows64<T, DK, kT> k, q;
-    k.load(a.k, b, hk, c * kChunk, a.t, a.dkp);
-    q.load(a.q, b, hk, c * kChunk, a.t, a.dkp);
     const f32x4_t enter = *(const f32x4_t*)(s.gates + own), leave = *(const f32x4_t*)(s.gates + kChunk + own);
 #pragma unroll
     for (int t = 0; t < DT; ++t)
@@ -341,12 +356,15 @@ struct Grad {
       s.red[tid / 8][0] = dxv;
       s.red[tid / 8][1] = db;
     }
-    const bool wild = __syncthreads_or(!k.finite() || !q.finite());  // the slices are read: their room is the matrices' now
+    if (!k.finite() || !q.finite()) s.wild = 1;
+    f32x4_t decay[2];
+    get_decay(decay);
     renew();
-    put_matrix<true, kParts>(s.p, dp, a.scale);
-    put_matrix<false, GP>(s.l, dl, -1.f);
+    put_matrix<true, kParts>(s.p, dp, decay, a.scale);
+    put_matrix<false, GP>(s.l, dl, decay, -1.f);
     k.put(s.rows);
     __syncthreads();
+    const bool wild = s.wild;
     renew();
     add<false, kParts>(s.p, dq, wild);
     renew();
@@ -391,12 +409,9 @@ struct Grad {
   }
 };
 
-template <typename T>
-constexpr int kGradWaves = 2;  // waves a SIMD
-
-template <typename T, int DK>
-__global__ __launch_bounds__(kT, kGradWaves<T>) void delta_grad_kernel(DeltaArgs a) {
-  typedef Grad<T, DK> F;
+template <typename T, int DK, bool WHOLE>
+__global__ __launch_bounds__(kT, 2) void delta_grad_kernel(DeltaArgs a) {
+  typedef Grad<T, DK, WHOLE> F;
   __shared__ __attribute__((aligned(16))) typename F::Lds s;
   // neighbouring chunks on one die: each reads the gradient of a state that its neighbour reads too
   const int id = convfwd::xcd_tile(blockIdx.x, gridDim.x);
@@ -430,7 +445,9 @@ __global__ __launch_bounds__(kT, kGradWaves<T>) void delta_grad_kernel(DeltaArgs
 template <typename T>
 hipError_t delta_grad_of(const DeltaArgs& a, hipStream_t s) {
   return for_dk(a.dk, [&](auto dk) {
-    hipLaunchKernelGGL((delta_grad_kernel<T, decltype(dk)::value>), dim3(a.b * a.hk * a.chunks), dim3(kT), 0, s, a);
+    constexpr int DK = decltype(dk)::value;
+    hipLaunchKernelGGL((a.whole ? delta_grad_kernel<T, DK, true> : delta_grad_kernel<T, DK, false>), dim3(a.b * a.hk * a.chunks),
+                       dim3(kT), 0, s, a);
     return hipGetLastError();
   });
 }
