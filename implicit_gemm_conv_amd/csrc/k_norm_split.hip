@@ -1,6 +1,6 @@
 // k_norm_split.hip -- group norm over images and volumes: the sums of tiles of
-// positions, their join for each (n, group), and a second pass over x that writes
-// the result.
+// positions, and a second pass over x that writes the result.  The sums are joined at
+// the second pass's beginning, or by a launch between.
 #include "norm_device.h"
 
 namespace convnorm {
@@ -16,11 +16,10 @@ struct Part {
   bool live;
 };
 template <int V>
-__device__ __forceinline__ Part part_of(const NormArgs& a) {
+__device__ __forceinline__ Part part_of(const NormArgs& a, unsigned b = blockIdx.x) {
   const Plan& pl = a.plan;
   Part t;
   const int cg = a.c / a.groups;
-  unsigned b = blockIdx.x;
   const int cb = b % pl.cblocks;
   b /= pl.cblocks;
   t.tile = b % pl.tiles;
@@ -163,48 +162,108 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
   return v;
 }
 
-// One workgroup for each (n, group): the parts' means, then the squares about the whole mean.
-__global__ __launch_bounds__(kThreads) void norm_join_kernel(NormArgs a) {
-  __shared__ double lds[kThreads / 64];
+// Sum over `of` neighbouring threads, a power of two up to a wave, or the whole workgroup.
+__device__ __forceinline__ double sum_over(double v, int of, double* lds) {
+  if (of > 64) return block_sum(v, lds);
+  for (int o = 1; o < of; o <<= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// The mean and 1 / deviation of a group from its parts, over `of` threads: the parts' means, then the squares about
+// the whole mean.
+__device__ __forceinline__ float2 join_stats(const NormArgs& a, int64_t group, int lane, int of, double* lds) {
   const int parts = a.plan.slices * a.plan.tiles;
-  const float2* part = (const float2*)a.part + (int64_t)blockIdx.x * parts;
-  double sum = 0;
-  for (int i = threadIdx.x; i < parts; i += kThreads) sum += count_of(a, i) * part[i].x;
+  const float2* part = (const float2*)a.part + group * parts;
   const double all = (double)a.p * (a.c / a.groups);
-  const double mean = block_sum(sum, lds) / all;
+  double sum = 0;
+#pragma unroll 4
+  for (int i = lane; i < parts; i += of) sum += count_of(a, i) * part[i].x;
+  const double mean = sum_over(sum, of, lds) / all;
   sum = 0;
-  for (int i = threadIdx.x; i < parts; i += kThreads) {
+#pragma unroll 4
+  for (int i = lane; i < parts; i += of) {
     const double d = part[i].x - mean;
     sum += part[i].y + count_of(a, i) * d * d;
   }
-  sum = block_sum(sum, lds) / all;
+  sum = sum_over(sum, of, lds) / all;
+  return make_float2((float)mean, (float)(1.0 / sqrt(sum + a.eps)));
+}
+// ... and the two means of the backward pass
+__device__ __forceinline__ float2 join_means(const NormArgs& a, int64_t group, int lane, int of, double* lds) {
+  const int parts = a.plan.slices * a.plan.tiles;
+  const float2* part = (const float2*)a.part + group * parts;
+  const double all = (double)a.p * (a.c / a.groups);
+  double s1 = 0, s2 = 0;
+#pragma unroll 4
+  for (int i = lane; i < parts; i += of) {
+    s1 += part[i].x;
+    s2 += part[i].y;
+  }
+  s1 = sum_over(s1, of, lds);
+  s2 = sum_over(s2, of, lds);
+  return make_float2((float)(s1 / all), (float)(s2 / all));
+}
+// A workgroup's own groups: out[g] = f(the group's number, lane of `of` threads)
+template <typename F>
+__device__ __forceinline__ void join_groups(const NormArgs& a, const Part& t, float2* out, const F& f) {
+  const int groups = a.plan.slices == 1 ? t.width / (a.c / a.groups) : 1, of = join_lanes(groups);
+  for (int g0 = 0; g0 < groups; g0 += kThreads / of) {
+    const int g = min(g0 + (int)threadIdx.x / of, groups - 1);
+    const float2 o = f((int64_t)t.n * a.groups + t.g0 + g, threadIdx.x % of, of);
+    if (threadIdx.x % of == 0) out[g] = o;
+  }
+  __syncthreads();
+}
+
+// One workgroup for each (n, group).
+__global__ __launch_bounds__(kThreads) void norm_join_kernel(NormArgs a) {
+  __shared__ double lds[kThreads / 64];
+  const float2 o = join_stats(a, blockIdx.x, threadIdx.x, kThreads, lds);
   if (threadIdx.x == 0) {
-    a.mean[blockIdx.x] = (float)mean;
-    a.rstd[blockIdx.x] = (float)(1.0 / sqrt(sum + a.eps));
+    a.mean[blockIdx.x] = o.x;
+    a.rstd[blockIdx.x] = o.y;
   }
 }
 
+// What a thread's channels are normalised with: the mean and 1 / deviation of their groups by f(group).
 template <int V>
 struct Channels {
   float mean[V], rstd[V], w[V], b[V];
-  __device__ __forceinline__ Channels(const NormArgs& a, const Part& t, const float* mu, const float* rs) {
+  template <typename F>
+  __device__ __forceinline__ Channels(const NormArgs& a, const Part& t, const F& f) {
     const int cg = a.c / a.groups;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const int c = t.c0 + t.col * V + e, g = c / cg;
-      mean[e] = mu[(int64_t)t.n * a.groups + g];
-      rstd[e] = rs[(int64_t)t.n * a.groups + g];
+      const int c = t.c0 + t.col * V + e;
+      const float2 o = f(c / cg - t.g0);
+      mean[e] = o.x;
+      rstd[e] = o.y;
       w[e] = param(a.weight, a.param_f32, a.dtype, c, 1.f);
       b[e] = param(a.bias, a.param_f32, a.dtype, c, 0.f);
     }
   }
 };
+__device__ __forceinline__ float2 stats_in(const NormArgs& a, const Part& t, const float* mean, const float* rstd, int g) {
+  const int64_t at = (int64_t)t.n * a.groups + t.g0 + g;
+  return make_float2(mean[at], rstd[at]);
+}
 
-template <typename T, int V, bool SILU>
+template <typename T, int V, bool SILU, bool JOINT>
 __global__ __launch_bounds__(kThreads) void norm_apply_kernel(NormArgs a) {
+  __shared__ float2 stats[JOINT ? 1 : kThreads * V];
+  __shared__ double lds[kThreads / 64];
   const Part t = part_of<V>(a);
+  if (!JOINT)
+    join_groups(a, t, stats, [&](int64_t group, int lane, int of) {
+      const float2 o = join_stats(a, group, lane, of, lds);
+      if (lane == 0 && t.tile == 0 && t.slice == 0) {
+        a.mean[group] = o.x;
+        a.rstd[group] = o.y;
+      }
+      return o;
+    });
   if (!t.live) return;
-  const Channels<V> k(a, t, a.mean, a.rstd);
+  const Channels<V> k(a, t, [&](int g) { return JOINT ? stats_in(a, t, a.mean, a.rstd, g) : stats[g]; });
   T* y = (T*)a.y + (int64_t)t.n * a.p * a.c + t.c0 + t.col * V;
   walk<T, V>(t, a.x, t.n, [&](int p, const Pack<T, V>& q) {
     Pack<T, V> o;
@@ -245,7 +304,7 @@ __global__ __launch_bounds__(kThreads) void norm_sums_kernel(NormArgs a) {
 #pragma unroll
   for (int e = 0; e < V; ++e) dw[e] = db[e] = 0.f;
   if (t.live) {
-    const Channels<V> k(a, t, a.mean_in, a.rstd_in);
+    const Channels<V> k(a, t, [&](int g) { return stats_in(a, t, a.mean_in, a.rstd_in, g); });
     walk2<T, V>(a, t, [&](int, const Pack<T, V>& q, const Pack<T, V>& r) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -297,13 +356,13 @@ __global__ __launch_bounds__(kThreads) void norm_sums_kernel(NormArgs a) {
   });
 }
 
-// The first N * groups workgroups: the two means of an (n, group); the others: dweight and dbias of
-// kCols channels each, from the sums of all tiles.
+// dweight and dbias of kCols channels a workgroup, from the sums of all tiles.
 constexpr int kCols = 8;
 __device__ void columns(const NormArgs& a, int block, double* lds) {
   const int c = block * kCols + threadIdx.x % kCols, lane = threadIdx.x / kCols;
   double dw = 0, db = 0;
   if (c < a.c)
+#pragma unroll 8
     for (int64_t r = lane; r < a.plan.rows; r += kThreads / kCols) {
       const float2 o = ((const float2*)a.chan)[r * a.c + c];
       dw += o.x;
@@ -325,38 +384,39 @@ __device__ void columns(const NormArgs& a, int block, double* lds) {
   }
 }
 
-__global__ __launch_bounds__(kThreads) void norm_join_bwd_kernel(NormArgs a) {
-  __shared__ double lds[2 * kThreads];
-  const int64_t slabs = (int64_t)a.n * a.groups;
-  if (blockIdx.x >= slabs) return columns(a, (int)(blockIdx.x - slabs), lds);
-  const int parts = a.plan.slices * a.plan.tiles;
-  const float2* part = (const float2*)a.part + (int64_t)blockIdx.x * parts;
-  double s1 = 0, s2 = 0;
-  for (int i = threadIdx.x; i < parts; i += kThreads) {
-    s1 += part[i].x;
-    s2 += part[i].y;
-  }
-  s1 = block_sum(s1, lds);
-  s2 = block_sum(s2, lds);
-  const double all = (double)a.p * (a.c / a.groups);
-  if (threadIdx.x == 0) ((float2*)a.two)[blockIdx.x] = make_float2((float)(s1 / all), (float)(s2 / all));
-}
-
 __global__ __launch_bounds__(kThreads) void norm_columns_kernel(NormArgs a) {
   __shared__ double lds[2 * kThreads];
   columns(a, blockIdx.x, lds);
 }
 
-template <typename T, int V, bool SILU>
-__global__ __launch_bounds__(kThreads) void norm_apply_bwd_kernel(NormArgs a) {
-  const Part t = part_of<V>(a);
+// The first N * groups workgroups: the two means of an (n, group); the others: the parameters' columns.
+__global__ __launch_bounds__(kThreads) void norm_join_bwd_kernel(NormArgs a) {
+  __shared__ double lds[2 * kThreads];
+  const int64_t slabs = (int64_t)a.n * a.groups;
+  if (blockIdx.x >= slabs) return columns(a, (int)(blockIdx.x - slabs), lds);
+  const float2 o = join_means(a, blockIdx.x, threadIdx.x, kThreads, lds);
+  if (threadIdx.x == 0) ((float2*)a.two)[blockIdx.x] = o;
+}
+
+// Not JOINT: the first `cols` workgroups add the parameters' columns, the others write dx.
+template <typename T, int V, bool SILU, bool JOINT>
+__global__ __launch_bounds__(kThreads) void norm_apply_bwd_kernel(NormArgs a, int cols) {
+  __shared__ union {
+    float2 means[JOINT ? 1 : kThreads * V];
+    double sums[JOINT ? 1 : 2 * kThreads];
+  } s;
+  __shared__ double lds[kThreads / 64];
+  if (!JOINT && (int)blockIdx.x < cols) return columns(a, blockIdx.x, s.sums);
+  const Part t = part_of<V>(a, blockIdx.x - (JOINT ? 0 : cols));
+  if (!JOINT) join_groups(a, t, s.means, [&](int64_t group, int lane, int of) { return join_means(a, group, lane, of, lds); });
   if (!t.live) return;
-  const Channels<V> k(a, t, a.mean_in, a.rstd_in);
-  float s1[V], s2[V];
   const int cg = a.c / a.groups;
+  const Channels<V> k(a, t, [&](int g) { return stats_in(a, t, a.mean_in, a.rstd_in, g); });
+  float s1[V], s2[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const float2 o = ((const float2*)a.two)[(int64_t)t.n * a.groups + (t.c0 + t.col * V + e) / cg];
+    const int g = (t.c0 + t.col * V + e) / cg - t.g0;
+    const float2 o = JOINT ? ((const float2*)a.two)[(int64_t)t.n * a.groups + t.g0 + g] : s.means[g];
     s1[e] = o.x;
     s2[e] = o.y;
   }
@@ -387,8 +447,10 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s) {
     constexpr bool SILU = decltype(silu)::value;
     const dim3 grid((unsigned)a.plan.blocks), block(kThreads);
     hipLaunchKernelGGL((norm_stats_kernel<T, V>), grid, block, 0, s, a);
-    hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((int64_t)a.n * a.groups)), block, 0, s, a);
-    hipLaunchKernelGGL((norm_apply_kernel<T, V, SILU>), grid, block, 0, s, a);
+    const dim3 slabs((unsigned)((int64_t)a.n * a.groups));
+    if (a.plan.joint) hipLaunchKernelGGL(norm_join_kernel, slabs, block, 0, s, a);
+    hipLaunchKernelGGL((a.plan.joint ? norm_apply_kernel<T, V, SILU, true> : norm_apply_kernel<T, V, SILU, false>), grid, block, 0,
+                       s, a);
     return hipGetLastError();
   });
 }
@@ -398,11 +460,15 @@ hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
     typedef decltype(t) T;
     constexpr int V = decltype(v)::value;
     constexpr bool SILU = decltype(silu)::value;
-    const dim3 grid((unsigned)a.plan.blocks), block(kThreads);
+    const dim3 block(kThreads);
     const int cols = a.dweight || a.dbias ? (a.c + kCols - 1) / kCols : 0;
-    hipLaunchKernelGGL((norm_sums_kernel<T, V, SILU>), grid, block, 0, s, a);
-    hipLaunchKernelGGL(norm_join_bwd_kernel, dim3((unsigned)((int64_t)a.n * a.groups + cols)), block, 0, s, a);
-    hipLaunchKernelGGL((norm_apply_bwd_kernel<T, V, SILU>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((norm_sums_kernel<T, V, SILU>), dim3((unsigned)a.plan.blocks), block, 0, s, a);
+    if (a.plan.joint) {
+      hipLaunchKernelGGL(norm_join_bwd_kernel, dim3((unsigned)((int64_t)a.n * a.groups + cols)), block, 0, s, a);
+      hipLaunchKernelGGL((norm_apply_bwd_kernel<T, V, SILU, true>), dim3((unsigned)a.plan.blocks), block, 0, s, a, 0);
+    } else {
+      hipLaunchKernelGGL((norm_apply_bwd_kernel<T, V, SILU, false>), dim3((unsigned)(a.plan.blocks + cols)), block, 0, s, a, cols);
+    }
     return hipGetLastError();
   });
 }

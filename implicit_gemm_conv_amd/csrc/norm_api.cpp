@@ -32,11 +32,10 @@ Plan make_plan(int n, int p, int c, int groups, int elem, bool whole_pieces, boo
     if (pieces > (int64_t)pl.team * held) pl.team = kThreads;
     pl.held = (int)std::max<int64_t>(1, ceil_div(pieces, pl.team));
     const int teams = kThreads / pl.team;
-    int64_t rows = n;
-    // backward: as many lanes as the chip holds at once, each walking over n
-    if (backward) rows = std::min<int64_t>(n, std::max<int64_t>(1, (int64_t)512 * teams / groups));
-    pl.blocks = ceil_div(rows * groups, teams);
-    pl.rows = rows * p;
+    // as many lanes as the chip holds at once, each walking over n with its channels' parameters in registers
+    pl.step = std::min<int64_t>(n, std::max<int64_t>(1, (int64_t)(backward ? 512 : 2048) * teams / groups));
+    pl.blocks = ceil_div(pl.step * groups, teams);
+    pl.rows = pl.step * p;
     return pl;
   }
   // ---- tiles of positions ----
@@ -69,6 +68,10 @@ Plan make_plan(int n, int p, int c, int groups, int elem, bool whole_pieces, boo
   pl.tiles = (int)ceil_div(p, pl.per);
   pl.blocks = (int64_t)n * pl.tiles * pl.cblocks;
   pl.rows = (int64_t)n * pl.tiles;
+  // Every workgroup of the second pass joins the sums of its own groups where a thread has few of them, for a launch
+  // less (1 group of 64^3 x 64, fp16: both passes 65 us for 79); else that is left to a launch between the passes
+  // (32^3 x 128 in 32 groups: the second pass took 31 us for 12).
+  pl.joint = (int64_t)pl.slices * pl.tiles > (int64_t)kJoinEach * join_lanes(pl.slices == 1 ? pl.k : 1);
   return pl;
 }
 
@@ -78,11 +81,13 @@ int64_t part_bytes(const Plan& pl, int n, int groups) {
   return pl.team ? 0 : ceil_div((int64_t)n * groups * pl.slices * pl.tiles * 8, 16) * 16;
 }
 
+int64_t two_bytes(const Plan& pl, int n, int groups) { return pl.joint ? ceil_div((int64_t)n * groups * 8, 16) * 16 : 0; }
+
 }  // namespace
 
 int64_t fwd_work_bytes(const Plan& pl, int n, int groups) { return part_bytes(pl, n, groups); }
 int64_t bwd_work_bytes(const Plan& pl, int n, int c, int groups) {
-  return part_bytes(pl, n, groups) + (pl.team ? 0 : ceil_div((int64_t)n * groups * 8, 16) * 16) + pl.rows * c * 8;
+  return part_bytes(pl, n, groups) + two_bytes(pl, n, groups) + pl.rows * c * 8;
 }
 
 }  // namespace convnorm
@@ -108,7 +113,7 @@ int check(const convnorm_desc* d) {
 
 int check_plan(const Plan& pl, const convnorm_desc* d) {
   const int64_t lim = (int64_t)1 << 24;  // workgroups of 256 threads
-  if (pl.blocks >= lim || (!pl.team && (int64_t)d->n * d->groups + d->c >= lim)) return CONVFWD_ERR_TOO_LARGE;
+  if (pl.blocks >= lim || (!pl.team && std::max(pl.blocks, (int64_t)d->n * d->groups) + d->c >= lim)) return CONVFWD_ERR_TOO_LARGE;
   return CONVFWD_OK;
 }
 
@@ -198,10 +203,8 @@ int convnorm_group_bwd(const convnorm_desc* d, const convseq_rows* dy, const con
   char* w = (char*)workspace;
   a.part = (float*)w;
   w += part_bytes(a.plan, d->n, d->groups);
-  if (!a.plan.team) {
-    a.two = (float*)w;
-    w += ceil_div((int64_t)d->n * d->groups * 8, 16) * 16;
-  }
+  a.two = (float*)w;
+  w += two_bytes(a.plan, d->n, d->groups);
   a.chan = (float*)w;
   if (!a.plan.team) return launched(launch_norm_bwd(a, s));
   const int rc = launched(launch_norm_team_bwd(a, s));

@@ -25,6 +25,8 @@ struct Plan {
   int v, team, held;
   int cw, k, cblocks, slices, per, tiles;
   int64_t blocks;  // of the team kernels
+  int joint;       // tiles: a launch of its own joins their sums
+  int64_t step;    // of the team kernels: they walk over n, this many in a turn
   int64_t rows;    // sums per channel that the backward pass leaves for the last step
 };
 
@@ -39,9 +41,18 @@ struct NormArgs {
   const float *mean_in, *rstd_in;
   float *dweight, *dbias;
   float* part;  // sums of tiles: (N, groups, slices, tiles) pairs
+  float* two;   // backward, joint: the two means of each (n, group)
   float* chan;  // backward: sums per channel, (rows, C) pairs
-  float* two;   // backward: the two means of each (n, group)
 };
+
+// Threads of a workgroup that join the sums of one group, of its `groups`: a power of two of neighbouring ones, at most
+// a wave, or all.
+inline __host__ __device__ int join_lanes(int groups) {
+  int of = kThreads;
+  while (of > 1 && (of > kThreads / groups || (groups > 1 && of > 64))) of >>= 1;
+  return of;
+}
+constexpr int kJoinEach = 8;  // sums that a thread joins at most where that is not a launch of its own
 
 Plan make_plan(int n, int p, int c, int groups, int elem, bool whole_pieces, bool backward);
 int64_t fwd_work_bytes(const Plan& pl, int n, int groups);
