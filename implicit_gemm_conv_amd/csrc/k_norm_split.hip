@@ -74,68 +74,70 @@ __device__ __forceinline__ void each_group(const NormArgs& a, const Part& t, con
   }
 }
 
+// What the rows of a workgroup hold for each of its channels: f(channel, the first row's pair, the distance of the
+// rows' pairs), by one thread a channel.
+template <int V, typename F>
+__device__ __forceinline__ void add_rows(const NormArgs& a, const Part& t, const float (&x)[V], const float (&y)[V], float2* lds,
+                                         const F& f) {
+  if (t.live)
+#pragma unroll
+    for (int e = 0; e < V; ++e) lds[t.row * a.plan.cw + t.col * V + e] = make_float2(x[e], y[e]);
+  __syncthreads();
+  for (int c = threadIdx.x; c < t.width; c += kThreads) f(c, lds + c, a.plan.cw);
+  __syncthreads();
+}
+
 template <typename T, int V>
 __global__ __launch_bounds__(kThreads) void norm_stats_kernel(NormArgs a) {
-  __shared__ float3 lds[kThreads * V];
+  __shared__ float2 lds[kThreads * V];
   const Part t = part_of<V>(a);
-  float cnt = 0.f, m[V], s[V];
+  const int each = max(t.p1 - t.p0, 0) / t.rw, over = max(t.p1 - t.p0, 0) % t.rw;
+  const auto rows_of = [&](int row) { return (float)(each + (row < over)); };
+  float m[V], s[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) m[e] = s[e] = 0.f;
-  if (t.live) {
+  if (t.live && t.p0 + t.row < t.p1) {
     // about the thread's own first row: the squares are of differences within the data's spread
-    float first[V];
+    const Pack<T, V> first =
+        *(const Pack<T, V>*)((const T*)a.x.p + t.n * a.x.sb + (t.p0 + t.row) * a.x.st + t.c0 + t.col * V);
     walk<T, V>(t, a.x, t.n, [&](int, const Pack<T, V>& q) {
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        if (cnt == 0.f) first[e] = q.get(e);
-        const float d = q.get(e) - first[e];
+        const float d = q.get(e) - first.get(e);
         m[e] += d;
         s[e] = fmaf(d, d, s[e]);
       }
-      cnt += 1.f;
     });
-    if (cnt > 0.f)
+    const float inv = 1.f / rows_of(t.row);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float d = m[e] / cnt;
-        s[e] = fmaf(-d, m[e], s[e]);
-        m[e] = first[e] + d;
-      }
-  }
-  // the rows of the workgroup, halves at a time
-  int top = 1;
-  while (top < t.rw) top <<= 1;
-  for (int half = top; half >= 1; half >>= 1) {
-    __syncthreads();
-    if (t.live && t.row >= half && t.row < 2 * half)
-#pragma unroll
-      for (int e = 0; e < V; ++e) lds[((t.row - half) * (a.plan.cw / V) + t.col) * V + e] = make_float3(cnt, m[e], s[e]);
-    __syncthreads();
-    if (t.live && t.row < half && t.row + half < t.rw) {
-      float n = cnt;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float3 o = lds[(t.row * (a.plan.cw / V) + t.col) * V + e];
-        n = cnt;
-        join(n, m[e], s[e], o.x, o.y, o.z);
-      }
-      cnt = n;
+    for (int e = 0; e < V; ++e) {
+      const float d = m[e] * inv;
+      s[e] = fmaf(-d, m[e], s[e]);
+      m[e] = first.get(e) + d;
     }
   }
-  __syncthreads();
-  if (t.live && t.row == 0)
-#pragma unroll
-    for (int e = 0; e < V; ++e) lds[t.col * V + e] = make_float3(cnt, m[e], s[e]);
-  __syncthreads();
+  // each channel's mean, then the squares about it
+  const float all = 1.f / (float)max(t.p1 - t.p0, 1);
+  add_rows<V>(a, t, m, s, lds, [&](int c, const float2* at, int ld) {
+    float mean = 0.f, sq = 0.f;
+    for (int r = 0; r < t.rw; ++r) mean = fmaf(rows_of(r) * all, at[r * ld].x - at[0].x, mean);
+    mean += at[0].x;
+    for (int r = 0; r < t.rw; ++r) {
+      const float2 o = at[r * ld];
+      const float d = o.x - mean;
+      sq += fmaf(d * d, rows_of(r), o.y);
+    }
+    lds[c] = make_float2(mean, sq);
+  });
   const float rows = (float)max(t.p1 - t.p0, 0);
   each_group(a, t, [&](int g, int lane, int of, int cg) {
     float mean = 0.f, sq = 0.f;
-    for (int c = lane; c < cg; c += of) mean += lds[g * cg + c].y;
+    for (int c = lane; c < cg; c += of) mean += lds[g * cg + c].x;
     mean = team_sum(mean, of) / (float)cg;
     for (int c = lane; c < cg; c += of) {
-      const float3 o = lds[g * cg + c];
-      const float d = o.y - mean;
-      sq += fmaf(d * d, rows, o.z);
+      const float2 o = lds[g * cg + c];
+      const float d = o.x - mean;
+      sq += fmaf(d * d, rows, o.y);
     }
     sq = team_sum(sq, of);
     if (lane == 0)
@@ -315,33 +317,17 @@ __global__ __launch_bounds__(kThreads) void norm_sums_kernel(NormArgs a) {
       }
     });
   }
-  int top = 1;
-  while (top < t.rw) top <<= 1;
-  for (int half = top; half >= 1; half >>= 1) {
-    __syncthreads();
-    if (t.live && t.row >= half && t.row < 2 * half)
-#pragma unroll
-      for (int e = 0; e < V; ++e) lds[((t.row - half) * (a.plan.cw / V) + t.col) * V + e] = make_float2(dw[e], db[e]);
-    __syncthreads();
-    if (t.live && t.row < half && t.row + half < t.rw)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float2 o = lds[(t.row * (a.plan.cw / V) + t.col) * V + e];
-        dw[e] += o.x;
-        db[e] += o.y;
-      }
-  }
-  __syncthreads();
-  if (t.live && t.row == 0) {
-    float2* to = (float2*)a.chan + ((int64_t)t.n * a.plan.tiles + t.tile) * a.c + t.c0 + t.col * V;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float w = param(a.weight, a.param_f32, a.dtype, t.c0 + t.col * V + e, 1.f);
-      to[e] = make_float2(dw[e], db[e]);
-      lds[t.col * V + e] = make_float2(dw[e] * w, db[e] * w);
+  float2* to = (float2*)a.chan + ((int64_t)t.n * a.plan.tiles + t.tile) * a.c + t.c0;
+  add_rows<V>(a, t, dw, db, lds, [&](int c, const float2* at, int ld) {
+    float2 o = at[0];
+    for (int r = 1; r < t.rw; ++r) {
+      o.x += at[r * ld].x;
+      o.y += at[r * ld].y;
     }
-  }
-  __syncthreads();
+    const float w = param(a.weight, a.param_f32, a.dtype, t.c0 + c, 1.f);
+    to[c] = o;
+    lds[c] = make_float2(o.x * w, o.y * w);
+  });
   each_group(a, t, [&](int g, int lane, int of, int cg) {
     float s1 = 0.f, s2 = 0.f;
     for (int c = lane; c < cg; c += of) {

@@ -41,15 +41,6 @@ __device__ __forceinline__ float team_sum(float v, int team) {
   return v;
 }
 
-// Joins the count, mean and sum of squares about the mean of two sets.
-__device__ __forceinline__ void join(float& n, float& m, float& s, float nb, float mb, float sb) {
-  if (nb == 0.f) return;
-  const float all = n + nb, d = mb - m, w = nb / all;
-  m = fmaf(d, w, m);
-  s = s + sb + d * d * (n * w);
-  n = all;
-}
-
 template <int N>
 struct Int {
   static constexpr int value = N;
