@@ -30,7 +30,9 @@
  * pass it may reach all rows of its sequence within its 64 rows.
  *
  * Ownership, streams, workspaces and errors are those of convseq.h.  B = 0 and
- * T = 0 are valid: the state passes through.
+ * T = 0 are valid: the state passes through.  CONVFWD_ERR_TOO_LARGE: Hv * Dv of
+ * 2^23 elements, Dv of 2^22, a row stride of v or dy of 2^23, or more, T of 2^30,
+ * or 2^23 workgroups of a launch (heads times 64 rows, heads times 16 columns).
  */
 #ifndef CONVDELTA_H
 #define CONVDELTA_H

@@ -147,3 +147,15 @@ def test_the_binding_refuses_what_does_not_fit():
             (ValueError, lambda: igc.delta_rule_step(*one, h, slots=torch.zeros(3, dtype=torch.int32, device=dev)))):
         with pytest.raises(error):
             call()
+
+
+def test_rows_that_are_too_far_apart():
+    """Offsets of 64 rows have to fit 32 bits: v, dy and y are refused where they would not."""
+    far = _heads(1 << 40, 4, row=1 << 23, batch=0)
+    near = _heads(1 << 40, 4, row=(1 << 23) - 1, batch=0)
+    assert _fwd(_desc(), v=far) == LARGE
+    assert _bwd(_desc(), v=far) == LARGE and _bwd(_desc(), dy=far) == LARGE
+    assert _fwd(_desc(), v=near, beta=None) == NULL and _fwd(_desc(dv=1 << 22)) == LARGE
+    lib = dl._delta()
+    assert lib.convdelta_fwd_workspace(_desc(b=1, t=1, hk=1, hv=8, dv=1 << 20)) == LARGE
+    assert lib.convdelta_fwd_workspace(_desc(b=1, t=1, hk=1, hv=8, dv=(1 << 20) - 1)) > 0
