@@ -1,5 +1,5 @@
 // delta_bwd.h -- gated delta rule, the backward recurrence: a workgroup carries 16
-// columns of the gradient of one head's state back through the chunks.  With dS the
+// or 32 columns of the gradient of one head's state back through the chunks.  With dS the
 // gradient of the state after a chunk and dy that of y,
 //
 //   du = leave * (k dS) + scale * R^T dy,  z = du + H^T (beta du)
@@ -19,27 +19,26 @@ namespace {
 
 constexpr int kReadLd = kChunk + 4;  // spreads the columns over the banks
 
-template <typename T, int DK>
+template <typename T, int DK, int NC>
 struct BwdLds {
-  typedef Team<T, DK> F;
+  typedef Team<T, DK, NC> F;
   __bf16 k[F::NP * RowsAt<DK>::part], q[F::NP * RowsAt<DK>::part];
-  __bf16 state[kParts * F::State::part];
-  __bf16 dy[2][F::NP * F::Rows::part];  // of the chunk, and of the one it goes on to
-  float ry[16 * kReadLd];               // scale * R^T dy by columns
-  __bf16 bd[kParts * F::Rows::part], in[kParts * F::Rows::part], out[kParts * F::Rows::part];
+  __bf16 state[NC][kParts * F::State::part];
+  __bf16 dy[2][NC][F::NP * F::Rows::part];  // of the chunk, and of the one it goes on to
+  float ry[NC][16 * kReadLd];               // scale * R^T dy by columns
+  __bf16 bd[NC][kParts * F::Rows::part], in[NC][kParts * F::Rows::part], out[NC][kParts * F::Rows::part];
   float step[kChunk];
   int bad[2];
 };
 
-template <typename T, int DK, bool FIRST>
-struct Backward : Team<T, DK> {
-  typedef Team<T, DK> F;
-  typedef BwdLds<T, DK> Lds;
+template <typename T, int DK, int NC, bool FIRST>
+struct Backward : Team<T, DK, NC> {
+  typedef Team<T, DK, NC> F;
+  typedef BwdLds<T, DK, NC> Lds;
   using F::a;
   using F::q4;
   using F::m;
   using F::wave;
-  using F::col;
   using F::row;
   static constexpr int NP = F::NP, KS = F::KS;
   typedef typename F::Rows Rows;
@@ -49,11 +48,11 @@ struct Backward : Team<T, DK> {
     Parts<kParts> mat[2];  // of H^T, or the next chunk's R^T
     f32x4_t enter, leave, beta;
     float stay;
-    T dy[4];               // second role, the next chunk's
+    T dy[NC][4];           // second role, the next chunk's
   };
 
   Lds& s;
-  f32x4_t state;
+  f32x4_t state[NC];
   int turn = 0;
 
   __device__ __forceinline__ Backward(const DeltaArgs& a_, Lds& s_, int bh_, int cb) : F(a_, bh_, cb), s(s_) {}
@@ -67,28 +66,33 @@ struct Backward : Team<T, DK> {
     x.stay = F::load_stay(c);
   }
   // dy of chunk c into LDS (second role)
-  __device__ __forceinline__ f32x4_t put_dy(int c, const Chunk& x) const {
-    f32x4_t d;
+  __device__ __forceinline__ void put_dy(int c, const Chunk& x, f32x4_t (&d)[NC]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = c * kChunk + row() + i < a.t ? to_f32(x.dy[i]) : 0.f;
-    F::template put<NP, Rows>(s.dy[c & 1], row(), d);
-    return d;
+    for (int n = 0; n < NC; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[n][i] = c * kChunk + row() + i < a.t ? to_f32(x.dy[n][i]) : 0.f;
+      F::template put<NP, Rows>(s.dy[c & 1][n], row(), d[n]);
+    }
   }
   // scale * R^T dy of chunk c (second role), from the rows [lo, hi) where masked
   __device__ __forceinline__ void put_read(int c, const Parts<kParts> (&read)[2], bool masked, int lo, int hi) const {
-    f32x4_t ry = {0.f, 0.f, 0.f, 0.f}, more = ry;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (F::template has<true>(k)) {
-        Parts<NP> d = F::template get<NP, Rows>(s.dy[c & 1], k);
-        if (masked) keep(d, 32 * k + 8 * q4, lo, hi);
-        (k ? more : ry) = mma(read[k], d, k ? more : ry);
-      }
-    *(f32x4_t*)(s.ry + m * kReadLd + row()) = a.scale * (ry + more);
+    for (int n = 0; n < NC; ++n) {
+      f32x4_t ry = {0.f, 0.f, 0.f, 0.f}, more = ry;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (F::template has<true>(k)) {
+          Parts<NP> d = F::template get<NP, Rows>(s.dy[c & 1][n], k);
+          if (masked) keep(d, 32 * k + 8 * q4, lo, hi);
+          (k ? more : ry) = mma(read[k], d, k ? more : ry);
+        }
+      *(f32x4_t*)(s.ry[n] + m * kReadLd + row()) = a.scale * (ry + more);
+    }
   }
 
   // (1) and (2) for all rows, or (masked) the rows [lo, hi) of one sequence, into z; kd is k dS.
-  __device__ __forceinline__ void solve(int c, Chunk& x, const f32x4_t& kd, bool masked, int lo, int hi, f32x4_t& z) {
+  __device__ __forceinline__ void solve(int c, Chunk& x, const f32x4_t (&kd)[NC], bool masked, int lo, int hi,
+                                        f32x4_t (&z)[NC]) {
     if (masked) {
       __syncthreads();  // what is read of the sequence before
       if (FIRST) {
@@ -105,64 +109,77 @@ struct Backward : Team<T, DK> {
       wait_for_memory();
       __syncthreads();
     }
-    f32x4_t du, more;
-    if (FIRST) {
-      f32x4_t bd;
-      const f32x4_t ry = *(const f32x4_t*)(s.ry + m * kReadLd + row());
+    f32x4_t du[NC], more[NC];
+    if (FIRST)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool out = row() + i < lo || row() + i >= hi;
-        du[i] = out ? 0.f : times(x.leave[i], kd[i]) + ry[i];
-        bd[i] = out ? 0.f : x.beta[i] * du[i];
+      for (int n = 0; n < NC; ++n) {
+        f32x4_t bd;
+        const f32x4_t ry = *(const f32x4_t*)(s.ry[n] + m * kReadLd + row());
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool out = row() + i < lo || row() + i >= hi;
+          du[n][i] = out ? 0.f : times(x.leave[i], kd[n][i]) + ry[i];
+          bd[i] = out ? 0.f : x.beta[i] * du[n][i];
+        }
+        F::template put<kParts, Rows>(s.bd[n], row(), bd);
+        more[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
-      F::template put<kParts, Rows>(s.bd, row(), bd);
-    }
     __syncthreads();
-    F::renew();
     if (FIRST) {
-      more = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        if (F::template has<true>(k)) {
-          const auto bp = F::template get<kParts, Rows>(s.bd, k);
-          (k ? more : du) = mma(x.mat[k], bp, k ? more : du);
-        }
+        if (F::template has<true>(k))
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (row() + i >= lo && row() + i < hi) z[i] = du[i] + more[i];
+          for (int n = 0; n < NC; ++n) {
+            const auto bp = F::template get<kParts, Rows>(s.bd[n], k);
+            (k ? more : du)[n] = mma(x.mat[k], bp, (k ? more : du)[n]);
+          }
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row() + i >= lo && row() + i < hi) z[n][i] = du[n][i] + more[n][i];
     }
   }
 
-  __device__ __forceinline__ void chunk(int c, Chunk& x, f32x4_t& dy) {
+  __device__ __forceinline__ void chunk(int c, Chunk& x, f32x4_t (&dy)[NC]) {
     const int next = max(c - 1, 0), then = max(c - 2, 0);
     __syncthreads();  // the state's parts and dy are there
-    F::renew();
     F::put_rows(FIRST ? s.k : s.q, x.rows);
-    f32x4_t kd = {0.f, 0.f, 0.f, 0.f};
+    f32x4_t kd[NC];
     if (FIRST) {
-      f32x4_t more = kd;
+      f32x4_t more[NC];
+#pragma unroll
+      for (int n = 0; n < NC; ++n) kd[n] = more[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const auto sp = F::template get<kParts, typename F::State>(s.state, k);
-        (k & 1 ? more : kd) = mma(F::rows_of(x.rows, k), sp, k & 1 ? more : kd);
-      }
-      kd += more;
-    } else {
-      f32x4_t in;
+        const Parts<NP> rows = F::rows_of(x.rows, k);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) in[i] = times(x.enter[i], a.scale * dy[i]);
-      F::template put<kParts, Rows>(s.in, row(), in);
+        for (int n = 0; n < NC; ++n) {
+          f32x4_t& to = (k & 1 ? more : kd)[n];
+          to = mma(rows, F::template get<kParts, typename F::State>(s.state[n], k), to);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NC; ++n) kd[n] += more[n];
+    } else {
+#pragma unroll
+      for (int n = 0; n < NC; ++n) {
+        f32x4_t in;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) in[i] = times(x.enter[i], a.scale * dy[n][i]);
+        F::template put<kParts, Rows>(s.in[n], row(), in);
+      }
     }
-    F::renew();
     F::load_rows(FIRST ? a.k : a.q, next, x.rows);
-    f32x4_t ahead;
+    f32x4_t ahead[NC];
     if (!FIRST) {
-      ahead = put_dy(next, x);
+      put_dy(next, x, ahead);
       F::load_col(a.dy, then, x.dy);
     }
     // All rows at once, and where something is not finite once more, each sequence by itself, so that nothing crosses a
     // start.  `first`: the rows that the state before the chunk reaches are those of the first sequence.
-    f32x4_t z;
+    f32x4_t z[NC];
     bool masked = false;
     int first = kChunk;
 #pragma clang loop unroll(disable)
@@ -181,14 +198,17 @@ struct Backward : Team<T, DK> {
       } while (hi > 0);
       if (FIRST) {
         float test = 0.f;
-        f32x4_t out;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          test = fmaf(z[i], 0.f, test);
-          if (c * kChunk + row() + i >= a.t) z[i] = 0.f;  // rows past T hold nothing, whatever the state's gradient is
-          out[i] = -times(x.enter[i], x.beta[i] * z[i]);
+        for (int n = 0; n < NC; ++n) {
+          f32x4_t out;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            test = fmaf(z[n][i], 0.f, test);
+            if (c * kChunk + row() + i >= a.t) z[n][i] = 0.f;  // rows past T hold nothing, whatever the state's gradient is
+            out[i] = -times(x.enter[i], x.beta[i] * z[n][i]);
+          }
+          F::template put<kParts, Rows>(s.out[n], row(), out);
         }
-        F::template put<kParts, Rows>(s.out, row(), out);
         if (__any(test != 0.f)) s.bad[turn & 1] = 1;  // NaN
       }
       __syncthreads();
@@ -201,7 +221,6 @@ struct Backward : Team<T, DK> {
       wait_for_memory();
       __syncthreads();
     }
-    F::renew();
     if (FIRST) {
       fetch_matrix(next, x.mat);
     } else {
@@ -210,37 +229,50 @@ struct Backward : Team<T, DK> {
     }
     // (3), from the rows [0, first) where masked
     if (F::has_tile()) {
-      f32x4_t n, more = {0.f, 0.f, 0.f, 0.f};
+      f32x4_t more[NC];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n[i] = times(x.stay, state[i]);
+      for (int n = 0; n < NC; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) state[n][i] = times(x.stay, state[n][i]);
+        more[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const auto ip = F::template get<kParts, Rows>(s.in, k), op = F::template get<kParts, Rows>(s.out, k);
         Parts<NP> qt = F::cols_of(s.q, F::tile, k), kt = F::cols_of(s.k, F::tile, k);
         if (masked) keep(qt, 32 * k + 8 * q4, 0, first), keep(kt, 32 * k + 8 * q4, 0, first);
-        n = mma(qt, ip, n);
-        more = mma(kt, op, more);
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          state[n] = mma(qt, F::template get<kParts, Rows>(s.in[n], k), state[n]);
+          more[n] = mma(kt, F::template get<kParts, Rows>(s.out[n], k), more[n]);
+        }
       }
-      state = n + more;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) state[n] += more[n];
       F::put_state(s.state, state);
     }
     // stores come after the loads of the next chunk (see delta_fwd.h)
     if (FIRST) {
       const Range zs(a.w.z + chunk_index(a, F::bh, c) * kChunk * a.dvp, (int64_t)kChunk * a.dvp * 4);
-      const uint32_t at = col < a.dvp ? (uint32_t)(row() * a.dvp + col) * 4u : kNowhere;
-      f32x4_t dx;
+      f32x4_t dx[NC];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        dx[i] = x.beta[i] * z[i];
-        z[i] = F::live ? z[i] : 0.f;
-      }
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dx[n][i] = x.beta[i] * z[n][i];
+          if (F::col(n) >= a.dv) z[n][i] = 0.f;
+        }
       fetch_gates(next, x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) zs.store(at + (uint32_t)(i * a.dvp) * 4u, z[i]);
+      for (int n = 0; n < NC; ++n) {
+        const uint32_t at = F::col(n) < a.dvp ? (uint32_t)(row() * a.dvp + F::col(n)) * 4u : kNowhere;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) zs.store(at + (uint32_t)(i * a.dvp) * 4u, z[n][i]);
+      }
       F::template store_col<T>(a.dv_, c, dx);
     } else {
       fetch_gates(next, x);
-      dy = ahead;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) dy[n] = ahead[n];
     }
     keep_state(c - 1);
   }
@@ -251,15 +283,15 @@ struct Backward : Team<T, DK> {
 
   __device__ __forceinline__ void run() {
     const int64_t size = (int64_t)a.dk * a.dv;
-    state = F::load_state(a.dh_last ? a.dh_last + F::bh * size : nullptr);
+    F::load_state(a.dh_last ? a.dh_last + F::bh * size : nullptr, state);
     F::put_state(s.state, state);
     if (a.chunks > 0) {
       Chunk x;
       const int last = a.chunks - 1, next = max(last - 1, 0);
-      f32x4_t dy;
+      f32x4_t dy[NC];
       if (!FIRST) {
         F::load_col(a.dy, last, x.dy);
-        dy = put_dy(last, x);
+        put_dy(last, x, dy);
       }
       fetch_matrix(last, x.mat);
       __syncthreads();
@@ -277,16 +309,16 @@ struct Backward : Team<T, DK> {
   }
 };
 
-template <typename T, int DK>
+template <typename T, int DK, int NC>
 __global__ __launch_bounds__(kTeam, 2) void delta_bwd_kernel(DeltaArgs a, int blocks) {
-  __shared__ __attribute__((aligned(16))) BwdLds<T, DK> s;
+  __shared__ __attribute__((aligned(16))) BwdLds<T, DK, NC> s;
   int bh, cb;
   if (!head_of(a.b * a.hv, blocks, bh, cb)) return;
   if (threadIdx.x < 2) s.bad[threadIdx.x] = 0;
   if (wave_id() < 4)
-    Backward<T, DK, true>(a, s, bh, cb).run();
+    Backward<T, DK, NC, true>(a, s, bh, cb).run();
   else
-    Backward<T, DK, false>(a, s, bh, cb).run();
+    Backward<T, DK, NC, false>(a, s, bh, cb).run();
 }
 
 }  // namespace
@@ -294,10 +326,14 @@ __global__ __launch_bounds__(kTeam, 2) void delta_bwd_kernel(DeltaArgs a, int bl
 template <typename T>
 hipError_t delta_bwd_of(const DeltaArgs& a, hipStream_t s) {
   return for_dk(a.dk, [&](auto dk) {
-    const int blocks = a.dvp / 16;
-    hipLaunchKernelGGL((delta_bwd_kernel<T, decltype(dk)::value>), dim3((a.b * a.hv + 7) / 8 * 8 * blocks), dim3(kTeam), 0, s, a,
-                       blocks);
-    return hipGetLastError();
+    constexpr int DK = decltype(dk)::value;
+    return for_columns(a, [&](auto nc) {
+      // two tiles need more LDS than there is with the widest heads in fp32 and fp16
+      constexpr int NC = sizeof(BwdLds<T, DK, decltype(nc)::value>) <= 160 * 1024 ? decltype(nc)::value : 1;
+      const int blocks = a.dvp / (16 * NC);
+      hipLaunchKernelGGL((delta_bwd_kernel<T, DK, NC>), dim3((a.b * a.hv + 7) / 8 * 8 * blocks), dim3(kTeam), 0, s, a, blocks);
+      return hipGetLastError();
+    });
   });
 }
 

@@ -273,4 +273,11 @@ inline hipError_t for_dk(int dk, const F& f) {
   return f(Int<128>{});
 }
 
+// The recurrences' columns a workgroup, in tiles of 16: one where the workgroups are then no more than the 256 CUs, and
+// two, which read q, k and the chunks' matrices once for both, where they are more.
+template <typename F>
+inline hipError_t for_columns(const DeltaArgs& a, const F& f) {
+  return (int64_t)a.b * a.hv * ((a.dv + 15) / 16) > 256 ? f(Int<2>{}) : f(Int<1>{});
+}
+
 }  // namespace convdelta

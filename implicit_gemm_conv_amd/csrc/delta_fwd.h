@@ -1,4 +1,4 @@
-// delta_fwd.h -- gated delta rule forward: a workgroup carries 16 columns of one
+// delta_fwd.h -- gated delta rule forward: a workgroup carries 16 or 32 columns of one
 // head's state through the chunks.  Included by one source for each type.
 //
 // A chunk takes three steps between barriers: (1) k S and r; (2) x = r + H (beta r), u;
@@ -12,28 +12,25 @@ namespace convdelta {
 
 namespace {
 
-template <typename T, int DK>
+template <typename T, int DK, int NC>
 struct FwdLds {
-  typedef Team<T, DK> F;
+  typedef Team<T, DK, NC> F;
   __bf16 k[F::NP * RowsAt<DK>::part];
-  __bf16 state[kParts * F::State::part];
-  __bf16 br[kParts * F::Rows::part], u[kParts * F::Rows::part], out[2][F::YP * F::Rows::part];
+  __bf16 state[NC][kParts * F::State::part];
+  __bf16 br[NC][kParts * F::Rows::part], u[NC][kParts * F::Rows::part], out[2][NC][F::YP * F::Rows::part];
   int bad[2];
 };
 
-template <typename T, int DK, bool FIRST, bool TRAIN>
-struct Forward : Team<T, DK> {
-  typedef Team<T, DK> F;
-  typedef FwdLds<T, DK> Lds;
+template <typename T, int DK, int NC, bool FIRST, bool TRAIN>
+struct Forward : Team<T, DK, NC> {
+  typedef Team<T, DK, NC> F;
+  typedef FwdLds<T, DK, NC> Lds;
   using F::a;
   using F::q4;
   using F::m;
   using F::wave;
   using F::row;
   static constexpr int NP = F::NP, KS = F::KS, YP = F::YP;
-  // With the states' stores two workgroups a CU are faster (4x4096, 16 heads, bf16: 0.39 ms for 0.42), without them one
-  // that loads ahead (1x16387: 0.54 ms for 0.66).
-  static constexpr bool SHARE = TRAIN && 2 * sizeof(Lds) <= 160 * 1024;
   typedef typename F::Rows Rows;
 
   // what a chunk needs
@@ -42,11 +39,11 @@ struct Forward : Team<T, DK> {
     Parts<FIRST ? kParts : YP> mat[2];  // of H; of the decayed q k^T of the chunk whose y is next
     f32x4_t enter, leave, beta;
     float stay;
-    T v[4];
+    T v[NC][4];
   };
 
   Lds& s;
-  f32x4_t state, read;
+  f32x4_t state[NC], read[NC];
   int turn = 0, was = 0, was_first = 0, was_end = 0;  // the chunk whose y is to be finished
 
   __device__ __forceinline__ Forward(const DeltaArgs& a_, Lds& s_, int bh_, int cb) : F(a_, bh_, cb), s(s_) {}
@@ -69,17 +66,24 @@ struct Forward : Team<T, DK> {
 
   // y of the chunk before, of its rows [first, end): what q S was is in `read`, u in LDS.
   __device__ __forceinline__ void finish(int c, const Chunk& x, int first, int end) const {
-    f32x4_t y = read, more = {0.f, 0.f, 0.f, 0.f};
+    f32x4_t y[NC], more[NC];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) y[n] = read[n], more[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       if (F::template has<false>(k)) {
         Parts<YP> mat = x.mat[k];
         if (end - first < kChunk) keep(mat, 32 * k + 8 * q4, first, end);
-        const auto op = F::template get<YP, Rows>(s.out[~turn & 1], k);
-        (k ? more : y) = mma_first<YP>(mat, op, k ? more : y);
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          const auto op = F::template get<YP, Rows>(s.out[~turn & 1][n], k);
+          (k ? more : y)[n] = mma_first<YP>(mat, op, (k ? more : y)[n]);
+        }
       }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = a.scale * (y[i] + more[i]);
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[n][i] = a.scale * (y[n][i] + more[n][i]);
     F::template store_col<T>(a.y, c, y, first, end);
   }
 
@@ -101,44 +105,48 @@ struct Forward : Team<T, DK> {
       wait_for_memory();
     }
     __syncthreads();  // the state's parts are there
-    if (SHARE) F::renew();
     if (FIRST) F::put_rows(s.k, x.rows);
-    f32x4_t xs = zero, more = zero;  // k S, or q S; then r, x
+    f32x4_t xs[NC], more[NC];  // k S, or q S; then r, x
     const auto times_state = [&] {
 #pragma unroll
+      for (int n = 0; n < NC; ++n) xs[n] = more[n] = zero;
+#pragma unroll
       for (int k = 0; k < KS; ++k) {
-        const auto sp = F::template get<kParts, typename F::State>(s.state, k);
-        if (FIRST)
-          (k & 1 ? more : xs) = mma(F::rows_of(x.rows, k), sp, k & 1 ? more : xs);
-        else
-          (k & 1 ? more : xs) = mma_first<YP>(F::rows_of(x.rows, k), sp, k & 1 ? more : xs);
+        const Parts<NP> rows = F::rows_of(x.rows, k);
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          f32x4_t& to = (k & 1 ? more : xs)[n];
+          const auto sp = F::template get<kParts, typename F::State>(s.state[n], k);
+          to = FIRST ? mma(rows, sp, to) : mma_first<YP>(rows, sp, to);
+        }
       }
-      xs += more;
       f32x4_t enter = x.enter;
       if (alone) {
         enter = F::load_gate(3, c);
         x.stay = a.w.rows[(chunk_index(a, F::bh, c) * 4 + 3) * kChunk + only];
         wait_for_memory();
-        // a state that is not finite, behind a start (with all rows such a chunk comes to nothing)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (enter[i] == 0.f) xs[i] = 0.f;
-          if (x.stay == 0.f) state[i] = 0.f;
-        }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xs[i] *= enter[i];
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // alone: a state that is not finite, behind a start (with all rows such a chunk comes to nothing)
+          xs[n][i] = alone && enter[i] == 0.f ? 0.f : enter[i] * (xs[n][i] + more[n][i]);
+          if (alone && x.stay == 0.f) state[n][i] = 0.f;
+        }
     };
-    f32x4_t u, lu;
+    f32x4_t u[NC], lu;
     if constexpr (FIRST) {
       times_state();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        xs[i] = to_f32(x.v[i]) - xs[i];
-        u[i] = alone && row() + i != only ? 0.f : x.beta[i] * xs[i];
+      for (int n = 0; n < NC; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          xs[n][i] = to_f32(x.v[n][i]) - xs[n][i];
+          u[n][i] = alone && row() + i != only ? 0.f : x.beta[i] * xs[n][i];
+        }
+        F::template put<kParts, Rows>(s.br[n], row(), u[n]);
       }
-      F::template put<kParts, Rows>(s.br, row(), u);
-      if (SHARE) F::renew();
       used();
       x.enter = F::load_gate(0, next);
       fetch_rows(next, x);
@@ -148,52 +156,55 @@ struct Forward : Team<T, DK> {
       fetch_matrix(c, x);
     }
     __syncthreads();
-    if (SHARE) F::renew();
     if (FIRST) {
       if (!alone) {
-        more = zero;
+#pragma unroll
+        for (int n = 0; n < NC; ++n) more[n] = zero;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          if (F::template has<false>(k)) {
-            const auto bp = F::template get<kParts, Rows>(s.br, k);
-            (k ? more : xs) = mma(x.mat[k], bp, k ? more : xs);
-          }
-        xs += more;
+          if (F::template has<false>(k))
 #pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = x.beta[i] * xs[i];
+            for (int n = 0; n < NC; ++n) {
+              const auto bp = F::template get<kParts, Rows>(s.br[n], k);
+              (k ? more : xs)[n] = mma(x.mat[k], bp, (k ? more : xs)[n]);
+            }
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          xs[n] += more[n];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[n][i] = x.beta[i] * xs[n][i];
+        }
       }
       float test = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lu[i] = x.leave[i] * u[i];
-        test = fmaf(u[i], 0.f, test);
+      for (int n = 0; n < NC; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lu[i] = x.leave[i] * u[n][i];
+          test = fmaf(u[n][i], 0.f, test);
+        }
+        F::template put<kParts, Rows>(s.u[n], row(), lu);
+        F::template put<YP, Rows>(s.out[turn & 1][n], row(), u[n]);
       }
-      F::template put<kParts, Rows>(s.u, row(), lu);
-      F::template put<YP, Rows>(s.out[turn & 1], row(), u);
       if (__any(test != 0.f)) s.bad[turn & 1] = 1;  // NaN
     } else {
       times_state();
-      read = xs;
+#pragma unroll
+      for (int n = 0; n < NC; ++n) read[n] = xs[n];
       used();
       x.enter = F::load_gate(0, next);
       fetch_rows(next, x);
     }
-    // As early as possible: what the state's step has of k, and all that is left to load for the next chunk.  Where two
-    // workgroups are to share a CU, which takes 128 registers, it has to wait until it is used.
+    // what the state's step has of k, which is there already, and all that is left to load
     Parts<NP> kt[2];
-    const auto get_kt = [&] {
+    if (F::has_tile())
 #pragma unroll
       for (int k = 0; k < 2; ++k) kt[k] = F::cols_of(s.k, F::tile, k);
-    };
     const float stay = x.stay;
-    if (!SHARE) {
-      if (F::has_tile()) get_kt();
-      used();
-      fetch_gates(next, x);
-    }
+    used();
+    fetch_gates(next, x);
     if (FIRST) fetch_matrix(next, x);
     __syncthreads();
-    if (SHARE) F::renew();
     const bool bad = s.bad[turn & 1];
     // the other flag: read before the last barrier, set after the next one but one
     if (threadIdx.x == 0) s.bad[~turn & 1] = 0;
@@ -205,22 +216,25 @@ struct Forward : Team<T, DK> {
     was_end = alone ? only + 1 : kChunk;
     // the state moves on
     if (F::has_tile()) {
-      f32x4_t n;
-      if (SHARE) get_kt();
-      more = zero;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) n[i] = stay * state[i];
+      for (int n = 0; n < NC; ++n) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const auto up = F::template get<kParts, Rows>(s.u, k);
-        (k ? more : n) = mma(kt[k], up, k ? more : n);
+        for (int i = 0; i < 4; ++i) state[n][i] *= stay;
+        more[n] = zero;
       }
-      state = n + more;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+          const auto up = F::template get<kParts, Rows>(s.u[n], k);
+          (k ? more : state)[n] = mma(kt[k], up, (k ? more : state)[n]);
+        }
+#pragma unroll
+      for (int n = 0; n < NC; ++n) state[n] += more[n];
       F::put_state(s.state, state);
     }
     // Stores come after the loads of the next chunk: waits for memory are counted in the order of issue, and a load
     // issued after a store would be waited for together with it.
-    if (SHARE) fetch_gates(next, x);
     if (FIRST && TRAIN) F::template store_col<float>(a.x, c, xs, was_first, was_end);
     return true;
   }
@@ -242,13 +256,14 @@ struct Forward : Team<T, DK> {
   // (Both roles take the same turns: they wait for each other at every barrier.)
   __device__ __forceinline__ void run() {
     const int64_t size = (int64_t)a.dk * a.dv;
-    state = F::load_state(a.h0 ? a.h0 + F::bh * size : nullptr);
+    F::load_state(a.h0 ? a.h0 + F::bh * size : nullptr, state);
     F::put_state(s.state, state);
     if (a.chunks > 0) {
       Chunk x;
       fetch(0, x);
       if (!FIRST) fetch_matrix(0, x);
-      read = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int n = 0; n < NC; ++n) read[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       bool alone = false;
       int c = 0, only = 0;
       keep_state(0);
@@ -276,16 +291,16 @@ struct Forward : Team<T, DK> {
   }
 };
 
-template <typename T, int DK, bool TRAIN>
+template <typename T, int DK, int NC, bool TRAIN>
 __global__ __launch_bounds__(kTeam, 2) void delta_fwd_kernel(DeltaArgs a, int blocks) {
-  __shared__ __attribute__((aligned(16))) FwdLds<T, DK> s;
+  __shared__ __attribute__((aligned(16))) FwdLds<T, DK, NC> s;
   int bh, cb;
   if (!head_of(a.b * a.hv, blocks, bh, cb)) return;
   if (threadIdx.x < 2) s.bad[threadIdx.x] = 0;
   if (wave_id() < 4)
-    Forward<T, DK, true, TRAIN>(a, s, bh, cb).run();
+    Forward<T, DK, NC, true, TRAIN>(a, s, bh, cb).run();
   else
-    Forward<T, DK, false, TRAIN>(a, s, bh, cb).run();
+    Forward<T, DK, NC, false, TRAIN>(a, s, bh, cb).run();
 }
 
 }  // namespace
@@ -293,11 +308,14 @@ __global__ __launch_bounds__(kTeam, 2) void delta_fwd_kernel(DeltaArgs a, int bl
 template <typename T>
 hipError_t delta_fwd_of(const DeltaArgs& a, hipStream_t s) {
   return for_dk(a.dk, [&](auto dk) {
-    const int blocks = (a.dv + 15) / 16;
     constexpr int DK = decltype(dk)::value;
-    hipLaunchKernelGGL((a.states ? delta_fwd_kernel<T, DK, true> : delta_fwd_kernel<T, DK, false>),
-                       dim3((a.b * a.hv + 7) / 8 * 8 * blocks), dim3(kTeam), 0, s, a, blocks);
-    return hipGetLastError();
+    return for_columns(a, [&](auto nc) {
+      constexpr int NC = InParts<T>::n == 3 && DK == 128 ? 1 : decltype(nc)::value;  // two would need more registers
+      const int blocks = (a.dv + 16 * NC - 1) / (16 * NC);
+      hipLaunchKernelGGL((a.states ? delta_fwd_kernel<T, DK, NC, true> : delta_fwd_kernel<T, DK, NC, false>),
+                         dim3((a.b * a.hv + 7) / 8 * 8 * blocks), dim3(kTeam), 0, s, a, blocks);
+      return hipGetLastError();
+    });
   });
 }
 

@@ -29,7 +29,7 @@ constexpr int kT = 512, kCols = 32, kSlice = kCols + 8, kLdM = kChunk + 8;
 
 template <typename T, int DK>
 struct GradLds {
-  typedef Team<T, DK> F;
+  typedef Team<T, DK, 1> F;
   static constexpr int NP = F::NP, GP = F::YP;
   union {
     struct {
@@ -48,7 +48,7 @@ struct GradLds {
 
 template <typename T, int DK, bool WHOLE>
 struct Grad {
-  typedef Team<T, DK> F;
+  typedef Team<T, DK, 1> F;
   typedef GradLds<T, DK> Lds;
   static constexpr int NP = F::NP, GP = F::YP, DT = DK / 32;  // DT: 16-row tiles of a half of dq's columns
   static constexpr int each = DK * kCols / 4 / kT;                          // pieces of 4 floats of a slice a thread

@@ -15,7 +15,8 @@ struct ColsAt {
   static constexpr int ld = LEN + 8, part = 16 * ld;
 };
 
-template <typename T, int DK>
+// A workgroup's columns: NC tiles of 16.
+template <typename T, int DK, int NC>
 struct Team {
   static constexpr int NP = InParts<T>::n, KS = DK / 32, DT = DK / 16;
   static constexpr int YP = NP == 3 ? 3 : 2;                // parts that an output of type T can tell apart
@@ -23,48 +24,42 @@ struct Team {
   typedef ColsAt<kChunk> Rows;
 
   const DeltaArgs& a;
-  int wave, tile, m, q4, lane, b, h, hk, bh, block, col;  // tile: the wave's 16 rows of the state, where it is below DT
-  bool live;
+  int wave, tile, m, q4, lane, b, h, hk, bh, block;  // tile: the wave's 16 rows of the state, where it is below DT
 
-  __device__ __forceinline__ Team(const DeltaArgs& a_, int bh_, int cb) : a(a_), bh(bh_) {
+  __device__ __forceinline__ Team(const DeltaArgs& a_, int bh_, int cb) : a(a_), bh(bh_), block(cb * 16 * NC) {
+    lane = threadIdx.x % 64;
     wave = wave_id() % 4;
     // the second role has less to do before the state: with few tiles it takes them
     tile = DT == 8 ? wave_id() : wave_id() - 4;
-    block = cb * 16;
+    m = lane % 16;
+    q4 = lane / 16;
     b = bh / a.hv;
     h = bh % a.hv;
     hk = h / (a.hv / a.hk);
-    renew();
   }
-  // Where the lane stands, as something new: what the compiler makes of it (addresses, mostly) is made again
-  // where it is needed next, and not held in registers, or spilled, from the kernel's start on.
-  __device__ __forceinline__ void renew() {
-    lane = threadIdx.x % 64;
-    asm volatile("" : "+v"(lane));
-    m = lane % 16;
-    q4 = lane / 16;
-    col = block + m;
-    live = col < a.dv;
-  }
+  __device__ __forceinline__ int col(int n) const { return block + 16 * n + m; }  // the lane's column of tile n
   __device__ __forceinline__ int row() const { return 16 * wave + 4 * q4; }  // the first of the lane's four
   __device__ __forceinline__ bool has_tile() const { return tile >= 0 && tile < DT; }
 
-  // the lane's 4 values of a (Dk, Dv) state, zero outside
-  __device__ __forceinline__ f32x4_t load_state(const float* from) const {
-    f32x4_t s;
+  // the lane's 4 values a tile of a (Dk, Dv) state, zero outside
+  __device__ __forceinline__ void load_state(const float* from, f32x4_t (&s)[NC]) const {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int d = 16 * tile + 4 * q4 + r;
-      s[r] = from && live && has_tile() && d < a.dk ? from[(int64_t)d * a.dv + col] : 0.f;
-    }
-    return s;
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = 16 * tile + 4 * q4 + r;
+        s[n][r] = from && col(n) < a.dv && has_tile() && d < a.dk ? from[(int64_t)d * a.dv + col(n)] : 0.f;
+      }
   }
   // ... into a (Dk, ld) state of which the columns below `width` are there; nowhere if `to` is NULL
-  __device__ __forceinline__ void store_state(float* to, int ld, int width, const f32x4_t& s) const {
+  __device__ __forceinline__ void store_state(float* to, int ld, int width, const f32x4_t (&s)[NC]) const {
     const Range x(to, to ? (int64_t)a.dk * ld * 4 : 0);
-    const uint32_t at = col < width && has_tile() ? (uint32_t)((16 * tile + 4 * q4) * ld + col) * 4u : kNowhere;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) x.store(at + (uint32_t)(r * ld) * 4u, s[r]);
+    for (int n = 0; n < NC; ++n) {
+      const uint32_t at = col(n) < width && has_tile() ? (uint32_t)((16 * tile + 4 * q4) * ld + col(n)) * 4u : kNowhere;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x.store(at + (uint32_t)(r * ld) * 4u, s[n][r]);
+    }
   }
   // four neighbouring rows of the lane's column, as parts
   template <int N, typename AT>
@@ -80,8 +75,10 @@ struct Team {
 #pragma unroll
     for (int n = 0; n < N; ++n) *(bf164_t*)(cols + n * AT::part + m * AT::ld + at) = o[n];
   }
-  __device__ __forceinline__ void put_state(__bf16* cols, const f32x4_t& s) const {
-    if (has_tile()) put<kParts, State>(cols, 16 * tile + 4 * q4, s);
+  __device__ __forceinline__ void put_state(__bf16 (&cols)[NC][kParts * State::part], const f32x4_t (&s)[NC]) const {
+    if (!has_tile()) return;
+#pragma unroll
+    for (int n = 0; n < NC; ++n) put<kParts, State>(cols[n], 16 * tile + 4 * q4, s[n]);
   }
   // the operand of step k of a contraction over the state's rows, or over the chunk's
   template <int N, typename AT>
@@ -109,22 +106,29 @@ struct Team {
       for (int n = 0; n < NP; ++n) *(bf168_t*)(to + n * RowsAt<DK>::part + (16 * wave + m) * RowsAt<DK>::stride + 32 * k + 8 * q4) = p.p[n];
     }
   }
-  // the lane's four rows of its column of v or of y's gradient; zero past Dv (and past T, if rows do not overlap)
-  __device__ __forceinline__ void load_col(const Heads& x, int c, T (&to)[4]) const {
+  // the lane's four rows of its columns of v or of y's gradient; zero past Dv (and past T, if rows do not overlap)
+  __device__ __forceinline__ void load_col(const Heads& x, int c, T (&to)[NC][4]) const {
     const Range p = rows_range<T>(x, b, h, c * kChunk, a.t, a.dv);
-    const uint32_t ld = row_bytes<T>(x), at = live ? row() * ld + (uint32_t)col * (uint32_t)sizeof(T) : kNowhere;
+    const uint32_t ld = row_bytes<T>(x);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) to[r] = p.load<T>(at + r * ld);
+    for (int n = 0; n < NC; ++n) {
+      const uint32_t at = col(n) < a.dv ? row() * ld + (uint32_t)col(n) * (uint32_t)sizeof(T) : kNowhere;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) to[n][r] = p.load<T>(at + r * ld);
+    }
   }
-  // ... and of y, x or v's gradient, dense, rows past T left out; nowhere if `to` is NULL
+  // ... and of y, x or v's gradient, dense, rows past T left out
   template <typename E>
-  __device__ __forceinline__ void store_col(void* to, int c, const f32x4_t& v, int first = 0, int end = kChunk) const {
+  __device__ __forceinline__ void store_col(void* to, int c, const f32x4_t (&v)[NC], int first = 0, int end = kChunk) const {
     const uint32_t ld = (uint32_t)(a.hv * a.dv) * (uint32_t)sizeof(E);
     const Range p((E*)to + ((int64_t)b * a.t + c * kChunk) * (a.hv * a.dv) + (int64_t)h * a.dv,
-                  to ? (int64_t)min(kChunk, a.t - c * kChunk) * ld : 0);
-    const uint32_t at = live ? row() * ld + (uint32_t)col * (uint32_t)sizeof(E) : kNowhere;
+                  (int64_t)min(kChunk, a.t - c * kChunk) * ld);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) p.store(row() + r >= first && row() + r < end ? at + r * ld : kNowhere, from_f32<E>(v[r]));
+    for (int n = 0; n < NC; ++n) {
+      const uint32_t at = col(n) < a.dv ? row() * ld + (uint32_t)col(n) * (uint32_t)sizeof(E) : kNowhere;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) p.store(row() + r >= first && row() + r < end ? at + r * ld : kNowhere, from_f32<E>(v[n][r]));
+    }
   }
   __device__ __forceinline__ f32x4_t load_gate(int which, int c) const {
     return load_at<f32x4_t>(a.w.rows + (chunk_index(a, bh, c) * 4 + which) * kChunk, 4u * row());

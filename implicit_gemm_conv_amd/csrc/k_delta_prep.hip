@@ -116,7 +116,7 @@ struct PrepLds {
 template <typename T, int DK>
 __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backward) {
   constexpr int NP = InParts<T>::n, KS = DK / 32;
-  typedef Team<T, DK> F;
+  typedef Team<T, DK, 1> F;
   __shared__ __attribute__((aligned(16))) PrepLds<T, DK> s;
   const int c = blockIdx.x % a.chunks, t0 = c * kChunk;
   const F f(a, blockIdx.x / a.chunks, 0);

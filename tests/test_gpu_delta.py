@@ -40,6 +40,37 @@ def test_forward_and_gradients(shape, dtype):
         _check_all(_both(x, None, s, use, use), definition(x, None, s, use, use))
 
 
+# enough heads and columns that a workgroup carries 32 columns: a last tile of few columns, an odd number of tiles, both
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape", [(5, 130, 3, 9, 40, 100), (9, 70, 4, 8, 128, 66), (17, 3, 2, 16, 17, 5)], ids=str)
+def test_many_heads(shape, dtype):
+    b, t = shape[:2]
+    x = inputs(b + t, *shape, DT[dtype], DEV)
+    s = starts_of("some", b, t, DEV)
+    _check_all(_both(x, None, s), definition(x, None, s))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_many_heads_are_each_their_own(dtype):
+    """A value that is not finite in one of many heads, and the heads one by one."""
+    x = inputs(3, 9, 90, 8, 8, 64, 96, DT[dtype], DEV)
+    clean = _both(x)
+    x["v"][4, 50, 3, 17] = float("nan")
+    got = _both(x)
+    for n in ("y", "h", "dv", "dh0", "dbeta"):
+        same = torch.ones(9, 8, dtype=torch.bool, device=DEV)
+        same[4, 3] = False
+        a, b = (t[n] if n in ("h", "dh0") else t[n].transpose(1, 2) for t in (got, clean))
+        assert torch.equal(a[same], b[same]), n
+    bad = ~torch.isfinite(got["y"].float())
+    assert bad[4, 50:, 3, 17].all() and int(bad.sum()) == 40
+    one = {n: t[4:5, 2:3] if n in ("h0", "dh") else t[4:5, :, 2:3] for n, t in x.items()}
+    few = _both({n: t.contiguous() for n, t in one.items()})
+    for n in ("y", "h", "dv", "dlog_decay"):
+        a = got[n][4:5, 2:3] if n == "h" else got[n][4:5, :, 2:3]
+        assert torch.equal(a, few[n]), n
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_long_memory_and_a_given_scale(dtype):
     x = inputs(5, 1, 700, 1, 2, 64, 64, DT[dtype], DEV, slow=True)
