@@ -55,14 +55,18 @@ struct Forward : Team<T, DK, NC> {
   __device__ __forceinline__ void fetch_matrix(int c, Chunk& x) const {
     F::template load_matrix<false>(FIRST ? a.w.solve : a.w.read, c, x.mat);
   }
-  __device__ __forceinline__ void fetch_gates(int c, Chunk& x) const {
-    if (FIRST) x.leave = F::load_gate(1, c), x.beta = F::load_gate(2, c);
-    x.stay = F::load_stay(c);
-  }
 
   // What is loaded next takes its registers over: a load that moves up, past the last use of what they hold, takes
-  // others, and its result has to be waited for and moved at the turn's end.
+  // others, and its result has to be waited for and moved at the turn's end.  So has one whose use moves down.
   static __device__ __forceinline__ void used() { __builtin_amdgcn_sched_barrier(0); }
+  static __device__ __forceinline__ void used(f32x4_t& v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float e = v[i];
+      asm volatile("" : "+v"(e));
+      v[i] = e;
+    }
+  }
 
   // y of the chunk before, of its rows [first, end): what q S was is in `read`, u in LDS.
   __device__ __forceinline__ void finish(int c, const Chunk& x, int first, int end) const {
@@ -107,6 +111,7 @@ struct Forward : Team<T, DK, NC> {
     __syncthreads();  // the state's parts are there
     if (FIRST) F::put_rows(s.k, x.rows);
     f32x4_t xs[NC], more[NC];  // k S, or q S; then r, x
+    float stay = x.stay;
     const auto times_state = [&] {
 #pragma unroll
       for (int n = 0; n < NC; ++n) xs[n] = more[n] = zero;
@@ -123,7 +128,7 @@ struct Forward : Team<T, DK, NC> {
       f32x4_t enter = x.enter;
       if (alone) {
         enter = F::load_gate(3, c);
-        x.stay = a.w.rows[(chunk_index(a, F::bh, c) * 4 + 3) * kChunk + only];
+        stay = a.w.rows[(chunk_index(a, F::bh, c) * 4 + 3) * kChunk + only];
         wait_for_memory();
       }
 #pragma unroll
@@ -132,7 +137,7 @@ struct Forward : Team<T, DK, NC> {
         for (int i = 0; i < 4; ++i) {
           // alone: a state that is not finite, behind a start (with all rows such a chunk comes to nothing)
           xs[n][i] = alone && enter[i] == 0.f ? 0.f : enter[i] * (xs[n][i] + more[n][i]);
-          if (alone && x.stay == 0.f) state[n][i] = 0.f;
+          if (alone && stay == 0.f) state[n][i] = 0.f;
         }
     };
     f32x4_t u[NC], lu;
@@ -156,6 +161,7 @@ struct Forward : Team<T, DK, NC> {
       fetch_matrix(c, x);
     }
     __syncthreads();
+    const float stay_next = F::load_stay(next);
     if (FIRST) {
       if (!alone) {
 #pragma unroll
@@ -190,7 +196,7 @@ struct Forward : Team<T, DK, NC> {
     } else {
       times_state();
 #pragma unroll
-      for (int n = 0; n < NC; ++n) read[n] = xs[n];
+      for (int n = 0; n < NC; ++n) used(read[n] = xs[n]);
       used();
       x.enter = F::load_gate(0, next);
       fetch_rows(next, x);
@@ -200,10 +206,12 @@ struct Forward : Team<T, DK, NC> {
     if (F::has_tile())
 #pragma unroll
       for (int k = 0; k < 2; ++k) kt[k] = F::cols_of(s.k, F::tile, k);
-    const float stay = x.stay;
     used();
-    fetch_gates(next, x);
-    if (FIRST) fetch_matrix(next, x);
+    if (FIRST) {
+      x.leave = F::load_gate(1, next);
+      x.beta = F::load_gate(2, next);
+      fetch_matrix(next, x);
+    }
     __syncthreads();
     const bool bad = s.bad[turn & 1];
     // the other flag: read before the last barrier, set after the next one but one
@@ -236,6 +244,7 @@ struct Forward : Team<T, DK, NC> {
     // Stores come after the loads of the next chunk: waits for memory are counted in the order of issue, and a load
     // issued after a store would be waited for together with it.
     if (FIRST && TRAIN) F::template store_col<float>(a.x, c, xs, was_first, was_end);
+    x.stay = stay_next;
     return true;
   }
 
@@ -247,9 +256,13 @@ struct Forward : Team<T, DK, NC> {
   }
   __device__ __forceinline__ void fetch(int c, Chunk& x) const {
     fetch_rows(c, x);
-    if (FIRST) fetch_matrix(c, x);
-    fetch_gates(c, x);
+    if (FIRST) {
+      fetch_matrix(c, x);
+      x.leave = F::load_gate(1, c);
+      x.beta = F::load_gate(2, c);
+    }
     x.enter = F::load_gate(0, c);
+    x.stay = F::load_stay(c);
   }
 
   // All chunks.  One in which something is not finite goes row by row, so that it reaches only what comes after it.
