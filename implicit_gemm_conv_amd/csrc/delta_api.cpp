@@ -53,7 +53,6 @@ int64_t lay_out(const convdelta_desc* d, bool backward, char* base, Work* w) {
     w->solve = take(kMatrix);
     w->read = take(kMatrix);
   } else {
-    w->solve = take(kMatrix);
     w->solve_t = take(kMatrix);
     w->read_t = take(kMatrix);
     w->sums = (double*)take(8 * kChunk);

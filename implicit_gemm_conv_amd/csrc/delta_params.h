@@ -23,8 +23,8 @@ struct Heads {
 // What the preparing kernel leaves for each chunk of each head (index
 // ((b * Hv + h) * chunks + c) throughout).
 struct Work {
-  char* solve;     // H as operands of x = r + H (beta r): kMatrix bytes
-  char* read;      // forward: the decayed q k^T, the same way
+  char* solve;     // forward: H as operands of x = r + H (beta r), kMatrix bytes
+  char* read;      // ... and the decayed q k^T, the same way
   char* solve_t;   // backward: the transposes of both
   char* read_t;
   float* rows;     // 4 x 64: enter, leave, beta, step (see delta_device.h)

@@ -18,8 +18,8 @@ __device__ __forceinline__ const float* place(const float* m, int i, int j0) {
   return UP ? m + j0 * kLd + i : m + i * kLd + j0;
 }
 
-// Writes a 64x64 lower triangle of LDS as operands of a product with its rows (or, UP, its columns) as rows.
-template <bool UP, bool H>
+// Writes a 64x64 lower triangle of LDS as operands of a product with its rows (or, UP, its columns) as rows, in N parts.
+template <bool UP, bool H, int N>
 __device__ __forceinline__ void put_matrix(const float* m, char* to) {
   const int wave = wave_id(), lane = threadIdx.x % 64, q = lane / 16;
   for (int f = wave; f < kTri; f += kT / 64) {
@@ -29,9 +29,9 @@ __device__ __forceinline__ void put_matrix(const float* m, char* to) {
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = none ? 0.f : from[UP ? e * kLd : e];
-    const Parts<kParts> p = split<kParts>(x);
+    const Parts<N> p = split<N>(x);
 #pragma unroll
-    for (int n = 0; n < kParts; ++n) *(bf168_t*)(to + (f * kParts + n) * kFrag + lane * 16) = p.p[n];
+    for (int n = 0; n < N; ++n) *(bf168_t*)(to + (f * kParts + n) * kFrag + lane * 16) = p.p[n];
   }
 }
 
@@ -192,12 +192,12 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
   }
   __syncthreads();
   invert(s.low, s.beta, s.x);
-  put_matrix<false, true>(s.low, a.w.solve + at * kMatrix);
   if (!backward) {
-    put_matrix<false, false>(s.read, a.w.read + at * kMatrix);
+    put_matrix<false, true, kParts>(s.low, a.w.solve + at * kMatrix);
+    put_matrix<false, false, F::YP>(s.read, a.w.read + at * kMatrix);
   } else {
-    put_matrix<true, true>(s.low, a.w.solve_t + at * kMatrix);
-    put_matrix<true, false>(s.read, a.w.read_t + at * kMatrix);
+    put_matrix<true, true, kParts>(s.low, a.w.solve_t + at * kMatrix);
+    put_matrix<true, false, kParts>(s.read, a.w.read_t + at * kMatrix);
   }
 }
 
