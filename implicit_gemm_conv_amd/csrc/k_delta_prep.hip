@@ -177,15 +177,20 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
         qk[tj] = mma(f.rows_of(q, e), kb, qk[tj]);
       }
   }
+  double si[4];
+  int ni[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) si[r] = s.sums[f.row() + r], ni[r] = s.seq[f.row() + r];
   __syncthreads();  // k is read: its room is the matrices' now
 #pragma unroll
   for (int tj = 0; tj < 4; ++tj) {
-    const int j = 16 * tj + m;
+    const int j = 16 * tj + m, nj = s.seq[j];
+    const double sj = s.sums[j];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = f.row() + r;
-      const bool same = j <= i && s.seq[i] == s.seq[j];
-      const float d = same ? expf((float)(s.sums[i] - s.sums[j])) : 0.f;
+      const bool same = j <= i && ni[r] == nj;
+      const float d = expf((float)fmin(si[r] - sj, 0.));  // no branch: what is not wanted is selected away
       s.low[i * kLd + j] = same && j < i ? d * kk[tj][r] : 0.f;
       s.read[i * kLd + j] = same ? d * qk[tj][r] : 0.f;
     }
