@@ -85,14 +85,19 @@ struct Grad {
     Raw8<T> dy;
   };
   // N neighbouring elements of a row, zero past its end: as pieces of at most 16 bytes, where rows are whole ones (WHOLE)
+  // or of fp32, whose pieces need no more than their own alignment.
   template <typename E, int N>
   __device__ __forceinline__ void load(const Range& x, uint32_t row, int col, int width, void* to) const {
-    constexpr int n = WHOLE ? (N * sizeof(E) > 16 ? 16 / sizeof(E) : N) : 1;
+    constexpr int n = WHOLE || sizeof(E) == 4 ? (N * sizeof(E) > 16 ? 16 / sizeof(E) : N) : 1;
     struct alignas(n * sizeof(E)) Piece { E e[n]; };
 #pragma unroll
     for (int k = 0; k < N / n; ++k) {
       const int at = col + k * n;
-      const Piece p = x.load<Piece>(at < width ? row + (uint32_t)at * (uint32_t)sizeof(E) : kNowhere);
+      Piece p = x.load<Piece>(at < width ? row + (uint32_t)at * (uint32_t)sizeof(E) : kNowhere);
+      if constexpr (!WHOLE && n > 1)
+#pragma unroll
+        for (int e = 1; e < n; ++e)
+          if (at + e >= width) p.e[e] = 0;
       __builtin_memcpy((E*)to + k * n, &p, sizeof(p));
     }
   }
