@@ -41,7 +41,8 @@ struct GradLds {
       __bf16 rows[NP * RowsAt<DK>::part];                            // k, then q
     };
   };
-  float gates[3 * kChunk], red[kChunk][4];  // enter, leave, beta; dx.v, z.x and both halves of q.dq
+  float gates[3 * kChunk], zx[kChunk];  // enter, leave, beta; z.x
+  double red[kChunk][3];                // dx.v and both halves of q.dq
   double sums[kChunk], a[kT / 64];
   int seq[kChunk], wild;
 };
@@ -229,7 +230,7 @@ struct Grad {
     }
   }
 
-  __device__ __forceinline__ float over_lanes(float v) const {
+  __device__ __forceinline__ double over_lanes(double v) const {
     for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o);
     return v;
   }
@@ -261,7 +262,8 @@ struct Grad {
       load<T, 8>(dys, row() * row_bytes<T>(a.dy), v0 + 8 * q4, a.dv, x.dy.w);
     };
     Parts<NP> yp;
-    float dot = 0.f, db = 0.f, dxv = 0.f;
+    float db = 0.f;
+    double dot = 0, dxv = 0;
     // what was fetched, into LDS, and dy into yp
     const auto put = [&](auto& to) {
       put_state<kParts>(to.s, x.st);
@@ -269,7 +271,7 @@ struct Grad {
 #pragma unroll
       for (int n = 0; n < held; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dot = fmaf(x.st[n][e], x.be[n][e], dot);
+        for (int e = 0; e < 4; ++e) dot = fma((double)x.st[n][e], (double)x.be[n][e], dot);
       f32x4_t u, dx;
       T v[4];
       __builtin_memcpy(v, &x.v, sizeof(v));
@@ -278,7 +280,7 @@ struct Grad {
         u[e] = my_beta * x.x[e];
         dx[e] = my_beta * x.z[e];
         db = fmaf(x.x[e], x.z[e], db);
-        dxv = fmaf(dx[e], to_f32(v[e]), dxv);
+        dxv = fma((double)dx[e], (double)to_f32(v[e]), dxv);
       }
       put_row<kParts>(to.u, u);
       put_row<GP>(to.dx, dx);
@@ -359,7 +361,7 @@ struct Grad {
     }
     if (tid % 8 == 0) {
       s.red[tid / 8][0] = dxv;
-      s.red[tid / 8][1] = db;
+      s.zx[tid / 8] = db;
     }
     if (!k.finite() || !q.finite()) s.wild = 1;
     f32x4_t decay[2];
@@ -384,16 +386,16 @@ struct Grad {
     renew();
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      float g = 0.f;
+      double g = 0;
 #pragma unroll
-      for (int t = 0; t < DT; ++t) g = fmaf(value(s.rows, own + r, 16 * (half * DT + t) + m), dq[t][r], g);
+      for (int t = 0; t < DT; ++t) g = fma((double)value(s.rows, own + r, 16 * (half * DT + t) + m), (double)dq[t][r], g);
       g = over_lanes(g);
-      if (m == 0) s.red[own + r][2 + half] = g;
+      if (m == 0) s.red[own + r][1 + half] = g;
     }
     __syncthreads();
     if (tid < kChunk) {
       const int mine = s.seq[lane], t = c * kChunk + lane;
-      double sum = (double)s.red[lane][0] - ((double)s.red[lane][2] + s.red[lane][3]), g = 0;
+      double sum = s.red[lane][0] - (s.red[lane][1] + s.red[lane][2]), g = 0;
       if (mine == 0)
         for (int w = 0; w < kT / 64; ++w) g += s.a[w];
       // the rows before, of the same sequence
@@ -408,7 +410,7 @@ struct Grad {
       if (t < a.t) {
         const int64_t to = ((int64_t)b * a.t + t) * a.hv + h;
         a.dlog_decay[to] = (float)g;
-        a.dbeta[to] = s.red[lane][1];
+        a.dbeta[to] = s.zx[lane];
       }
     }
   }
