@@ -21,15 +21,18 @@ int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 // `whole_pieces`: every row of the inputs and outputs is 16-byte aligned.
 Plan make_plan(int n, int p, int c, int groups, int elem, bool whole_pieces, bool backward) {
   Plan pl{};
-  const int cg = c / groups, wide = 16 / elem, held = backward ? kTeamHeldBwd : kTeamHeld;
+  const int cg = c / groups, wide = 16 / elem, held = p >= kFewRows ? 1 : backward ? kTeamHeldBwd : kTeamHeld;
   // ---- a team for each (n, group) ----
+  // Up to 256 pieces a lane holds one (8 positions of 1024 channels in 8 groups, n 4096, bf16, forward and backward: 41 and
+  // 59 us, in tiles 60 and 99; one position of 8192 in 4 groups, n 16384: 147 and 186 us, in tiles 684 and 1398).  More
+  // pieces a lane are faster than tiles only where these would be of few rows (one position of 4096 channels in one group,
+  // n 4096: 59 and 64 us, in tiles 92 and 158; 4 positions of 2048, n 2048: 55 and 70, in tiles 39 and 67).
   const int v = whole_pieces && cg % wide == 0 ? wide : 1;
   const int64_t pieces = (int64_t)p * (cg / v);
   if (pieces <= (int64_t)kThreads * held) {
     pl.v = v;
     pl.team = 1;
-    while (pl.team < pieces && pl.team < 64) pl.team *= 2;
-    if (pieces > (int64_t)pl.team * held) pl.team = kThreads;
+    while (pl.team < pieces && pl.team < kThreads) pl.team *= 2;
     pl.held = (int)std::max<int64_t>(1, ceil_div(pieces, pl.team));
     const int teams = kThreads / pl.team;
     // as many lanes as the chip holds at once, each walking over n with its channels' parameters in registers (16384 rows

@@ -12,7 +12,8 @@ namespace convnorm {
 using convseq::Rows;
 
 constexpr int kThreads = 256;
-constexpr int kTeamHeld = 4;     // pieces of 16 bytes (or values) of x that a lane of a team holds, forward
+constexpr int kFewRows = 4;      // with fewer positions a lane may hold several pieces
+constexpr int kTeamHeld = 4;     // pieces of 16 bytes (or values) of x that it then holds, forward
 constexpr int kTeamHeldBwd = 2;  // backward, where it holds as many of dy and sums for the parameters
 
 // How one problem is cut.

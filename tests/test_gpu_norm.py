@@ -41,6 +41,16 @@ def test_forward_and_gradients(shape, dtype):
         _check_all(got, x, dy, g, w, b, act)
 
 
+# several pieces a lane (fewer than 4 positions) and the tiles that take over; more n than a launch's teams
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shape", [(5, 1, 8192, 1), (3, 3, 2720, 1), (3, 4, 2048, 1), (4, 2, 771, 1), (2, 1, 520, 1),
+                                   (2100, 1, 2056, 1), (1500, 3, 104, 1)], ids=str)
+def test_wide_groups(shape, dtype):
+    n, p, c, g = shape
+    x, dy, w, b = inputs(n + 7 * p + c, n, p, c, DT[dtype], DEV)
+    _check_all(_both(x, dy, g, w, b, "silu"), x, dy, g, w, b, "silu")
+
+
 @pytest.mark.parametrize("only", ["weight", "bias"])
 def test_one_parameter_alone(only):
     x, dy, w, b = inputs(5, 2, 40, 48, torch.bfloat16, DEV)
