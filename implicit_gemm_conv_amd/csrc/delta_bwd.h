@@ -10,7 +10,9 @@
 // (delta_grad.h).  The steps between barriers are those of delta_fwd.h: (1) du, (2) z,
 // (3) the state's gradient.  The waves of the first role go the way from state to state,
 // those of the second bring q and
-// dy, and R^T dy a chunk ahead.  Included by one source for each type.
+// dy, and R^T dy a chunk ahead.  Bound as the forward recurrence is; 4 sequences of 4096 rows, 16 heads
+// of 128 x 128, bf16: 319 us (431 us with 16 columns a workgroup, 468 us before R^T dy moved to the
+// second role).  Included by one source for each type.
 #include "delta_team.h"
 
 namespace convdelta {

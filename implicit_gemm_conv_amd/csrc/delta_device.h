@@ -265,7 +265,8 @@ template <int N>
 struct Int {
   static constexpr int value = N;
 };
-// Head sizes are padded to 32, 64 or 128 inside the kernels.
+// Head sizes are padded to 32, 64 or 128 inside the kernels (4x4096 rows, 16 heads of Dk x 128, bf16, forward and backward:
+// Dk = 64 takes 286 and 651 us, padded to 128 308 and 731; Dk = 32 265 and 562, padded 291 and 687).
 template <typename F>
 inline hipError_t for_dk(int dk, const F& f) {
   if (dk <= 32) return f(Int<32>{});
@@ -273,8 +274,9 @@ inline hipError_t for_dk(int dk, const F& f) {
   return f(Int<128>{});
 }
 
-// The recurrences' columns a workgroup, in tiles of 16: one where the workgroups are then no more than the 256 CUs, and
-// two, which read q, k and the chunks' matrices once for both, where they are more.
+// The recurrences' columns a workgroup, in tiles of 16: one where the workgroups are then no more than the 256 CUs (two
+// would leave more of them idle), and two, which read q, k and the chunks' matrices once for both, where they are more
+// (4x4096 rows, 16 heads of 128 x 128, bf16: forward 291 us for 387, backward 319 for 434).
 template <typename F>
 inline hipError_t for_columns(const DeltaArgs& a, const F& f) {
   return (int64_t)a.b * a.hv * ((a.dv + 15) / 16) > 256 ? f(Int<2>{}) : f(Int<1>{});

@@ -6,6 +6,18 @@
 // those of the second compute q S in step (2) and finish y in step (1) of the next chunk, while
 // the first role is at work; the state's rows are all waves'.  Each wave fetches what it needs
 // of the next chunk, which no other wave needs, as soon as this chunk's is used.
+//
+// Why columns: the columns of a state go their own ways through the sequence, so splitting them
+// needs no exchange, and it is the only axis besides the heads that a single sequence offers; what it
+// costs is that q, k and the chunks' matrices are read by every workgroup of a head, which sit on
+// one die and share its L2.  States in fp32 (accumulators in registers, three bf16 parts in LDS for
+// the products), matrices in three parts on the state's way and in as many as the output's type can
+// tell apart on y's.
+//
+// Bound by the chain of a chunk's steps: LDS, two to four matrix instructions one after the other,
+// LDS, a barrier, three times over, about 4500 clocks a chunk (on the CUs in use matrix units busy 14%, vector units 26%).
+// One sequence of 16387 rows, 16 heads of 128 x 128, bf16: 545 us, 2.1 us a chunk (prefill, 128
+// workgroups on 256 CUs); 4 sequences of 4096, states kept: 291 us, 2.1 TB/s of HBM traffic.
 #include "delta_team.h"
 
 namespace convdelta {

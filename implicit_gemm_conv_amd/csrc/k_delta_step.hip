@@ -1,5 +1,7 @@
 // k_delta_step.hip -- gated delta rule, one row of each of many streams: the state
-// is read once, written once, and held in registers in between.
+// is read once, written once, and held in registers in between.  Bound by memory: 128
+// streams of 16 heads of 128 x 128 move 268 MB in 47 us, 5.7 TB/s; one stream of 4 heads
+// of 64 x 64 takes 4.1 us, most of it latency.
 #include "delta_device.h"
 
 namespace convdelta {

@@ -1,6 +1,11 @@
 // k_norm_split.hip -- group norm over images and volumes: the sums of tiles of
 // positions, and a second pass over x that writes the result.  The sums are joined at
 // the second pass's beginning, or by a launch between.
+//
+// Bound by memory, x being read twice (a group of 56 x 56 x 8 channels is 50 KB of 16-byte
+// pieces 512 bytes apart, so that no workgroup can hold whole lines of it): 32 images of
+// 56 x 56 x 256, silu, bf16: sums 12.8 us (4.0 TB/s), result 29 (5.3 with what the caches
+// hold); backward 29 and 37 (3.5 and 4.2 TB/s).
 #include "norm_device.h"
 
 namespace convnorm {
