@@ -123,11 +123,12 @@ __global__ __launch_bounds__(kThreads) void norm_stats_kernel(NormArgs a) {
   }
   // each channel's mean, then the squares about it
   const float all = 1.f / (float)max(t.p1 - t.p0, 1);
+  const int filled = min(t.rw, t.p1 - t.p0);  // of the workgroup's rows
   add_rows<V>(a, t, m, s, lds, [&](int c, const float2* at, int ld) {
     float mean = 0.f, sq = 0.f;
-    for (int r = 0; r < t.rw; ++r) mean = fmaf(rows_of(r) * all, at[r * ld].x - at[0].x, mean);
+    for (int r = 0; r < filled; ++r) mean = fmaf(rows_of(r) * all, at[r * ld].x - at[0].x, mean);
     mean += at[0].x;
-    for (int r = 0; r < t.rw; ++r) {
+    for (int r = 0; r < filled; ++r) {
       const float2 o = at[r * ld];
       const float d = o.x - mean;
       sq += fmaf(d * d, rows_of(r), o.y);

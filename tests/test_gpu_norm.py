@@ -209,3 +209,15 @@ def test_offsets_past_32_bits():
     assert f64(f.rstd) == pytest.approx((mean * (1 - mean)) ** -0.5, rel=2.0 ** -18)
     assert f64(f.y[0, -1]) == pytest.approx((1 - mean) * (mean * (1 - mean)) ** -0.5, rel=2.0 ** -11)
     assert f64(f.y[0, p - 2]) == pytest.approx(-mean * (mean * (1 - mean)) ** -0.5, rel=2.0 ** -10)
+
+
+@pytest.mark.parametrize("shape", [(2, 1030, 32, 2), (1, 700, 65, 5), (3, 1, 256, 2)], ids=str)
+def test_values_whose_squares_overflow(shape):
+    """A mean whose square is past fp32's range over a spread that is not: 2^-64 of the values gives the same bits
+    (nothing is rounded by a power of two), also where a last tile has fewer rows than a workgroup.  (The squares of
+    2^14 differences of 2^54 add up to 2^122.)"""
+    n, p, c, g = shape
+    x = (1 + 2.0 ** -12 * normal(8, (n, p, c), torch.float32, 1.0, DEV)) * 2.0 ** 66
+    big, small = igc.group_norm(x, g, eps=0.0), igc.group_norm(x * 2.0 ** -64, g, eps=0.0)
+    assert torch.isfinite(big.y).all() and torch.equal(big.y, small.y)
+    assert torch.equal(big.mean, small.mean * 2.0 ** 64) and torch.equal(big.rstd, small.rstd * 2.0 ** -64)
