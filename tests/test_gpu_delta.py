@@ -345,3 +345,22 @@ def test_offsets_past_32_bits():
     assert (f.y[:, -40:].float() - alone.y.float()).abs().max() <= 2.0 ** -9 * alone.y.float().abs().max()
     assert (f.h - alone.h).abs().max() <= 2.0 ** -16 * alone.h.abs().max()
     assert (f.y[:, :-40] == 0).all()
+
+
+@pytest.mark.parametrize("dv", [64, 37])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_kept_tensors_at_any_element(dtype, dv):
+    """What the forward pass kept, and the states, may start at any fp32 element: the bits are those of aligned ones."""
+    x = inputs(9, 2, 130, 1, 2, 48, dv, DT[dtype], DEV)
+    f = igc.delta_rule(*_ins(x), h0=x["h0"], train=True)
+    want = igc.delta_rule_bwd(x["dy"], *_ins(x), f.states, dh=x["dh"])
+
+    def moved(t):
+        to = torch.empty(t.numel() + 1, device=DEV)[1:].view(t.shape)
+        return to.copy_(t)
+
+    again = igc.delta_rule(*_ins(x), h0=moved(x["h0"]), train=True)
+    assert torch.equal(again.y, f.y) and torch.equal(again.states.x, f.states.x)
+    got = igc.delta_rule_bwd(x["dy"], *_ins(x), igc.DeltaStates(*map(moved, f.states)), dh=moved(x["dh"]))
+    for n, t in got._asdict().items():
+        assert torch.equal(t, getattr(want, n)), n
