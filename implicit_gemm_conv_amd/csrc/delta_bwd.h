@@ -111,7 +111,7 @@ struct Backward : Team<T, DK, NC> {
       wait_for_memory();
       __syncthreads();
     }
-    f32x4_t du[NC], more[NC];
+    f32x4_t du[NC], hd[NC], more[NC];  // sums of their own, added once (see delta_fwd.h)
     if (FIRST)
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
@@ -124,7 +124,7 @@ struct Backward : Team<T, DK, NC> {
           bd[i] = out ? 0.f : x.beta[i] * du[n][i];
         }
         F::template put<kParts, Rows>(s.bd[n], row(), bd);
-        more[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        hd[n] = more[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       }
     __syncthreads();
     if (FIRST) {
@@ -134,13 +134,13 @@ struct Backward : Team<T, DK, NC> {
 #pragma unroll
           for (int n = 0; n < NC; ++n) {
             const auto bp = F::template get<kParts, Rows>(s.bd[n], k);
-            (k ? more : du)[n] = mma(x.mat[k], bp, (k ? more : du)[n]);
+            (k ? more : hd)[n] = mma(x.mat[k], bp, (k ? more : hd)[n]);
           }
 #pragma unroll
       for (int n = 0; n < NC; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (row() + i >= lo && row() + i < hi) z[n][i] = du[n][i] + more[n][i];
+          if (row() + i >= lo && row() + i < hi) z[n][i] = du[n][i] + (hd[n][i] + more[n][i]);
     }
   }
 
@@ -231,25 +231,23 @@ struct Backward : Team<T, DK, NC> {
     }
     // (3), from the rows [0, first) where masked
     if (F::has_tile()) {
-      f32x4_t more[NC];
+      f32x4_t qi[NC], more[NC];
 #pragma unroll
-      for (int n = 0; n < NC; ++n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) state[n][i] = times(x.stay, state[n][i]);
-        more[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      }
+      for (int n = 0; n < NC; ++n) qi[n] = more[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         Parts<NP> qt = F::cols_of(s.q, F::tile, k), kt = F::cols_of(s.k, F::tile, k);
         if (masked) keep(qt, 32 * k + 8 * q4, 0, first), keep(kt, 32 * k + 8 * q4, 0, first);
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-          state[n] = mma(qt, F::template get<kParts, Rows>(s.in[n], k), state[n]);
+          qi[n] = mma(qt, F::template get<kParts, Rows>(s.in[n], k), qi[n]);
           more[n] = mma(kt, F::template get<kParts, Rows>(s.out[n], k), more[n]);
         }
       }
 #pragma unroll
-      for (int n = 0; n < NC; ++n) state[n] += more[n];
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) state[n][i] = times(x.stay, state[n][i]) + (qi[n][i] + more[n][i]);
       F::put_state(s.state, state);
     }
     // stores come after the loads of the next chunk (see delta_fwd.h)

@@ -176,19 +176,22 @@ struct Forward : Team<T, DK, NC> {
     const float stay_next = F::load_stay(next);
     if (FIRST) {
       if (!alone) {
+        // sums of their own, added to r (and to the state) once: a sum that starts from them is rounded to their size at
+        // every product
+        f32x4_t hx[NC];
 #pragma unroll
-        for (int n = 0; n < NC; ++n) more[n] = zero;
+        for (int n = 0; n < NC; ++n) hx[n] = more[n] = zero;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           if (F::template has<false>(k))
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
               const auto bp = F::template get<kParts, Rows>(s.br[n], k);
-              (k ? more : xs)[n] = mma(x.mat[k], bp, (k ? more : xs)[n]);
+              (k ? more : hx)[n] = mma(x.mat[k], bp, (k ? more : hx)[n]);
             }
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-          xs[n] += more[n];
+          xs[n] += hx[n] + more[n];
 #pragma unroll
           for (int i = 0; i < 4; ++i) u[n][i] = x.beta[i] * xs[n][i];
         }
@@ -236,21 +239,20 @@ struct Forward : Team<T, DK, NC> {
     was_end = alone ? only + 1 : kChunk;
     // the state moves on
     if (F::has_tile()) {
+      f32x4_t ku[NC];
 #pragma unroll
-      for (int n = 0; n < NC; ++n) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) state[n][i] *= stay;
-        more[n] = zero;
-      }
+      for (int n = 0; n < NC; ++n) ku[n] = more[n] = zero;
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
           const auto up = F::template get<kParts, Rows>(s.u[n], k);
-          (k ? more : state)[n] = mma(kt[k], up, (k ? more : state)[n]);
+          (k ? more : ku)[n] = mma(kt[k], up, (k ? more : ku)[n]);
         }
 #pragma unroll
-      for (int n = 0; n < NC; ++n) state[n] += more[n];
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) state[n][i] = fmaf(stay, state[n][i], ku[n][i] + more[n][i]);
       F::put_state(s.state, state);
     }
     // Stores come after the loads of the next chunk: waits for memory are counted in the order of issue, and a load
