@@ -337,7 +337,7 @@ hipError_t delta_fwd_of(const DeltaArgs& a, hipStream_t s) {
   return for_dk(a.dk, [&](auto dk) {
     constexpr int DK = decltype(dk)::value;
     return for_columns(a, [&](auto nc) {
-      constexpr int NC = InParts<T>::n == 3 && DK == 128 ? 1 : decltype(nc)::value;  // two would need more registers
+      constexpr int NC = decltype(nc)::value;
       const int blocks = (a.dv + 16 * NC - 1) / (16 * NC);
       hipLaunchKernelGGL((a.states ? delta_fwd_kernel<T, DK, NC, true> : delta_fwd_kernel<T, DK, NC, false>),
                          dim3((a.b * a.hv + 7) / 8 * 8 * blocks), dim3(kTeam), 0, s, a, blocks);

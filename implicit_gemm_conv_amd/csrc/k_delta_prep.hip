@@ -131,16 +131,19 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
   Raw8<T> k[KS], q[KS];
   f.load_rows(a.k, c, k);
   f.load_rows(a.q, c, q);
+  // rows past T decay nothing and write nothing
+  const int t = t0 + lane;
+  const bool in = wave == 0 && t < a.t;
+  const int64_t row = ((int64_t)f.b * a.t + t) * a.hv + f.h;
+  const float bt = in ? a.beta[row] : 0.f;
+  float g = in ? a.log_decay[row] : 0.f;
+  const int start = in && a.starts ? a.starts[(int64_t)f.b * a.t + t] != 0 : 0;
+  f.put_rows(s.k, k);
+  __syncthreads();
   if (wave == 0) {
-    // running sums over the rows, a lane a row; rows past T decay nothing and write nothing
-    const int t = t0 + lane;
-    const bool in = t < a.t;
-    const int64_t row = ((int64_t)f.b * a.t + t) * a.hv + f.h;
-    const float bt = in ? a.beta[row] : 0.f;
+    // running sums over the rows, a lane a row (this wave has the fewest products)
     // a decay of nothing at all is exp(-10^4), which is zero too and leaves differences of sums finite
-    float g = in ? a.log_decay[row] : 0.f;
     g = g < -1e4f ? -1e4f : g;
-    const int start = in && a.starts ? a.starts[(int64_t)f.b * a.t + t] != 0 : 0;
     double sum = g;
     int n = start;
     for (int o = 1; o < 64; o <<= 1) {
@@ -168,8 +171,6 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
       a.w.seq[at * kChunk + lane] = n;
     }
   }
-  f.put_rows(s.k, k);
-  __syncthreads();
   // this wave's rows of k k^T and q k^T
   f32x4_t kk[4], qk[4];
 #pragma unroll
@@ -183,11 +184,11 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
         qk[tj] = mma(f.rows_of(q, e), kb, qk[tj]);
       }
   }
+  __syncthreads();  // k is read: its room is the matrices' now
   double si[4];
   int ni[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) si[r] = s.sums[f.row() + r], ni[r] = s.seq[f.row() + r];
-  __syncthreads();  // k is read: its room is the matrices' now
 #pragma unroll
   for (int tj = 0; tj < 4; ++tj) {
     const int j = 16 * tj + m, nj = s.seq[j];
