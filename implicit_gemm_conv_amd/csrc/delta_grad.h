@@ -291,11 +291,12 @@ struct Grad {
       }
       put_row<kParts>(to.u, u);
       put_row<GP>(to.dx, dx);
-      float e8[8];
-      x.dy.get(e8);
+      Raw8<T> dy = x.dy;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) e8[e] = row() < rows ? e8[e] : 0.f;
-      yp = split<NP>(e8);
+      for (unsigned n = 0; n < sizeof(T) / 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dy.w[n][e] = row() < rows ? dy.w[n][e] : 0u;
+      yp = dy.parts();
     };
     fetch(0);
     if (tid == 0) s.wild = 0;

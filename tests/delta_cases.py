@@ -64,7 +64,8 @@ def definition(x, scale=None, starts=None, use_h0=True, use_dh=True):
         size = torch.maximum(size, frob(S) + _norm(err) + _norm(v[:, i]))
         olds.append(old), errs.append(err), us.append(u), news.append(S)
     last = S
-    out = {"y": y, "h": last, "x": torch.stack(errs, 1) if errs else torch.zeros_like(v), "states": torch.stack(kept, 1) if kept else torch.zeros((b, 0, hv, dk, dv), dtype=torch.float64)}
+    out = {"y": y, "h": last, "x": torch.stack(errs, 1) if errs else torch.zeros_like(v),
+           "states": torch.stack(kept, 1) if kept else torch.zeros((b, 0, hv, dk, dv), dtype=torch.float64)}
     dy = d["dy"]
     dS = d["dh"] if use_dh else torch.zeros_like(S)
     back = torch.maximum(back, frob(dS))
@@ -110,7 +111,8 @@ def check(got, ref, name, where=None):
         bad &= np.broadcast_to(where, bad.shape)
     if bad.any():
         k = np.unravel_index(np.argmax(np.where(bad, np.abs(g - value) / allowed, 0)), g.shape)
-        raise AssertionError(f"{name}: {bad.sum()} of {bad.size} outside; at {k}: got {g[k]!r}, expected {value[k]!r} +- {np.broadcast_to(allowed, g.shape)[k]:.3g}")
+        raise AssertionError(f"{name}: {bad.sum()} of {bad.size} outside; at {k}: got {g[k]!r}, expected {value[k]!r} +- "
+                             f"{np.broadcast_to(allowed, g.shape)[k]:.3g}")
     if where is None:
         # gradients of log decays are sums of 64 rows' shares that cancel: 8 times more
         chunks = value.shape[1] // 64 + 2 if value.ndim > 1 else 1

@@ -142,7 +142,8 @@ def test_the_binding_refuses_what_does_not_fit():
             (ValueError, lambda: igc.delta_rule_bwd(v, q, q, v, g, g, st._replace(states=torch.zeros(2, 2, 4, 8, 6, device=dev)))),
             (ValueError, lambda: igc.delta_rule_bwd(v, q, q, v, g, g, st._replace(x=v[:, :19]))),
             (ValueError, lambda: igc.delta_rule_bwd(v, q, q, v, g, g, st, dh=h.half())),
-            (ValueError, lambda: igc.delta_rule_step(*one, h[:, :2])), (ValueError, lambda: igc.delta_rule_step(*one, torch.zeros(3, 4, 8, 6, device=dev))),
+            (ValueError, lambda: igc.delta_rule_step(*one, h[:, :2])),
+            (ValueError, lambda: igc.delta_rule_step(*one, torch.zeros(3, 4, 8, 6, device=dev))),
             (TypeError, lambda: igc.delta_rule_step(*one, h, slots=torch.zeros(2, dtype=torch.int64, device=dev))),
             (ValueError, lambda: igc.delta_rule_step(*one, h, slots=torch.zeros(3, dtype=torch.int32, device=dev)))):
         with pytest.raises(error):
