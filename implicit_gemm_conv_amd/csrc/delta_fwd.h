@@ -11,8 +11,8 @@
 // needs no exchange, and it is the only axis besides the heads that a single sequence offers; what it
 // costs is that q, k and the chunks' matrices are read by every workgroup of a head, which sit on
 // one die and share its L2.  States in fp32 (accumulators in registers, three bf16 parts in LDS for
-// the products), matrices in three parts on the state's way and in as many as the output's type can
-// tell apart on y's.
+// the products), matrices in three parts, on y's way too: q S and R u may cancel, and two parts there leave 2^-17 of
+// their terms in a 16-bit y (they took 44 us less of 653 for the sequence below, with the preparing).
 //
 // Bound by the chain of a chunk's steps: LDS, two to four matrix instructions one after the other,
 // LDS, a barrier, three times over, about 4500 clocks a chunk (on the CUs in use matrix units busy 14%, vector units 26%).
@@ -29,7 +29,7 @@ struct FwdLds {
   typedef Team<T, DK, NC> F;
   __bf16 k[F::NP * RowsAt<DK>::part];
   __bf16 state[NC][kParts * F::State::part];
-  __bf16 br[NC][kParts * F::Rows::part], u[NC][kParts * F::Rows::part], out[2][NC][F::YP * F::Rows::part];
+  __bf16 br[NC][kParts * F::Rows::part], u[NC][kParts * F::Rows::part], out[2][NC][kParts * F::Rows::part];
   int bad[2];
 };
 
@@ -42,13 +42,13 @@ struct Forward : Team<T, DK, NC> {
   using F::m;
   using F::wave;
   using F::row;
-  static constexpr int NP = F::NP, KS = F::KS, YP = F::YP;
+  static constexpr int NP = F::NP, KS = F::KS;
   typedef typename F::Rows Rows;
 
   // what a chunk needs
   struct Chunk {
-    Raw8<T> rows[KS];                   // of k, or of q
-    Parts<FIRST ? kParts : YP> mat[2];  // of H; of the decayed q k^T of the chunk whose y is next
+    Raw8<T> rows[KS];      // of k, or of q
+    Parts<kParts> mat[2];  // of H; of the decayed q k^T of the chunk whose y is next
     f32x4_t enter, leave, beta;
     float stay;
     T v[NC][4];
@@ -88,12 +88,12 @@ struct Forward : Team<T, DK, NC> {
 #pragma unroll
     for (int k = 0; k < 2; ++k)
       if (F::template has<false>(k)) {
-        Parts<YP> mat = x.mat[k];
+        Parts<kParts> mat = x.mat[k];
         if (end - first < kChunk) keep(mat, 32 * k + 8 * q4, first, end);
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-          const auto op = F::template get<YP, Rows>(s.out[~turn & 1][n], k);
-          (k ? more : y)[n] = mma_first<YP>(mat, op, (k ? more : y)[n]);
+          const auto op = F::template get<kParts, Rows>(s.out[~turn & 1][n], k);
+          (k ? more : y)[n] = mma(mat, op, (k ? more : y)[n]);
         }
       }
 #pragma unroll
@@ -134,7 +134,7 @@ struct Forward : Team<T, DK, NC> {
         for (int n = 0; n < NC; ++n) {
           f32x4_t& to = (k & 1 ? more : xs)[n];
           const auto sp = F::template get<kParts, typename F::State>(s.state[n], k);
-          to = FIRST ? mma(rows, sp, to) : mma_first<YP>(rows, sp, to);
+          to = mma(rows, sp, to);
         }
       }
       f32x4_t enter = x.enter;
@@ -205,7 +205,7 @@ struct Forward : Team<T, DK, NC> {
           test = fmaf(u[n][i], 0.f, test);
         }
         F::template put<kParts, Rows>(s.u[n], row(), lu);
-        F::template put<YP, Rows>(s.out[turn & 1][n], row(), u[n]);
+        F::template put<kParts, Rows>(s.out[turn & 1][n], row(), u[n]);
       }
       if (__any(test != 0.f)) s.bad[turn & 1] = 1;  // NaN
     } else {

@@ -206,7 +206,7 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
   invert(s.low, s.beta, s.x);
   if (!backward) {
     put_matrix<false, true, kParts>(s.low, a.w.solve + at * kMatrix);
-    put_matrix<false, false, F::YP>(s.read, a.w.read + at * kMatrix);
+    put_matrix<false, false, kParts>(s.read, a.w.read + at * kMatrix);
   } else {
     put_matrix<true, true, kParts>(s.low, a.w.solve_t + at * kMatrix);
     put_matrix<true, false, kParts>(s.read, a.w.read_t + at * kMatrix);

@@ -1,0 +1,67 @@
+"""Gated delta rule on the GPU: sums of 16-bit inputs' products that cancel to their last bits.
+
+Decays are one, keys orthogonal, and every product and every partial sum here is a multiple of 2^-21 below 4 and
+so exact in fp32; what is left, one or two units of 2^-21, is exact in 16 bits as well.  Arithmetic at fp32's precision has
+no freedom then: the results are equal to the definition's.  1 + 2^-9 + 2^-20 has bits in three groups of 8, and an operand
+held in two of them loses the last.
+"""
+import pytest
+import torch
+
+import implicit_gemm_conv_amd as igc
+from tests.seq_cases import DT
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+E = 2.0 ** -20
+F = 1 + 2.0 ** -9
+
+
+def _zeros(t, dtype):
+    """One head of 8 x 4: q, k, v, dy, no decay, beta one, states of zero."""
+    rows = {n: torch.zeros(1, t, 1, d, dtype=DT[dtype], device=DEV) for n, d in (("q", 8), ("k", 8), ("v", 4), ("dy", 4))}
+    return dict(rows, log_decay=torch.zeros(1, t, 1, device=DEV), beta=torch.ones(1, t, 1, device=DEV),
+                h0=torch.zeros(1, 1, 8, 4, device=DEV), dh=torch.zeros(1, 1, 8, 4, device=DEV))
+
+
+def _row(x, name, t, *values):
+    x[name][0, t, 0, :len(values)] = torch.tensor(values, device=DEV)
+
+
+def _forward(x, train=False):
+    return igc.delta_rule(x["q"], x["k"], x["v"], x["log_decay"], x["beta"], scale=1.0, h0=x["h0"], train=train)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_y_of_the_state_before(dtype):
+    """q S = (F + 2^-20) - F."""
+    x = _zeros(1, dtype)
+    _row(x, "q", 0, 1, 1)
+    x["h0"][0, 0, 0, :2] = F + E
+    x["h0"][0, 0, 1, :2] = -F
+    assert _forward(x).y[0, 0, 0].tolist() == [E, E, 0, 0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_y_of_corrections_of_many_bits(dtype):
+    """R u = u_0 + u_1, with u = beta v = (F + 2^-20) / 2 and -F / 2."""
+    x = _zeros(3, dtype)
+    _row(x, "k", 0, 1)
+    _row(x, "k", 1, 0, 1)
+    _row(x, "q", 2, 1, 1)
+    _row(x, "v", 0, 1, 1)
+    _row(x, "v", 1, -1, -1)
+    x["beta"][0, :2, 0] = torch.tensor([(F + E) / 2, F / 2])
+    assert _forward(x).y[0, 2, 0].tolist() == [E / 2, E / 2, 0, 0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_y_of_products_of_many_bits(dtype):
+    """R u = (q k_0) - (q k_1), with q k = F + 2^-20 and F."""
+    x = _zeros(3, dtype)
+    _row(x, "k", 0, 1, 2.0 ** -10, 1)
+    _row(x, "k", 1, 0, 0, 0, 1, 1)
+    _row(x, "q", 2, 1, 2.0 ** -10, 2.0 ** -9, 1, 2.0 ** -9)
+    _row(x, "v", 0, 1, 1)
+    _row(x, "v", 1, -1, -1)
+    assert _forward(x).y[0, 2, 0].tolist() == [E, E, 0, 0]
