@@ -15,10 +15,11 @@
 //
 // and from zero at a start, where the decay acts on nothing.
 //
-// The columns are taken 32 at a time, through LDS; wave (w, half) owns rows 16 w .. + 15
-// and half of dq's and dk's columns.  What dlog_decay and dbeta are made of has fp32's
-// precision (three parts); what ends in a 16-bit dk alone has two parts, 2^-17.  The sums of
-// q . dq, dx . v and <S, dS>, whose difference dlog_decay is, are fp64.
+// The columns are taken 32 at a time, through LDS (one slice there: with two, which fit up to Dk = 64, both
+// passes took 954 us for 953 at Dk = 64); wave (w, half) owns rows 16 w .. + 15 and half of dq's and dk's
+// columns.  All operands have three parts: with two in what ends in a 16-bit dk alone (2^-17 of its terms) both passes
+// took 30 us less of 1221 at the size below.  The sums of q . dq, dx . v and <S, dS>, whose difference dlog_decay
+// is, are fp64.
 //
 // Reading x instead of solving for it again took 830 to 534 us (4 sequences of 4096 rows, 16 heads of
 // 128 x 128, bf16), loads of a slice ahead of its products 495 us, two slices in LDS and decays without
@@ -36,14 +37,14 @@ constexpr int kT = 512, kCols = 32, kSlice = kCols + 8, kLdM = kChunk + 8;
 template <typename T, int DK>
 struct GradLds {
   typedef Team<T, DK, 1> F;
-  static constexpr int NP = F::NP, GP = F::YP;
+  static constexpr int NP = F::NP;
   union {
     struct {
-      __bf16 s[kParts * DK * kSlice], ds[GP * DK * kSlice];          // 32 columns of both states, rows d
-      __bf16 u[kParts * kChunk * kSlice], dx[GP * kChunk * kSlice];  // rows of the chunk
-    } slice[NP == 3 ? 1 : 2];
+      __bf16 s[kParts * DK * kSlice], ds[kParts * DK * kSlice];          // 32 columns of both states, rows d
+      __bf16 u[kParts * kChunk * kSlice], dx[kParts * kChunk * kSlice];  // rows of the chunk
+    } slice;
     struct {
-      __bf16 p[kParts * kChunk * kLdM], l[GP * kChunk * kLdM];       // dP and dL
+      __bf16 p[kParts * kChunk * kLdM], l[kParts * kChunk * kLdM];       // dP and dL
       __bf16 rows[NP * RowsAt<DK>::part];                            // k, then q
     };
   };
@@ -57,7 +58,7 @@ template <typename T, int DK, bool WHOLE>
 struct Grad {
   typedef Team<T, DK, 1> F;
   typedef GradLds<T, DK> Lds;
-  static constexpr int NP = F::NP, GP = F::YP, DT = DK / 32;  // DT: 16-row tiles of a half of dq's columns
+  static constexpr int NP = F::NP, DT = DK / 32;  // DT: 16-row tiles of a half of dq's columns
   static constexpr int each = DK * kCols / 4 / kT;                          // pieces of 4 floats of a slice a thread
   static_assert(each >= 1 || DK == 32, "slices");
   static constexpr int held = each ? each : 1;
@@ -272,9 +273,10 @@ struct Grad {
     float db = 0.f;
     double dot = 0, dxv = 0;
     // what was fetched, into LDS, and dy into yp
-    const auto put = [&](auto& to) {
+    const auto put = [&] {
+      auto& to = s.slice;
       put_state<kParts>(to.s, x.st);
-      put_state<GP>(to.ds, x.ds);
+      put_state<kParts>(to.ds, x.ds);
 #pragma unroll
       for (int n = 0; n < held; ++n)
 #pragma unroll
@@ -290,7 +292,7 @@ struct Grad {
         dxv = fma((double)dx[e], (double)to_f32(v[e]), dxv);
       }
       put_row<kParts>(to.u, u);
-      put_row<GP>(to.dx, dx);
+      put_row<kParts>(to.dx, dx);
       Raw8<T> dy = x.dy;
 #pragma unroll
       for (unsigned n = 0; n < sizeof(T) / 2; ++n)
@@ -309,41 +311,38 @@ struct Grad {
     f32x4_t dkr[DT], dkc[DT], dp[2] = {zero, zero}, dl[2] = {zero, zero};
 #pragma unroll
     for (int t = 0; t < DT; ++t) dq[t] = dkr[t] = dkc[t] = zero;
-    put(s.slice[0]);
+    put();
     fetch(kCols);
     __syncthreads();
     Rows64<T, DK, kT> k, q;
-    constexpr int kTurns = NP == 3 ? 1 : 2;
-    int turn = 0;
 #pragma clang loop unroll(disable)
     for (int v0 = 0; v0 < a.dvp; v0 += kCols) {
       renew();
       {
-        auto& at = s.slice[turn];
+        auto& at = s.slice;
         const auto up = slice<kParts>(at.u, row(), kChunk);
-        const auto xp = slice<GP>(at.dx, row(), kChunk);
+        const auto xp = slice<kParts>(at.dx, row(), kChunk);
 #pragma unroll
         for (int t = 0; t < DT; ++t) {
           const int d = 16 * (half * DT + t) + m;
           const auto sp = slice<kParts>(at.s, d, DK);
-          const auto dsp = slice<GP>(at.ds, d, DK);
+          const auto dsp = slice<kParts>(at.ds, d, DK);
           dq[t] = mma(yp, sp, dq[t]);
-          dkr[t] = mma_first<GP>(xp, sp, dkr[t]);
-          dkc[t] = mma_first<GP>(up, dsp, dkc[t]);
+          dkr[t] = mma(xp, sp, dkr[t]);
+          dkc[t] = mma(up, dsp, dkc[t]);
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n)
           if (half + 2 * n <= wave) {
             const auto uj = slice<kParts>(at.u, 16 * (half + 2 * n) + m, kChunk);
             dp[n] = mma(yp, uj, dp[n]);
-            dl[n] = mma_first<GP>(xp, uj, dl[n]);
+            dl[n] = mma(xp, uj, dl[n]);
           }
       }
-      turn = (turn + 1) % kTurns;
       if (v0 + kCols < a.dvp) {
-        if (kTurns == 1) __syncthreads();  // what is read of the slice
+        __syncthreads();  // what is read of the slice
         renew();
-        put(s.slice[turn]);
+        put();
         __builtin_amdgcn_sched_barrier(0);  // the next slice takes this one's registers over
         fetch(v0 + 2 * kCols);
       } else {
@@ -376,21 +375,21 @@ struct Grad {
     get_decay(decay);
     renew();
     put_matrix<true, kParts>(s.p, dp, decay, a.scale);
-    put_matrix<false, GP>(s.l, dl, decay, -1.f);
+    put_matrix<false, kParts>(s.l, dl, decay, -1.f);
     k.put(s.rows);
     __syncthreads();
     const bool wild = s.wild;
     renew();
     add<false, kParts>(s.p, dq, wild);
     renew();
-    add<false, GP>(s.l, dk, wild);
+    add<false, kParts>(s.l, dk, wild);
     renew();
-    add<true, GP>(s.l, dk, wild);
+    add<true, kParts>(s.l, dk, wild);
     __syncthreads();
     q.put(s.rows);
     __syncthreads();
     renew();
-    add<true, GP>(s.p, dk, wild);
+    add<true, kParts>(s.p, dk, wild);
     renew();
 #pragma unroll
     for (int r = 0; r < 4; ++r) {

@@ -19,7 +19,6 @@ struct ColsAt {
 template <typename T, int DK, int NC>
 struct Team {
   static constexpr int NP = InParts<T>::n, KS = DK / 32, DT = DK / 16;
-  static constexpr int YP = NP == 3 ? 3 : 2;                // parts that an output of type T can tell apart
   typedef ColsAt<DK> State;
   typedef ColsAt<kChunk> Rows;
 
@@ -153,16 +152,5 @@ struct Team {
     }
   }
 };
-
-// acc += A B where the first N of B's parts are used.
-template <int N, int NA, int NB>
-__device__ __forceinline__ f32x4_t mma_first(const Parts<NA>& a, const Parts<NB>& b, f32x4_t acc) {
-#pragma unroll
-  for (int i = NA - 1; i >= 0; --i)
-#pragma unroll
-    for (int j = N - 1; j >= 0; --j)
-      if (i + j < (N > NA ? N : NA)) acc = convfwd::mfma16x16x32(a.p[i], b.p[j], acc);
-  return acc;
-}
 
 }  // namespace convdelta

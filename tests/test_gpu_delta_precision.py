@@ -65,3 +65,75 @@ def test_y_of_products_of_many_bits(dtype):
     _row(x, "v", 0, 1, 1)
     _row(x, "v", 1, -1, -1)
     assert _forward(x).y[0, 2, 0].tolist() == [E, E, 0, 0]
+
+
+def _dk(x):
+    f = _forward(x, train=True)
+    g = igc.delta_rule_bwd(x["dy"], x["q"], x["k"], x["v"], x["log_decay"], x["beta"], f.states, scale=1.0, dh=x["dh"])
+    return g.dk[0, :, 0]
+
+
+@pytest.mark.parametrize("bits_in", ["state", "gradient"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_dk_of_the_state_before(dtype, bits_in):
+    """dk = -S dx = -((F + 2^-20) - F), the many bits in S or in dx."""
+    x = _zeros(1, dtype)
+    _row(x, "k", 0, 0, 1)
+    many, ones = torch.tensor([F + E, F]), torch.tensor([1.0, 1.0])
+    x["h0"][0, 0, 0, :2] = (many if bits_in == "state" else ones) * torch.tensor([1, -1])
+    x["dh"][0, 0, 1, :2] = ones if bits_in == "state" else many
+    assert _dk(x).tolist() == [[-E] + [0] * 7]
+
+
+@pytest.mark.parametrize("bits_in", ["gradient", "correction"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_dk_of_the_gradient_behind(dtype, bits_in):
+    """dk = dS u = (F + 2^-20) - F, the many bits in dS or in u = v - S k."""
+    x = _zeros(1, dtype)
+    _row(x, "k", 0, 0, 1)
+    _row(x, "v", 0, 1, 1)
+    if bits_in == "gradient":
+        x["dh"][0, 0, 0, :2] = torch.tensor([F + E, -F])
+    else:
+        x["dh"][0, 0, 0, :2] = torch.tensor([1, -1])
+        x["h0"][0, 0, 1, :2] = 1 - torch.tensor([F + E, F])
+    assert _dk(x).tolist() == [[E] + [0] * 7]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_dk_of_the_rows_before(dtype):
+    """dk_2 = -(dx_2 u_0) k_0 - (dx_2 u_1) k_1 = -((F + 2^-20) - F) in its first element."""
+    x = _zeros(3, dtype)
+    _row(x, "k", 0, 1, 1)
+    _row(x, "k", 1, -1, 1)
+    _row(x, "k", 2, 0, 0, 1)
+    _row(x, "v", 0, 1)
+    _row(x, "v", 1, 0, 1)
+    x["dh"][0, 0, 2, :2] = torch.tensor([F + E, F])
+    assert _dk(x)[2, 0].item() == -E
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_dk_of_the_rows_after(dtype):
+    """dk_0 = dS u_0 - (dx_1 u_0) k_1 - (dx_2 u_0) k_2 = 2^-21 - ((F + 2^-20) - F) in its second element."""
+    x = _zeros(3, dtype)
+    _row(x, "k", 0, 1)
+    _row(x, "k", 1, 0, 1, 1)
+    _row(x, "k", 2, 0, -1, 1)
+    _row(x, "v", 0, 1)
+    x["dh"][0, 0, 1:3, 0] = torch.tensor([E / 2, F + E / 2])
+    assert _dk(x)[0, 1].item() == -E / 2
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_dk_of_the_reads_after(dtype):
+    """dk_0 = (dy_1 u_0) q_1 + (dy_2 u_0) q_2 = (F + 2^-20) - F in its second element."""
+    x = _zeros(3, dtype)
+    _row(x, "k", 0, 1)
+    _row(x, "v", 0, 1, 1)
+    x["h0"][0, 0, 0, :2] = 1 - torch.tensor([F + E, F])
+    _row(x, "q", 1, 0, 1)
+    _row(x, "q", 2, 0, -1)
+    _row(x, "dy", 1, 1)
+    _row(x, "dy", 2, 0, 1)
+    assert _dk(x)[0, 1].item() == E
