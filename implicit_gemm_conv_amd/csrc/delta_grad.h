@@ -216,7 +216,7 @@ struct Grad {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = own + r;
-        const bool in = decay[n][r] >= 0.f && (EDGE ? j <= i : j < i);
+        const bool in = !(decay[n][r] < 0.f) && (EDGE ? j <= i : j < i);  // a NaN decay is wanted
         __bf16 w[N];
         split_one<N>(in ? factor * decay[n][r] * acc[n][r] : 0.f, w);
 #pragma unroll
@@ -232,7 +232,7 @@ struct Grad {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = own + r;
-        const float d = expf((float)fmin(s.sums[i] - s.sums[j], 0.));
+        const float d = expf((float)(s.sums[i] - s.sums[j]));
         decay[n][r] = s.seq[i] == s.seq[j] ? d : -1.f;
       }
     }

@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
     for (int r = 0; r < 4; ++r) {
       const int i = f.row() + r;
       const bool same = j <= i && ni[r] == nj;
-      const float d = expf((float)fmin(si[r] - sj, 0.));  // no branch: what is not wanted is selected away
+      const float d = expf((float)(si[r] - sj));  // no branch: what is not wanted is selected away
       s.low[i * kLd + j] = same && j < i ? d * kk[tj][r] : 0.f;
       s.read[i * kLd + j] = same ? d * qk[tj][r] : 0.f;
     }

@@ -22,6 +22,10 @@
  * rounded once, to nearest even, and sums are added in a fixed order: the same
  * call gives the same bits.
  *
+ * log_decay may have either sign.  Rows are taken 64 at a time (0 .. 63, 64 .. 127, ...), and errors are relative to what a
+ * state would grow to inside them if nothing were subtracted from it: log decays above zero whose sum there is g cost a
+ * factor of up to exp(g).  Where that overflows, the forward pass goes row by row, and gradients are not finite.
+ *
  * starts (B, T), bytes, may be NULL: a nonzero byte marks a row that begins a
  * new sequence, as in convseq.h.  Nothing, NaN and infinities included, crosses
  * a start.  A decay that is zero in fp32 drops the state as a start does.  In the
