@@ -143,7 +143,8 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
   if (wave == 0) {
     // running sums over the rows, a lane a row (this wave has the fewest products)
     // a decay of nothing at all is exp(-10^4), which is zero too and leaves differences of sums finite
-    g = g < -1e4f ? -1e4f : g;
+    // what is at a start acts on nothing, whatever it is
+    g = start ? 0.f : g < -1e4f ? -1e4f : g;
     double sum = g;
     int n = start;
     for (int o = 1; o < 64; o <<= 1) {

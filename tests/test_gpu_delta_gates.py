@@ -35,8 +35,7 @@ def _grown(x, starts=None):
 
 def _check_all(got, ref):
     for n in got:
-        if n != "states":
-            check(got[n], ref[n], n, np.ones(1, dtype=bool))
+        check(got[n], ref[n], n, np.ones(1, dtype=bool))
 
 
 GROWTHS = {"0.01": lambda g: torch.full_like(g, 0.01), "0.05": lambda g: torch.full_like(g, 0.05),
@@ -52,11 +51,7 @@ def test_log_decays_above_zero(shape, dtype, growth):
         x = inputs(b + t, *shape, DT[dtype], DEV)
         x["log_decay"] = GROWTHS[growth](x["log_decay"])
         s = starts_of(starts, b, t, DEV)
-        got = _both(x, s)
-        kept = got.pop("states")
-        ref = _grown(x, s)
-        _check_all(got, ref)
-        check(kept, ref["states"], "states", np.ones(1, dtype=bool))
+        _check_all(_both(x, s), _grown(x, s))
 
 
 @pytest.mark.parametrize("dtype", list(DT))
@@ -125,3 +120,17 @@ def test_growth_that_overflows_goes_row_by_row():
     want = 16 ** -0.5 * x["q"][..., :1].double() * x["v"].double()
     bound = 8 * 2.0 ** -24 * np.exp(3.0) * x["v"].abs().max().item() * 16 ** -0.5 * x["q"][..., :1].double().abs()
     assert ((y - want).abs() <= bound + 2.0 ** -24 * want.abs()).all()
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf"), 100.0])
+def test_a_decay_at_a_start_acts_on_nothing(what):
+    """Whatever it is: at the first row of all, inside a chunk, at a chunk's edge, twice in a row."""
+    x = inputs(22, 1, 190, 2, 2, 32, 32, torch.float32, DEV)
+    starts = torch.zeros((1, 190), dtype=torch.bool, device=DEV)
+    at = [0, 20, 64, 100, 101, 189]
+    starts[0, at] = True
+    x["log_decay"][0, at, 1] = what
+    got, ref = _both(x, starts), definition(x, None, starts)
+    for n in got:
+        check(got[n], ref[n], n)
+    assert (got["dlog_decay"][:, at] == 0).all()
