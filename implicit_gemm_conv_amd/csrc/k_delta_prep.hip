@@ -136,16 +136,17 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
   const bool in = wave == 0 && t < a.t;
   const int64_t row = ((int64_t)f.b * a.t + t) * a.hv + f.h;
   const float bt = in ? a.beta[row] : 0.f;
-  float g = in ? a.log_decay[row] : 0.f;
-  const int start = in && a.starts ? a.starts[(int64_t)f.b * a.t + t] != 0 : 0;
+  const float g = in ? a.log_decay[row] : 0.f;
+  int start = in && a.starts ? a.starts[(int64_t)f.b * a.t + t] != 0 : 0;
   f.put_rows(s.k, k);
   __syncthreads();
   if (wave == 0) {
     // running sums over the rows, a lane a row (this wave has the fewest products)
-    // a decay of nothing at all is exp(-10^4), which is zero too and leaves differences of sums finite
+    // a decay that is zero in fp32 drops the state: its row begins a sequence too, and its gradient is zero
+    const float step = start ? 0.f : expf(g);
+    start |= step == 0.f;
     // what is at a start acts on nothing, whatever it is
-    g = start ? 0.f : g < -1e4f ? -1e4f : g;
-    double sum = g;
+    double sum = start ? 0.f : g;
     int n = start;
     for (int o = 1; o < 64; o <<= 1) {
       const int p = __shfl_up(n, o);
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(kT) void delta_prep_kernel(DeltaArgs a, int backwar
     rows[lane] = n == 0 ? expf((float)sum) : 0.f;
     rows[kChunk + lane] = n == last ? expf((float)(all - sum)) : 0.f;
     rows[2 * kChunk + lane] = bt;
-    rows[3 * kChunk + lane] = start ? 0.f : expf(g);
+    rows[3 * kChunk + lane] = step;
     if (backward) {
       a.w.sums[at * kChunk + lane] = sum;
       a.w.seq[at * kChunk + lane] = n;

@@ -28,10 +28,10 @@
  *
  * starts (B, T), bytes, may be NULL: a nonzero byte marks a row that begins a
  * new sequence, as in convseq.h.  Nothing, NaN and infinities included, crosses
- * a start.  A decay that is zero in fp32 drops the state as a start does.  In the
- * forward pass a NaN or an infinity reaches no earlier row and, where it came
- * with v, no other column; an infinity may come back as NaN.  In the backward
- * pass it may reach all rows of its sequence within its 64 rows.
+ * a start.  A decay that is zero in fp32 makes its row a start (its gradient is
+ * zero).  In the forward pass a NaN or an infinity reaches no earlier row and,
+ * where it came with v, no other column; an infinity may come back as NaN.  In the
+ * backward pass it may reach all rows of its sequence within its 64 rows.
  *
  * Ownership, streams, workspaces and errors are those of convseq.h.  B = 0 and
  * T = 0 are valid: the state passes through.  CONVFWD_ERR_TOO_LARGE: Hv * Dv of

@@ -134,3 +134,22 @@ def test_a_decay_at_a_start_acts_on_nothing(what):
     for n in got:
         check(got[n], ref[n], n)
     assert (got["dlog_decay"][:, at] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("zero", [-float("inf"), -200.0, -3e38])
+def test_a_decay_of_zero_is_a_start(zero, dtype):
+    """A log decay whose exponential is zero in fp32: the same bits as a start at its row, whatever large values stand before
+    it, and a gradient that is exactly zero."""
+    x = inputs(23, 1, 190, 1, 2, 40, 32, DT[dtype], DEV)
+    for n in ("v", "dy"):
+        x[n][:, :100] *= 64
+    at = [20, 64, 100, 101, 189]
+    starts = torch.zeros((1, 190), dtype=torch.bool, device=DEV)
+    starts[0, at] = True
+    want = _both(x, starts)
+    x["log_decay"][0, at] = zero
+    got = _both(x)
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
+    assert (got["dlog_decay"][:, at] == 0).all()
