@@ -254,7 +254,8 @@ struct Grad {
     const Range before(c ? a.w.dstate + (at - 1) * size_p : a.dh0 + bh * size, (c ? size_p : size) * 4);
     const int ldb = c ? a.dvp : a.dv;
     const Range zs(a.w.z + at * kChunk * a.dvp, (int64_t)kChunk * a.dvp * 4);
-    const Range xs(a.x_in + ((int64_t)b * a.t + c * kChunk) * a.hv * a.dv + (int64_t)h * a.dv, (int64_t)rows * a.hv * a.dv * 4);
+    const Span kept = dense_rows(a, b, h, c, 4);
+    const Range xs((const char*)a.x_in + kept.at, kept.bytes);
     const Range vs = rows_range<T>(a.v, b, h, c * kChunk, a.t, a.dv), dys = rows_range<T>(a.dy, b, h, c * kChunk, a.t, a.dv);
     __syncthreads();  // what is read of the head before
     const float my_beta = load_at<float>(a.w.rows + (at * 4 + 2) * kChunk, (uint32_t)(tid / 8) * 4u);

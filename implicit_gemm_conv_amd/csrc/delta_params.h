@@ -49,6 +49,17 @@ struct DeltaArgs {
   Work w;
 };
 
+// Rows of one chunk c of one head of a dense (B, T, Hv, Dv) tensor: where they begin, and the bytes to the end of the last
+// row's own Dv, both in bytes.  (The rest of that row, other heads, may be past the tensor's end.)
+struct Span {
+  int64_t at, bytes;
+};
+inline __host__ __device__ Span dense_rows(const DeltaArgs& a, int b, int h, int c, int elem) {
+  const int left = a.t - c * kChunk, rows = left < kChunk ? left : kChunk;
+  const int64_t row = (int64_t)a.hv * a.dv;
+  return {(((int64_t)b * a.t + c * kChunk) * row + (int64_t)h * a.dv) * elem, ((rows - 1) * row + a.dv) * elem};
+}
+
 struct DeltaStepArgs {
   int b, hk, hv, dk, dv, dtype, n_slots;
   float scale;

@@ -120,8 +120,8 @@ struct Team {
   template <typename E>
   __device__ __forceinline__ void store_col(void* to, int c, const f32x4_t (&v)[NC], int first = 0, int end = kChunk) const {
     const uint32_t ld = (uint32_t)(a.hv * a.dv) * (uint32_t)sizeof(E);
-    const Range p((E*)to + ((int64_t)b * a.t + c * kChunk) * (a.hv * a.dv) + (int64_t)h * a.dv,
-                  (int64_t)min(kChunk, a.t - c * kChunk) * ld);
+    const Span rows = dense_rows(a, b, h, c, sizeof(E));
+    const Range p((char*)to + rows.at, rows.bytes);
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       const uint32_t at = col(n) < a.dv ? row() * ld + (uint32_t)col(n) * (uint32_t)sizeof(E) : kNowhere;
