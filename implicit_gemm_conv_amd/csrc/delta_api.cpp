@@ -115,9 +115,8 @@ int prepare(DeltaArgs* a, bool backward, hipStream_t s) {
   if (!pieces(a->q, a->dk, eb) || !pieces(a->k, a->dk, eb)) {
     const int rc = launched(launch_delta_pack(*a, a->q, a->k, s));
     if (rc < 0) return rc;
-    const int64_t row = (int64_t)a->hk * a->dkp;
-    a->q = Heads{a->w.q, a->t * row, row, a->dkp};
-    a->k = Heads{a->w.k, a->t * row, row, a->dkp};
+    a->q = packed_rows(a->w.q, a->t, a->hk, a->dkp);
+    a->k = packed_rows(a->w.k, a->t, a->hk, a->dkp);
   }
   return launched(launch_delta_prep(*a, backward, s));
 }

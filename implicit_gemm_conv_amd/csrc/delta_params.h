@@ -32,7 +32,7 @@ struct Work {
   int* seq;        // backward: 64 sequence numbers inside the chunk
   float* z;        // backward: z, (B * Hv, chunks * 64, dvp)
   float* dstate;   // backward: the gradient of the state after each chunk, (.., Dk, dvp)
-  void *q, *k;     // (B, T, Hk, dkp) copies, where q or k are not 16-byte aligned rows of whole 16 bytes
+  void *q, *k;     // (B, Hk, T, dkp) copies, where q or k are not 16-byte aligned rows of whole 16 bytes, or far apart
 };
 
 struct DeltaArgs {
@@ -58,6 +58,11 @@ inline __host__ __device__ Span dense_rows(const DeltaArgs& a, int b, int h, int
   const int left = a.t - c * kChunk, rows = left < kChunk ? left : kChunk;
   const int64_t row = (int64_t)a.hv * a.dv;
   return {(((int64_t)b * a.t + c * kChunk) * row + (int64_t)h * a.dv) * elem, ((rows - 1) * row + a.dv) * elem};
+}
+
+// Those copies: a head's rows one after the other, so that 64 of them have offsets of 32 bits however many heads there are.
+inline __host__ __device__ Heads packed_rows(const void* p, int t, int hk, int dkp) {
+  return {p, (int64_t)hk * t * dkp, dkp, (int64_t)t * dkp};
 }
 
 struct DeltaStepArgs {

@@ -229,8 +229,10 @@ __global__ __launch_bounds__(kT) void delta_pack_kernel(DeltaArgs a, Heads q, He
     vq[e] = d0 + e < a.dk ? fq[d0 + e] : (T)0.f;
     vk[e] = d0 + e < a.dk ? fk[d0 + e] : (T)0.f;
   }
-  __builtin_memcpy(__builtin_assume_aligned((T*)a.w.q + i * 8, 16), vq, sizeof(vq));
-  __builtin_memcpy(__builtin_assume_aligned((T*)a.w.k + i * 8, 16), vk, sizeof(vk));
+  const Heads to = packed_rows(nullptr, a.t, a.hk, a.dkp);
+  const int64_t at = b * to.sb + t * to.st + h * to.sh + d0;
+  __builtin_memcpy(__builtin_assume_aligned((T*)a.w.q + at, 16), vq, sizeof(vq));
+  __builtin_memcpy(__builtin_assume_aligned((T*)a.w.k + at, 16), vk, sizeof(vk));
 }
 
 }  // namespace

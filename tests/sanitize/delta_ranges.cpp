@@ -38,9 +38,25 @@ void dense(int b, int t, int hv, int dv, int elem) {
       }
 }
 
+// 64 rows of the copies of q and k, whatever the number of heads: offsets below 2^31, where the offset that marks what is
+// not there lies, and every element of the copy its own.
+void packed(int b, int t, int hk, int dkp, int elem) {
+  const Heads h = packed_rows(nullptr, t, hk, dkp);
+  const int64_t far = (63 * h.st + dkp) * elem;
+  expect(far < (int64_t)1 << 31, "64 rows of a copy", far, (int64_t)1 << 31);
+  const int64_t last = (b - 1) * h.sb + (t - 1) * h.st + (hk - 1) * h.sh + dkp, all = (int64_t)b * t * hk * dkp;
+  expect(last == all, "a copy's last element", last, all);
+  expect(h.st >= dkp && h.sh == t * h.st && h.sb == hk * h.sh, "a copy's strides", h.st, dkp);
+}
+
 }  // namespace
 
 int main() {
+  for (const int elem : {2, 4})
+    for (const int b : {1, 3})
+      for (const int t : {1, 64, 1000})
+        for (const int hk : {1, 7, 1 << 17, 1 << 18, (1 << 21) - 1})
+          for (const int dkp : {8, 72, 120, 128}) packed(b, t, hk, dkp, elem);
   for (const int elem : {2, 4})
     for (const int b : {1, 2})
       for (const int t : {1, 2, 63, 64, 65, 130})
