@@ -105,7 +105,7 @@ __global__ __launch_bounds__(kThreads) void norm_team_fwd_kernel(NormArgs a) {
     off = sum_of<WIDE>(off, team, lds) * inv;
     mean += off;
     const float var = fmaf(-off, off, sum_of<WIDE>(sum, team, lds) * inv);
-    const float rstd = 1.f / sqrtf(fmaxf(var, 0.f) + a.eps);
+    const float rstd = 1.f / sqrtf((var < 0.f ? 0.f : var) + a.eps);  // NaN stays
     if (t.lane == 0 && t.n(turn) < a.n) {
       a.mean[t.n(turn) * a.groups + t.g] = mean;
       a.rstd[t.n(turn) * a.groups + t.g] = rstd;
