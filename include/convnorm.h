@@ -16,7 +16,11 @@
  * of weight and bias are fp32.  All arithmetic is fp32 (the sums of tiles are
  * joined in fp64), results are rounded once, to nearest even, and sums are added
  * in a fixed order: the same call gives the same bits.  The variance is taken
- * about each tile's own mean, never as a difference of large squares.
+ * about the mean where a group fits one workgroup's registers.  In larger groups
+ * each channel's runs of r positions (8, or more of large tensors) take theirs
+ * about their first value, which costs up to r times fp32's error where that
+ * value is an outlier, and are joined about the mean: nothing depends on how far
+ * the mean is from zero.
  *
  * An infinity or a NaN in a group makes the whole group NaN, as the formula
  * has it, and touches no other group; in the backward pass it also reaches the

@@ -27,3 +27,25 @@ def test_statistics_of_a_bad_group(dtype, bad, n, p, c, groups):
         got = igc.group_norm(broken, groups, weight=w, bias=b, activation="silu", eps=eps)
         assert got.rstd[hit].isnan().all() and not got.mean[hit].isfinite().any()
         assert torch.equal(got.rstd[~hit], clean.rstd[~hit]) and torch.equal(got.mean[~hit], clean.mean[~hit])
+
+
+def test_runs_that_begin_with_an_outlier():
+    """128 positions a thread, of which the first is 2^10 off.  A run of r values about its first one, with squares s and sum m:
+    s - m^2 / r has (r + 1) half steps of s from the first term, 2 r from the second (m has r half steps of the sum of |d|, at
+    most sqrt(r s)) and three more, and r times 2^20 for s; the whole variance is 2^20 / r and the spread's."""
+    n, p, c, groups, r = 128, 2048, 1024, 64, 128
+    gen = torch.Generator(DEV).manual_seed(3)
+    x = torch.randn((n, p, c), generator=gen, device=DEV)
+    x[:, ::r] += 2.0 ** 10
+    f = igc.group_norm(x, groups)
+    for i in (0, 77, n - 1):
+        d = x[i].double().view(p, groups, c // groups)
+        mean = d.mean((0, 2))
+        var = ((d - mean[:, None]) ** 2).mean((0, 2))
+        error = (3 * r + 4) * 2.0 ** -24 * 2.0 ** 20 / var
+        rstd = torch.rsqrt(var + 1e-5)
+        assert ((f.rstd[i].double() / rstd - 1).abs() <= 0.5 * error + 2.0 ** -21).all()
+        # a run's mean: its first value, r half steps of the mean distance to it, and one of each
+        assert ((f.mean[i].double() - mean).abs() <= (r + 3) * 2.0 ** -24 * 2.0 ** 10).all()
+        y = ((d - mean[:, None]) * rstd[:, None]).view(p, c)
+        assert ((f.y[i].double() - y).abs() <= (0.5 * error.max() + 2.0 ** -20) * y.abs() + (r + 3) * 2.0 ** -14 * rstd.max()).all()
