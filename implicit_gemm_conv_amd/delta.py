@@ -101,6 +101,8 @@ def _inputs(q, k, v, log_decay, beta, scale, dims):
         if t.shape != (*rows, hk, dk) or t.dtype is not dtype or t.device != device:
             raise ValueError(f"{what} must be {dtype} of shape {(*rows, hk, dk)} on {device}, "
                              f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if dk < 1 or dv < 1:
+        raise ValueError(f"heads must have at least one element, got {dk} of q and k and {dv} of v")
     if hk < 1 or hv < 1 or hv % hk:
         raise ValueError(f"the heads of v must be a multiple of those of q and k, got {hv} and {hk}")
     gates = (*rows, hv)

@@ -160,3 +160,17 @@ def test_rows_that_are_too_far_apart():
     lib = dl._delta()
     assert lib.convdelta_fwd_workspace(_desc(b=1, t=1, hk=1, hv=8, dv=1 << 20)) == LARGE
     assert lib.convdelta_fwd_workspace(_desc(b=1, t=1, hk=1, hv=8, dv=(1 << 20) - 1)) > 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [None, 1.0])
+@pytest.mark.parametrize("dk,dv", [(0, 8), (8, 0), (0, 0)])
+def test_heads_without_elements_are_refused(dk, dv, scale):
+    dev = "cuda:0"
+    q, v, g = torch.zeros(1, 4, 1, dk, device=dev), torch.zeros(1, 4, 1, dv, device=dev), torch.zeros(1, 4, 1, device=dev)
+    h = torch.zeros(1, 1, dk, dv, device=dev)
+    for call in (lambda: igc.delta_rule(q, q, v, g, g, scale=scale),
+                 lambda: igc.delta_rule_bwd(v, q, q, v, g, g, igc.DeltaStates(h[:, None], v), scale=scale),
+                 lambda: igc.delta_rule_step(q[:, 0], q[:, 0], v[:, 0], g[:, 0], g[:, 0], h, scale=scale)):
+        with pytest.raises(ValueError, match="at least one element"):
+            call()
