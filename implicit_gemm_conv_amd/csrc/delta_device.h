@@ -15,9 +15,11 @@
 // Products run on the bf16 matrix units at fp32's precision: an fp32 value is the
 // sum of three bf16 parts (8 significant bits each), and of the parts' products
 // those that matter to 24 bits are added in fp32.  A bf16 input is one part, an
-// fp16 input two.  bf16 has fp32's range, so nothing overflows on the way.
+// fp16 input two.  bf16 has fp32's range but not its last value's neighbourhood: from 2^128 - 2^119
+// on the first part rounds to infinity and the value counts as one (as NaN, with what is left of it).  At the other
+// end the third part runs out of bf16's range first: from about 2^-95 down bits are lost, at 2^-110 the last.
 //
-// A workgroup of eight waves carries 16 columns of one head's state (or of its
+// A workgroup of eight waves carries 16 or 32 columns of one head's state (or of its
 // gradient), four of them in each of two roles.  Wave w of a role computes rows 16 w
 // .. + 15 of a chunk's r, x and y, and each wave 16 rows of the state; the parts of what
 // one step makes and the next one contracts over go through LDS, column by column, so
@@ -275,8 +277,14 @@ inline hipError_t for_dk(int dk, const F& f) {
 }
 
 // The recurrences' columns a workgroup, in tiles of 16: one where the workgroups are then no more than the 256 CUs (two
-// would leave more of them idle), and two, which read q, k and the chunks' matrices once for both, where they are more
-// (4x4096 rows, 16 heads of 128 x 128, bf16: forward 291 us for 387, backward 319 for 434).
+// would leave more of them idle), and two, which read q, k and the chunks' matrices once for both, where they are more.
+// 4096 rows of 128 x 128, states kept, one tile and two, forward and backward pass as called:
+//   16 heads, bf16 (128 workgroups of one tile)   181 and 308 us, 255 and 371
+//   32 heads, bf16 (256)                          231 and 474,    279 and 530
+//   36 heads, bf16 (288)                          415 and 677,    302 and 575
+//   64 heads, bf16 (512)                          511 and 955,    368 and 836
+//   32 and 36 heads, fp32, forward alone          343 and 611,    411 and 433
+// and with heads of 64 x 64 the same way (64 heads 254 and 281 us forward, 80 heads 441 and 320).
 template <typename F>
 inline hipError_t for_columns(const DeltaArgs& a, const F& f) {
   return (int64_t)a.b * a.hv * ((a.dv + 15) / 16) > 256 ? f(Int<2>{}) : f(Int<1>{});

@@ -20,11 +20,14 @@
  * log_decay, beta and the gradients of those are fp32.  Arithmetic has fp32's
  * precision throughout (sums of log decays within 64 rows are fp64), results are
  * rounded once, to nearest even, and sums are added in a fixed order: the same
- * call gives the same bits.
+ * call gives the same bits.  Values of less than 2^-95 lose bits, and fp32 values of
+ * 2^128 - 2^119 or more count as infinities.
  *
- * log_decay may have either sign.  Rows are taken 64 at a time (0 .. 63, 64 .. 127, ...), and errors are relative to what a
- * state would grow to inside them if nothing were subtracted from it: log decays above zero whose sum there is g cost a
- * factor of up to exp(g).  Where that overflows, the forward pass goes row by row, and gradients are not finite.
+ * log_decay may have either sign.  Rows are taken 64 at a time (0 .. 63, 64 ..
+ * 127, ...), and errors are relative to what a state would grow to inside them if
+ * nothing were subtracted from it: log decays above zero whose sum there is g cost
+ * a factor of up to exp(g).  Where that overflows, the forward pass goes row by
+ * row, and gradients are not finite.
  *
  * starts (B, T), bytes, may be NULL: a nonzero byte marks a row that begins a
  * new sequence, as in convseq.h.  Nothing, NaN and infinities included, crosses

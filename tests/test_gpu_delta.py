@@ -364,3 +364,13 @@ def test_kept_tensors_at_any_element(dtype, dv):
     got = igc.delta_rule_bwd(x["dy"], *_ins(x), igc.DeltaStates(*map(moved, f.states)), dh=moved(x["dh"]))
     for n, t in got._asdict().items():
         assert torch.equal(t, getattr(want, n)), n
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_one_row_at_every_position(dtype):
+    """Inputs whose rows are all one row in memory (a row stride of zero), in a last chunk that is not whole."""
+    x = inputs(24, 2, 90, 2, 2, 32, 24, DT[dtype], DEV)
+    for n in ("q", "k", "v", "dy"):
+        x[n] = x[n][:, :1].expand_as(x[n])
+    a, b = _both(x), _both({n: t.contiguous() for n, t in x.items()})
+    assert all(torch.equal(a[n], b[n]) for n in a)

@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import implicit_gemm_conv_amd as igc
+from tests.delta_cases import inputs
 from tests.seq_cases import DT
 
 pytestmark = pytest.mark.gpu
@@ -137,3 +138,14 @@ def test_dk_of_the_reads_after(dtype):
     _row(x, "dy", 1, 1)
     _row(x, "dy", 2, 0, 1)
     assert _dk(x)[0, 1].item() == E
+
+
+@pytest.mark.parametrize("power", [-90, -60, 60, 120])
+def test_powers_of_two_change_no_bits(power):
+    """v and the first state times 2^power: y and the last state are that much larger, bit for bit, where the smallest of an
+    fp32 value's three parts is still a bf16 number and nothing overflows."""
+    x = inputs(25, 1, 130, 1, 2, 32, 24, torch.float32, DEV)
+    big = {n: (x[n].double() * 2.0 ** power).float() for n in ("v", "h0")}
+    a, b = _forward(x), _forward({**x, **big})
+    for n in ("y", "h"):
+        assert torch.equal((getattr(a, n).double() * 2.0 ** power).float(), getattr(b, n)), n
