@@ -204,7 +204,7 @@ int convdelta_bwd(const convdelta_desc* d, const convdelta_heads* dy, const conv
   a.x_in = (const float*)x;
   a.starts = (const uint8_t*)starts; a.dh_last = (const float*)dh_last;
   a.dq = dq; a.dk_ = dk; a.dv_ = dv; a.dlog_decay = (float*)dlog_decay; a.dbeta = (float*)dbeta; a.dh0 = (float*)dh0;
-  a.whole = pieces(a.dy, d->dv, eb) && pieces(a.v, d->dv, eb);
+  a.whole = pieces(a.dy, d->dv, eb);
   lay_out(d, true, (char*)workspace, &a.w);
   const hipStream_t s = (hipStream_t)stream;
   static const Launch bwd[3] = {launch_delta_bwd_f32, launch_delta_bwd_f16, launch_delta_bwd_bf16};

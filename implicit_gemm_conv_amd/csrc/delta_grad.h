@@ -8,18 +8,18 @@
 //   dk = -enter * (dx S^T) + leave * (u dS^T) + dL k + dL^T k + dP^T q
 //   dbeta = z . x
 //
-// A row's decay scales what the row's q and v take part in, the one way and the other: with
-// A the product <state before the chunk, its gradient>,
-//
-//   dlog_decay_i = A - sum over j < i of (q_j . dq_j - dx_j . v_j)
-//
-// and from zero at a start, where the decay acts on nothing.
+// The gradient of a row's log decay is the sum of all terms that its decay is a factor of: with
+//   e_i = scale * enter_i (q_i S) . dy_i - enter_i (k_i S) . dx_i,  f_j = leave_j k_j . (dS u_j)
+//   M_ij = dP_ij (q_i . k_j) + dL_ij (k_i . k_j)  (j < i)
+// dlog_decay_i is the sum of e_l over l >= i, of f_j over j < i, of M_lj over l >= i > j, and stay * <S, dS>.  Every term is
+// as much decayed as the gradient itself, so that its error is fp32's relative to it also where the decay is
+// next to nothing.  (The same as a difference, <S, its gradient> less the rows' q . dq - dx . v, has the error of what is
+// subtracted: with decays of e^-16 it is mostly rounding.)
 //
 // The columns are taken 32 at a time, through LDS (one slice there: with two, which fit up to Dk = 64, both
 // passes took 954 us for 953 at Dk = 64); wave (w, half) owns rows 16 w .. + 15 and half of dq's and dk's
 // columns.  All operands have three parts: with two in what ends in a 16-bit dk alone (2^-17 of its terms) both passes
-// took 30 us less of 1221 at the size below.  The sums of q . dq, dx . v and <S, dS>, whose difference dlog_decay
-// is, are fp64.
+// took 30 us less of 1221 at the size below.
 //
 // Reading x instead of solving for it again took 830 to 534 us (4 sequences of 4096 rows, 16 heads of
 // 128 x 128, bf16), loads of a slice ahead of its products 495 us, two slices in LDS and decays without
@@ -45,11 +45,12 @@ struct GradLds {
     } slice;
     struct {
       __bf16 p[kParts * kChunk * kLdM], l[kParts * kChunk * kLdM];       // dP and dL
-      __bf16 rows[NP * RowsAt<DK>::part];                            // k, then q
+      __bf16 k[NP * RowsAt<DK>::part], q[NP * RowsAt<DK>::part];
     };
   };
-  float gates[3 * kChunk], zx[kChunk];  // enter, leave, beta; z.x
-  double red[kChunk][3];                // dx.v and both halves of q.dq
+  float gates[2 * kChunk], zx[kChunk];  // enter, leave; z.x
+  float red[3][2][kChunk];              // both halves' shares of e, f and the sums of M
+  float after[3][kChunk];               // sums of M's columns over the rows of the waves 1, 2 and 3
   double sums[kChunk], a[kT / 64];
   int seq[kChunk], wild;
 };
@@ -84,17 +85,15 @@ struct Grad {
     own = 16 * wave + 4 * q4;
   }
 
-  // What a slice of 32 columns is made of: pieces of both states and of the gradient before the chunk; 4 columns of a
-  // row of z, x and v; 8 of the lane's row of dy, an operand.
+  // What a slice of 32 columns is made of: pieces of both states; 4 columns of a row of z and x; 8 of the lane's row of
+  // dy, an operand.
   struct Slice {
-    f32x4_t st[held], ds[held], be[held], z, x;
-    typedef uint32_t V __attribute__((ext_vector_type(sizeof(T))));
-    V v;  // as it is in memory
+    f32x4_t st[held], ds[held], z, x;
     Raw8<T> dy;
   };
   // N neighbouring elements of a row, zero past its end: as pieces of at most 16 bytes, where rows are whole ones (WHOLE)
   // or of fp32, whose pieces need no more than their own alignment (4x4096 rows, 16 heads of 128 x 128, bf16: 820 us for
-  // the whole backward pass, 899 with v and dy element by element).
+  // the whole backward pass, 899 with v and dy element by element; v is no longer read here).
   template <typename E, int N>
   __device__ __forceinline__ void load(const Range& x, uint32_t row, int col, int width, void* to) const {
     constexpr int n = WHOLE || sizeof(E) == 4 ? (N * sizeof(E) > 16 ? 16 / sizeof(E) : N) : 1;
@@ -165,7 +164,7 @@ struct Grad {
   // out (own rows, own columns) += M x or M^T x, of M the first N parts; masked: over the rows [lo, hi), which are the
   // only ones added to
   template <bool UP, int N>
-  __device__ __forceinline__ void add_range(const __bf16* mat, f32x4_t (&out)[DT], bool masked, int lo, int hi) const {
+  __device__ __forceinline__ void add_range(const __bf16* mat, const __bf16* rows, f32x4_t (&out)[DT], bool masked, int lo, int hi) const {
     Parts<N> am[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -179,7 +178,7 @@ struct Grad {
       for (int k = 0; k < 2; ++k) {
         // a triangle: rows of this wave's tile hold nothing in the other half
         if (UP ? k < wave / 2 : k > wave / 2) continue;
-        Parts<NP> bm = transposed<NP>(s.rows + (32 * k + 8 * q4 + m / 4) * RowsAt<DK>::stride + 16 * (half * DT + t) + 4 * (m % 4),
+        Parts<NP> bm = transposed<NP>(rows + (32 * k + 8 * q4 + m / 4) * RowsAt<DK>::stride + 16 * (half * DT + t) + 4 * (m % 4),
                                       RowsAt<DK>::stride, RowsAt<DK>::part);
         if (masked) keep(bm, 32 * k + 8 * q4, lo, hi);
         n = mma(am[k], bm, n);
@@ -195,34 +194,42 @@ struct Grad {
   }
   // with something in k or q that is not finite (wild), each sequence by itself
   template <bool UP, int N>
-  __device__ __forceinline__ void add(const __bf16* mat, f32x4_t (&out)[DT], bool wild) const {
+  __device__ __forceinline__ void add(const __bf16* mat, const __bf16* rows, f32x4_t (&out)[DT], bool wild) const {
     int hi = kChunk;
 #pragma clang loop unroll(disable)
     do {
       int lo = 0;
       if (wild)
         for (lo = hi - 1; lo > 0 && s.seq[lo] == s.seq[lo - 1];) --lo;
-      add_range<UP, N>(mat, out, wild, lo, hi);
+      add_range<UP, N>(mat, rows, out, wild, lo, hi);
       hi = lo;
     } while (hi > 0);
   }
 
-  // M = factor * D * acc below (and, EDGE, on) the diagonal, as N parts into LDS.  A half has the columns' tiles half, half + 2.
-  template <bool EDGE, int N>
-  __device__ __forceinline__ void put_matrix(__bf16* to, const f32x4_t (&acc)[2], const f32x4_t (&decay)[2], float factor) const {
+  // acc = factor * D * acc below (and, EDGE, on) the diagonal, zero elsewhere.  A half has the columns' tiles half, half + 2.
+  template <bool EDGE>
+  __device__ __forceinline__ void decayed(f32x4_t (&acc)[2], const f32x4_t (&decay)[2], float factor) const {
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int j = 16 * (half + 2 * n) + m;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = own + r;
-        const bool in = !(decay[n][r] < 0.f) && (EDGE ? j <= i : j < i);  // a NaN decay is wanted
-        __bf16 w[N];
-        split_one<N>(in ? factor * decay[n][r] * acc[n][r] : 0.f, w);
-#pragma unroll
-        for (int p = 0; p < N; ++p) to[(p * kChunk + i) * kLdM + j] = w[p];
+        const bool in = !(decay[n][r] < 0.f) && (EDGE ? j <= own + r : j < own + r);  // a NaN decay is wanted
+        acc[n][r] = in ? factor * decay[n][r] * acc[n][r] : 0.f;
       }
     }
+  }
+  // ... as parts into LDS
+  __device__ __forceinline__ void put_matrix(__bf16* to, const f32x4_t (&acc)[2]) const {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        __bf16 w[kParts];
+        split_one<kParts>(acc[n][r], w);
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) to[(p * kChunk + own + r) * kLdM + 16 * (half + 2 * n) + m] = w[p];
+      }
   }
   // D of those tiles, -1 where the rows are not of one sequence
   __device__ __forceinline__ void get_decay(f32x4_t (&decay)[2]) const {
@@ -238,9 +245,40 @@ struct Grad {
     }
   }
 
-  __device__ __forceinline__ double over_lanes(double v) const {
+  __device__ __forceinline__ float over_lanes(float v) const {
     for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o);
     return v;
+  }
+
+  // M's columns of this wave's tiles, each element with those below it in the wave's 16 rows added
+  __device__ __forceinline__ void columns_of_m(const f32x4_t (&dp)[2], const f32x4_t (&dl)[2], f32x4_t (&sum)[2]) const {
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int tile = half + 2 * n;
+      sum[n] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (tile > wave) continue;
+      f32x4_t qk = sum[n], kk = sum[n];
+#pragma unroll
+      for (int e = 0; e < DK / 32; ++e) {
+        const auto at = [&](const __bf16* x, int row) { return natural<NP>(x + row * RowsAt<DK>::stride + 32 * e + 8 * q4, RowsAt<DK>::part); };
+        const auto kj = at(s.k, 16 * tile + m);
+        qk = mma(at(s.q, 16 * wave + m), kj, qk);
+        kk = mma(at(s.k, 16 * wave + m), kj, kk);
+      }
+      const int j = 16 * tile + m;
+#pragma unroll
+      for (int r = 3; r >= 0; --r)  // zeros of dP and dL stay zero, whatever a row of another sequence holds
+        sum[n][r] = (j < own + r ? times(dp[n][r], qk[r]) + times(dl[n][r], kk[r]) : 0.f) + (r < 3 ? sum[n][r + 1] : 0.f);
+      float below = 0.f;
+#pragma unroll
+      for (int o = 3; o >= 1; --o) {
+        const float x = __shfl(sum[n][0], min(lane + 16 * o, 63));
+        if (q4 + o < 4) below += x;
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) sum[n][r] += below;
+      if (wave > 0 && q4 == 0) s.after[wave - 1][j] = sum[n][0];
+    }
   }
 
   // The gradients of one value head; its share of dq and dk.
@@ -251,28 +289,24 @@ struct Grad {
     const int64_t size = (int64_t)a.dk * a.dv, size_p = (int64_t)a.dk * a.dvp;
     const Range states(a.states_in + (((int64_t)b * a.chunks + c) * a.hv + h) * size, size * 4);
     const Range dstate(a.w.dstate + at * size_p, size_p * 4);
-    const Range before(c ? a.w.dstate + (at - 1) * size_p : a.dh0 + bh * size, (c ? size_p : size) * 4);
-    const int ldb = c ? a.dvp : a.dv;
     const Range zs(a.w.z + at * kChunk * a.dvp, (int64_t)kChunk * a.dvp * 4);
     const Span kept = dense_rows(a, b, h, c, 4);
     const Range xs((const char*)a.x_in + kept.at, kept.bytes);
-    const Range vs = rows_range<T>(a.v, b, h, c * kChunk, a.t, a.dv), dys = rows_range<T>(a.dy, b, h, c * kChunk, a.t, a.dv);
+    const Range dys = rows_range<T>(a.dy, b, h, c * kChunk, a.t, a.dv);
     __syncthreads();  // what is read of the head before
     const float my_beta = load_at<float>(a.w.rows + (at * 4 + 2) * kChunk, (uint32_t)(tid / 8) * 4u);
     Slice x;
     const auto fetch = [&](int v0) {
       load_state(states, v0, a.dv, x.st);
       load_state(dstate, v0, a.dvp, x.ds);
-      load_state(before, v0, ldb, x.be);
       const int col = v0 + tid % 8 * 4;
       load<float, 4>(zs, (uint32_t)(tid / 8 * a.dvp) * 4u, col, a.dvp, &x.z);
       load<float, 4>(xs, (uint32_t)(tid / 8 * a.hv * a.dv) * 4u, col, a.dv, &x.x);
-      load<T, 4>(vs, tid / 8 * row_bytes<T>(a.v), col, a.dv, &x.v);
       load<T, 8>(dys, row() * row_bytes<T>(a.dy), v0 + 8 * q4, a.dv, x.dy.w);
     };
     Parts<NP> yp;
     float db = 0.f;
-    double dot = 0, dxv = 0;
+    double dot = 0;
     // what was fetched, into LDS, and dy into yp
     const auto put = [&] {
       auto& to = s.slice;
@@ -281,16 +315,13 @@ struct Grad {
 #pragma unroll
       for (int n = 0; n < held; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dot = fma((double)x.st[n][e], (double)x.be[n][e], dot);
+        for (int e = 0; e < 4; ++e) dot = fma((double)x.st[n][e], (double)x.ds[n][e], dot);
       f32x4_t u, dx;
-      T v[4];
-      __builtin_memcpy(v, &x.v, sizeof(v));
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         u[e] = my_beta * x.x[e];
         dx[e] = my_beta * x.z[e];
         db = fmaf(x.x[e], x.z[e], db);
-        dxv = fma((double)dx[e], (double)to_f32(v[e]), dxv);
       }
       put_row<kParts>(to.u, u);
       put_row<kParts>(to.dx, dx);
@@ -303,7 +334,7 @@ struct Grad {
     };
     fetch(0);
     if (tid == 0) s.wild = 0;
-    if (tid < 3 * kChunk) s.gates[tid] = a.w.rows[at * 4 * kChunk + tid];
+    if (tid < 2 * kChunk) s.gates[tid] = a.w.rows[at * 4 * kChunk + tid];
     if (tid < kChunk) {
       s.sums[tid] = a.w.sums[at * kChunk + tid];
       s.seq[tid] = a.w.seq[at * kChunk + tid];
@@ -359,62 +390,92 @@ struct Grad {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         dq[t][r] = times(enter[r], a.scale * dq[t][r]);
-        dk[t][r] = times(leave[r], dkc[t][r]) - times(enter[r], dkr[t][r]);
+        dkr[t][r] = times(enter[r], dkr[t][r]);
+        dkc[t][r] = times(leave[r], dkc[t][r]);
       }
     for (int o = 1; o < 64; o <<= 1) dot += __shfl_xor(dot, o);
     if (lane == 0) s.a[4 * half + wave] = dot;
-    for (int o = 1; o < 8; o <<= 1) {
-      db += __shfl_xor(db, o);
-      dxv += __shfl_xor(dxv, o);
-    }
-    if (tid % 8 == 0) {
-      s.red[tid / 8][0] = dxv;
-      s.zx[tid / 8] = db;
-    }
+    for (int o = 1; o < 8; o <<= 1) db += __shfl_xor(db, o);
+    if (tid % 8 == 0) s.zx[tid / 8] = db;
     if (!k.finite() || !q.finite()) s.wild = 1;
-    f32x4_t decay[2];
-    get_decay(decay);
-    renew();
-    put_matrix<true, kParts>(s.p, dp, decay, a.scale);
-    put_matrix<false, kParts>(s.l, dl, decay, -1.f);
-    k.put(s.rows);
+    {
+      f32x4_t decay[2];
+      get_decay(decay);
+      renew();
+      decayed<true>(dp, decay, a.scale);
+      decayed<false>(dl, decay, -1.f);
+    }
+    put_matrix(s.p, dp);
+    put_matrix(s.l, dl);
+    k.put(s.k);
+    q.put(s.q);
     __syncthreads();
     const bool wild = s.wild;
     renew();
-    add<false, kParts>(s.p, dq, wild);
-    renew();
-    add<false, kParts>(s.l, dk, wild);
-    renew();
-    add<true, kParts>(s.l, dk, wild);
-    __syncthreads();
-    q.put(s.rows);
-    __syncthreads();
-    renew();
-    add<true, kParts>(s.p, dk, wild);
-    renew();
+    f32x4_t below[2];
+    columns_of_m(dp, dl, below);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      double g = 0;
+      float e = 0.f, f = 0.f;
 #pragma unroll
-      for (int t = 0; t < DT; ++t) g = fma((double)value(s.rows, own + r, 16 * (half * DT + t) + m), (double)dq[t][r], g);
-      g = over_lanes(g);
-      if (m == 0) s.red[own + r][1 + half] = g;
+      for (int t = 0; t < DT; ++t) {
+        const int d = 16 * (half * DT + t) + m;
+        const float kd = value(s.k, own + r, d);
+        e = fmaf(value(s.q, own + r, d), dq[t][r], e);
+        e = fmaf(-kd, dkr[t][r], e);
+        f = fmaf(kd, dkc[t][r], f);
+      }
+      e = over_lanes(e);
+      f = over_lanes(f);
+      // rows that the state does not reach, or that do not reach it, whatever they hold
+      if (m == 0) s.red[0][half][own + r] = s.gates[own + r] == 0.f ? 0.f : e;
+      if (m == 0) s.red[1][half][own + r] = s.gates[kChunk + own + r] == 0.f ? 0.f : f;
     }
+#pragma unroll
+    for (int t = 0; t < DT; ++t) dk[t] = dkc[t] - dkr[t];
+    __syncthreads();
+    renew();
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int w = 1; w < 4; ++w)
+        if (half + 2 * n <= wave && wave < w) {
+          const float x = s.after[w - 1][16 * (half + 2 * n) + m];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) below[n][r] += x;
+        }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      float g = 0.f;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+        if (16 * (half + 2 * n) + m < own + r) g += below[n][r];
+      g = over_lanes(g);
+      if (m == 0) s.red[2][half][own + r] = g;
+    }
+    renew();
+    add<false, kParts>(s.p, s.k, dq, wild);
+    renew();
+    add<false, kParts>(s.l, s.k, dk, wild);
+    renew();
+    add<true, kParts>(s.l, s.k, dk, wild);
+    renew();
+    add<true, kParts>(s.p, s.q, dk, wild);
     __syncthreads();
     if (tid < kChunk) {
-      const int mine = s.seq[lane], t = c * kChunk + lane;
-      double sum = s.red[lane][0] - (s.red[lane][1] + s.red[lane][2]), g = 0;
-      if (mine == 0)
-        for (int w = 0; w < kT / 64; ++w) g += s.a[w];
-      // the rows before, of the same sequence
+      const int t = c * kChunk + lane;
+      double e = (double)s.red[0][0][lane] + s.red[0][1][lane], f = (double)s.red[1][0][lane] + s.red[1][1][lane], all = 0;
       for (int o = 1; o < 64; o <<= 1) {
-        const double p = __shfl_up(sum, o);
-        const int of = __shfl_up(mine, o);
-        if (lane >= o && of == mine) sum += p;
+        const double x = __shfl_down(e, o), y = __shfl_up(f, o);
+        if (lane + o < 64) e += x;
+        if (lane >= o) f += y;
       }
-      const double p = __shfl_up(sum, 1);
-      const int of = __shfl_up(mine, 1);
-      if (lane > 0 && of == mine) g += p;
+      f = __shfl_up(f, 1);
+      for (int w = 0; w < kT / 64; ++w) all += s.a[w];
+      const float stay = s.gates[kChunk - 1];
+      double g = e + ((double)s.red[2][0][lane] + s.red[2][1][lane]);
+      if (lane > 0) g += f;
+      if (stay != 0.f) g += stay * all;
       if (t < a.t) {
         const int64_t to = ((int64_t)b * a.t + t) * a.hv + h;
         a.dlog_decay[to] = (float)g;
@@ -428,9 +489,7 @@ template <typename T, int DK, bool WHOLE>
 __global__ __launch_bounds__(kT, 2) void delta_grad_kernel(DeltaArgs a) {
   typedef Grad<T, DK, WHOLE> F;
   __shared__ __attribute__((aligned(16))) typename F::Lds s;
-  // neighbouring chunks on one die: each reads the gradient of a state that its neighbour reads too
-  const int id = convfwd::xcd_tile(blockIdx.x, gridDim.x);
-  const int c = id % a.chunks, hk = id / a.chunks % a.hk, b = id / a.chunks / a.hk;
+  const int c = blockIdx.x % a.chunks, hk = blockIdx.x / a.chunks % a.hk, b = blockIdx.x / a.chunks / a.hk;
   F f(a, s, b, c);
   const int share = a.hv / a.hk;
   f32x4_t dq[F::DT], dk[F::DT], sq[F::DT], sk[F::DT];

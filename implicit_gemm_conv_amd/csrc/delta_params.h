@@ -39,7 +39,7 @@ struct DeltaArgs {
   int b, t, hk, hv, dk, dv, dtype;
   int chunks, dvp;  // ceil(T / 64); Dv rounded up to 32
   int dkp;          // elements of a row of q and k as the kernels read them: Dk rounded up to 8
-  int whole;        // dy's and v's rows are whole pieces of 8 elements, 16-byte aligned
+  int whole;        // dy's rows are whole pieces of 8 elements, 16-byte aligned
   float scale;
   Heads q, k, v, dy;
   const float *log_decay, *beta, *h0, *states_in, *x_in, *dh_last;

@@ -153,3 +153,20 @@ def test_a_decay_of_zero_is_a_start(zero, dtype):
     for n in got:
         assert torch.equal(got[n], want[n]), n
     assert (got["dlog_decay"][:, at] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("shape", [(1, 40, 1, 1, 16, 16), (2, 150, 1, 2, 64, 48), (1, 130, 2, 2, 128, 20)], ids=str)
+def test_gradients_of_strong_decays(shape, dtype):
+    """Decays of e^-5 to e^-20, in every row or in one of three.  All that a log decay's gradient is made of has the decay as a
+    factor, so the bound on its error has it too."""
+    b, t = shape[:2]
+    for every, starts in ((1, None), (3, None), (3, "some")):
+        x = inputs(b + t + every, *shape, DT[dtype], DEV, slow=True)
+        strong = -5 - 15 * torch.sigmoid(3 + x["log_decay"])
+        x["log_decay"][:, ::every] = strong[:, ::every]
+        s = starts_of(starts, b, t, DEV)
+        ref = definition(x, None, s)
+        value, bound = ref["dlog_decay"]
+        ref["dlog_decay"] = (value, bound * torch.exp(x["log_decay"].double().cpu()))
+        _check_all(_both(x, s), ref)
