@@ -268,7 +268,7 @@ struct Int {
   static constexpr int value = N;
 };
 // Head sizes are padded to 32, 64 or 128 inside the kernels (4x4096 rows, 16 heads of Dk x 128, bf16, forward and backward:
-// Dk = 64 takes 286 and 651 us, padded to 128 308 and 731; Dk = 32 265 and 562, padded 291 and 687).
+// Dk = 64 takes 298 and 635 us, padded to 128 320 and 752; Dk = 32 278 and 563, padded 303 and 714).
 template <typename F>
 inline hipError_t for_dk(int dk, const F& f) {
   if (dk <= 32) return f(Int<32>{});

@@ -12,12 +12,12 @@
 // costs is that q, k and the chunks' matrices are read by every workgroup of a head, which sit on
 // one die and share its L2.  States in fp32 (accumulators in registers, three bf16 parts in LDS for
 // the products), matrices in three parts, on y's way too: q S and R u may cancel, and two parts there leave 2^-17 of
-// their terms in a 16-bit y (they took 44 us less of 653 for the sequence below, with the preparing).
+// their terms in a 16-bit y (with them the sequence below took 545 us).
 //
 // Bound by the chain of a chunk's steps: LDS, two to four matrix instructions one after the other,
-// LDS, a barrier, three times over, about 4500 clocks a chunk (on the CUs in use matrix units busy 14%, vector units 26%).
-// One sequence of 16387 rows, 16 heads of 128 x 128, bf16: 545 us, 2.1 us a chunk (prefill, 128
-// workgroups on 256 CUs); 4 sequences of 4096, states kept: 291 us, 2.1 TB/s of HBM traffic.
+// LDS, a barrier, three times over, about 4900 clocks a chunk (on the CUs in use matrix units busy 16%, vector units 26%).
+// One sequence of 16387 rows, 16 heads of 128 x 128, bf16: 595 us, 2.3 us a chunk (prefill, 128
+// workgroups on 256 CUs); 4 sequences of 4096, states kept: 316 us, 2.1 TB/s of HBM traffic.
 #include "delta_team.h"
 
 namespace convdelta {

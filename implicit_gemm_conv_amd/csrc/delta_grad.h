@@ -21,11 +21,11 @@
 // columns.  All operands have three parts: with two in what ends in a 16-bit dk alone (2^-17 of its terms) both passes
 // took 30 us less of 1221 at the size below.
 //
-// Reading x instead of solving for it again took 830 to 534 us (4 sequences of 4096 rows, 16 heads of
-// 128 x 128, bf16), loads of a slice ahead of its products 495 us, two slices in LDS and decays without
-// branches 471 us; now 465 us, 1.4 TB/s of HBM traffic.  Bound by vector work (busy 42%: parts of fp32
-// values for the matrix units) in turns with LDS, in one workgroup of 232 registers and 157 KB a CU, whose
-// start and end (20 of 66 thousand clocks) nothing covers.  Included by one source for each type.
+// 4 sequences of 4096 rows, 16 heads of 128 x 128, bf16: 504 us, 1.4 TB/s of HBM traffic.  (Reading x instead of
+// solving for it again took 830 to 534 us, loads of a slice ahead of its products 495 us, decays without branches
+// 471 us, all of them with two parts in dk's operands; three added 30 us.)  Bound by vector work (busy
+// 43%: parts of fp32 values for the matrix units; these 17%) in turns with LDS, in one workgroup of 226 registers
+// a CU, whose start and end nothing covers.  Included by one source for each type.
 #include "delta_team.h"
 
 namespace convdelta {
@@ -92,8 +92,8 @@ struct Grad {
     Raw8<T> dy;
   };
   // N neighbouring elements of a row, zero past its end: as pieces of at most 16 bytes, where rows are whole ones (WHOLE)
-  // or of fp32, whose pieces need no more than their own alignment (4x4096 rows, 16 heads of 128 x 128, bf16: 820 us for
-  // the whole backward pass, 899 with v and dy element by element; v is no longer read here).
+  // or of fp32, whose pieces need no more than their own alignment (4x4096 rows, 16 heads of 128 x 128, bf16: 842 us for
+  // the whole backward pass, 915 with dy element by element).
   template <typename E, int N>
   __device__ __forceinline__ void load(const Range& x, uint32_t row, int col, int width, void* to) const {
     constexpr int n = WHOLE || sizeof(E) == 4 ? (N * sizeof(E) > 16 ? 16 / sizeof(E) : N) : 1;
