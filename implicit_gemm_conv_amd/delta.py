@@ -130,8 +130,9 @@ def delta_rule(q, k, v, log_decay, beta, scale=None, h0=None, starts=None, train
     q, k (B, T, Hk, Dk), Dk <= 128, and v (B, T, Hv, Dv) of one dtype, Hv a multiple of Hk (value head h reads
     key head h // (Hv / Hk)); log_decay and beta (B, T, Hv) fp32.  With a = exp(log_decay):
     S' = a S, S = S' + k (beta (v - S'^T k))^T, y = scale S^T q; scale is Dk^-0.5 if None.  q and k are
-    taken as they are: a layer brings them to length one itself.  h0 (B, Hv, Dk, Dv) fp32 is the state
-    before the first row (zeros if None); starts (B, T), bool or uint8, marks rows that begin a new
+    taken as they are: a layer brings them to length one itself.  Log decays above zero cost precision, and a
+    decay of zero begins a sequence.  h0 (B, Hv, Dk, Dv) fp32 is the state before the first row (zeros if
+    None); starts (B, T), bool or uint8, marks rows that begin a new
     sequence.  train returns what delta_rule_bwd needs in `states`."""
     q, k, v, log_decay, beta, scale = _inputs(q, k, v, log_decay, beta, scale, 4)
     b, t, hv, dv = v.shape
